@@ -322,6 +322,83 @@ nq_status nq_balance_factors(const float* u_hat, int64_t d_out, int64_t ldu, con
                              size_t workspace_bytes, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection: adapter a of
+ * a pool adds scale[a] * B_a A_a to a linear, A_a [r][d_in], B_a [d_out][r]
+ * real (an adapter of a smaller rank has zero rows in A_a or zero columns in
+ * B_a).  Tokens of one call may take different adapters.
+ */
+typedef struct {
+  int64_t n;               /* adapters in the pool, 1 .. NQ_LORA_MAX_ADAPTERS */
+  int64_t d_out, d_in, r;  /* all >= 1 */
+  nq_dtype dtype;          /* of a and b: NQ_F32 or NQ_BF16 */
+  const void* a;           /* A_a[k][j] at a[a*stride_a + k*lda + j], lda >= d_in */
+  int64_t lda, stride_a;   /* in elements */
+  const void* b;           /* B_a[i][k] at b[a*stride_b + i*ldb + k], ldb >= r */
+  int64_t ldb, stride_b;
+  const float* scale;      /* [n] fp32 */
+} nq_lora;
+#define NQ_LORA_MAX_ADAPTERS 8192
+#define NQ_LORA_MAX_RANK 1024
+
+/*
+ * nq_lora_linear -- y[t] = base[t] + scale[a] * B_a (A_a x[t]),  a = ids[t].
+ *   x: [T][d_in] row-major, fp32 or bf16 (x_dtype); ids: [T] int32 device;
+ *   base: [T][d_out] fp32, the shared projection's output, or null (zeros);
+ *   y: [T][d_out] fp32, fully overwritten; y may be base (in place).
+ *   ids[t] < 0: no adapter, y[t] = base[t].  ids[t] >= n: row t of y is NaN
+ *   (ids is device data, which a call cannot check on the host).
+ * The hidden vectors A_a x[t] and all sums are fp32: nothing is rounded to
+ * fewer bits, whatever the types of x and of the factors.  Values that are not
+ * finite stay within the rows whose x, base or adapter holds them.  Summation
+ * order is fixed: results are run-to-run deterministic, but the order depends
+ * on T and n.
+ *   workspace: at least nq_lora_workspace_bytes(P, T) bytes, 256-byte aligned;
+ *   calls that may overlap (streams, graphs replayed beside other calls) need a
+ *   workspace each.
+ * Errors: NQ_ERR_ARG for null pointers, sizes < 1, lda < d_in, ldb < r, a
+ * negative adapter stride, T < 1, an unknown dtype or a pointer not aligned to
+ * its elements; NQ_ERR_UNSUPPORTED for n > NQ_LORA_MAX_ADAPTERS,
+ * r > NQ_LORA_MAX_RANK, d_out or d_in > 2^24 or T > 2^24; NQ_ERR_WORKSPACE when workspace_bytes
+ * is too small; NQ_ERR_HIP when a launch fails.  The size query returns 0 for
+ * invalid arguments.
+ */
+size_t nq_lora_workspace_bytes(const nq_lora* P, int64_t T);
+nq_status nq_lora_linear(const nq_lora* P, const void* x, nq_dtype x_dtype, const int32_t* ids, int64_t T,
+                         const float* base, float* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * nq_lrb_lora_linear -- nq_lrb_linear followed by nq_lora_linear on its output:
+ *   y = W x (W the packed layer L) plus each token's adapter.  P's d_out and
+ *   d_in must be L's.  The same y as the two calls, bit for bit.
+ *   workspace: at least nq_lrb_lora_workspace_bytes(L, P, T) bytes, 256-byte
+ *   aligned.  Errors: as for the two calls; NQ_ERR_ARG if the sizes differ.
+ */
+size_t nq_lrb_lora_workspace_bytes(const nq_lrb* L, const nq_lora* P, int64_t T);
+nq_status nq_lrb_lora_linear(const nq_lrb* L, const nq_lora* P, const void* x, nq_dtype x_dtype, const int32_t* ids,
+                             int64_t T, float* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * nq_lora_grads -- the gradients of nq_lora_linear for g = dL/dy:
+ *     dx[t]   = dx_base[t] + scale[a] * A_a^T (B_a^T g[t])
+ *     da[a]   = scale[a] * sum over a's tokens of (B_a^T g[t]) x[t]^T    [r][d_in]
+ *     db[a]   = scale[a] * sum over a's tokens of g[t] (A_a x[t])^T      [d_out][r]
+ *   x: [T][d_in] (x_dtype), g: [T][d_out] (g_dtype), fp32 or bf16; dx_base:
+ *   [T][d_in] fp32 (the shared projection's dx, as from nq_lrb_scale_grads) or
+ *   null (zeros); dx: [T][d_in] fp32, may be dx_base (in place); da:
+ *   [n][r][d_in] and db: [n][d_out][r] fp32, contiguous and fully overwritten
+ *   (zeros for adapters without tokens).  ids as in nq_lora_linear: a token
+ *   without an adapter has dx[t] = dx_base[t], one with an id out of range a NaN
+ *   row of dx, and neither enters da or db.  Arithmetic, determinism and errors
+ *   as for nq_lora_linear.
+ *   workspace: at least nq_lora_grads_workspace_bytes(P, T) bytes, 256-byte
+ *   aligned.
+ */
+size_t nq_lora_grads_workspace_bytes(const nq_lora* P, int64_t T);
+nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const void* g, nq_dtype g_dtype,
+                        const int32_t* ids, int64_t T, const float* dx_base, float* dx, float* da, float* db,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * nq_fill_random_words -- synthetic sign words for large benchmark matrices:
  *   dst[i] = low 32 bits of SplitMix64(seed, i), i < n, where SplitMix64(seed,
  *   i) is output number i+1 of the SplitMix64 stream started at `seed`

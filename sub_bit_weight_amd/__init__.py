@@ -8,7 +8,8 @@ Names follow the C ABI in include/nq.h:
   pack_signs, unpack_signs, lrb_linear, lrb_workspace_bytes, reconstruct,
   storage_bits, fill_random_words, Seq (nq_seq_*), transpose_signs,
   lrb_scale_grads (nq_lrb_scale_grads*), lrb_scale_grads_batch
-  (nq_lrb_scale_grads_batch*), last_error.
+  (nq_lrb_scale_grads_batch*), Lora (nq_lora), lora_linear, lora_grads,
+  lrb_lora_linear, last_error.
 """
 from __future__ import annotations
 
@@ -34,6 +35,8 @@ EXPORTED = [
     "nq_lrb_scale_grads_workspace_bytes", "nq_lrb_scale_grads", "nq_lrb_scale_grads_batch_workspace_bytes",
     "nq_lrb_scale_grads_batch", "nq_balance_workspace_bytes",
     "nq_balance_factors", "nq_lrb_latent_workspace_bytes", "nq_lrb_linear_latent", "nq_lrb_linear_noalloc",
+    "nq_lora_workspace_bytes", "nq_lora_linear", "nq_lrb_lora_workspace_bytes", "nq_lrb_lora_linear",
+    "nq_lora_grads_workspace_bytes", "nq_lora_grads",
 ]
 
 # Size of the library's fixed per-GPU workspace array (NQ_NOALLOC_SCRATCH_BYTES in nq.h).
@@ -52,6 +55,16 @@ class nq_lrb(ctypes.Structure):
         ("u_bits", ctypes.c_void_p), ("ldu", ctypes.c_int64),
         ("vt_bits", ctypes.c_void_p), ("ldv", ctypes.c_int64),
         ("s1", ctypes.c_void_p), ("s2", ctypes.c_void_p),
+    ]
+
+
+class nq_lora(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("d_out", ctypes.c_int64), ("d_in", ctypes.c_int64), ("r", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("stride_a", ctypes.c_int64),
+        ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+        ("scale", ctypes.c_void_p),
     ]
 
 
@@ -113,6 +126,18 @@ def lib() -> ctypes.CDLL:
     L.nq_balance_workspace_bytes.restype = sz
     L.nq_balance_factors.argtypes = [vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp]
     L.nq_balance_factors.restype = st
+    L.nq_lora_workspace_bytes.argtypes = [P(nq_lora), i64]
+    L.nq_lora_workspace_bytes.restype = sz
+    L.nq_lora_linear.argtypes = [P(nq_lora), vp, ctypes.c_int, vp, i64, vp, vp, vp, sz, vp]
+    L.nq_lora_linear.restype = st
+    L.nq_lrb_lora_workspace_bytes.argtypes = [P(nq_lrb), P(nq_lora), i64]
+    L.nq_lrb_lora_workspace_bytes.restype = sz
+    L.nq_lrb_lora_linear.argtypes = [P(nq_lrb), P(nq_lora), vp, ctypes.c_int, vp, i64, vp, vp, sz, vp]
+    L.nq_lrb_lora_linear.restype = st
+    L.nq_lora_grads_workspace_bytes.argtypes = [P(nq_lora), i64]
+    L.nq_lora_grads_workspace_bytes.restype = sz
+    L.nq_lora_grads.argtypes = [P(nq_lora), vp, ctypes.c_int, vp, ctypes.c_int, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.nq_lora_grads.restype = st
     L.nq_last_error.argtypes = []
     L.nq_last_error.restype = ctypes.c_char_p
     L.nq_version.argtypes = []
@@ -452,6 +477,171 @@ def lrb_scale_grads_batch(layers, adjs, xs, gs, workspace: torch.Tensor | None =
         ptrs([o[1] for o in outs]), ptrs([o[2] for o in outs]), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
     return outs
+
+
+# ---------------------------------------------------------------- adapters
+
+
+@dataclass
+class Lora:
+    """A pool of low-rank adapters of one linear on the device: adapter i adds
+    scale[i] * b[i] @ a[i].  a and b share a dtype (float32 or bfloat16) and may
+    be strided views whose last dimension is contiguous."""
+    a: torch.Tensor      # [n][r][d_in]
+    b: torch.Tensor      # [n][d_out][r]
+    scale: torch.Tensor  # [n] float32
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_struct", None)  # any field change re-validates
+
+    @property
+    def n(self) -> int:
+        return self.a.shape[0]
+
+    @property
+    def r(self) -> int:
+        return self.a.shape[1]
+
+    @property
+    def d_in(self) -> int:
+        return self.a.shape[2]
+
+    @property
+    def d_out(self) -> int:
+        return self.b.shape[1]
+
+    def struct(self) -> nq_lora:
+        """The C struct, after checking what the C ABI cannot see.  Built once and
+        kept until a field is assigned again; tensors must not be resized in place
+        while the pool is in use."""
+        cached = self.__dict__.get("_struct")
+        if cached is not None:
+            return cached
+        a, b, scale = self.a, self.b, self.scale
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError(f"a must be [n][r][d_in] and b [n][d_out][r], got {tuple(a.shape)} and {tuple(b.shape)}")
+        if a.numel() == 0 or b.numel() == 0:
+            raise ValueError(f"sizes must be >= 1: a {tuple(a.shape)}, b {tuple(b.shape)}")
+        if b.dtype != a.dtype:
+            raise ValueError(f"a and b must share a dtype, got {a.dtype} and {b.dtype}")
+        dtype = _x_dtype(a)
+        if scale.dtype != torch.float32 or tuple(scale.shape) != (a.shape[0],):
+            raise ValueError(f"scale must be float32 [{a.shape[0]}], got {scale.dtype} {tuple(scale.shape)}")
+        _dev(scale, "scale")
+        for t, name in ((a, "a"), (b, "b")):
+            if not t.is_cuda or t.device != scale.device:
+                raise ValueError(f"{name} must be a device tensor on the device of scale")
+            if t.stride(2) != 1 and t.shape[2] > 1:
+                raise ValueError(f"{name} must have a contiguous last dimension")
+        # a dimension of one element may carry any stride
+        lda = a.stride(1) if a.shape[1] > 1 else max(a.stride(1), a.shape[2])
+        ldb = b.stride(1) if b.shape[1] > 1 else max(b.stride(1), b.shape[2])
+        st = nq_lora(a.shape[0], b.shape[1], a.shape[2], a.shape[1], dtype, a.data_ptr(), lda, a.stride(0),
+                     b.data_ptr(), ldb, b.stride(0), scale.data_ptr())
+        object.__setattr__(self, "_struct", st)
+        return st
+
+
+def _lora_args(pool: Lora, x: torch.Tensor, ids: torch.Tensor) -> int:
+    _dev(x, "x")
+    _dev(ids, "ids")
+    if x.dim() != 2 or x.shape[1] != pool.d_in:
+        raise ValueError(f"x must be [T][{pool.d_in}], got {tuple(x.shape)}")
+    T = x.shape[0]
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (T,):
+        raise ValueError(f"ids must be int32 [{T}], got {ids.dtype} {tuple(ids.shape)}")
+    if not x.device == ids.device == pool.scale.device:
+        raise ValueError(f"x, ids and the adapters must share a device: {x.device}, {ids.device}, {pool.scale.device}")
+    return T
+
+
+def _f32_rows(t: torch.Tensor, name: str, shape: tuple, device) -> None:
+    _dev(t, name)
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be float32 {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def lora_workspace_bytes(pool: Lora, T: int) -> int:
+    return int(lib().nq_lora_workspace_bytes(ctypes.byref(pool.struct()), T))
+
+
+def lora_linear(pool: Lora, x: torch.Tensor, ids: torch.Tensor, base: torch.Tensor | None = None,
+                y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] = base[t] + scale[i] * b[i] @ (a[i] @ x[t]), i = ids[t]; x [T][d_in] fp32/bf16, ids [T]
+    int32 (negative: no adapter; >= n: a NaN row), base [T][d_out] fp32 or None (zeros); y may be base."""
+    T = _lora_args(pool, x, ids)
+    s = pool.struct()
+    dev = x.device
+    if base is not None:
+        _f32_rows(base, "base", (T, pool.d_out), dev)
+    if y is not None:
+        _f32_rows(y, "y", (T, pool.d_out), dev)
+    with torch.cuda.device(dev), _on(stream):
+        if y is None:
+            y = torch.empty((T, pool.d_out), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(max(int(lib().nq_lora_workspace_bytes(ctypes.byref(s), T)), 1), dtype=torch.uint8,
+                                    device=dev)
+        _check(lib().nq_lora_linear(ctypes.byref(s), _ptr(x), _x_dtype(x), _ptr(ids), T, _ptr(base), _ptr(y),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream, dev.index)))
+    return y
+
+
+def lrb_lora_workspace_bytes(layer: Lrb, pool: Lora, T: int) -> int:
+    return int(lib().nq_lrb_lora_workspace_bytes(ctypes.byref(layer.struct()), ctypes.byref(pool.struct()), T))
+
+
+def lrb_lora_linear(layer: Lrb, pool: Lora, x: torch.Tensor, ids: torch.Tensor, y: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """lrb_linear(layer, x) with each token's adapter added (lora_linear on its output, in place)."""
+    T = _lora_args(pool, x, ids)
+    s, p = layer.struct(), pool.struct()
+    dev = x.device
+    if y is not None:
+        _f32_rows(y, "y", (T, layer.d_out), dev)
+    with torch.cuda.device(dev), _on(stream):
+        if y is None:
+            y = torch.empty((T, layer.d_out), dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = int(lib().nq_lrb_lora_workspace_bytes(ctypes.byref(s), ctypes.byref(p), T))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _check(lib().nq_lrb_lora_linear(ctypes.byref(s), ctypes.byref(p), _ptr(x), _x_dtype(x), _ptr(ids), T, _ptr(y),
+                                        _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                        _stream(stream, dev.index)))
+    return y
+
+
+def lora_grads_workspace_bytes(pool: Lora, T: int) -> int:
+    return int(lib().nq_lora_grads_workspace_bytes(ctypes.byref(pool.struct()), T))
+
+
+def lora_grads(pool: Lora, x: torch.Tensor, g: torch.Tensor, ids: torch.Tensor, dx_base: torch.Tensor | None = None,
+               dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """(dx, da, db) of lora_linear for g = dL/dy [T][d_out] (fp32/bf16): dx [T][d_in] (dx_base added when given;
+    dx may be dx_base), da [n][r][d_in], db [n][d_out][r], all fp32."""
+    T = _lora_args(pool, x, ids)
+    _dev(g, "g")
+    if tuple(g.shape) != (T, pool.d_out) or g.device != x.device:
+        raise ValueError(f"g must be [{T}][{pool.d_out}] on {x.device}, got {tuple(g.shape)} on {g.device}")
+    s = pool.struct()
+    dev = x.device
+    for t, name in ((dx_base, "dx_base"), (dx, "dx")):
+        if t is not None:
+            _f32_rows(t, name, (T, pool.d_in), dev)
+    with torch.cuda.device(dev), _on(stream):
+        if dx is None:
+            dx = torch.empty((T, pool.d_in), dtype=torch.float32, device=dev)
+        da = torch.empty((pool.n, pool.r, pool.d_in), dtype=torch.float32, device=dev)
+        db = torch.empty((pool.n, pool.d_out, pool.r), dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = int(lib().nq_lora_grads_workspace_bytes(ctypes.byref(s), T))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _check(lib().nq_lora_grads(ctypes.byref(s), _ptr(x), _x_dtype(x), _ptr(g), _x_dtype(g), _ptr(ids), T,
+                                   _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream, dev.index)))
+    return dx, da, db
 
 
 def balance_factors(u_hat: torch.Tensor, v_hat: torch.Tensor, r: int | None = None, balanced: bool = True,

@@ -703,6 +703,121 @@ nq_status nq_lrb_scale_grads_batch(int64_t n, const nq_lrb* L, const uint32_t* c
   return hip_status(e, "nq_lrb_scale_grads_batch launch");
 }
 
+namespace {
+
+nq_status check_lora(const char* who, const nq_lora* P) {
+  if (!P) return set_error("%s: null adapter pool", who), NQ_ERR_ARG;
+  if (P->n < 1 || P->d_out < 1 || P->d_in < 1 || P->r < 1)
+    return set_error("%s: adapters n=%lld d_out=%lld d_in=%lld r=%lld must be >= 1", who, (long long)P->n,
+                     (long long)P->d_out, (long long)P->d_in, (long long)P->r),
+           NQ_ERR_ARG;
+  if (P->n > NQ_LORA_MAX_ADAPTERS || P->r > NQ_LORA_MAX_RANK)
+    return set_error("%s: %lld adapters of rank %lld exceed %d of rank %d", who, (long long)P->n, (long long)P->r,
+                     NQ_LORA_MAX_ADAPTERS, NQ_LORA_MAX_RANK),
+           NQ_ERR_UNSUPPORTED;
+  if (P->d_out > (int64_t(1) << 24) || P->d_in > (int64_t(1) << 24))
+    return set_error("%s: dimension exceeds 2^24", who), NQ_ERR_UNSUPPORTED;
+  if (P->dtype != NQ_F32 && P->dtype != NQ_BF16)
+    return set_error("%s: unknown adapter dtype %d", who, (int)P->dtype), NQ_ERR_ARG;
+  if (!P->a || !P->b || !P->scale) return set_error("%s: null adapter factor or scale", who), NQ_ERR_ARG;
+  const size_t e = P->dtype == NQ_F32 ? 4 : 2;
+  if (!aligned(P->a, e) || !aligned(P->b, e) || !aligned(P->scale, 4))
+    return set_error("%s: adapter factor or scale misaligned", who), NQ_ERR_ARG;
+  if (P->lda < P->d_in || P->ldb < P->r || P->stride_a < 0 || P->stride_b < 0)
+    return set_error("%s: adapter strides lda=%lld ldb=%lld (%lld, %lld) do not fit d_in=%lld r=%lld", who,
+                     (long long)P->lda, (long long)P->ldb, (long long)P->stride_a, (long long)P->stride_b,
+                     (long long)P->d_in, (long long)P->r),
+           NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+nq_status check_ids(const char* who, const int32_t* ids) {
+  if (!ids || !aligned(ids, 4)) return set_error("%s: ids null or misaligned", who), NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+nq_status check_workspace(const char* who, const void* workspace, size_t bytes, size_t need) {
+  if (!workspace || bytes < need)
+    return set_error("%s: workspace %zu bytes, need %zu", who, workspace ? bytes : 0, need), NQ_ERR_WORKSPACE;
+  if (!aligned(workspace, kAlign)) return set_error("%s: workspace not 256-byte aligned", who), NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+bool lora_query_ok(const char* who, const nq_lora* P, int64_t T) {
+  return check_lora(who, P) == NQ_OK && T >= 1 && T <= (int64_t(1) << 24);
+}
+
+}  // namespace
+
+size_t nq_lora_workspace_bytes(const nq_lora* P, int64_t T) {
+  return lora_query_ok("nq_lora_workspace_bytes", P, T) ? lora_workspace(*P, T, false) : 0;
+}
+
+nq_status nq_lora_linear(const nq_lora* P, const void* x, nq_dtype x_dtype, const int32_t* ids, int64_t T,
+                         const float* base, float* y, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "nq_lora_linear";
+  nq_status st = check_lora(who, P);
+  if (st == NQ_OK) st = check_io(who, nullptr, x, x_dtype, T, y);
+  if (st == NQ_OK) st = check_ids(who, ids);
+  if (st != NQ_OK) return st;
+  if (!aligned(base, 4)) return set_error("%s: base misaligned", who), NQ_ERR_ARG;
+  if ((st = check_workspace(who, workspace, workspace_bytes, lora_workspace(*P, T, false))) != NQ_OK) return st;
+  return hip_status(launch_lora_linear(*P, x, x_dtype, ids, T, base, y, workspace, (hipStream_t)stream),
+                    "nq_lora_linear launch");
+}
+
+size_t nq_lrb_lora_workspace_bytes(const nq_lrb* L, const nq_lora* P, int64_t T) {
+  const char* who = "nq_lrb_lora_workspace_bytes";
+  if (check_lrb(who, L) != NQ_OK || !lora_query_ok(who, P, T)) return 0;
+  return align_up(linear_workspace(*L, T)) + lora_workspace(*P, T, false);
+}
+
+nq_status nq_lrb_lora_linear(const nq_lrb* L, const nq_lora* P, const void* x, nq_dtype x_dtype, const int32_t* ids,
+                             int64_t T, float* y, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "nq_lrb_lora_linear";
+  nq_status st = check_lrb(who, L);
+  if (st == NQ_OK) st = check_lora(who, P);
+  if (st == NQ_OK) st = check_io(who, L, x, x_dtype, T, y);
+  if (st == NQ_OK) st = check_ids(who, ids);
+  if (st != NQ_OK) return st;
+  if (P->d_out != L->d_out || P->d_in != L->d_in)
+    return set_error("%s: adapters of a %lld x %lld linear beside a %lld x %lld layer", who, (long long)P->d_out,
+                     (long long)P->d_in, (long long)L->d_out, (long long)L->d_in),
+           NQ_ERR_ARG;
+  const size_t lin = align_up(linear_workspace(*L, T));
+  if ((st = check_workspace(who, workspace, workspace_bytes, lin + lora_workspace(*P, T, false))) != NQ_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = launch_linear(*L, x, x_dtype, T, y, workspace, s);
+  if (e == hipSuccess)
+    e = launch_lora_linear(*P, x, x_dtype, ids, T, y, y, static_cast<char*>(workspace) + lin, s);
+  return hip_status(e, "nq_lrb_lora_linear launch");
+}
+
+size_t nq_lora_grads_workspace_bytes(const nq_lora* P, int64_t T) {
+  return lora_query_ok("nq_lora_grads_workspace_bytes", P, T) ? lora_workspace(*P, T, true) : 0;
+}
+
+nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const void* g, nq_dtype g_dtype,
+                        const int32_t* ids, int64_t T, const float* dx_base, float* dx, float* da, float* db,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "nq_lora_grads";
+  nq_status st = check_lora(who, P);
+  if (st == NQ_OK) st = check_io(who, nullptr, x, x_dtype, T, dx);
+  if (st == NQ_OK) st = check_ids(who, ids);
+  if (st != NQ_OK) return st;
+  if (g_dtype != NQ_F32 && g_dtype != NQ_BF16) return set_error("%s: unknown g dtype %d", who, (int)g_dtype), NQ_ERR_ARG;
+  if (!g || !da || !db) return set_error("%s: null g, da or db", who), NQ_ERR_ARG;
+  if (!aligned(g, g_dtype == NQ_F32 ? 4 : 2) || !aligned(da, 4) || !aligned(db, 4) || !aligned(dx_base, 4))
+    return set_error("%s: g, dx_base, da or db misaligned", who), NQ_ERR_ARG;
+  if ((st = check_workspace(who, workspace, workspace_bytes, lora_workspace(*P, T, true))) != NQ_OK) return st;
+  return hip_status(
+      launch_lora_grads(*P, x, x_dtype, g, g_dtype, ids, T, dx_base, dx, da, db, workspace, (hipStream_t)stream),
+      "nq_lora_grads launch");
+}
+
 size_t nq_balance_workspace_bytes(int64_t d_out, int64_t d_in) {
   if (d_out < 1 || d_in < 1 || d_out > (int64_t(1) << 30) || d_in > (int64_t(1) << 30)) return 0;
   return balance_workspace_bytes(d_out, d_in);

@@ -169,4 +169,15 @@ int64_t prefill_row_blocks(int64_t T);  // the 128-row blocks of a T-token outpu
 hipError_t launch_prefill(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y,
                           void* ws, hipStream_t s, bool split = true, const ProdEpilogue* pe = nullptr);
 
+// Low-rank adapters beside a shared projection (lora.hip): tokens are grouped
+// into tiles of kLoraTile slots of one adapter.  grads: the workspace of the
+// gradients, otherwise of the forward product.
+constexpr int kLoraTile = 32;
+size_t lora_workspace(const nq_lora& P, int64_t T, bool grads);
+hipError_t launch_lora_linear(const nq_lora& P, const void* x, nq_dtype xd, const int32_t* ids, int64_t T,
+                              const float* base, float* y, void* workspace, hipStream_t s);
+hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const void* g, nq_dtype gd,
+                             const int32_t* ids, int64_t T, const float* dx_base, float* dx, float* da, float* db,
+                             void* workspace, hipStream_t s);
+
 }  // namespace nq
