@@ -399,6 +399,40 @@ nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * nq_orthogonalize -- Newton-Schulz orthogonalisation of a batch of matrices:
+ * the update that takes a factor's gradient (latent U or V, an adapter's A or
+ * B) and sets its singular values near one.  From X0 = X / ||X||_F, `steps`
+ * times
+ *     X <- ca X + (cb G + cc G^2) X,   G = X X^T
+ * (X^T in place of X where rows > cols: the same result), that is, every
+ * singular value s becomes ca s + cb s^3 + cc s^5.
+ *   x: [batch] matrices of rows x cols, element (i, j) of matrix k at
+ *   x[k*stride_x + i*ldx + j], fp32 or bf16; y: [batch][rows][cols] contiguous,
+ *   fp32 or bf16 (y_dtype), must not overlap x.
+ * A zero matrix gives zeros; one with a value that is not finite gives NaN
+ * throughout and leaves the other matrices of the batch alone.  Entries of any
+ * size are fine (the norm is fp64).
+ * Arithmetic: a shorter side up to 64 is computed in fp64 and rounded once.  A
+ * longer one keeps the iterate in fp32 and multiplies fp16 operands with fp32
+ * accumulation: one fp16 term each for y in bf16, two (22 bits) for y in fp32.
+ * Deterministic.
+ *   steps: 1 .. 64; the coefficients must be finite and must map [0, 1.25] into
+ *   [-1.25, 1.25], so that no iterate leaves the operands' range (3.4445,
+ *   -4.7750, 2.0315 and 1.5, -0.5, 0 do).
+ *   workspace: at least nq_orthogonalize_workspace_bytes(batch, rows, cols,
+ *   y_dtype) bytes, 256-byte aligned (the query returns 0 for invalid
+ *   arguments).
+ * Errors: NQ_ERR_ARG for null or misaligned pointers, sizes < 1, ldx < cols, a
+ * negative stride_x, unknown dtypes, steps or coefficients outside the above;
+ * NQ_ERR_UNSUPPORTED for batch > 65535, a side above 2^24 or both sides above
+ * 65536; NQ_ERR_WORKSPACE; NQ_ERR_HIP.
+ */
+size_t nq_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, nq_dtype y_dtype);
+nq_status nq_orthogonalize(const void* x, nq_dtype x_dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ldx,
+                           int64_t stride_x, int32_t steps, double ca, double cb, double cc, void* y, nq_dtype y_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * nq_fill_random_words -- synthetic sign words for large benchmark matrices:
  *   dst[i] = low 32 bits of SplitMix64(seed, i), i < n, where SplitMix64(seed,
  *   i) is output number i+1 of the SplitMix64 stream started at `seed`

@@ -50,3 +50,19 @@ def lora_abs(a, b, scale, x, ids, base=None):
 def lora_grads_abs(a, b, scale, x, g, ids, dx_base=None):
     return lora_grads_ref(np.abs(a), np.abs(b), np.abs(scale), np.abs(x), np.abs(g), ids,
                           None if dx_base is None else np.abs(dx_base))
+
+
+def orthogonalize_ref(x, steps, coeffs):
+    """`steps` times X <- a X + (b G + c G^2) X, G = X X^T, from X / ||X||_F; a zero matrix stays zero."""
+    x = np.asarray(x, dtype=np.float64)
+    norm = np.linalg.norm(x)
+    x = x / norm if norm != 0 else x
+    a, b, c = coeffs
+    for _ in range(steps):
+        if x.shape[0] <= x.shape[1]:
+            g = x @ x.T
+            x = a * x + b * (g @ x) + c * (g @ (g @ x))
+        else:  # the same polynomial from the other side
+            g = x.T @ x
+            x = a * x + b * (x @ g) + c * ((x @ g) @ g)
+    return x

@@ -9,7 +9,7 @@ Names follow the C ABI in include/nq.h:
   storage_bits, fill_random_words, Seq (nq_seq_*), transpose_signs,
   lrb_scale_grads (nq_lrb_scale_grads*), lrb_scale_grads_batch
   (nq_lrb_scale_grads_batch*), Lora (nq_lora), lora_linear, lora_grads,
-  lrb_lora_linear, last_error.
+  lrb_lora_linear, orthogonalize, last_error.
 """
 from __future__ import annotations
 
@@ -36,7 +36,7 @@ EXPORTED = [
     "nq_lrb_scale_grads_batch", "nq_balance_workspace_bytes",
     "nq_balance_factors", "nq_lrb_latent_workspace_bytes", "nq_lrb_linear_latent", "nq_lrb_linear_noalloc",
     "nq_lora_workspace_bytes", "nq_lora_linear", "nq_lrb_lora_workspace_bytes", "nq_lrb_lora_linear",
-    "nq_lora_grads_workspace_bytes", "nq_lora_grads",
+    "nq_lora_grads_workspace_bytes", "nq_lora_grads", "nq_orthogonalize_workspace_bytes", "nq_orthogonalize",
 ]
 
 # Size of the library's fixed per-GPU workspace array (NQ_NOALLOC_SCRATCH_BYTES in nq.h).
@@ -138,6 +138,12 @@ def lib() -> ctypes.CDLL:
     L.nq_lora_grads_workspace_bytes.restype = sz
     L.nq_lora_grads.argtypes = [P(nq_lora), vp, ctypes.c_int, vp, ctypes.c_int, vp, i64, vp, vp, vp, vp, vp, sz, vp]
     L.nq_lora_grads.restype = st
+    f64 = ctypes.c_double
+    L.nq_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64, ctypes.c_int]
+    L.nq_orthogonalize_workspace_bytes.restype = sz
+    L.nq_orthogonalize.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, ctypes.c_int32, f64, f64, f64, vp,
+                                   ctypes.c_int, vp, sz, vp]
+    L.nq_orthogonalize.restype = st
     L.nq_last_error.argtypes = []
     L.nq_last_error.restype = ctypes.c_char_p
     L.nq_version.argtypes = []
@@ -642,6 +648,56 @@ def lora_grads(pool: Lora, x: torch.Tensor, g: torch.Tensor, ids: torch.Tensor, 
                                    _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(), _stream(stream, dev.index)))
     return dx, da, db
+
+
+# ---------------------------------------------------------------- updates
+
+
+# A quintic that drives singular values to around one in five steps from a flat start.
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize_workspace_bytes(batch: int, rows: int, cols: int, out_dtype: torch.dtype = torch.float32) -> int:
+    code = NQ_BF16 if out_dtype == torch.bfloat16 else NQ_F32
+    return int(lib().nq_orthogonalize_workspace_bytes(batch, rows, cols, code))
+
+
+def orthogonalize(x: torch.Tensor, steps: int = 5, coeffs=NEWTON_SCHULZ, out_dtype: torch.dtype | None = None,
+                  y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation of x [rows][cols] or [batch][rows][cols] (fp32 or bf16; strided
+    views with a contiguous last dimension are fine): `steps` times X <- a X + (b G + c G^2) X with
+    G = X X^T, from X / ||X||_F.  The result is fp32 or bf16 (out_dtype, default x's); bf16 takes a
+    third of the products of fp32 when the shorter side exceeds 64."""
+    if x.dim() not in (2, 3) or x.numel() == 0:
+        raise ValueError(f"x must be [rows][cols] or [batch][rows][cols], got {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("x must have a contiguous last dimension")
+    batch = x.shape[0] if x.dim() == 3 else 1
+    rows, cols = x.shape[-2:]
+    if y is not None:
+        _dev(y, "y")
+        if tuple(y.shape) != tuple(x.shape) or y.device != x.device or (out_dtype is not None and y.dtype != out_dtype):
+            raise ValueError(f"y must be {tuple(x.shape)} on {x.device}, got {y.dtype} {tuple(y.shape)} on {y.device}")
+    out_dtype = y.dtype if y is not None else (x.dtype if out_dtype is None else out_dtype)
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"output dtype {out_dtype} not supported (float32 or bfloat16)")
+    xd, yd = _x_dtype(x), NQ_BF16 if out_dtype == torch.bfloat16 else NQ_F32
+    ldx = x.stride(-2) if rows > 1 else max(x.stride(-2), cols)
+    stride = x.stride(0) if x.dim() == 3 and batch > 1 else 0
+    a, b, c = (float(v) for v in coeffs)
+    dev = x.device
+    with torch.cuda.device(dev), _on(stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        if workspace is None:
+            need = int(lib().nq_orthogonalize_workspace_bytes(batch, rows, cols, yd))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _check(lib().nq_orthogonalize(_ptr(x), xd, batch, rows, cols, ldx, stride, steps, a, b, c, _ptr(y), yd,
+                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                      _stream(stream, dev.index)))
+    return y
 
 
 def balance_factors(u_hat: torch.Tensor, v_hat: torch.Tensor, r: int | None = None, balanced: bool = True,

@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <new>
 #include <string>
@@ -816,6 +817,71 @@ nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const
   return hip_status(
       launch_lora_grads(*P, x, x_dtype, g, g_dtype, ids, T, dx_base, dx, da, db, workspace, (hipStream_t)stream),
       "nq_lora_grads launch");
+}
+
+namespace {
+
+nq_status check_ortho_sizes(const char* who, int64_t batch, int64_t rows, int64_t cols, nq_dtype yd) {
+  if (batch < 1 || rows < 1 || cols < 1)
+    return set_error("%s: batch=%lld rows=%lld cols=%lld must be >= 1", who, (long long)batch, (long long)rows,
+                     (long long)cols),
+           NQ_ERR_ARG;
+  const int64_t longer = std::max(rows, cols), shorter = std::min(rows, cols);
+  if (batch > 65535 || longer > (int64_t(1) << 24) || (longer > 65536 && shorter > 64))
+    return set_error("%s: %lld matrices of %lld x %lld are too large", who, (long long)batch, (long long)rows,
+                     (long long)cols),
+           NQ_ERR_UNSUPPORTED;
+  if (yd != NQ_F32 && yd != NQ_BF16) return set_error("%s: unknown y dtype %d", who, (int)yd), NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+// Whether s -> ca s + cb s^3 + cc s^5 maps [0, 1.25] into [-1.25, 1.25] (its
+// ends and the zeros of its derivative, a quadratic in s^2).
+bool keeps_range(double ca, double cb, double cc) {
+  const double top = 1.25;
+  auto inside = [&](double s) {
+    const double l = s * s;
+    return s * fabs(ca + cb * l + cc * l * l) <= top;
+  };
+  auto at = [&](double l) { return !(l > 0.0 && l < top * top) || inside(sqrt(l)); };
+  if (!inside(top)) return false;
+  // ca + 3 cb l + 5 cc l^2 = 0
+  const double p = 3.0 * cb, q = 5.0 * cc;
+  if (q == 0.0) return p == 0.0 || at(-ca / p);
+  const double disc = p * p - 4.0 * q * ca;
+  return disc < 0.0 || (at((-p + sqrt(disc)) / (2.0 * q)) && at((-p - sqrt(disc)) / (2.0 * q)));
+}
+
+}  // namespace
+
+size_t nq_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, nq_dtype y_dtype) {
+  if (check_ortho_sizes("nq_orthogonalize_workspace_bytes", batch, rows, cols, y_dtype) != NQ_OK) return 0;
+  return ortho_workspace(batch, rows, cols, y_dtype);
+}
+
+nq_status nq_orthogonalize(const void* x, nq_dtype x_dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ldx,
+                           int64_t stride_x, int32_t steps, double ca, double cb, double cc, void* y, nq_dtype y_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "nq_orthogonalize";
+  nq_status st = check_ortho_sizes(who, batch, rows, cols, y_dtype);
+  if (st != NQ_OK) return st;
+  if (x_dtype != NQ_F32 && x_dtype != NQ_BF16) return set_error("%s: unknown x dtype %d", who, (int)x_dtype), NQ_ERR_ARG;
+  if (!x || !y) return set_error("%s: null x or y", who), NQ_ERR_ARG;
+  if (!aligned(x, x_dtype == NQ_F32 ? 4 : 2) || !aligned(y, y_dtype == NQ_F32 ? 4 : 2))
+    return set_error("%s: x or y misaligned", who), NQ_ERR_ARG;
+  if (ldx < cols || stride_x < 0)
+    return set_error("%s: ldx=%lld below cols=%lld or stride_x=%lld negative", who, (long long)ldx, (long long)cols,
+                     (long long)stride_x),
+           NQ_ERR_ARG;
+  if (steps < 1 || steps > 64) return set_error("%s: steps=%d outside 1..64", who, (int)steps), NQ_ERR_ARG;
+  if (!std::isfinite(ca) || !std::isfinite(cb) || !std::isfinite(cc) || !keeps_range(ca, cb, cc))
+    return set_error("%s: coefficients %g, %g, %g do not map [0, 1.25] into [-1.25, 1.25]", who, ca, cb, cc), NQ_ERR_ARG;
+  if ((st = check_workspace(who, workspace, workspace_bytes, ortho_workspace(batch, rows, cols, y_dtype))) != NQ_OK)
+    return st;
+  return hip_status(launch_ortho(x, x_dtype, batch, rows, cols, ldx, stride_x, steps, ca, cb, cc, y, y_dtype, workspace,
+                                 (hipStream_t)stream),
+                    "nq_orthogonalize launch");
 }
 
 size_t nq_balance_workspace_bytes(int64_t d_out, int64_t d_in) {
