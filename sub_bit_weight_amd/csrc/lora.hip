@@ -32,7 +32,9 @@
 //
 // Rows and columns of a matrix product do not mix: slots without a row and
 // rank rows past r load some valid address and are set to zero when stored;
-// only tails of a reduction need zero operands.
+// only tails of a reduction need zero operands.  A 16x16 tile's rows may stand
+// for any rows of the operand, so each kernel assigns them such that lanes load
+// and store 8 or 16 consecutive bytes.
 #include "nq_internal.h"
 
 namespace nq {
@@ -216,19 +218,41 @@ __device__ inline f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
 // One workgroup per group: adapters 0..n-1, then the tokens without an adapter
 // (n) and those whose id is out of range (n + 1).  Each counts every group
 // (integer counters in LDS), which gives its first tile, and then lists its own
-// tokens in order.
+// tokens in order.  A wave owns a stretch of tokens, whose groups stay in
+// registers between the two passes (up to 16384 tokens; the rest is read again).
 __global__ __launch_bounds__(kRouteThreads) void lora_route_kernel(const int32_t* __restrict__ ids, int T, int n,
                                                                    int* __restrict__ tile_off, int* __restrict__ tile_ad,
-                                                                   int* __restrict__ slot_row) {
+                                                                   int* __restrict__ slot_row, int* __restrict__ arrived,
+                                                                   int per_tile) {
   extern __shared__ int hist[];  // [n + 2] counts, then [16] per-wave sums
-  constexpr int NW = kRouteThreads / 64;
+  constexpr int NW = kRouteThreads / 64, HELD = 16;
   int* red = hist + n + 2;
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int me = blockIdx.x;
+  const int per = ((T + NW - 1) / NW + 63) / 64 * 64;
+  const int t0 = wave * per, t1 = min(T, t0 + per);
+  auto group = [&](int id) { return id < 0 ? n : (id >= n ? n + 1 : id); };
+  int held[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int t = t0 + 64 * i + lane;
+    held[i] = t < t1 ? group(ids[t]) : -1;
+  }
   for (int i = tid; i < n + 2; i += kRouteThreads) hist[i] = 0;
   __syncthreads();
-  auto group = [&](int id) { return id < 0 ? n : (id >= n ? n + 1 : id); };
-  for (int t = tid; t < T; t += kRouteThreads) atomicAdd(&hist[group(ids[t])], 1);
+  int mine = 0;
+  auto count = [&](int g) {
+    // neighbours usually share a group: the first lane's is counted at once
+    const int g0 = __builtin_amdgcn_readfirstlane(g);
+    const unsigned long long same = __ballot(g == g0);
+    if (lane == 0 && g0 >= 0) atomicAdd(&hist[g0], __popcll(same));
+    if (g != g0 && g >= 0) atomicAdd(&hist[g], 1);
+    mine += __popcll(__ballot(g == me));
+  };
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (t0 + 64 * i < t1) count(held[i]);
+  for (int t = t0 + 64 * HELD; t < t1; t += 64) count(t + lane < t1 ? group(ids[t + lane]) : -1);
   __syncthreads();
   int before = 0;
   for (int i = tid; i < me; i += kRouteThreads) before += (hist[i] + kTile - 1) / kTile;
@@ -238,29 +262,29 @@ __global__ __launch_bounds__(kRouteThreads) void lora_route_kernel(const int32_t
   int tile0 = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) tile0 += red[w];
-  const int count = hist[me], tiles = (count + kTile - 1) / kTile;
+  __syncthreads();
+  if (lane == 0) red[wave] = mine;
+  __syncthreads();
+  const int total = hist[me], tiles = (total + kTile - 1) / kTile;
   if (tid == 0) {
     tile_off[me] = tile0;
     if (me == n + 1) tile_off[n + 2] = tile0 + tiles;
   }
   for (int i = tid; i < tiles; i += kRouteThreads) tile_ad[tile0 + i] = me < n ? me : n - 1 - me;  // -1, -2
-  for (int i = count + tid; i < tiles * kTile; i += kRouteThreads) slot_row[(int64_t)tile0 * kTile + i] = -1;
-  // each wave lists the tokens of its own stretch behind those of the waves before it
-  const int per = ((T + NW - 1) / NW + 63) / 64 * 64;
-  const int t0 = wave * per, t1 = min(T, t0 + per);
-  int mine = 0;
-  for (int t = t0; t < t1; t += 64) mine += __popcll(__ballot(t + lane < t1 && group(ids[t + lane]) == me));
-  __syncthreads();  // red is read above
-  if (lane == 0) red[wave] = mine;
-  __syncthreads();
+  for (int64_t i = tid; i < (int64_t)tiles * per_tile; i += kRouteThreads) arrived[(int64_t)tile0 * per_tile + i] = 0;
+  int* rows = slot_row + (int64_t)tile0 * kTile;
+  for (int i = total + tid; i < tiles * kTile; i += kRouteThreads) rows[i] = -1;
   int at = 0;
   for (int w = 0; w < wave; ++w) at += red[w];
-  for (int t = t0; t < t1; t += 64) {
-    const bool hit = t + lane < t1 && group(ids[t + lane]) == me;
-    const unsigned long long m = __ballot(hit);
-    if (hit) slot_row[(int64_t)tile0 * kTile + at + __popcll(m & ((1ull << lane) - 1))] = t + lane;
+  auto list = [&](int g, int t) {
+    const unsigned long long m = __ballot(g == me);
+    if (g == me) rows[at + __popcll(m & ((1ull << lane) - 1))] = t;
     at += __popcll(m);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < HELD; ++i)
+    if (t0 + 64 * i < t1) list(held[i], t0 + 64 * i + lane);
+  for (int t = t0 + 64 * HELD; t < t1; t += 64) list(t + lane < t1 ? group(ids[t + lane]) : -1, t + lane);
 }
 
 // The rows of a tile as a workgroup sees them.
@@ -293,43 +317,56 @@ __device__ inline bool direct_rows(const int32_t* __restrict__ ids, int T, int n
 }
 
 // ---------------------------------------------------------------- shrink
-// h[slot][k] = sum_j W[k][j] x[row][j] over a span of j (TW: W stored [j][k]).
-// A workgroup takes MT groups of 16 slots of one adapter and 16 NT rank rows;
-// its four waves take 64-deep steps of the span in turn and add their sums
-// through LDS in wave order.
+// h[slot][k] = scale * sum_j W[k][j] x[row][j] (TW: W stored [j][k]).
+// A workgroup takes MT groups of 16 slots of one adapter, 16 NT rank rows and a
+// span of the reduction; its eight waves take 64-deep steps of the span in turn
+// and add their sums through LDS in wave order.  With several spans, each
+// writes its sum and counts itself in; the workgroup that comes last adds them
+// in span order (nobody waits).  Direct calls leave that sum to the reader.
+//
+// Rank rows of the NT tiles: 16n + row, or (TW) NT * row + n, so that a lane's
+// NT ranks are consecutive in a row of W.
 struct ShrinkArgs {
   const void* x;       // [T][d]
   const void* w;       // adapters stride_w apart, rows ldw apart
   int64_t d, ldw, stride_w;
   const int32_t* ids;
-  const int* tile_ad;   // null: direct (T <= 64)
+  const int* tile_ad;
   const int* tile_off;  // [n + 3]
   const int* slot_row;
+  const float* scale;
   int T, n, r, rp;
-  int64_t span;        // reduction span of a workgroup (a multiple of 256, or all)
+  int64_t span;        // reduction span of a workgroup (a multiple of 64 * 8, or all)
+  int spans;
   int64_t nslots;
-  float* hpart;        // [spans][nslots][rp]
+  float* hpart;        // [spans][nslots][rp] (spans > 1, and direct)
+  int* arrived;        // [tiles][rank blocks] (spans > 1)
+  float* h;            // [nslots][rp]
+  void* ht;            // transposed: fp32 [rp][nslots], or bf16 terms [3][rp][nslots]; may be null
+  int ht_bf16;
 };
 
-template <typename F, typename EX, typename EW, bool TW, int MT, int NT, bool TAIL>
-__device__ inline void shrink_step(const EX* (&xp)[MT], const EW* (&wp)[NT], int64_t ldw, int64_t j, int64_t j1, int q,
-                                   f32x4 (&acc)[MT][NT]) {
-  // 64-deep step: lane group q takes elements 16q .. 16q+15 as two fragments
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int64_t at = j + 16 * q + 8 * s;
-    const int64_t nv = TAIL ? j1 - at : 8;
-    Frag<F> xf[MT], wf[NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) xf[m] = load8<F, EX>(xp[m] + at, nv);
-#pragma unroll
-    for (int k = 0; k < NT; ++k)
-      wf[k] = TW ? load8s<F, EW>(wp[k] + at * ldw, ldw, nv) : load8<F, EW>(wp[k] + at, nv);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int k = 0; k < NT; ++k) mma(wf[k], xf[m], acc[m][k]);
+constexpr int kShrinkWaves = 8;
+
+// Partial sums that another workgroup of the launch reads: agent-scope stores
+// (they write through by themselves, where a release fence would write back
+// the XCD's whole L2: 90 us instead of 12 for 2048 tokens of 8192), then, once
+// every thread's stores have completed and the workgroup has met, a relaxed
+// count; the last workgroup acquires before it reads.
+__device__ inline void store_agent(float* p, float v) {
+  typedef __attribute__((address_space(1))) float* gptr;
+  __hip_atomic_store((gptr)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline bool last_to_arrive(int* ctr, int n, int* s_last) {
+  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // vmcnt(0)
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    typedef __attribute__((address_space(1))) int* gptr;
+    *s_last = __hip_atomic_fetch_add((gptr)ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+    if (*s_last) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   }
+  __syncthreads();
+  return *s_last != 0;
 }
 
 template <typename EX, typename EW>
@@ -341,16 +378,104 @@ struct FragOf<Bf16, Bf16> {
   typedef Bf16 type;
 };
 
+// Ranks k .. k + NT - 1 of 8 rows of W (reduction rows at .. at + 7): one
+// fragment per rank tile.  whole: those ranks exist; otherwise ranks past r
+// repeat the last.
+template <typename F, typename E, int NT, bool TAIL>
+__device__ inline void load_ranks(const E* w, int64_t ldw, int64_t at, int64_t nv, int k, int r, bool whole,
+                                  Frag<F> (&f)[NT]) {
+  if constexpr (sizeof(E) == 2) {
+    constexpr int ND = (NT + 1) / 2;  // words of a lane's ranks
+    uint32_t d[8][ND];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int i = 0; i < ND; ++i) d[e][i] = 0;
+      if (TAIL && e >= nv) continue;
+      const E* p = w + (at + e) * ldw;
+      if (NT > 1 && whole) {
+        typedef uint32_t words __attribute__((ext_vector_type(ND), aligned(2)));
+        const words v = *reinterpret_cast<const words*>(p + k);
+        if constexpr (ND == 1)
+          d[e][0] = v[0];
+        else
+          d[e][0] = v[0], d[e][1] = v[1];
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) d[e][n / 2] |= (uint32_t)p[min(k + n, r - 1)].u << (16 * (n % 2));
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = __builtin_amdgcn_perm(d[2 * i + 1][n / 2], d[2 * i][n / 2], n % 2 ? 0x07060302 : 0x05040100);
+        if constexpr (sizeof(F) == 2)
+          f[n].d[i] = v;
+        else
+          f[n].v[2 * i] = __uint_as_float(v << 16), f[n].v[2 * i + 1] = __uint_as_float(v & 0xFFFF0000u);
+      }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float v[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[n] = 0.0f;
+      if (!TAIL || e < nv) {
+        const E* p = w + (at + e) * ldw;
+        if (whole) {
+          struct __attribute__((packed, aligned(4))) Pack {
+            float v[NT];
+          };
+          const Pack a = *reinterpret_cast<const Pack*>(p + k);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) v[n] = a.v[n];
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) v[n] = to_f32(p[min(k + n, r - 1)]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) f[n].v[e] = v[n];
+    }
+  }
+}
+
+template <typename F, typename EX, typename EW, bool TW, int MT, int NT, bool TAIL>
+__device__ inline void shrink_step(const EX* (&xp)[MT], const EW* w, const int (&wrow)[NT], const ShrinkArgs& p, int k,
+                                   bool whole, int64_t j, int64_t j1, int q, f32x4 (&acc)[MT][NT]) {
+  // 64-deep step: lane group q takes elements 16q .. 16q+15 as two fragments
+  Frag<F> xf[2][MT], wf[2][NT];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int64_t at = j + 16 * q + 8 * s;
+    const int64_t nv = TAIL ? j1 - at : 8;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xf[s][m] = load8<F, EX>(xp[m] + at, nv);
+    if constexpr (TW) {
+      load_ranks<F, EW, NT, TAIL>(w, p.ldw, at, nv, k, p.r, whole, wf[s]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) wf[s][n] = load8<F, EW>(w + (int64_t)wrow[n] * p.ldw + at, nv);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma(wf[s][n], xf[s][m], acc[m][n]);
+}
+
 template <typename EX, typename EW, bool TW, int MT, int NT>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(ShrinkArgs p) {
+__device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
   typedef typename FragOf<EX, EW>::type F;
-  __shared__ float part[4][MT * NT][4][64];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, c = lane % 16;
+  constexpr int NW = kShrinkWaves, R = 16 * NT;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, q = lane / 16, c = lane % 16;
   Rows g[MT];
-  int64_t slot0;
+  int64_t slot0 = 0;
   if (MT == 1) {  // direct: slots are the tokens themselves
     if (!direct_rows(p.ids, p.T, p.n, (int)blockIdx.x, g[0]) || g[0].ad < 0) return;
-    slot0 = 0;
   } else {
     const int tile = (int)blockIdx.x;
     if (tile >= p.tile_off[p.n]) return;  // tiles without an adapter have no h
@@ -363,89 +488,146 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(ShrinkArgs p) {
   }
   const int ad = __builtin_amdgcn_readfirstlane(g[0].ad);
   const int first = __builtin_amdgcn_readfirstlane(g[0].row);  // slot 0 always has a row
-  const int k0 = (int)blockIdx.z * 16 * NT;
+  const int k0 = (int)blockIdx.z * R;
   const EX* xp[MT];
-  const EW* wp[NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     xp[m] = static_cast<const EX*>(p.x) + (int64_t)(g[m].row < 0 ? first : g[m].row) * p.d;
+  const EW* w = static_cast<const EW*>(p.w) + ad * p.stride_w;
+  int wrow[NT];
 #pragma unroll
-  for (int k = 0; k < NT; ++k) {
-    const int kr = min(k0 + 16 * k + c, p.r - 1);
-    wp[k] = static_cast<const EW*>(p.w) + ad * p.stride_w + (TW ? (int64_t)kr : kr * p.ldw);
-  }
+  for (int n = 0; n < NT; ++n) wrow[n] = min(k0 + 16 * n + c, p.r - 1);
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int k = 0; k < NT; ++k) acc[m][k] = zero4();
-  const int64_t j0 = (int64_t)blockIdx.y * p.span, j1 = imin(p.d, j0 + p.span);
+    for (int n = 0; n < NT; ++n) acc[m][n] = zero4();
+  const int64_t j0 = (int64_t)span * p.span, j1 = imin(p.d, j0 + p.span);
   int64_t j = j0 + 64 * wave;
-#pragma unroll 2
-  for (; j + 64 <= j1; j += 256) shrink_step<F, EX, EW, TW, MT, NT, false>(xp, wp, p.ldw, j, j1, q, acc);
-  if (j < j1) shrink_step<F, EX, EW, TW, MT, NT, true>(xp, wp, p.ldw, j, j1, q, acc);
+  const bool whole = k0 + R <= p.r;
+  const int k = k0 + NT * c;
+  if (whole || !TW) {
+#pragma unroll(TW || NT == 4 ? 1 : 2)
+    for (; j + 64 <= j1; j += 64 * NW)
+      shrink_step<F, EX, EW, TW, MT, NT, false>(xp, w, wrow, p, k, true, j, j1, q, acc);
+  }
+  for (; j < j1; j += 64 * NW) shrink_step<F, EX, EW, TW, MT, NT, true>(xp, w, wrow, p, k, whole, j, j1, q, acc);
+  // [wave][block][i][lane], then the sums as [slot][rank] in the same memory
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int b = 0; b < MT * NT; ++b)
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[wave][m * NT + k][i][lane] = acc[m][k][i];
+    for (int i = 0; i < 4; ++i) lds[((wave * MT * NT + b) * 4 + i) * 64 + lane] = acc[b / NT][b % NT][i];
   __syncthreads();
-  // the wave's share of the MT x NT blocks
-  float* out = p.hpart + (int64_t)blockIdx.y * p.nslots * p.rp;
+  float sum[(MT * NT * 4 + NW - 1) / NW];
 #pragma unroll
-  for (int b = 0; b < MT * NT; ++b) {
-    if (b % 4 != wave) continue;
-    const int m = b / NT, k = b % NT;
-    const int kr = k0 + 16 * k + 4 * q;
-    if (kr >= p.rp) continue;
-    f32x4 v;
+  for (int u = 0; u < (MT * NT * 4 + NW - 1) / NW; ++u) {
+    const int bi = wave + NW * u;  // block and register
+    float v = 0.0f;
+    if (bi < MT * NT * 4)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float s = ((part[0][b][i][lane] + part[1][b][i][lane]) + part[2][b][i][lane]) + part[3][b][i][lane];
-      v[i] = g[m].row >= 0 && kr + i < p.r ? s : 0.0f;
+      for (int ww = 0; ww < NW; ++ww) v += lds[(ww * MT * NT * 4 + bi) * 64 + lane];
+    sum[u] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < (MT * NT * 4 + NW - 1) / NW; ++u) {
+    const int bi = wave + NW * u;
+    if (bi < MT * NT * 4) {
+      const int b = bi / 4, row = 4 * q + bi % 4, n = b % NT, m = b / NT;
+      const int rank = TW ? NT * row + n : 16 * n + row;
+      const int have = MT == 1 ? g[0].row : (m == 0 ? g[0].row : g[MT - 1].row);
+      lds[(16 * m + c) * (R + 1) + rank] = have >= 0 && k0 + rank < p.r ? sum[u] : 0.0f;
     }
-    if (MT == 1) {
-      if (g[0].row >= 0) *reinterpret_cast<f32x4*>(out + (int64_t)g[0].row * p.rp + kr) = v;
-    } else {
-      *reinterpret_cast<f32x4*>(out + (slot0 + 16 * m + c) * p.rp + kr) = v;
+  }
+  __syncthreads();
+  constexpr int SLOTS = 16 * MT, COUNT = SLOTS * R;
+  if (MT == 1) {
+    float* out = p.hpart + (int64_t)span * p.nslots * p.rp;
+    __shared__ int rows[16];
+    if (tid < 16) rows[tid] = g[0].row;
+    __syncthreads();
+    for (int i = tid; i < COUNT; i += 64 * NW) {
+      const int s = i / R, rank = i % R;
+      if (rows[s] >= 0 && k0 + rank < p.rp) out[(int64_t)rows[s] * p.rp + k0 + rank] = lds[s * (R + 1) + rank];
+    }
+    return;
+  }
+  if (p.spans > 1) {
+    __shared__ int last;
+    for (int i = tid; i < COUNT; i += 64 * NW)
+      if (k0 + i % R < p.rp)
+        store_agent(p.hpart + ((int64_t)span * p.nslots + slot0 + i / R) * p.rp + k0 + i % R,
+                    lds[i / R * (R + 1) + i % R]);
+    if (!last_to_arrive(p.arrived + (int64_t)blockIdx.x * gridDim.z + blockIdx.z, p.spans, &last)) return;
+    for (int i = tid; i < COUNT; i += 64 * NW) {
+      if (k0 + i % R >= p.rp) continue;
+      const float* hp = p.hpart + (slot0 + i / R) * p.rp + k0 + i % R;
+      float v = 0.0f;
+#pragma unroll 4
+      for (int s = 0; s < p.spans; ++s) v += hp[(int64_t)s * p.nslots * p.rp];
+      lds[i / R * (R + 1) + i % R] = v;
+    }
+    __syncthreads();
+  }
+  const float sc = p.scale[ad];
+  for (int i = tid; i < COUNT; i += 64 * NW)
+    if (k0 + i % R < p.rp) p.h[(slot0 + i / R) * p.rp + k0 + i % R] = lds[i / R * (R + 1) + i % R] * sc;
+  if (p.ht) {
+    for (int i = tid; i < COUNT; i += 64 * NW) {
+      const int rank = i / SLOTS, s = i % SLOTS;
+      if (k0 + rank >= p.rp) continue;
+      const float v = lds[s * (R + 1) + rank] * sc;
+      const int64_t at = (int64_t)(k0 + rank) * p.nslots + slot0 + s;
+      if (p.ht_bf16) {
+        uint32_t t[3];
+        split3(v, t[0], t[1], t[2]);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) static_cast<uint16_t*>(p.ht)[e * p.rp * p.nslots + at] = (uint16_t)(t[e] >> 16);
+      } else {
+        static_cast<float*>(p.ht)[at] = v;
+      }
     }
   }
 }
 
-// ---------------------------------------------------------------- join
-// h[slot][k] = scale * sum over spans, in order; ht is its transpose.  Either
-// may be null.
-__global__ __launch_bounds__(256) void lora_join_kernel(const float* __restrict__ hpart, int spans, int64_t nslots, int rp,
-                                                        const float* __restrict__ scale, const int* __restrict__ tile_ad,
-                                                        const int* __restrict__ tile_off, int n, float* __restrict__ h,
-                                                        float* __restrict__ ht) {
-  const int tile = (int)blockIdx.x;
-  if (tile >= tile_off[n]) return;
-  const float sc = scale[tile_ad[tile]];
-  for (int i = threadIdx.x; i < kTile * rp / 4; i += 256) {
-    const int64_t slot = (int64_t)tile * kTile + i % kTile;
-    const int k = i / kTile * 4;
-    f32x4 v = *reinterpret_cast<const f32x4*>(hpart + slot * rp + k);
-    for (int s = 1; s < spans; ++s) v += *reinterpret_cast<const f32x4*>(hpart + ((int64_t)s * nslots + slot) * rp + k);
-    v *= sc;
-    if (h) *reinterpret_cast<f32x4*>(h + slot * rp + k) = v;
-    if (ht)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ht[(int64_t)(k + e) * nslots + slot] = v[e];
-  }
+template <int MT, int NT>
+constexpr int shrink_lds() {  // floats
+  const int a = kShrinkWaves * MT * NT * 256, b = 16 * MT * (16 * NT + 1);
+  return a > b ? a : b;
+}
+
+template <typename EX, typename EW, int MT, int NT>
+__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkArgs p) {
+  __shared__ float lds[shrink_lds<MT, NT>()];
+  shrink<EX, EW, false, MT, NT>(p, (int)blockIdx.y, lds);
+}
+
+// Both hidden vectors of the gradients in one launch: g with B (the slower one,
+// first), then x with A.
+template <typename EX, typename EG, typename EW, int NT>
+__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink2_kernel(ShrinkArgs px, ShrinkArgs pg) {
+  __shared__ float lds[shrink_lds<2, NT>()];
+  const int y = (int)blockIdx.y;
+  if (y < pg.spans)
+    shrink<EG, EW, true, 2, NT>(pg, y, lds);
+  else
+    shrink<EX, EW, false, 2, NT>(px, y - pg.spans, lds);
 }
 
 // ---------------------------------------------------------------- expand
 // y[row][j] = base[row][j] + sum_k W[j][k] h[slot][k] (TW: W stored [k][j]).
-// A wave takes 128 columns: eight 16x16 tiles, tile v holding columns 8c + v,
-// so that lane (q, c) ends with 8 consecutive columns of row c for each i.
+// A wave takes 128 columns as eight 16x16 tiles and keeps their factors (32 KB
+// rank rows) in registers while consecutive groups of 16 slots have the same
+// adapter; base of the next group is loaded before this one is stored.
+// Columns: tile v, row p holds 16v + p, or (TW) tile 2u + b holds 32u + 2p + b,
+// so that a lane loads two consecutive columns of a row of W and either way
+// ends with float4 pieces that fill 64 bytes of a row across lanes.
 struct ExpandArgs {
-  const float* h;       // [nslots][rp]; direct: [spans][nslots][rp] partial sums
+  const float* h;       // [nslots][rp]; direct calls: [spans][nslots][rp] unscaled sums
   const void* w;
   int64_t d, ldw, stride_w;
-  const float* scale;   // direct only
-  const int32_t* ids;
+  const float* scale;   // direct calls
+  const int32_t* ids;   // direct calls
   const int* tile_ad;
   const int* tile_off;
   const int* slot_row;
@@ -460,132 +642,290 @@ template <typename EW, bool TW>
 __device__ inline void expand_weights(const ExpandArgs& p, int ad, int64_t n0, int kb, int q, int c, Frag<EW> (&w)[8]) {
   const EW* base = static_cast<const EW*>(p.w) + ad * p.stride_w;
   const int k = 32 * kb + 8 * q;
-  if constexpr (TW) {  // rows k, columns j consecutive: 8 rows of 8 columns, transposed in registers
-    Frag<EW> in[8];
-    const int64_t j = n0 + 8 * c;
+  if constexpr (TW) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t nv = k + e < p.r ? p.d - j : 0;
-      in[e] = load8<EW, EW>(base + (k + e) * p.ldw + j, nv);
+    for (int u = 0; u < 4; ++u) {
+      const int64_t j = n0 + 32 * u + 2 * c;
+      EW v[8][2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const EW* a = base + (int64_t)(k + e) * p.ldw + j;
+        if (k + e < p.r && j + 2 <= p.d) {
+          struct __attribute__((packed, aligned(sizeof(EW)))) Pair {
+            EW v[2];
+          };
+          const Pair t = *reinterpret_cast<const Pair*>(a);
+          v[e][0] = t.v[0], v[e][1] = t.v[1];
+        } else {
+          v[e][0] = k + e < p.r && j < p.d ? a[0] : EW{};
+          v[e][1] = EW{};
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if constexpr (sizeof(EW) == 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[2 * u + b].d[i] = (uint32_t)v[2 * i][b].u | ((uint32_t)v[2 * i + 1][b].u << 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[2 * u + b].v[e] = v[e][b];
+        }
+      }
     }
-    transpose8(in, w);
   } else {
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      const int64_t j = n0 + 8 * c + v;
+      const int64_t j = n0 + 16 * v + c;
       w[v] = load8<EW, EW>(base + j * p.ldw + k, j < p.d ? p.r - k : 0);
     }
   }
 }
 
-template <typename EW, bool TW, bool DIRECT>
-__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandArgs p) {
-  const int lane = threadIdx.x % 64, q = lane / 16, c = lane % 16;
-  const int64_t n0 = ((int64_t)blockIdx.y * 4 + threadIdx.x / 64) * 128;
-  if (n0 >= p.d) return;
-  const int kbs = (p.r + 31) / 32;
-  Frag<EW> w[8];
-  int have = -1;  // adapter whose factors w holds (one 32-deep block only)
-  const int ntiles = DIRECT ? 1 : p.tile_off[p.n + 2];
-  const int t_begin = DIRECT ? 0 : (int)blockIdx.x * p.tiles_per_wg;
-  const int t_end = DIRECT ? 1 : min(ntiles, t_begin + p.tiles_per_wg);
-  for (int tile = t_begin; tile < t_end; ++tile) {
-#pragma unroll 1
-    for (int sub = 0; sub < (DIRECT ? 1 : kTile / 16); ++sub) {
-      Rows g;
-      int64_t slot;
-      if (DIRECT) {
-        if (!direct_rows(p.ids, p.T, p.n, (int)blockIdx.x, g)) return;
-        slot = imax(g.row, 0);
+// Piece t (of 8) of a lane's columns: its first column, and its values in acc.
+template <bool TW>
+__device__ inline int piece_col(int t, int q) {
+  return TW ? 32 * (t / 2) + 8 * q + 4 * (t % 2) : 16 * t + 4 * q;
+}
+template <bool TW>
+__device__ inline f32x4 piece(const f32x4 (&acc)[8], int t) {
+  if constexpr (TW) {
+    const int u = t / 2, i = 2 * (t % 2);
+    return f32x4{acc[2 * u][i], acc[2 * u + 1][i], acc[2 * u][i + 1], acc[2 * u + 1][i + 1]};
+  } else {
+    return acc[t];
+  }
+}
+
+template <bool TW>
+__device__ inline void load_base(const ExpandArgs& p, int row, int64_t n0, int q, f32x4 (&b)[8]) {
+  if (p.base && n0 + 128 <= p.d) {  // a slot without a row loads row 0 and is not stored
+    const float* at = p.base + (int64_t)max(row, 0) * p.d + n0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) b[t] = *reinterpret_cast<const f32x4u*>(at + piece_col<TW>(t, q));
+    return;
+  }
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const int64_t j = n0 + piece_col<TW>(t, q);
+    b[t] = zero4();
+    if (p.base && row >= 0) {
+      const float* at = p.base + (int64_t)row * p.d + j;
+      if (j + 4 <= p.d) {
+        b[t] = *reinterpret_cast<const f32x4u*>(at);
       } else {
-        slot = (int64_t)tile * kTile + 16 * sub + c;
-        g.ad = p.tile_ad[tile];
-        g.row = p.slot_row[slot];
-        if (__ballot(g.row >= 0) == 0) break;
-      }
-      const int ad = __builtin_amdgcn_readfirstlane(g.ad);
-      f32x4 acc[8];
 #pragma unroll
-      for (int v = 0; v < 8; ++v) acc[v] = zero4();
-      if (ad >= 0) {
-        for (int kb = 0; kb < kbs; ++kb) {
-          if (kbs > 1 || have != ad) expand_weights<EW, TW>(p, ad, n0, kb, q, c, w);
-          have = ad;
-          float hv[8];
-          const int k = 32 * kb + 8 * q;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) hv[e] = 0.0f;
-          if (k < p.rp && g.row >= 0) {
-            for (int s = 0; s < (DIRECT ? p.spans : 1); ++s) {
-              const float* hp = p.h + (s * p.nslots + slot) * p.rp + k;
-              const f32x4 a = *reinterpret_cast<const f32x4*>(hp), b = *reinterpret_cast<const f32x4*>(hp + 4);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hv[e] += a[e], hv[4 + e] += b[e];
-            }
-            if (DIRECT) {
-              const float sc = p.scale[ad];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) hv[e] *= sc;
-            }
-          }
-          Wide<EW> hw;
-          widen(hv, hw);
-#pragma unroll
-          for (int v = 0; v < 8; ++v) mma(w[v], hw, acc[v]);
-        }
-      }
-      if (g.row < 0) continue;
-      const float* bp = p.base ? p.base + (int64_t)g.row * p.d : nullptr;
-      float* yp = p.y + (int64_t)g.row * p.d;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t j = n0 + (4 * q + i) * 8;
-        float o[8];
-#pragma unroll
-        for (int v = 0; v < 8; ++v) o[v] = ad == -2 ? __builtin_nanf("") : acc[v][i];
-        if (j + 8 <= p.d) {
-          f32x4 lo = {o[0], o[1], o[2], o[3]}, hi = {o[4], o[5], o[6], o[7]};
-          if (bp) {
-            lo += *reinterpret_cast<const f32x4u*>(bp + j);
-            hi += *reinterpret_cast<const f32x4u*>(bp + j + 4);
-          }
-          *reinterpret_cast<f32x4u*>(yp + j) = lo;
-          *reinterpret_cast<f32x4u*>(yp + j + 4) = hi;
-        } else {
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            if (j + v < p.d) yp[j + v] = (bp ? bp[j + v] : 0.0f) + o[v];
-        }
+        for (int e = 0; e < 4; ++e)
+          if (j + e < p.d) b[t][e] = at[e];
       }
     }
   }
 }
 
+template <bool TW>
+__device__ inline void store_rows(const ExpandArgs& p, int row, int64_t n0, int q, const f32x4 (&acc)[8],
+                                  const f32x4 (&b)[8], bool bad) {
+  if (row < 0) return;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const int64_t j = n0 + piece_col<TW>(t, q);
+    const float nan = __builtin_nanf("");
+    const f32x4 v = bad ? f32x4{nan, nan, nan, nan} : piece<TW>(acc, t) + b[t];
+    float* at = p.y + (int64_t)row * p.d + j;
+    if (j + 4 <= p.d) {
+      *reinterpret_cast<f32x4u*>(at) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < p.d) at[e] = v[e];
+    }
+  }
+}
+
+template <typename EW, bool TW, int KB>
+__global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kernel(ExpandArgs p) {
+  const int lane = threadIdx.x % 64, q = lane / 16, c = lane % 16;
+  const int64_t n0 = ((int64_t)blockIdx.y * 4 + threadIdx.x / 64) * 128;
+  if (n0 >= p.d) return;
+  const int kbs = (p.r + 31) / 32;
+  Frag<EW> w[KB][8];
+  f32x4 acc[8], bcur[8], bnext[8];
+  // the product of one group of slots, in blocks of KB 32-deep steps
+  auto product = [&](int ad, int64_t slot, bool have_row, bool fresh) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) acc[v] = zero4();
+    if (ad < 0) return;
+    for (int kb0 = 0; kb0 < kbs; kb0 += KB) {
+      float hv[KB][8];
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const int k = 32 * (kb0 + b) + 8 * q;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hv[b][e] = 0.0f;
+        if (k < p.rp && have_row) {
+          const float* hp = p.h + slot * p.rp + k;
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(hp), hi = *reinterpret_cast<const f32x4*>(hp + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hv[b][e] = lo[e], hv[b][4 + e] = hi[e];
+        }
+      }
+      if (fresh || kbs > KB)
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          if (b == 0 || kb0 + b < kbs) expand_weights<EW, TW>(p, ad, n0, kb0 + b, q, c, w[b]);
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        if (b > 0 && kb0 + b >= kbs) break;
+        Wide<EW> hw;
+        widen(hv[b], hw);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) mma(w[b][v], hw, acc[v]);
+      }
+    }
+  };
+  constexpr int SUB = kTile / 16;
+  const int begin = (int)blockIdx.x * p.tiles_per_wg;
+  const int end = min(p.tile_off[p.n + 2], begin + p.tiles_per_wg);
+  if (begin >= end) return;
+  int have = -1;  // adapter whose factors w holds
+  int row = p.slot_row[(int64_t)begin * kTile + c];
+  load_base<TW>(p, row, n0, q, bcur);
+  for (int it = begin * SUB; it < end * SUB; ++it) {
+    const int64_t slot = (int64_t)it * 16 + c;
+    const int ad = __builtin_amdgcn_readfirstlane(p.tile_ad[it / SUB]);
+    const int next = it + 1 < end * SUB ? p.slot_row[slot + 16] : -1;
+    const bool any = __ballot(row >= 0) != 0;
+    if (any) {
+      product(ad, slot, row >= 0, have != ad);
+      have = ad;
+    }
+    load_base<TW>(p, next, n0, q, bnext);
+    if (any) store_rows<TW>(p, row, n0, q, acc, bcur, ad == -2);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) bcur[t] = bnext[t];
+    row = next;
+  }
+}
+
+// Calls of up to 64 tokens: most groups hold a token or two, where 16-wide
+// tiles would leave the matrix cores and the lanes that load rows mostly idle.
+// One thread per column j of W instead, whose rank row it reads whole, and
+// fp32 products with the group's hidden vectors, which lie in LDS.
+constexpr int kDirectRanks = 64;  // ranks held in LDS at a time
+
+template <typename EW>
+__global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
+  __shared__ float hs[16][kDirectRanks];
+  __shared__ int rows[16];
+  const int tid = threadIdx.x;
+  Rows g;
+  if (!direct_rows(p.ids, p.T, p.n, (int)blockIdx.x, g)) return;
+  const int ad = __builtin_amdgcn_readfirstlane(g.ad);
+  if (tid < 16) rows[tid] = g.row;
+  const int count = __popcll(__ballot(g.row >= 0) & 0xFFFF);
+  const int64_t j = (int64_t)blockIdx.y * 256 + tid;
+  const int64_t jc = imin(j, p.d - 1);  // columns past the last are not stored
+  float acc[16], b[16];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) acc[t] = b[t] = 0.0f;
+  __syncthreads();
+  if (p.base)
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      if (t >= count) break;
+      b[t] = p.base[(int64_t)rows[t] * p.d + jc];
+    }
+  if (ad >= 0) {
+    const EW* w = static_cast<const EW*>(p.w) + ad * p.stride_w + jc * p.ldw;
+    const float sc = p.scale[ad];
+    for (int k0 = 0; k0 < p.r; k0 += kDirectRanks) {
+      const int kn = min(p.r - k0, kDirectRanks);
+      if (k0 > 0) __syncthreads();
+      for (int i = tid; i < count * kDirectRanks; i += 256) {
+        const int t = i / kDirectRanks, k = i % kDirectRanks;
+        float v = 0.0f;
+        if (k < kn) {
+          const float* hp = p.h + (int64_t)rows[t] * p.rp + k0 + k;
+#pragma unroll 8
+          for (int s = 0; s < p.spans; ++s) v += hp[(int64_t)s * p.nslots * p.rp];
+        }
+        hs[t][k] = v * sc;
+      }
+      Frag<float> wf[2];
+      wf[0] = load8<float, EW>(w + k0, kn);
+      wf[1] = load8<float, EW>(w + k0 + 8, kn - 8);
+      __syncthreads();
+      for (int kk = 0; kk < kn; kk += 16) {
+        Frag<float> cur[2] = {wf[0], wf[1]};
+        if (kk + 16 < kn) {
+          wf[0] = load8<float, EW>(w + k0 + kk + 16, kn - kk - 16);
+          wf[1] = load8<float, EW>(w + k0 + kk + 24, kn - kk - 24);
+        }
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          if (t >= count) break;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            // ranks past r: a zero h, and a zero factor
+            acc[t] = fmaf(cur[e / 8].v[e % 8], hs[t][kk + e], acc[t]);
+          }
+        }
+      }
+    }
+  }
+  if (j >= p.d) return;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    if (t >= count) break;
+    p.y[(int64_t)rows[t] * p.d + j] = ad == -2 ? __builtin_nanf("") : b[t] + acc[t];
+  }
+}
+
 // ---------------------------------------------------------------- factor gradients
 // The sum over an adapter's tokens of x_t (128 columns of a workgroup) times
-// ht (16 NT rank rows).  Lane (q, c) loads 8 consecutive columns 8c .. of the
+// ht (16 NT RW rank rows).  Lane (q, c) loads 8 consecutive columns 8c .. of the
 // rows of slots 8q .. 8q+7 of a tile and transposes them in registers, so tile v
-// of the eight holds columns 8c + v.  The four waves take tiles in turn and add
-// their sums through LDS in wave order.
+// of the eight holds columns 8c + v.  The eight waves are 8 / RW that take tiles
+// in turn times RW that take 16 NT ranks each (RW = 2 for more than 32 ranks:
+// four rank tiles a wave leave no registers for the next tile's rows, 222 us
+// instead of the figure below); each loads the next tile's rows before it
+// multiplies.  Their sums are added through LDS in wave order.
 // DB false: out[k][j] (dA: x and dh), true: out[j][k] (dB: g and h).
 struct WgradArgs {
   const void* x;     // [T][d]
-  const float* ht;   // [rp][nslots]
+  const void* ht;    // fp32 [rp][nslots], or bf16 terms [3][rp][nslots] beside bf16 x
   const int* tile_off;
   const int* slot_row;
   int64_t d, nslots;
-  int n, r;
+  int n, r, rp;
   int chunks;        // token chunks (blockIdx.z / rank blocks)
   float* out;        // [chunks][n][r][d] or [chunks][n][d][r]
+  int64_t chunk_stride;
 };
 
-template <typename EX, int NT, bool DB>
-__global__ __launch_bounds__(256) void lora_wgrad_kernel(WgradArgs p) {
-  __shared__ float part[4][8][4][64];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, q = lane / 16, c = lane % 16;
-  const int64_t n0 = (int64_t)blockIdx.x * 128;
+constexpr int kWgradWaves = 8;
+
+template <typename EX>
+__device__ inline void load_wide(const WgradArgs& p, int64_t at, Wide<EX>& w);
+template <>
+__device__ inline void load_wide<float>(const WgradArgs& p, int64_t at, Wide<float>& w) {
+  w.f = load8<float, float>(static_cast<const float*>(p.ht) + at, 8);
+}
+template <>
+__device__ inline void load_wide<Bf16>(const WgradArgs& p, int64_t at, Wide<Bf16>& w) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+    w.t[t].d = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.ht) + (int64_t)t * p.rp * p.nslots + at);
+}
+
+template <typename EX, int NT, int RW, bool DB>
+__device__ inline void wgrad(const WgradArgs& p, int64_t block, float (*part)[8][4][64]) {
+  constexpr int TWN = kWgradWaves / RW;
+  const int lane = threadIdx.x % 64, q = lane / 16, c = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), tw = wave / RW;
+  const int64_t n0 = block * 128;
   const int ad = (int)blockIdx.y;
-  const int chunk = (int)blockIdx.z % p.chunks, k0 = (int)blockIdx.z / p.chunks * 16 * NT;
+  const int chunk = (int)blockIdx.z % p.chunks, kb = (int)blockIdx.z / p.chunks * 16 * NT * RW;
+  const int k0 = kb + wave % RW * 16 * NT;
   const int a0 = p.tile_off[ad], a1 = p.tile_off[ad + 1];
   const int per = (a1 - a0 + p.chunks - 1) / p.chunks;
   const int t0 = a0 + chunk * per, t1 = min(a1, t0 + per);
@@ -595,35 +935,42 @@ __global__ __launch_bounds__(256) void lora_wgrad_kernel(WgradArgs p) {
 #pragma unroll
     for (int k = 0; k < NT; ++k) acc[v][k] = zero4();
   const int64_t j = n0 + 8 * c;
-  for (int tile = t0 + wave; tile < t1; tile += 4) {
+  const bool full = n0 + 128 <= p.d;
+  Frag<EX> in[8];
+  auto load = [&](int tile) {
     const int* rows = p.slot_row + (int64_t)tile * kTile + 8 * q;
-    Frag<EX> in[8], xf[8];
+    int row[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int row = rows[e];
-      in[e] = load8<EX, EX>(static_cast<const EX*>(p.x) + (int64_t)row * p.d + j, row >= 0 ? p.d - j : 0);
+    for (int e = 0; e < 8; ++e) row[e] = rows[e];
+    const EX* x = static_cast<const EX*>(p.x) + j;
+    if (full && __ballot(row[7] < 0) == 0) {  // rows fill a tile from its front
+#pragma unroll
+      for (int e = 0; e < 8; ++e) in[e] = load8<EX, EX>(x + (int64_t)row[e] * p.d, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) in[e] = load8<EX, EX>(x + (int64_t)row[e] * p.d, row[e] >= 0 ? p.d - j : 0);
     }
+  };
+  if (t0 + tw < t1) load(t0 + tw);
+  for (int tile = t0 + tw; tile < t1; tile += TWN) {
+    Frag<EX> xf[8];
     transpose8(in, xf);
+    Wide<EX> hw[NT];
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      const int kr = min(k0 + 16 * k + c, p.r - 1);
-      const float* hp = p.ht + (int64_t)kr * p.nslots + (int64_t)tile * kTile + 8 * q;
-      float hv[8];
-      const f32x4 a = *reinterpret_cast<const f32x4*>(hp), b = *reinterpret_cast<const f32x4*>(hp + 4);
+    for (int k = 0; k < NT; ++k)
+      load_wide<EX>(p, (int64_t)min(k0 + 16 * k + c, p.r - 1) * p.nslots + (int64_t)tile * kTile + 8 * q, hw[k]);
+    if (tile + TWN < t1) load(tile + TWN);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) hv[e] = a[e], hv[4 + e] = b[e];
-      Wide<EX> hw;
-      widen(hv, hw);
+    for (int k = 0; k < NT; ++k)
 #pragma unroll
       for (int v = 0; v < 8; ++v) {
         if constexpr (DB)
-          mma(hw, xf[v], acc[v][k]);
+          mma(hw[k], xf[v], acc[v][k]);
         else
-          mma(xf[v], hw, acc[v][k]);
+          mma(xf[v], hw[k], acc[v][k]);
       }
-    }
   }
-  float* out = p.out + ((int64_t)chunk * p.n + ad) * p.r * p.d;
+  float* out = p.out + chunk * p.chunk_stride + (int64_t)ad * p.r * p.d;
 #pragma unroll
   for (int k = 0; k < NT; ++k) {
     if (k > 0) __syncthreads();
@@ -632,37 +979,63 @@ __global__ __launch_bounds__(256) void lora_wgrad_kernel(WgradArgs p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) part[wave][v][i][lane] = acc[v][k][i];
     __syncthreads();
-    auto sum = [&](int v, int i) {
-      return ((part[0][v][i][lane] + part[1][v][i][lane]) + part[2][v][i][lane]) + part[3][v][i][lane];
+    auto sum = [&](int rw, int v, int i) {
+      float s = part[rw][v][i][lane];
+#pragma unroll
+      for (int w = 1; w < TWN; ++w) s += part[w * RW + rw][v][i][lane];
+      return s;
     };
-    if constexpr (DB) {  // lane: column 8c + v, ranks 4q .. 4q+3; wave: two of the v
-      const int kr = k0 + 16 * k + 4 * q;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int v = 2 * wave + u;
+    for (int u = 0; u < RW; ++u) {
+      if constexpr (DB) {  // lane: column 8c + v, ranks 4q .. 4q+3
+        const int v = wave, kr = kb + u * 16 * NT + 16 * k + 4 * q;
         if (j + v >= p.d) continue;
+        float* at = out + (j + v) * p.r + kr;
+        const f32x4 s = {sum(u, v, 0), sum(u, v, 1), sum(u, v, 2), sum(u, v, 3)};
+        if (kr + 4 <= p.r) {
+          *reinterpret_cast<f32x4u*>(at) = s;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (kr + i < p.r) out[(j + v) * p.r + kr + i] = sum(v, i);
+          for (int i = 0; i < 4; ++i)
+            if (kr + i < p.r) at[i] = s[i];
+        }
+      } else {  // lane: rank c, columns 8 (4q + i) + 4 half ..
+        const int unit = wave + kWgradWaves * u, half = unit % 2, i = unit / 2 % 4, rw = unit / 8;
+        const int kr = kb + rw * 16 * NT + 16 * k + c;
+        const int64_t jj = n0 + (4 * q + i) * 8 + 4 * half;
+        if (kr >= p.r) continue;
+        float* at = out + (int64_t)kr * p.d + jj;
+        const f32x4 s = {sum(rw, 4 * half, i), sum(rw, 4 * half + 1, i), sum(rw, 4 * half + 2, i), sum(rw, 4 * half + 3, i)};
+        if (jj + 4 <= p.d) {
+          *reinterpret_cast<f32x4u*>(at) = s;
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (jj + v < p.d) at[v] = s[v];
+        }
       }
-    } else {  // lane: rank c, columns 8 (4q + i) ..; wave: one of the i
-      const int kr = k0 + 16 * k + c;
-      const int64_t jj = n0 + (4 * q + wave) * 8;
-      if (kr < p.r)
-#pragma unroll
-        for (int v = 0; v < 8; ++v)
-          if (jj + v < p.d) out[(int64_t)kr * p.d + jj + v] = sum(v, wave);
     }
   }
 }
 
-// out[i] = sum over chunks of part[chunk][i], in order
-__global__ __launch_bounds__(256) void lora_sum_kernel(const float* __restrict__ part, int chunks, int64_t count,
-                                                       float* __restrict__ out) {
+// dB (g and h) and dA (x and dh) in one launch.
+template <typename EX, typename EG, int NT, int RW>
+__global__ __launch_bounds__(64 * kWgradWaves, 2) void lora_wgrad_kernel(WgradArgs pa, WgradArgs pb) {
+  __shared__ float part[kWgradWaves][8][4][64];
+  const int64_t blocks = cdiv(pb.d, 128), b = blockIdx.x;
+  if (b < blocks)
+    wgrad<EG, NT, RW, true>(pb, b, part);
+  else
+    wgrad<EX, NT, RW, false>(pa, b - blocks, part);
+}
+
+// da and db: the sums over chunks, in order (both lie one after the other in a chunk)
+__global__ __launch_bounds__(256) void lora_sum_kernel(const float* __restrict__ part, int chunks, int64_t count_a,
+                                                       int64_t count, float* __restrict__ da, float* __restrict__ db) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
     float v = part[i];
     for (int s = 1; s < chunks; ++s) v += part[(int64_t)s * count + i];
-    out[i] = v;
+    (i < count_a ? da[i] : db[i - count_a]) = v;
   }
 }
 
@@ -670,25 +1043,19 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const float* __restrict__
 
 int64_t max_tiles(int64_t n, int64_t T) { return T / kTile + imin(n + 2, T); }
 
-// Spans of a shrink's reduction: enough workgroups for the chip, at least 256
-// elements (one 64-deep step per wave) each.
-constexpr int64_t kWantGroups = 768;
-int shrink_spans(int64_t groups, int64_t d) {
-  return (int)imax(1, imin(imin(cdiv(kWantGroups, groups), cdiv(d, 512)), 16));
-}
-int64_t span_len(int64_t d, int spans) { return round_up(cdiv(d, spans), 256); }
+// Spans of a shrink's reduction: enough workgroups of eight waves for the chip,
+// 1024 elements (two 64-deep steps a wave) or more each.
+constexpr int64_t kWantGroups = 256;
+int shrink_spans(int64_t groups, int64_t d) { return (int)imax(1, imin(imin(kWantGroups / groups, d / 1024), 8)); }
+int64_t span_len(int64_t d, int spans) { return round_up(cdiv(d, spans), 64); }
 
 struct LoraLayout {
   bool direct;
   int64_t tiles, nslots;
-  int rp, nt, kblocks, spans_x, spans_g, chunks_a, chunks_b;
-  size_t off_toff, off_tad, off_rows, off_hp, off_h, off_gp, off_dh, off_ht, off_dht, off_pa, off_pb, bytes;
+  int rp, nt, kblocks, spans_x, spans_g, chunks;
+  int64_t span_x, span_g;
+  size_t off_toff, off_tad, off_rows, off_arr, off_hp, off_h, off_ht, off_gp, off_dh, off_dht, off_part, bytes;
 };
-
-int wgrad_chunks(int64_t n, int64_t d, int64_t T, int kblocks) {
-  const int64_t wgs = n * cdiv(d, 128) * kblocks;
-  return (int)imax(1, imin(imin(512 / wgs, T / (n * 8 * kTile)), 16));
-}
 
 LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
   LoraLayout L{};
@@ -696,56 +1063,94 @@ LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
   L.tiles = max_tiles(P.n, T);
   L.nslots = L.direct ? T : L.tiles * kTile;
   L.rp = (int)round_up(P.r, 16);
-  L.nt = (int)imin(L.rp / 16, 4);
-  if (L.nt == 3) L.nt = 4;
+  L.nt = L.rp <= 16 ? 1 : (L.rp <= 32 ? 2 : 4);
   L.kblocks = (int)cdiv(L.rp, 16 * L.nt);
   // tiles in use lie between T / 32 and the maximum: the spans go by the former
-  const int64_t groups = (L.direct ? T : cdiv(T, kTile)) * L.kblocks;
-  L.spans_x = shrink_spans(groups, P.d_in);
-  L.spans_g = shrink_spans(groups, P.d_out);
+  const int64_t groups = (L.direct ? cdiv(T, 4) : cdiv(T, kTile)) * L.kblocks;
+  auto spans = [&](int64_t d, int64_t* len) {
+    const int s = shrink_spans(groups, d);
+    *len = span_len(d, s);
+    return (int)cdiv(d, *len);
+  };
+  L.spans_x = spans(P.d_in, &L.span_x);
+  if (grads) L.spans_g = spans(P.d_out, &L.span_g);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off = align_up(off + bytes);
     return at;
   };
-  if (!L.direct) {
+  const size_t hb = (size_t)L.nslots * L.rp * sizeof(float);
+  if (L.direct) {
+    L.off_hp = take(L.spans_x * hb);
+  } else {
     L.off_toff = take((size_t)(P.n + 3) * sizeof(int));
     L.off_tad = take((size_t)L.tiles * sizeof(int));
     L.off_rows = take((size_t)L.nslots * sizeof(int));
+    L.off_arr = take((size_t)L.tiles * L.kblocks * 2 * sizeof(int));
+    if (L.spans_x > 1) L.off_hp = take(L.spans_x * hb);
+    L.off_h = take(hb);
   }
-  const size_t hb = (size_t)L.nslots * L.rp * sizeof(float);
-  L.off_hp = take(L.spans_x * hb);
-  if (!grads) {
-    if (!L.direct) L.off_h = take(hb);
-  } else {
-    L.off_gp = take(L.spans_g * hb);
+  if (grads) {
+    if (L.spans_g > 1) L.off_gp = take(L.spans_g * hb);
+    L.off_ht = take(hb / 4 * 6);
     L.off_dh = take(hb);
-    L.off_ht = take(hb);
-    L.off_dht = take(hb);
-    L.chunks_a = wgrad_chunks(P.n, P.d_in, T, L.kblocks);
-    L.chunks_b = wgrad_chunks(P.n, P.d_out, T, L.kblocks);
-    const size_t per = (size_t)P.n * P.r * sizeof(float);
-    if (L.chunks_a > 1) L.off_pa = take(L.chunks_a * per * P.d_in);
-    if (L.chunks_b > 1) L.off_pb = take(L.chunks_b * per * P.d_out);
+    L.off_dht = take(hb / 4 * 6);
+    const int64_t wgs = P.n * (cdiv(P.d_in, 128) + cdiv(P.d_out, 128)) * L.kblocks;
+    L.chunks = (int)imax(1, imin(imin(512 / wgs, T / (P.n * 8 * kTile)), 16));
+    if (L.chunks > 1) L.off_part = take((size_t)L.chunks * P.n * P.r * (P.d_in + P.d_out) * sizeof(float));
   }
   L.bytes = off;
   return L;
 }
 
-template <typename EX, typename EW, bool TW>
-hipError_t launch_shrink(const ShrinkArgs& a, const LoraLayout& L, int spans, hipStream_t s) {
-  const dim3 grid((unsigned)(L.direct ? L.nslots : L.tiles), (unsigned)spans, (unsigned)L.kblocks);
-#define NQ_SHRINK(MT, NT) hipLaunchKernelGGL((lora_shrink_kernel<EX, EW, TW, MT, NT>), grid, dim3(256), 0, s, a)
+hipError_t launch_route(const int32_t* ids, int64_t T, int64_t n, const LoraLayout& L, char* ws, hipStream_t s) {
+  hipLaunchKernelGGL(lora_route_kernel, dim3((unsigned)(n + 2)), dim3(kRouteThreads),
+                     (size_t)(n + 2 + kRouteThreads / 64) * sizeof(int), s, ids, (int)T, (int)n,
+                     reinterpret_cast<int*>(ws + L.off_toff), reinterpret_cast<int*>(ws + L.off_tad),
+                     reinterpret_cast<int*>(ws + L.off_rows), reinterpret_cast<int*>(ws + L.off_arr), 2 * L.kblocks);
+  return hipGetLastError();
+}
+
+// side 0: h of x with A, 1: dh of g with B
+ShrinkArgs shrink_args(const nq_lora& P, const LoraLayout& L, char* ws, int side, const void* x, const int32_t* ids,
+                       int64_t T) {
+  ShrinkArgs a{};
+  a.x = x;
+  a.w = side ? P.b : P.a;
+  a.d = side ? P.d_out : P.d_in;
+  a.ldw = side ? P.ldb : P.lda;
+  a.stride_w = side ? P.stride_b : P.stride_a;
+  a.ids = ids;
+  a.tile_ad = reinterpret_cast<const int*>(ws + L.off_tad);
+  a.tile_off = reinterpret_cast<const int*>(ws + L.off_toff);
+  a.slot_row = reinterpret_cast<const int*>(ws + L.off_rows);
+  a.scale = P.scale;
+  a.T = (int)T;
+  a.n = (int)P.n;
+  a.r = (int)P.r;
+  a.rp = L.rp;
+  a.span = side ? L.span_g : L.span_x;
+  a.spans = side ? L.spans_g : L.spans_x;
+  a.nslots = L.nslots;
+  a.hpart = reinterpret_cast<float*>(ws + (side ? L.off_gp : L.off_hp));
+  a.arrived = reinterpret_cast<int*>(ws + L.off_arr) + side * L.tiles * L.kblocks;
+  a.h = reinterpret_cast<float*>(ws + (side ? L.off_dh : L.off_h));
+  return a;
+}
+
+template <typename EX, typename EW>
+hipError_t launch_shrink(const ShrinkArgs& a, const LoraLayout& L, hipStream_t s) {
+  const dim3 grid((unsigned)(L.direct ? L.nslots : L.tiles), (unsigned)a.spans, (unsigned)L.kblocks);
+#define NQ_SHRINK(MT, NT) \
+  hipLaunchKernelGGL((lora_shrink_kernel<EX, EW, MT, NT>), grid, dim3(64 * kShrinkWaves), 0, s, a)
   if (L.direct) {
-    if constexpr (!TW) {
-      if (L.nt == 1)
-        NQ_SHRINK(1, 1);
-      else if (L.nt == 2)
-        NQ_SHRINK(1, 2);
-      else
-        NQ_SHRINK(1, 4);
-    }
+    if (L.nt == 1)
+      NQ_SHRINK(1, 1);
+    else if (L.nt == 2)
+      NQ_SHRINK(1, 2);
+    else
+      NQ_SHRINK(1, 4);
   } else {
     if (L.nt == 1)
       NQ_SHRINK(2, 1);
@@ -758,98 +1163,68 @@ hipError_t launch_shrink(const ShrinkArgs& a, const LoraLayout& L, int spans, hi
   return hipGetLastError();
 }
 
-template <bool TW>
-hipError_t launch_shrink_types(const ShrinkArgs& a, const LoraLayout& L, int spans, nq_dtype xd, nq_dtype wd,
-                               hipStream_t s) {
-  if (xd == NQ_BF16)
-    return wd == NQ_BF16 ? launch_shrink<Bf16, Bf16, TW>(a, L, spans, s) : launch_shrink<Bf16, float, TW>(a, L, spans, s);
-  return wd == NQ_BF16 ? launch_shrink<float, Bf16, TW>(a, L, spans, s) : launch_shrink<float, float, TW>(a, L, spans, s);
+template <typename EX, typename EG, typename EW>
+hipError_t launch_shrink2(const ShrinkArgs& x, const ShrinkArgs& g, const LoraLayout& L, hipStream_t s) {
+  const dim3 grid((unsigned)L.tiles, (unsigned)(x.spans + g.spans), (unsigned)L.kblocks);
+#define NQ_SHRINK(NT) \
+  hipLaunchKernelGGL((lora_shrink2_kernel<EX, EG, EW, NT>), grid, dim3(64 * kShrinkWaves), 0, s, x, g)
+  if (L.nt == 1)
+    NQ_SHRINK(1);
+  else if (L.nt == 2)
+    NQ_SHRINK(2);
+  else
+    NQ_SHRINK(4);
+#undef NQ_SHRINK
+  return hipGetLastError();
 }
 
-template <bool TW, bool DIRECT>
+template <bool TW>
 hipError_t launch_expand(ExpandArgs a, const LoraLayout& L, nq_dtype wd, hipStream_t s) {
   const int64_t cols = cdiv(a.d, 512);
   // tiles of a workgroup: more keep the factors in registers for longer, fewer
   // fill the chip
-  a.tiles_per_wg = (int)imax(1, imin(4, L.tiles * cols / 1024));
-  const dim3 grid((unsigned)(DIRECT ? a.T : cdiv(L.tiles, a.tiles_per_wg)), (unsigned)cols);
-  if (wd == NQ_BF16)
-    hipLaunchKernelGGL((lora_expand_kernel<Bf16, TW, DIRECT>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((lora_expand_kernel<float, TW, DIRECT>), grid, dim3(256), 0, s, a);
+  a.tiles_per_wg = (int)imax(1, imin(8, L.tiles * cols / 1024));
+  const dim3 grid((unsigned)cdiv(L.tiles, a.tiles_per_wg), (unsigned)cols);
+#define NQ_EXPAND(E, KB) hipLaunchKernelGGL((lora_expand_kernel<E, TW, KB>), grid, dim3(256), 0, s, a)
+  if (wd == NQ_BF16) {
+    if (a.r <= 32)
+      NQ_EXPAND(Bf16, 1);
+    else
+      NQ_EXPAND(Bf16, 2);
+  } else {
+    if (a.r <= 32)
+      NQ_EXPAND(float, 1);
+    else
+      NQ_EXPAND(float, 2);
+  }
+#undef NQ_EXPAND
   return hipGetLastError();
 }
 
-template <bool DB>
-hipError_t launch_wgrad(const WgradArgs& a, const LoraLayout& L, nq_dtype xd, hipStream_t s) {
-  const dim3 grid((unsigned)cdiv(a.d, 128), (unsigned)a.n, (unsigned)(L.kblocks * a.chunks));
-#define NQ_WGRAD(E, NT) hipLaunchKernelGGL((lora_wgrad_kernel<E, NT, DB>), grid, dim3(256), 0, s, a)
-  if (xd == NQ_BF16) {
-    if (L.nt == 1)
-      NQ_WGRAD(Bf16, 1);
-    else if (L.nt == 2)
-      NQ_WGRAD(Bf16, 2);
-    else
-      NQ_WGRAD(Bf16, 4);
-  } else {
-    if (L.nt == 1)
-      NQ_WGRAD(float, 1);
-    else if (L.nt == 2)
-      NQ_WGRAD(float, 2);
-    else
-      NQ_WGRAD(float, 4);
-  }
+template <typename EX, typename EG>
+hipError_t launch_wgrad(const WgradArgs& a, const WgradArgs& b, const LoraLayout& L, hipStream_t s) {
+  const dim3 grid((unsigned)(cdiv(a.d, 128) + cdiv(b.d, 128)), (unsigned)a.n, (unsigned)(L.kblocks * L.chunks));
+#define NQ_WGRAD(NT, RW) \
+  hipLaunchKernelGGL((lora_wgrad_kernel<EX, EG, NT, RW>), grid, dim3(64 * kWgradWaves), 0, s, a, b)
+  if (L.nt == 1)
+    NQ_WGRAD(1, 1);
+  else if (L.nt == 2)
+    NQ_WGRAD(2, 1);
+  else
+    NQ_WGRAD(2, 2);
 #undef NQ_WGRAD
   return hipGetLastError();
 }
 
-hipError_t launch_route(const int32_t* ids, int64_t T, int64_t n, const LoraLayout& L, char* ws, hipStream_t s) {
-  hipLaunchKernelGGL(lora_route_kernel, dim3((unsigned)(n + 2)), dim3(kRouteThreads),
-                     (size_t)(n + 2 + kRouteThreads / 64) * sizeof(int), s, ids, (int)T, (int)n,
-                     reinterpret_cast<int*>(ws + L.off_toff), reinterpret_cast<int*>(ws + L.off_tad),
-                     reinterpret_cast<int*>(ws + L.off_rows));
-  return hipGetLastError();
-}
-
-ShrinkArgs shrink_args(const nq_lora& P, const LoraLayout& L, char* ws, const void* x, const void* w, int64_t d,
-                       int64_t ldw, int64_t stride_w, const int32_t* ids, int64_t T, int spans, size_t off_out) {
-  ShrinkArgs a;
-  a.x = x;
-  a.w = w;
-  a.d = d;
-  a.ldw = ldw;
-  a.stride_w = stride_w;
-  a.ids = ids;
-  a.tile_ad = reinterpret_cast<const int*>(ws + L.off_tad);
-  a.tile_off = reinterpret_cast<const int*>(ws + L.off_toff);
-  a.slot_row = reinterpret_cast<const int*>(ws + L.off_rows);
-  a.T = (int)T;
-  a.n = (int)P.n;
-  a.r = (int)P.r;
-  a.rp = L.rp;
-  a.span = span_len(d, spans);
-  a.nslots = L.nslots;
-  a.hpart = reinterpret_cast<float*>(ws + off_out);
-  return a;
-}
-
-hipError_t launch_join(const nq_lora& P, const LoraLayout& L, char* ws, size_t off_part, int spans, float* h, float* ht,
-                       hipStream_t s) {
-  hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)L.tiles), dim3(256), 0, s,
-                     reinterpret_cast<const float*>(ws + off_part), spans, L.nslots, L.rp, P.scale,
-                     reinterpret_cast<const int*>(ws + L.off_tad), reinterpret_cast<const int*>(ws + L.off_toff), (int)P.n,
-                     h, ht);
-  return hipGetLastError();
-}
-
-ExpandArgs expand_args(const nq_lora& P, const LoraLayout& L, char* ws, const float* h, const void* w, int64_t d,
-                       int64_t ldw, int64_t stride_w, const int32_t* ids, int64_t T, const float* base, float* y) {
-  ExpandArgs a;
+// h: the joined hidden vectors, or (direct) their sums per span
+ExpandArgs expand_args(const nq_lora& P, const LoraLayout& L, char* ws, bool grads, const float* h, const int32_t* ids,
+                       int64_t T, const float* base, float* y) {
+  ExpandArgs a{};
   a.h = h;
-  a.w = w;
-  a.d = d;
-  a.ldw = ldw;
-  a.stride_w = stride_w;
+  a.w = grads ? P.a : P.b;
+  a.d = grads ? P.d_in : P.d_out;
+  a.ldw = grads ? P.lda : P.ldb;
+  a.stride_w = grads ? P.stride_a : P.stride_b;
   a.scale = P.scale;
   a.ids = ids;
   a.tile_ad = reinterpret_cast<const int*>(ws + L.off_tad);
@@ -861,10 +1236,23 @@ ExpandArgs expand_args(const nq_lora& P, const LoraLayout& L, char* ws, const fl
   a.rp = L.rp;
   a.spans = L.spans_x;
   a.nslots = L.nslots;
-  a.tiles_per_wg = 1;
   a.base = base;
   a.y = y;
   return a;
+}
+
+template <typename EX, typename EG>
+hipError_t launch_lora_grads_types(const nq_lora& P, const LoraLayout& L, const ShrinkArgs& sx, const ShrinkArgs& sg,
+                                   const ExpandArgs& ea, const WgradArgs& wa, const WgradArgs& wb, float* da, float* db,
+                                   hipStream_t s) {
+  hipError_t e = P.dtype == NQ_BF16 ? launch_shrink2<EX, EG, Bf16>(sx, sg, L, s) : launch_shrink2<EX, EG, float>(sx, sg, L, s);
+  if (e == hipSuccess) e = launch_expand<true>(ea, L, P.dtype, s);
+  if (e == hipSuccess) e = launch_wgrad<EX, EG>(wa, wb, L, s);
+  if (e != hipSuccess || L.chunks == 1) return e;
+  const int64_t count_a = P.n * P.r * P.d_in, count = count_a + P.n * P.r * P.d_out;
+  hipLaunchKernelGGL(lora_sum_kernel, dim3((unsigned)imin(cdiv(count, 256), 2048)), dim3(256), 0, s, wa.out, L.chunks,
+                     count_a, count, da, db);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -878,18 +1266,20 @@ hipError_t launch_lora_linear(const nq_lora& P, const void* x, nq_dtype xd, cons
   hipError_t e = hipSuccess;
   if (!L.direct) e = launch_route(ids, T, P.n, L, ws, s);
   if (e != hipSuccess) return e;
-  const ShrinkArgs sa =
-      shrink_args(P, L, ws, x, P.a, P.d_in, P.lda, P.stride_a, ids, T, L.spans_x, L.off_hp);
-  if ((e = launch_shrink_types<false>(sa, L, (int)cdiv(P.d_in, sa.span), xd, P.dtype, s)) != hipSuccess) return e;
-  const float* h = sa.hpart;
-  if (!L.direct) {
-    float* hj = reinterpret_cast<float*>(ws + L.off_h);
-    if ((e = launch_join(P, L, ws, L.off_hp, (int)cdiv(P.d_in, sa.span), hj, nullptr, s)) != hipSuccess) return e;
-    h = hj;
-  }
-  ExpandArgs ea = expand_args(P, L, ws, h, P.b, P.d_out, P.ldb, P.stride_b, ids, T, base, y);
-  ea.spans = (int)cdiv(P.d_in, sa.span);
-  return L.direct ? launch_expand<false, true>(ea, L, P.dtype, s) : launch_expand<false, false>(ea, L, P.dtype, s);
+  const ShrinkArgs sa = shrink_args(P, L, ws, 0, x, ids, T);
+  if (xd == NQ_BF16)
+    e = P.dtype == NQ_BF16 ? launch_shrink<Bf16, Bf16>(sa, L, s) : launch_shrink<Bf16, float>(sa, L, s);
+  else
+    e = P.dtype == NQ_BF16 ? launch_shrink<float, Bf16>(sa, L, s) : launch_shrink<float, float>(sa, L, s);
+  if (e != hipSuccess) return e;
+  const ExpandArgs ea = expand_args(P, L, ws, false, L.direct ? sa.hpart : sa.h, ids, T, base, y);
+  if (!L.direct) return launch_expand<false>(ea, L, P.dtype, s);
+  const dim3 grid((unsigned)T, (unsigned)cdiv(P.d_out, 256));
+  if (P.dtype == NQ_BF16)
+    hipLaunchKernelGGL((lora_expand_direct_kernel<Bf16>), grid, dim3(256), 0, s, ea);
+  else
+    hipLaunchKernelGGL((lora_expand_direct_kernel<float>), grid, dim3(256), 0, s, ea);
+  return hipGetLastError();
 }
 
 hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const void* g, nq_dtype gd,
@@ -897,45 +1287,39 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
                              void* workspace, hipStream_t s) {
   const LoraLayout L = lora_layout(P, T, true);
   char* ws = static_cast<char*>(workspace);
-  float* ht = reinterpret_cast<float*>(ws + L.off_ht);
-  float* dh = reinterpret_cast<float*>(ws + L.off_dh);
-  float* dht = reinterpret_cast<float*>(ws + L.off_dht);
-  hipError_t e = launch_route(ids, T, P.n, L, ws, s);
+  const hipError_t e = launch_route(ids, T, P.n, L, ws, s);
   if (e != hipSuccess) return e;
-  const ShrinkArgs sx =
-      shrink_args(P, L, ws, x, P.a, P.d_in, P.lda, P.stride_a, ids, T, L.spans_x, L.off_hp);
-  if ((e = launch_shrink_types<false>(sx, L, (int)cdiv(P.d_in, sx.span), xd, P.dtype, s)) != hipSuccess) return e;
-  const ShrinkArgs sg =
-      shrink_args(P, L, ws, g, P.b, P.d_out, P.ldb, P.stride_b, ids, T, L.spans_g, L.off_gp);
-  if ((e = launch_shrink_types<true>(sg, L, (int)cdiv(P.d_out, sg.span), gd, P.dtype, s)) != hipSuccess) return e;
-  if ((e = launch_join(P, L, ws, L.off_hp, (int)cdiv(P.d_in, sx.span), nullptr, ht, s)) != hipSuccess) return e;
-  if ((e = launch_join(P, L, ws, L.off_gp, (int)cdiv(P.d_out, sg.span), dh, dht, s)) != hipSuccess) return e;
-  const ExpandArgs ea = expand_args(P, L, ws, dh, P.a, P.d_in, P.lda, P.stride_a, ids, T, dx_base, dx);
-  if ((e = launch_expand<true, false>(ea, L, P.dtype, s)) != hipSuccess) return e;
-  WgradArgs wa;
-  wa.tile_off = ea.tile_off;
-  wa.slot_row = ea.slot_row;
+  ShrinkArgs sx = shrink_args(P, L, ws, 0, x, ids, T), sg = shrink_args(P, L, ws, 1, g, ids, T);
+  sx.ht = ws + L.off_ht;  // h beside g, dh beside x
+  sx.ht_bf16 = gd == NQ_BF16;
+  sg.ht = ws + L.off_dht;
+  sg.ht_bf16 = xd == NQ_BF16;
+  const ExpandArgs ea = expand_args(P, L, ws, true, sg.h, ids, T, dx_base, dx);
+  const int64_t count_a = P.n * P.r * P.d_in, count = count_a + P.n * P.r * P.d_out;
+  float* part = reinterpret_cast<float*>(ws + L.off_part);
+  WgradArgs wa{};
+  wa.x = x;
+  wa.ht = sg.ht;
+  wa.tile_off = sx.tile_off;
+  wa.slot_row = sx.slot_row;
+  wa.d = P.d_in;
   wa.nslots = L.nslots;
   wa.n = (int)P.n;
   wa.r = (int)P.r;
-  for (int side = 0; side < 2; ++side) {
-    float* out = side ? db : da;
-    wa.d = side ? P.d_out : P.d_in;
-    wa.x = side ? g : x;
-    wa.ht = side ? ht : dht;
-    wa.chunks = side ? L.chunks_b : L.chunks_a;
-    float* part = reinterpret_cast<float*>(ws + (side ? L.off_pb : L.off_pa));
-    wa.out = wa.chunks > 1 ? part : out;
-    e = side ? launch_wgrad<true>(wa, L, gd, s) : launch_wgrad<false>(wa, L, xd, s);
-    if (e != hipSuccess) return e;
-    if (wa.chunks > 1) {
-      const int64_t count = P.n * P.r * wa.d;
-      hipLaunchKernelGGL(lora_sum_kernel, dim3((unsigned)imin(cdiv(count, 256), 2048)), dim3(256), 0, s, part, wa.chunks,
-                         count, out);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-  }
-  return hipSuccess;
+  wa.rp = L.rp;
+  wa.chunks = L.chunks;
+  wa.out = L.chunks > 1 ? part : da;
+  wa.chunk_stride = count;
+  WgradArgs wb = wa;
+  wb.x = g;
+  wb.ht = sx.ht;
+  wb.d = P.d_out;
+  wb.out = L.chunks > 1 ? part + count_a : db;
+  if (xd == NQ_BF16)
+    return gd == NQ_BF16 ? launch_lora_grads_types<Bf16, Bf16>(P, L, sx, sg, ea, wa, wb, da, db, s)
+                         : launch_lora_grads_types<Bf16, float>(P, L, sx, sg, ea, wa, wb, da, db, s);
+  return gd == NQ_BF16 ? launch_lora_grads_types<float, Bf16>(P, L, sx, sg, ea, wa, wb, da, db, s)
+                       : launch_lora_grads_types<float, float>(P, L, sx, sg, ea, wa, wb, da, db, s);
 }
 
 }  // namespace nq
