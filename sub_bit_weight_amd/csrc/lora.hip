@@ -30,6 +30,12 @@
 // fewer bits than fp32 anywhere.  Sums have a fixed order; there are no
 // atomics on floating data.
 //
+// A load of 16 bytes per lane costs a cache access per line that 16 neighbouring
+// lanes touch, and a fragment's 16 neighbours lie in 16 different rows.  Rows
+// therefore go through LDS (shrink, expand) or are loaded along columns and
+// transposed in registers (factor gradients), and the hidden vectors are stored
+// in the order in which fragments read them.
+//
 // Rows and columns of a matrix product do not mix: slots without a row and
 // rank rows past r load some valid address and are set to zero when stored;
 // only tails of a reduction need zero operands.  A 16x16 tile's rows may stand
@@ -319,8 +325,9 @@ __device__ inline bool direct_rows(const int32_t* __restrict__ ids, int T, int n
 // ---------------------------------------------------------------- shrink
 // h[slot][k] = scale * sum_j W[k][j] x[row][j] (TW: W stored [j][k]).
 // A workgroup takes MT groups of 16 slots of one adapter, 16 NT rank rows and a
-// span of the reduction; its eight waves take 64-deep steps of the span in turn
-// and add their sums through LDS in wave order.  With several spans, each
+// span of the reduction.  bf16 operands stream through LDS (staged_steps);
+// otherwise its eight waves take 64-deep steps of the span in turn, straight
+// from memory.  The waves' sums are added through LDS in wave order.  With several spans, each
 // writes its sum and counts itself in; the workgroup that comes last adds them
 // in span order (nobody waits).  Direct calls leave that sum to the reader.
 //
@@ -335,15 +342,19 @@ struct ShrinkArgs {
   const int* tile_off;  // [n + 3]
   const int* slot_row;
   const float* scale;
-  int T, n, r, rp;
-  int64_t span;        // reduction span of a workgroup (a multiple of 64 * 8, or all)
+  int T, n, r, rp;     // rp: r rounded up to 32
+  int64_t span;        // reduction span of a workgroup (a multiple of 64)
   int spans;
   int64_t nslots;
   float* hpart;        // [spans][nslots][rp] (spans > 1, and direct)
-  int* arrived;        // [tiles][rank blocks] (spans > 1)
-  float* h;            // [nslots][rp]
-  void* ht;            // transposed: fp32 [rp][nslots], or bf16 terms [3][rp][nslots]; may be null
-  int ht_bf16;
+  int* arrived;        // [tiles][rank blocks][2], this side's (spans > 1); zeroed by the routing
+  // the results as the fragments of their readers, 8 elements a lane, in fp32 or
+  // as three bf16 terms (`..._term` elements apart); either may be null
+  void* h;             // [16-slot groups][32-rank blocks][lane]: slot c, ranks 8q ..
+  void* ht;            // [tiles][16-rank blocks][lane]: rank c, slots 8q ..
+  int h_bf16, ht_bf16;
+  int64_t h_term, ht_term;
+  int staged;          // rows are 16-byte aligned and of whole 16-byte chunks
 };
 
 constexpr int kShrinkWaves = 8;
@@ -467,6 +478,103 @@ __device__ inline void shrink_step(const EX* (&xp)[MT], const EW* w, const int (
       for (int n = 0; n < NT; ++n) mma(wf[s][n], xf[s][m], acc[m][n]);
 }
 
+// Whole chunks of kChunk reduction elements of bf16 operands: the rows of x and
+// W (nt) or rows of R ranks (TW) come by direct global->LDS loads of 1 KB a wave,
+// two chunks ahead, and wave w multiplies 32-deep step w of each chunk.  A row of
+// 512 bytes keeps its 16-byte piece i at i ^ (row % 16), so that the 16 rows of a
+// fragment read meet 16 different bank groups.  Straight from memory the same
+// loads took 68 us instead of the figure above (8192 tokens of 8192, rank 64).
+constexpr int kChunk = 256, kStages = 3;
+
+template <bool TW, int NT>
+constexpr int stage_bytes() {
+  return (kTile + 16 * NT) * 512;
+}
+
+template <bool TW, int NT>
+__device__ inline void staged_steps(const ShrinkArgs& p, const Bf16* x, const int* rows, const Bf16* w, int k0, int64_t j0,
+                                    int chunks, char* lds, f32x4 (&acc)[2][NT]) {
+  constexpr int R = 16 * NT, NW = kShrinkWaves, XL = kTile / 2 / NW, WL = R / 2 / NW, STAGE = stage_bytes<TW, NT>();
+  static_assert(XL >= 1 && WL >= 1, "a load per wave and operand");
+  const int tid = threadIdx.x, lane = tid % 64, q = lane / 16, c = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const Bf16 *xa[XL], *wa[WL];
+#pragma unroll
+  for (int i = 0; i < XL; ++i) {
+    const int r = (wave * XL + i) * 2 + lane / 32;
+    xa[i] = x + (int64_t)rows[r] * p.d + j0 + ((lane % 32) ^ (r % 16)) * 8;
+  }
+#pragma unroll
+  for (int i = 0; i < WL; ++i) {
+    const int o = (wave * WL + i) * 1024 + lane * 16;  // byte of the staged block
+    if constexpr (TW) {  // [kChunk][R ranks]; ranks past r repeat the last eight
+      wa[i] = w + (j0 + o / (2 * R)) * p.ldw + min(k0 + o % (2 * R) / 2, p.r - 8);
+    } else {
+      const int r = o / 512;
+      wa[i] = w + (int64_t)min(k0 + r, p.r - 1) * p.ldw + j0 + ((o % 512 / 16) ^ (r % 16)) * 8;
+    }
+  }
+  const int64_t wstep = TW ? kChunk * p.ldw : kChunk;
+  auto issue = [&](int ch, int st) {
+    char* dst = lds + st * STAGE;
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      __builtin_amdgcn_global_load_lds((const void*)(xa[i] + (int64_t)ch * kChunk),
+                                       (__attribute__((address_space(3))) void*)(dst + (wave * XL + i) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < WL; ++i)
+      __builtin_amdgcn_global_load_lds(
+          (const void*)(wa[i] + ch * wstep),
+          (__attribute__((address_space(3))) void*)(dst + kTile * 512 + (wave * WL + i) * 1024), 16, 0, 0);
+  };
+  for (int ch = 0; ch < kStages - 1 && ch < chunks; ++ch) issue(ch, ch);
+  int st = 0;
+  for (int ch = 0; ch < chunks; ++ch) {
+    if (ch + 1 < chunks)
+      __builtin_amdgcn_s_waitcnt((XL + WL) | (7 << 4) | (15 << 8));  // the next chunk may stay in flight
+    else
+      __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // every wave's loads of this chunk have landed, the last one is consumed
+    asm volatile("" ::: "memory");
+    if (ch + kStages - 1 < chunks) issue(ch + kStages - 1, st + kStages - 1 < kStages ? st + kStages - 1 : st - 1);
+    const char* stage = lds + st * STAGE;
+    Frag<Bf16> xf[2], wf[NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      xf[m].d = *reinterpret_cast<const u32x4*>(stage + (16 * m + c) * 512 + (((4 * wave + q) ^ c) * 16));
+    const char* ws = stage + kTile * 512;
+    if constexpr (TW) {
+      load_ranks<Bf16, Bf16, NT, false>(reinterpret_cast<const Bf16*>(ws), R, 32 * wave + 8 * q, 8, NT * c, R, true, wf);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        wf[n].d = *reinterpret_cast<const u32x4*>(ws + (16 * n + c) * 512 + (((4 * wave + q) ^ c) * 16));
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma(wf[n], xf[m], acc[m][n]);
+    st = st + 1 < kStages ? st + 1 : 0;
+  }
+  __syncthreads();  // the stages are reused
+}
+
+// v[0..7] in fp32, or as bf16 terms `term` elements apart
+__device__ inline void store_frag(void* out, int bf16, int64_t term, int64_t frag, const float (&v)[8]) {
+  if (bf16) {
+    Wide<Bf16> w;
+    widen(v, w);
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + t * term + frag * 8) = w.t[t].d;
+  } else {
+    f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + frag * 8);
+    o[0] = f32x4{v[0], v[1], v[2], v[3]};
+    o[1] = f32x4{v[4], v[5], v[6], v[7]};
+  }
+}
+
 template <typename EX, typename EW, bool TW, int MT, int NT>
 __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
   typedef typename FragOf<EX, EW>::type F;
@@ -474,10 +582,11 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, q = lane / 16, c = lane % 16;
   Rows g[MT];
   int64_t slot0 = 0;
+  int tile = 0;
   if (MT == 1) {  // direct: slots are the tokens themselves
     if (!direct_rows(p.ids, p.T, p.n, (int)blockIdx.x, g[0]) || g[0].ad < 0) return;
   } else {
-    const int tile = (int)blockIdx.x;
+    tile = (int)blockIdx.x;
     if (tile >= p.tile_off[p.n]) return;  // tiles without an adapter have no h
     slot0 = (int64_t)tile * kTile;
 #pragma unroll
@@ -497,15 +606,28 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
   int wrow[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) wrow[n] = min(k0 + 16 * n + c, p.r - 1);
+  __shared__ int rows[16 * MT];
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = zero4();
   const int64_t j0 = (int64_t)span * p.span, j1 = imin(p.d, j0 + p.span);
-  int64_t j = j0 + 64 * wave;
+  int64_t js = j0;
   const bool whole = k0 + R <= p.r;
   const int k = k0 + NT * c;
+  if constexpr (MT == 2 && sizeof(F) == 2) {
+    const int chunks = p.staged ? (int)((j1 - j0) / kChunk) : 0;
+    if (chunks > 0) {  // slots without a row load the tile's first one
+      if (tid < 16 * MT) rows[tid] = p.slot_row[slot0 + tid];
+      __syncthreads();
+      if (tid < 16 * MT && rows[tid] < 0) rows[tid] = rows[0];
+      __syncthreads();
+      staged_steps<TW, NT>(p, static_cast<const Bf16*>(p.x), rows, w, k0, j0, chunks, reinterpret_cast<char*>(lds), acc);
+      js += (int64_t)chunks * kChunk;
+    }
+  }
+  int64_t j = js + 64 * wave;
   if (whole || !TW) {
 #pragma unroll(TW || NT == 4 ? 1 : 2)
     for (; j + 64 <= j1; j += 64 * NW)
@@ -543,7 +665,6 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
   constexpr int SLOTS = 16 * MT, COUNT = SLOTS * R;
   if (MT == 1) {
     float* out = p.hpart + (int64_t)span * p.nslots * p.rp;
-    __shared__ int rows[16];
     if (tid < 16) rows[tid] = g[0].row;
     __syncthreads();
     for (int i = tid; i < COUNT; i += 64 * NW) {
@@ -558,7 +679,7 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
       if (k0 + i % R < p.rp)
         store_agent(p.hpart + ((int64_t)span * p.nslots + slot0 + i / R) * p.rp + k0 + i % R,
                     lds[i / R * (R + 1) + i % R]);
-    if (!last_to_arrive(p.arrived + (int64_t)blockIdx.x * gridDim.z + blockIdx.z, p.spans, &last)) return;
+    if (!last_to_arrive(p.arrived + 2 * ((int64_t)tile * gridDim.z + blockIdx.z), p.spans, &last)) return;
     for (int i = tid; i < COUNT; i += 64 * NW) {
       if (k0 + i % R >= p.rp) continue;
       const float* hp = p.hpart + (slot0 + i / R) * p.rp + k0 + i % R;
@@ -570,60 +691,71 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
     __syncthreads();
   }
   const float sc = p.scale[ad];
-  for (int i = tid; i < COUNT; i += 64 * NW)
-    if (k0 + i % R < p.rp) p.h[(slot0 + i / R) * p.rp + k0 + i % R] = lds[i / R * (R + 1) + i % R] * sc;
-  if (p.ht) {
-    for (int i = tid; i < COUNT; i += 64 * NW) {
-      const int rank = i / SLOTS, s = i % SLOTS;
-      if (k0 + rank >= p.rp) continue;
-      const float v = lds[s * (R + 1) + rank] * sc;
-      const int64_t at = (int64_t)(k0 + rank) * p.nslots + slot0 + s;
-      if (p.ht_bf16) {
-        uint32_t t[3];
-        split3(v, t[0], t[1], t[2]);
+  if (p.h) {  // a rank block of 16 fills its 32-rank block with zeros
+    constexpr int KB = R < 32 ? 1 : R / 32;
+    for (int i = tid; i < MT * KB * 64; i += 64 * NW) {
+      const int m = i / (KB * 64), kb = i / 64 % KB, fq = i / 16 % 4, fc = i % 16;
+      float v[8];
 #pragma unroll
-        for (int e = 0; e < 3; ++e) static_cast<uint16_t*>(p.ht)[e * p.rp * p.nslots + at] = (uint16_t)(t[e] >> 16);
-      } else {
-        static_cast<float*>(p.ht)[at] = v;
+      for (int e = 0; e < 8; ++e) {
+        const int rank = 32 * kb + 8 * fq + e;
+        v[e] = rank < R ? lds[(16 * m + fc) * (R + 1) + rank] * sc : 0.0f;
       }
+      const int64_t group = slot0 / 16 + m, block = k0 / 32 + kb;
+      if (block * 32 < p.rp) store_frag(p.h, p.h_bf16, p.h_term, (group * (p.rp / 32) + block) * 64 + i % 64, v);
+    }
+  }
+  if (p.ht) {
+    for (int i = tid; i < NT * 64; i += 64 * NW) {
+      const int n = i / 64, fq = i / 16 % 4, fc = i % 16;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = lds[(8 * fq + e) * (R + 1) + 16 * n + fc] * sc;
+      const int64_t block = k0 / 16 + n;
+      if (block * 16 < p.rp) store_frag(p.ht, p.ht_bf16, p.ht_term, ((int64_t)tile * (p.rp / 16) + block) * 64 + i % 64, v);
     }
   }
 }
 
-template <int MT, int NT>
-constexpr int shrink_lds() {  // floats
-  const int a = kShrinkWaves * MT * NT * 256, b = 16 * MT * (16 * NT + 1);
-  return a > b ? a : b;
+// LDS of a shrink workgroup: the stages, or the waves' sums
+template <typename EX, typename EW, int MT, int NT>
+constexpr int shrink_lds() {
+  const int sums = 4 * kShrinkWaves * MT * NT * 256, out = 4 * 16 * MT * (16 * NT + 1);
+  const int stages = MT == 2 && sizeof(typename FragOf<EX, EW>::type) == 2 ? kStages * stage_bytes<false, NT>() : 0;
+  return stages > sums ? stages : (sums > out ? sums : out);
 }
 
 template <typename EX, typename EW, int MT, int NT>
 __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkArgs p) {
-  __shared__ float lds[shrink_lds<MT, NT>()];
-  shrink<EX, EW, false, MT, NT>(p, (int)blockIdx.y, lds);
+  extern __shared__ __attribute__((aligned(16))) float shrink_mem[];
+  shrink<EX, EW, false, MT, NT>(p, (int)blockIdx.y, shrink_mem);
 }
 
 // Both hidden vectors of the gradients in one launch: g with B (the slower one,
 // first), then x with A.
 template <typename EX, typename EG, typename EW, int NT>
 __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink2_kernel(ShrinkArgs px, ShrinkArgs pg) {
-  __shared__ float lds[shrink_lds<2, NT>()];
+  extern __shared__ __attribute__((aligned(16))) float shrink_mem[];
   const int y = (int)blockIdx.y;
   if (y < pg.spans)
-    shrink<EG, EW, true, 2, NT>(pg, y, lds);
+    shrink<EG, EW, true, 2, NT>(pg, y, shrink_mem);
   else
-    shrink<EX, EW, false, 2, NT>(px, y - pg.spans, lds);
+    shrink<EX, EW, false, 2, NT>(px, y - pg.spans, shrink_mem);
 }
 
 // ---------------------------------------------------------------- expand
 // y[row][j] = base[row][j] + sum_k W[j][k] h[slot][k] (TW: W stored [k][j]).
 // A wave takes 128 columns as eight 16x16 tiles and keeps their factors (32 KB
 // rank rows) in registers while consecutive groups of 16 slots have the same
-// adapter; base of the next group is loaded before this one is stored.
+// adapter.  The product of a group goes through the wave's part of LDS, so that
+// rows of base and y move as 512 consecutive bytes; base of the next group is
+// loaded before this one is stored.
 // Columns: tile v, row p holds 16v + p, or (TW) tile 2u + b holds 32u + 2p + b,
-// so that a lane loads two consecutive columns of a row of W and either way
-// ends with float4 pieces that fill 64 bytes of a row across lanes.
+// so that a lane loads two consecutive columns of a row of W; either way a
+// lane's results are eight float4 pieces.
 struct ExpandArgs {
-  const float* h;       // [nslots][rp]; direct calls: [spans][nslots][rp] unscaled sums
+  const void* h;        // fragments as shrink stores them; direct calls: fp32 [spans][nslots][rp] unscaled sums
+  int64_t h_term;
   const void* w;
   int64_t d, ldw, stride_w;
   const float* scale;   // direct calls
@@ -681,56 +813,69 @@ __device__ inline void expand_weights(const ExpandArgs& p, int ad, int64_t n0, i
   }
 }
 
-// Piece t (of 8) of a lane's columns: its first column, and its values in acc.
-template <bool TW>
-__device__ inline int piece_col(int t, int q) {
-  return TW ? 32 * (t / 2) + 8 * q + 4 * (t % 2) : 16 * t + 4 * q;
+// A fragment of hidden vectors as shrink stored it.
+template <typename E>
+__device__ inline void load_wide(const void* h, int64_t term, int64_t frag, Wide<E>& w);
+template <>
+__device__ inline void load_wide<float>(const void* h, int64_t term, int64_t frag, Wide<float>& w) {
+  w.f = load8<float, float>(static_cast<const float*>(h) + frag * 8, 8);
 }
-template <bool TW>
-__device__ inline f32x4 piece(const f32x4 (&acc)[8], int t) {
-  if constexpr (TW) {
-    const int u = t / 2, i = 2 * (t % 2);
-    return f32x4{acc[2 * u][i], acc[2 * u + 1][i], acc[2 * u][i + 1], acc[2 * u + 1][i + 1]};
-  } else {
-    return acc[t];
-  }
+template <>
+__device__ inline void load_wide<Bf16>(const void* h, int64_t term, int64_t frag, Wide<Bf16>& w) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) w.t[t].d = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(h) + t * term + frag * 8);
 }
 
-template <bool TW>
-__device__ inline void load_base(const ExpandArgs& p, int row, int64_t n0, int q, f32x4 (&b)[8]) {
-  if (p.base && n0 + 128 <= p.d) {  // a slot without a row loads row 0 and is not stored
-    const float* at = p.base + (int64_t)max(row, 0) * p.d + n0;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) b[t] = *reinterpret_cast<const f32x4u*>(at + piece_col<TW>(t, q));
-    return;
-  }
+// Row 2t + lane / 32 of a group (row: lane c's), as two scalars and a choice.
+__device__ inline int group_row(int row, int t, int lane) {
+  const int a = __builtin_amdgcn_readlane(row, 2 * t), b = __builtin_amdgcn_readlane(row, 2 * t + 1);
+  return lane < 32 ? a : b;
+}
+
+// Columns n0 + 4 (lane % 32) .. of the group's rows.
+__device__ inline void load_base(const ExpandArgs& p, int row, int64_t n0, int lane, f32x4 (&b)[8]) {
+  const int64_t j = n0 + lane % 32 * 4;
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    const int64_t j = n0 + piece_col<TW>(t, q);
+    const int rt = group_row(row, t, lane);
     b[t] = zero4();
-    if (p.base && row >= 0) {
-      const float* at = p.base + (int64_t)row * p.d + j;
-      if (j + 4 <= p.d) {
-        b[t] = *reinterpret_cast<const f32x4u*>(at);
-      } else {
+    if (!p.base || rt < 0) continue;
+    const float* at = p.base + (int64_t)rt * p.d + j;
+    if (j + 4 <= p.d) {
+      b[t] = *reinterpret_cast<const f32x4u*>(at);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < p.d) b[t][e] = at[e];
-      }
+      for (int e = 0; e < 4; ++e)
+        if (j + e < p.d) b[t][e] = at[e];
     }
   }
 }
 
+constexpr int kOutRow = 132;  // floats of a row in LDS: 128 and a pad of one float4
+
 template <bool TW>
-__device__ inline void store_rows(const ExpandArgs& p, int row, int64_t n0, int q, const f32x4 (&acc)[8],
-                                  const f32x4 (&b)[8], bool bad) {
-  if (row < 0) return;
+__device__ inline void store_rows(const ExpandArgs& p, int row, int64_t n0, int lane, const f32x4 (&acc)[8],
+                                  const f32x4 (&b)[8], bool bad, float* lds) {
+  const int q = lane / 16, c = lane % 16;
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    const int64_t j = n0 + piece_col<TW>(t, q);
-    const float nan = __builtin_nanf("");
-    const f32x4 v = bad ? f32x4{nan, nan, nan, nan} : piece<TW>(acc, t) + b[t];
-    float* at = p.y + (int64_t)row * p.d + j;
+    if constexpr (TW) {
+      const int u = t / 2, i = 2 * (t % 2);
+      *reinterpret_cast<f32x4*>(lds + c * kOutRow + 32 * u + 8 * q + 2 * i) =
+          f32x4{acc[2 * u][i], acc[2 * u + 1][i], acc[2 * u][i + 1], acc[2 * u + 1][i + 1]};
+    } else {
+      *reinterpret_cast<f32x4*>(lds + c * kOutRow + 16 * t + 4 * q) = acc[t];
+    }
+  }
+  const int64_t j = n0 + lane % 32 * 4;
+  const float nan = __builtin_nanf("");
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(lds + (2 * t + lane / 32) * kOutRow + lane % 32 * 4);
+    const int rt = group_row(row, t, lane);
+    if (rt < 0) continue;
+    const f32x4 v = bad ? f32x4{nan, nan, nan, nan} : a + b[t];
+    float* at = p.y + (int64_t)rt * p.d + j;
     if (j + 4 <= p.d) {
       *reinterpret_cast<f32x4u*>(at) = v;
     } else {
@@ -743,63 +888,47 @@ __device__ inline void store_rows(const ExpandArgs& p, int row, int64_t n0, int 
 
 template <typename EW, bool TW, int KB>
 __global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kernel(ExpandArgs p) {
+  __shared__ __attribute__((aligned(16))) float out[4][16 * kOutRow];
   const int lane = threadIdx.x % 64, q = lane / 16, c = lane % 16;
-  const int64_t n0 = ((int64_t)blockIdx.y * 4 + threadIdx.x / 64) * 128;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 128;
   if (n0 >= p.d) return;
-  const int kbs = (p.r + 31) / 32;
+  const int kbs = p.rp / 32;
   Frag<EW> w[KB][8];
   f32x4 acc[8], bcur[8], bnext[8];
-  // the product of one group of slots, in blocks of KB 32-deep steps
-  auto product = [&](int ad, int64_t slot, bool have_row, bool fresh) {
-#pragma unroll
-    for (int v = 0; v < 8; ++v) acc[v] = zero4();
-    if (ad < 0) return;
-    for (int kb0 = 0; kb0 < kbs; kb0 += KB) {
-      float hv[KB][8];
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const int k = 32 * (kb0 + b) + 8 * q;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) hv[b][e] = 0.0f;
-        if (k < p.rp && have_row) {
-          const float* hp = p.h + slot * p.rp + k;
-          const f32x4 lo = *reinterpret_cast<const f32x4*>(hp), hi = *reinterpret_cast<const f32x4*>(hp + 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) hv[b][e] = lo[e], hv[b][4 + e] = hi[e];
-        }
-      }
-      if (fresh || kbs > KB)
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-          if (b == 0 || kb0 + b < kbs) expand_weights<EW, TW>(p, ad, n0, kb0 + b, q, c, w[b]);
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        if (b > 0 && kb0 + b >= kbs) break;
-        Wide<EW> hw;
-        widen(hv[b], hw);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) mma(w[b][v], hw, acc[v]);
-      }
-    }
-  };
   constexpr int SUB = kTile / 16;
   const int begin = (int)blockIdx.x * p.tiles_per_wg;
   const int end = min(p.tile_off[p.n + 2], begin + p.tiles_per_wg);
   if (begin >= end) return;
   int have = -1;  // adapter whose factors w holds
   int row = p.slot_row[(int64_t)begin * kTile + c];
-  load_base<TW>(p, row, n0, q, bcur);
+  load_base(p, row, n0, lane, bcur);
   for (int it = begin * SUB; it < end * SUB; ++it) {
-    const int64_t slot = (int64_t)it * 16 + c;
     const int ad = __builtin_amdgcn_readfirstlane(p.tile_ad[it / SUB]);
-    const int next = it + 1 < end * SUB ? p.slot_row[slot + 16] : -1;
+    const int next = it + 1 < end * SUB ? p.slot_row[(int64_t)it * 16 + 16 + c] : -1;
     const bool any = __ballot(row >= 0) != 0;
-    if (any) {
-      product(ad, slot, row >= 0, have != ad);
+#pragma unroll
+    for (int v = 0; v < 8; ++v) acc[v] = zero4();
+    if (any && ad >= 0) {
+      for (int kb0 = 0; kb0 < kbs; kb0 += KB) {
+        Wide<EW> hw[KB];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          if (b == 0 || kb0 + b < kbs) load_wide<EW>(p.h, p.h_term, ((int64_t)it * kbs + kb0 + b) * 64 + lane, hw[b]);
+        if (have != ad || kbs > KB)
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+            if (b == 0 || kb0 + b < kbs) expand_weights<EW, TW>(p, ad, n0, kb0 + b, q, c, w[b]);
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          if (b == 0 || kb0 + b < kbs)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) mma(w[b][v], hw[b], acc[v]);
+      }
       have = ad;
     }
-    load_base<TW>(p, next, n0, q, bnext);
-    if (any) store_rows<TW>(p, row, n0, q, acc, bcur, ad == -2);
+    load_base(p, next, n0, lane, bnext);
+    if (any) store_rows<TW>(p, row, n0, lane, acc, bcur, ad == -2, out[wave]);
 #pragma unroll
     for (int t = 0; t < 8; ++t) bcur[t] = bnext[t];
     row = next;
@@ -814,6 +943,7 @@ constexpr int kDirectRanks = 64;  // ranks held in LDS at a time
 
 template <typename EW>
 __global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
+  constexpr int NC = 2;  // columns of a thread, 256 apart
   __shared__ float hs[16][kDirectRanks];
   __shared__ int rows[16];
   const int tid = threadIdx.x;
@@ -822,20 +952,30 @@ __global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
   const int ad = __builtin_amdgcn_readfirstlane(g.ad);
   if (tid < 16) rows[tid] = g.row;
   const int count = __popcll(__ballot(g.row >= 0) & 0xFFFF);
-  const int64_t j = (int64_t)blockIdx.y * 256 + tid;
-  const int64_t jc = imin(j, p.d - 1);  // columns past the last are not stored
-  float acc[16], b[16];
+  int64_t j[NC], jc[NC];  // columns past the last are not stored
+  const EW* w[NC];
 #pragma unroll
-  for (int t = 0; t < 16; ++t) acc[t] = b[t] = 0.0f;
-  __syncthreads();
-  if (p.base)
+  for (int u = 0; u < NC; ++u) {
+    j[u] = (int64_t)blockIdx.y * 256 * NC + 256 * u + tid;
+    jc[u] = imin(j[u], p.d - 1);
+    w[u] = static_cast<const EW*>(p.w) + imax(ad, 0) * p.stride_w + jc[u] * p.ldw;
+  }
+  Frag<float> wf[NC][2];
+  auto load = [&](int k, int left) {
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      if (t >= count) break;
-      b[t] = p.base[(int64_t)rows[t] * p.d + jc];
+    for (int u = 0; u < NC; ++u) {
+      wf[u][0] = load8<float, EW>(w[u] + k, left);
+      wf[u][1] = load8<float, EW>(w[u] + k + 8, left - 8);
     }
+  };
+  float acc[16][NC];
+#pragma unroll
+  for (int t = 0; t < 16; ++t)
+#pragma unroll
+    for (int u = 0; u < NC; ++u) acc[t][u] = 0.0f;
+  if (ad >= 0) load(0, p.r);
+  __syncthreads();
   if (ad >= 0) {
-    const EW* w = static_cast<const EW*>(p.w) + ad * p.stride_w + jc * p.ldw;
     const float sc = p.scale[ad];
     for (int k0 = 0; k0 < p.r; k0 += kDirectRanks) {
       const int kn = min(p.r - k0, kDirectRanks);
@@ -844,39 +984,39 @@ __global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
         const int t = i / kDirectRanks, k = i % kDirectRanks;
         float v = 0.0f;
         if (k < kn) {
-          const float* hp = p.h + (int64_t)rows[t] * p.rp + k0 + k;
+          const float* hp = static_cast<const float*>(p.h) + (int64_t)rows[t] * p.rp + k0 + k;
 #pragma unroll 8
           for (int s = 0; s < p.spans; ++s) v += hp[(int64_t)s * p.nslots * p.rp];
         }
-        hs[t][k] = v * sc;
+        hs[t][k] = v * sc;  // ranks past r: zero, beside a zero factor
       }
-      Frag<float> wf[2];
-      wf[0] = load8<float, EW>(w + k0, kn);
-      wf[1] = load8<float, EW>(w + k0 + 8, kn - 8);
       __syncthreads();
       for (int kk = 0; kk < kn; kk += 16) {
-        Frag<float> cur[2] = {wf[0], wf[1]};
-        if (kk + 16 < kn) {
-          wf[0] = load8<float, EW>(w + k0 + kk + 16, kn - kk - 16);
-          wf[1] = load8<float, EW>(w + k0 + kk + 24, kn - kk - 24);
-        }
+        Frag<float> cur[NC][2];
+#pragma unroll
+        for (int u = 0; u < NC; ++u) cur[u][0] = wf[u][0], cur[u][1] = wf[u][1];
+        if (k0 + kk + 16 < p.r) load(k0 + kk + 16, p.r - k0 - kk - 16);
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
           if (t >= count) break;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            // ranks past r: a zero h, and a zero factor
-            acc[t] = fmaf(cur[e / 8].v[e % 8], hs[t][kk + e], acc[t]);
-          }
+          for (int e = 0; e < 16; ++e)
+#pragma unroll
+            for (int u = 0; u < NC; ++u) acc[t][u] = fmaf(cur[u][e / 8].v[e % 8], hs[t][kk + e], acc[t][u]);
         }
       }
     }
   }
-  if (j >= p.d) return;
 #pragma unroll
   for (int t = 0; t < 16; ++t) {
     if (t >= count) break;
-    p.y[(int64_t)rows[t] * p.d + j] = ad == -2 ? __builtin_nanf("") : b[t] + acc[t];
+    const int64_t at = (int64_t)rows[t] * p.d;
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      if (j[u] >= p.d) continue;
+      const float b = p.base ? p.base[at + j[u]] : 0.0f;
+      p.y[at + j[u]] = ad == -2 ? __builtin_nanf("") : b + acc[t][u];
+    }
   }
 }
 
@@ -884,7 +1024,7 @@ __global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
 // The sum over an adapter's tokens of x_t (128 columns of a workgroup) times
 // ht (16 NT RW rank rows).  Lane (q, c) loads 8 consecutive columns 8c .. of the
 // rows of slots 8q .. 8q+7 of a tile and transposes them in registers, so tile v
-// of the eight holds columns 8c + v.  The eight waves are 8 / RW that take tiles
+// of the eight holds columns 8c + v.  The four waves are 4 / RW that take tiles
 // in turn times RW that take 16 NT ranks each (RW = 2 for more than 32 ranks:
 // four rank tiles a wave leave no registers for the next tile's rows, 222 us
 // instead of the figure below); each loads the next tile's rows before it
@@ -892,7 +1032,8 @@ __global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
 // DB false: out[k][j] (dA: x and dh), true: out[j][k] (dB: g and h).
 struct WgradArgs {
   const void* x;     // [T][d]
-  const void* ht;    // fp32 [rp][nslots], or bf16 terms [3][rp][nslots] beside bf16 x
+  const void* ht;    // fragments as shrink stores them
+  int64_t ht_term;
   const int* tile_off;
   const int* slot_row;
   int64_t d, nslots;
@@ -902,20 +1043,7 @@ struct WgradArgs {
   int64_t chunk_stride;
 };
 
-constexpr int kWgradWaves = 8;
-
-template <typename EX>
-__device__ inline void load_wide(const WgradArgs& p, int64_t at, Wide<EX>& w);
-template <>
-__device__ inline void load_wide<float>(const WgradArgs& p, int64_t at, Wide<float>& w) {
-  w.f = load8<float, float>(static_cast<const float*>(p.ht) + at, 8);
-}
-template <>
-__device__ inline void load_wide<Bf16>(const WgradArgs& p, int64_t at, Wide<Bf16>& w) {
-#pragma unroll
-  for (int t = 0; t < 3; ++t)
-    w.t[t].d = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.ht) + (int64_t)t * p.rp * p.nslots + at);
-}
+constexpr int kWgradWaves = 4;
 
 template <typename EX, int NT, int RW, bool DB>
 __device__ inline void wgrad(const WgradArgs& p, int64_t block, float (*part)[8][4][64]) {
@@ -958,7 +1086,7 @@ __device__ inline void wgrad(const WgradArgs& p, int64_t block, float (*part)[8]
     Wide<EX> hw[NT];
 #pragma unroll
     for (int k = 0; k < NT; ++k)
-      load_wide<EX>(p, (int64_t)min(k0 + 16 * k + c, p.r - 1) * p.nslots + (int64_t)tile * kTile + 8 * q, hw[k]);
+      load_wide<EX>(p.ht, p.ht_term, ((int64_t)tile * (p.rp / 16) + min(k0 / 16 + k, p.rp / 16 - 1)) * 64 + lane, hw[k]);
     if (tile + TWN < t1) load(tile + TWN);
 #pragma unroll
     for (int k = 0; k < NT; ++k)
@@ -986,12 +1114,13 @@ __device__ inline void wgrad(const WgradArgs& p, int64_t block, float (*part)[8]
       return s;
     };
 #pragma unroll
-    for (int u = 0; u < RW; ++u) {
+    for (int u = 0; u < 8 * RW / kWgradWaves; ++u) {
+      const int unit = wave + kWgradWaves * u, rw = unit / 8;
       if constexpr (DB) {  // lane: column 8c + v, ranks 4q .. 4q+3
-        const int v = wave, kr = kb + u * 16 * NT + 16 * k + 4 * q;
+        const int v = unit % 8, kr = kb + rw * 16 * NT + 16 * k + 4 * q;
         if (j + v >= p.d) continue;
         float* at = out + (j + v) * p.r + kr;
-        const f32x4 s = {sum(u, v, 0), sum(u, v, 1), sum(u, v, 2), sum(u, v, 3)};
+        const f32x4 s = {sum(rw, v, 0), sum(rw, v, 1), sum(rw, v, 2), sum(rw, v, 3)};
         if (kr + 4 <= p.r) {
           *reinterpret_cast<f32x4u*>(at) = s;
         } else {
@@ -1000,8 +1129,7 @@ __device__ inline void wgrad(const WgradArgs& p, int64_t block, float (*part)[8]
             if (kr + i < p.r) at[i] = s[i];
         }
       } else {  // lane: rank c, columns 8 (4q + i) + 4 half ..
-        const int unit = wave + kWgradWaves * u, half = unit % 2, i = unit / 2 % 4, rw = unit / 8;
-        const int kr = kb + rw * 16 * NT + 16 * k + c;
+        const int half = unit % 2, i = unit / 2 % 4, kr = kb + rw * 16 * NT + 16 * k + c;
         const int64_t jj = n0 + (4 * q + i) * 8 + 4 * half;
         if (kr >= p.r) continue;
         float* at = out + (int64_t)kr * p.d + jj;
@@ -1044,9 +1172,9 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const float* __restrict__
 int64_t max_tiles(int64_t n, int64_t T) { return T / kTile + imin(n + 2, T); }
 
 // Spans of a shrink's reduction: enough workgroups of eight waves for the chip,
-// 1024 elements (two 64-deep steps a wave) or more each.
-constexpr int64_t kWantGroups = 256;
-int shrink_spans(int64_t groups, int64_t d) { return (int)imax(1, imin(imin(kWantGroups / groups, d / 1024), 8)); }
+// 512 elements (one 64-deep step a wave) or more each.
+constexpr int64_t kWantGroups = 384;
+int shrink_spans(int64_t groups, int64_t d) { return (int)imax(1, imin(imin(kWantGroups / groups, d / 512), 16)); }
 int64_t span_len(int64_t d, int spans) { return round_up(cdiv(d, spans), 64); }
 
 struct LoraLayout {
@@ -1054,7 +1182,7 @@ struct LoraLayout {
   int64_t tiles, nslots;
   int rp, nt, kblocks, spans_x, spans_g, chunks;
   int64_t span_x, span_g;
-  size_t off_toff, off_tad, off_rows, off_arr, off_hp, off_h, off_ht, off_gp, off_dh, off_dht, off_part, bytes;
+  size_t off_toff, off_tad, off_rows, off_arr, off_hp, off_h, off_gp, off_dh, off_dht, off_part, bytes;
 };
 
 LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
@@ -1062,13 +1190,13 @@ LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
   L.direct = !grads && T <= 64;
   L.tiles = max_tiles(P.n, T);
   L.nslots = L.direct ? T : L.tiles * kTile;
-  L.rp = (int)round_up(P.r, 16);
-  L.nt = L.rp <= 16 ? 1 : (L.rp <= 32 ? 2 : 4);
-  L.kblocks = (int)cdiv(L.rp, 16 * L.nt);
+  L.rp = (int)round_up(P.r, 32);
+  L.nt = P.r <= 16 ? 1 : (P.r <= 32 ? 2 : 4);
+  L.kblocks = (int)cdiv(P.r, 16 * L.nt);
   // tiles in use lie between T / 32 and the maximum: the spans go by the former
   const int64_t groups = (L.direct ? cdiv(T, 4) : cdiv(T, kTile)) * L.kblocks;
   auto spans = [&](int64_t d, int64_t* len) {
-    const int s = shrink_spans(groups, d);
+    const int s = (int)imin(shrink_spans(groups, d), L.direct ? 8 : 16);
     *len = span_len(d, s);
     return (int)cdiv(d, *len);
   };
@@ -1089,12 +1217,11 @@ LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
     L.off_rows = take((size_t)L.nslots * sizeof(int));
     L.off_arr = take((size_t)L.tiles * L.kblocks * 2 * sizeof(int));
     if (L.spans_x > 1) L.off_hp = take(L.spans_x * hb);
-    L.off_h = take(hb);
+    L.off_h = take(hb / 4 * 6);  // three bf16 terms at most
   }
   if (grads) {
     if (L.spans_g > 1) L.off_gp = take(L.spans_g * hb);
-    L.off_ht = take(hb / 4 * 6);
-    L.off_dh = take(hb);
+    L.off_dh = take(hb / 4 * 6);
     L.off_dht = take(hb / 4 * 6);
     const int64_t wgs = P.n * (cdiv(P.d_in, 128) + cdiv(P.d_out, 128)) * L.kblocks;
     L.chunks = (int)imax(1, imin(imin(512 / wgs, T / (P.n * 8 * kTile)), 16));
@@ -1134,30 +1261,39 @@ ShrinkArgs shrink_args(const nq_lora& P, const LoraLayout& L, char* ws, int side
   a.spans = side ? L.spans_g : L.spans_x;
   a.nslots = L.nslots;
   a.hpart = reinterpret_cast<float*>(ws + (side ? L.off_gp : L.off_hp));
-  a.arrived = reinterpret_cast<int*>(ws + L.off_arr) + side * L.tiles * L.kblocks;
-  a.h = reinterpret_cast<float*>(ws + (side ? L.off_dh : L.off_h));
+  a.arrived = reinterpret_cast<int*>(ws + L.off_arr) + side;
+  a.h_term = a.ht_term = L.nslots * L.rp;
+  a.staged = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.d % 8 == 0 &&
+             a.ldw % 8 == 0 && a.stride_w % 8 == 0 && P.r % 8 == 0;
   return a;
 }
 
 template <typename EX, typename EW>
 hipError_t launch_shrink(const ShrinkArgs& a, const LoraLayout& L, hipStream_t s) {
   const dim3 grid((unsigned)(L.direct ? L.nslots : L.tiles), (unsigned)a.spans, (unsigned)L.kblocks);
-#define NQ_SHRINK(MT, NT) \
-  hipLaunchKernelGGL((lora_shrink_kernel<EX, EW, MT, NT>), grid, dim3(64 * kShrinkWaves), 0, s, a)
+  hipError_t e = hipSuccess;
+#define NQ_SHRINK(MT, NT)                                                                                  \
+  {                                                                                                        \
+    constexpr size_t lds = shrink_lds<EX, EW, MT, NT>();                                                   \
+    static std::atomic<uint64_t> done{0};                                                                  \
+    e = allow_lds(reinterpret_cast<const void*>(lora_shrink_kernel<EX, EW, MT, NT>), lds, done);           \
+    if (e != hipSuccess) return e;                                                                         \
+    hipLaunchKernelGGL((lora_shrink_kernel<EX, EW, MT, NT>), grid, dim3(64 * kShrinkWaves), lds, s, a);    \
+  }
   if (L.direct) {
     if (L.nt == 1)
-      NQ_SHRINK(1, 1);
+      NQ_SHRINK(1, 1)
     else if (L.nt == 2)
-      NQ_SHRINK(1, 2);
+      NQ_SHRINK(1, 2)
     else
-      NQ_SHRINK(1, 4);
+      NQ_SHRINK(1, 4)
   } else {
     if (L.nt == 1)
-      NQ_SHRINK(2, 1);
+      NQ_SHRINK(2, 1)
     else if (L.nt == 2)
-      NQ_SHRINK(2, 2);
+      NQ_SHRINK(2, 2)
     else
-      NQ_SHRINK(2, 4);
+      NQ_SHRINK(2, 4)
   }
 #undef NQ_SHRINK
   return hipGetLastError();
@@ -1166,14 +1302,22 @@ hipError_t launch_shrink(const ShrinkArgs& a, const LoraLayout& L, hipStream_t s
 template <typename EX, typename EG, typename EW>
 hipError_t launch_shrink2(const ShrinkArgs& x, const ShrinkArgs& g, const LoraLayout& L, hipStream_t s) {
   const dim3 grid((unsigned)L.tiles, (unsigned)(x.spans + g.spans), (unsigned)L.kblocks);
-#define NQ_SHRINK(NT) \
-  hipLaunchKernelGGL((lora_shrink2_kernel<EX, EG, EW, NT>), grid, dim3(64 * kShrinkWaves), 0, s, x, g)
+  hipError_t e = hipSuccess;
+#define NQ_SHRINK(NT)                                                                                      \
+  {                                                                                                        \
+    constexpr size_t lx = shrink_lds<EX, EW, 2, NT>(), lg = shrink_lds<EG, EW, 2, NT>();                   \
+    constexpr size_t lds = lx > lg ? lx : lg;                                                              \
+    static std::atomic<uint64_t> done{0};                                                                  \
+    e = allow_lds(reinterpret_cast<const void*>(lora_shrink2_kernel<EX, EG, EW, NT>), lds, done);          \
+    if (e != hipSuccess) return e;                                                                         \
+    hipLaunchKernelGGL((lora_shrink2_kernel<EX, EG, EW, NT>), grid, dim3(64 * kShrinkWaves), lds, s, x, g); \
+  }
   if (L.nt == 1)
-    NQ_SHRINK(1);
+    NQ_SHRINK(1)
   else if (L.nt == 2)
-    NQ_SHRINK(2);
+    NQ_SHRINK(2)
   else
-    NQ_SHRINK(4);
+    NQ_SHRINK(4)
 #undef NQ_SHRINK
   return hipGetLastError();
 }
@@ -1216,11 +1360,12 @@ hipError_t launch_wgrad(const WgradArgs& a, const WgradArgs& b, const LoraLayout
   return hipGetLastError();
 }
 
-// h: the joined hidden vectors, or (direct) their sums per span
-ExpandArgs expand_args(const nq_lora& P, const LoraLayout& L, char* ws, bool grads, const float* h, const int32_t* ids,
+// h: the hidden vectors' fragments, or (direct) their sums per span
+ExpandArgs expand_args(const nq_lora& P, const LoraLayout& L, char* ws, bool grads, const void* h, const int32_t* ids,
                        int64_t T, const float* base, float* y) {
   ExpandArgs a{};
   a.h = h;
+  a.h_term = L.nslots * L.rp;
   a.w = grads ? P.a : P.b;
   a.d = grads ? P.d_in : P.d_out;
   a.ldw = grads ? P.lda : P.ldb;
@@ -1266,15 +1411,18 @@ hipError_t launch_lora_linear(const nq_lora& P, const void* x, nq_dtype xd, cons
   hipError_t e = hipSuccess;
   if (!L.direct) e = launch_route(ids, T, P.n, L, ws, s);
   if (e != hipSuccess) return e;
-  const ShrinkArgs sa = shrink_args(P, L, ws, 0, x, ids, T);
+  ShrinkArgs sa = shrink_args(P, L, ws, 0, x, ids, T);
+  sa.h = ws + L.off_h;
+  sa.h_bf16 = P.dtype == NQ_BF16;
   if (xd == NQ_BF16)
     e = P.dtype == NQ_BF16 ? launch_shrink<Bf16, Bf16>(sa, L, s) : launch_shrink<Bf16, float>(sa, L, s);
   else
     e = P.dtype == NQ_BF16 ? launch_shrink<float, Bf16>(sa, L, s) : launch_shrink<float, float>(sa, L, s);
   if (e != hipSuccess) return e;
-  const ExpandArgs ea = expand_args(P, L, ws, false, L.direct ? sa.hpart : sa.h, ids, T, base, y);
+  const ExpandArgs ea =
+      expand_args(P, L, ws, false, L.direct ? static_cast<const void*>(sa.hpart) : sa.h, ids, T, base, y);
   if (!L.direct) return launch_expand<false>(ea, L, P.dtype, s);
-  const dim3 grid((unsigned)T, (unsigned)cdiv(P.d_out, 256));
+  const dim3 grid((unsigned)T, (unsigned)cdiv(P.d_out, 512));
   if (P.dtype == NQ_BF16)
     hipLaunchKernelGGL((lora_expand_direct_kernel<Bf16>), grid, dim3(256), 0, s, ea);
   else
@@ -1290,8 +1438,10 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
   const hipError_t e = launch_route(ids, T, P.n, L, ws, s);
   if (e != hipSuccess) return e;
   ShrinkArgs sx = shrink_args(P, L, ws, 0, x, ids, T), sg = shrink_args(P, L, ws, 1, g, ids, T);
-  sx.ht = ws + L.off_ht;  // h beside g, dh beside x
+  sx.ht = ws + L.off_h;  // h beside g; dh beside A and x
   sx.ht_bf16 = gd == NQ_BF16;
+  sg.h = ws + L.off_dh;
+  sg.h_bf16 = P.dtype == NQ_BF16;
   sg.ht = ws + L.off_dht;
   sg.ht_bf16 = xd == NQ_BF16;
   const ExpandArgs ea = expand_args(P, L, ws, true, sg.h, ids, T, dx_base, dx);
@@ -1300,6 +1450,7 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
   WgradArgs wa{};
   wa.x = x;
   wa.ht = sg.ht;
+  wa.ht_term = sg.ht_term;
   wa.tile_off = sx.tile_off;
   wa.slot_row = sx.slot_row;
   wa.d = P.d_in;

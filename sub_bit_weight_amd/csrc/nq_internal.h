@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "nq.h"
 
 namespace nq {
@@ -168,6 +170,19 @@ struct ProdEpilogue {
 int64_t prefill_row_blocks(int64_t T);  // the 128-row blocks of a T-token output
 hipError_t launch_prefill(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y,
                           void* ws, hipStream_t s, bool split = true, const ProdEpilogue* pe = nullptr);
+
+// Allows a kernel more than 64 KB of dynamic LDS, once per device (`done`: a bit
+// each; devices past 63 are set every time).
+inline hipError_t allow_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Low-rank adapters beside a shared projection (lora.hip): tokens are grouped
 // into tiles of kLoraTile slots of one adapter.  grads: the workspace of the

@@ -22,8 +22,6 @@
 //    product three fp16 products.  Operands are scaled by powers of two into
 //    fp16's range: |x| <= |G| bounds are known because the host checks that the
 //    polynomial maps [0, 1.25] into [-1.25, 1.25].
-#include <atomic>
-
 #include "nq_internal.h"
 
 namespace nq {
@@ -626,19 +624,6 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
   }
   L.bytes = off;
   return L;
-}
-
-// Allows a kernel more than 64 KB of dynamic LDS, once per device (`done`: a bit
-// each, devices past 63 every time).
-hipError_t allow_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 template <typename E, int PT>

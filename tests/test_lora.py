@@ -289,6 +289,24 @@ def test_grads_mixed_types_without_base(xd, wd):
 
 
 @gpu
+@pytest.mark.parametrize("T,n,d_in,d_out", [(33, 2, 130, 1030), (70, 9, 1500, 1100), (500, 30, 1100, 2100)])
+def test_grads_with_a_dirty_workspace(T, n, d_in, d_out):
+    """Reductions cut into spans, tiles fewer than the most there could be, and a workspace full of ones."""
+    c = _case(f"dirty/{T}", T, n, 20, d_in, d_out, ids=synth.rng(f"lora/dirty/{T}").integers(0, (n + 1) // 2, T))
+    pool, x, g, ids = _gpu_pool(c), _dev(c["x"], "bf16"), _dev(c["g"], "bf16"), _dev(c["ids"])
+    ws = torch.full((nq.lora_grads_workspace_bytes(pool, T),), 255, dtype=torch.uint8, device=DEV)
+    wl = torch.full((nq.lora_workspace_bytes(pool, T),), 255, dtype=torch.uint8, device=DEV)
+    got = nq.lora_grads(pool, x, g, ids, _dev(c["dx_base"]), workspace=ws)
+    args = (c["a"], c["b"], c["scale"], c["x"], c["g"], c["ids"], c["dx_base"])
+    for v, w, s, n_add in zip(got, A.lora_grads_ref(*args), A.lora_grads_abs(*args),
+                              (d_out + 3 * 20 + 16, d_out + 3 * T + 16, d_in + 3 * T + 16)):
+        _check(v, w, s, n_add, False)
+    y = nq.lora_linear(pool, x, ids, _dev(c["base"]), workspace=wl)
+    args = (c["a"], c["b"], c["scale"], c["x"], c["ids"], c["base"])
+    _check(y, A.lora_linear_ref(*args), A.lora_abs(*args), d_in + 3 * 20 + 16, False)
+
+
+@gpu
 def test_grads_of_few_adapters_with_many_tokens():
     """One adapter's tokens cut into chunks whose sums are joined."""
     _run_grads(_case("chunks", 2100, 1, 16, 40, 24))
