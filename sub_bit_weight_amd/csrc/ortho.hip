@@ -39,6 +39,26 @@ constexpr int kGramMax = 64;  // shorter sides up to this take the fp64 form
 __device__ inline float load1(const float* p) { return *p; }
 __device__ inline float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
+typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+__device__ inline void load4(const float* p, float (&v)[4]) {
+  const f32x4 a = *reinterpret_cast<const f32x4u*>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = a[e];
+}
+__device__ inline void load4(const uint16_t* p, float (&v)[4]) {
+  const u16x4u a = *reinterpret_cast<const u16x4u*>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float((uint32_t)a[e] << 16);
+}
+
+// The sum over a workgroup of 256 threads, in a fixed order, to every thread.
+__device__ inline double block_sum(double v, double* red) {
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
+  __syncthreads();
+  return ((red[0] + red[1]) + red[2]) + red[3];
+}
+
 __device__ inline uint16_t bf16_bits(float v) {  // round to nearest even
   const uint32_t u = __float_as_uint(v);
   if (v != v) return (uint16_t)((u >> 16) | 0x40);
@@ -268,42 +288,42 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
 // ---------------------------------------------------------------- p > 64
 constexpr int kBK = 64;
 constexpr float kScaleX = 16384.0f;  // operand scale of x: |x| <= 1.25
-constexpr int kSumBlocks = 128;  // partial sums of ||X||_F^2 per matrix
+constexpr int kSumBlocks = 512;  // partial sums of ||X||_F^2 per matrix
 
 template <typename E>
 __global__ __launch_bounds__(256) void ortho_sumsq_kernel(const E* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx,
                                                           int64_t stride_x, double* __restrict__ part) {
   __shared__ double red[4];
   x += (int64_t)blockIdx.y * stride_x;
-  double sum = 0.0;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t j = threadIdx.x; j < cols; j += 256) {
-      const double v = load1(x + r * ldx + j);
-      sum += v * v;
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const E* row = x + r * ldx;
+#pragma unroll 4
+    for (int64_t j = 4 * threadIdx.x; j + 4 <= cols; j += 1024) {
+      float v[4];
+      load4(row + j, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += (double)v[e] * v[e];
     }
-  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = ((red[0] + red[1]) + red[2]) + red[3];
+    const int64_t j = cols / 4 * 4 + threadIdx.x;
+    if (j < cols) {
+      const double v = load1(row + j);
+      sum[0] += v * v;
+    }
+  }
+  const double t = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), red);
+  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * kSumBlocks + blockIdx.x] = t;
 }
 
-__global__ __launch_bounds__(64) void ortho_norm_kernel(const double* __restrict__ part, int n, float* __restrict__ inv) {
-  double t = 0.0;
-  for (int i = threadIdx.x; i < n; i += 64) t += part[(int64_t)blockIdx.x * n + i];
-  for (int off = 32; off > 0; off >>= 1) t += __shfl_xor(t, off);
-  // 1 / ||X||_F as a power of two times a value in (0.5, 1]: the norm of fp32
-  // values may lie outside fp32
-  if (threadIdx.x == 0) {
-    float f = __builtin_nanf("");
-    int e = 0;
-    if (t == 0.0) {
-      f = 0.0f;
-    } else if (isfinite(t)) {
-      f = (float)frexp(1.0 / sqrt(t), &e);
-    }
-    inv[2 * blockIdx.x] = f;
-    inv[2 * blockIdx.x + 1] = (float)e;
-  }
+// 1 / ||X||_F as f 2^e with f in (0.5, 1]: the norm of fp32 values may lie
+// outside fp32.  Zero matrix: 0; a sum that is not finite: NaN.  Every thread of
+// the workgroup (256) gets it.
+__device__ inline float inverse_norm(const double* __restrict__ part, double* red, int& e) {
+  double t = block_sum(part[threadIdx.x] + part[threadIdx.x + 256], red);
+  e = 0;
+  if (t == 0.0) return 0.0f;
+  if (!isfinite(t)) return __builtin_nanf("");
+  return (float)frexp(1.0 / sqrt(t), &e);
 }
 
 // An operand value as fp16 terms: hi, and for two terms the rest.
@@ -323,7 +343,8 @@ struct LargeArgs {
   uint16_t* xt16[2];   // [batch][terms][q][pp]
   uint16_t* g16;       // [batch][terms][p][pp]
   uint16_t* b16;       // [batch][terms][p][pp]
-  const float* inv;    // [batch][2]
+  const double* part;  // [batch][kSumBlocks]
+  float* bad;          // [batch]: 0, or NaN for a matrix that is not finite
   float sx;            // operand scale of x
 };
 
@@ -333,12 +354,14 @@ template <typename E>
 __global__ __launch_bounds__(256) void ortho_prepare_kernel(LargeArgs s, const E* __restrict__ x, int64_t ldx,
                                                             int64_t stride_x, int tall) {
   __shared__ float tile[64][65];
+  __shared__ double red[4];
   const int64_t bi = blockIdx.z;
   const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;  // i < pp, j < qp
   x += bi * stride_x;
   const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
-  const float f = s.inv[2 * bi];
-  const int ex = (int)s.inv[2 * bi + 1];
+  int ex;
+  const float f = inverse_norm(s.part + bi * kSumBlocks, red, ex);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) s.bad[bi] = f * 0.0f;
   for (int k = ty; k < 64; k += 4) {
     const int i = i0 + (tall ? tx : k), j = j0 + (tall ? k : tx);
     float v = 0.0f;
@@ -399,7 +422,7 @@ struct GemmArgs {
   float* xf;
   void* y;
   int y_bf16, y_t;         // y_t: store transposed
-  const float* inv;
+  const float* bad;
 };
 
 // C = A B^T, workgroup tile BM x BN x 64: WM x WN waves of 32x32x16 fp16
@@ -528,59 +551,76 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
   uint16_t* outt = p.outt16 + bi * p.terms * p.term_t;
   const uint16_t* aux = p.aux16 + bi * p.terms * p.term_o;
   const bool mirror = (MODE == kGram || MODE == kPoly) && p.sym && tm != tn;
-  const float bad = MODE == kLast ? p.inv[2 * bi] * 0.0f : 0.0f;  // NaN for a matrix that is not finite
+  const float bad = MODE == kLast ? p.bad[bi] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
+  for (int i = 0; i < MB; ++i) {
+    const int mr = m0 + wm * (BM / WM) + i * 32 + 4 * h;
+    // what the block row reads, ahead of its stores (the compiler keeps their
+    // order: one load at a time cost 70 us a round of tiles); elements past the
+    // matrix repeat its last
+    float x[NB][16];
+    if constexpr (MODE != kGram) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int n = min(n0 + wn * (BN / WN) + j * 32 + l32, p.N - 1);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int m = min(mr + 8 * (r / 4) + r % 4, p.M - 1);
+          if constexpr (MODE == kPoly) {
+            x[j][r] = (float)__builtin_bit_cast(_Float16, aux[(int64_t)m * p.ldo + n]);
+            if (p.terms > 1) x[j][r] += (float)__builtin_bit_cast(_Float16, aux[(int64_t)m * p.ldo + n + p.term_o]);
+          } else {
+            x[j][r] = p.xf[(bi * p.M + m) * (int64_t)p.N + n];
+          }
+        }
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int n = n0 + wn * (BN / WN) + j * 32 + l32;
       if (n >= p.N) continue;
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const int mb = m0 + wm * (BM / WM) + i * 32 + 8 * a + 4 * h;
+        const int mb = mr + 8 * a;
         uint16_t hi[4], lo[4];
+        float v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[c] = acc[i][j][4 * a + c] * p.s_acc;
+          if constexpr (MODE != kGram) v[c] = fmaf(p.s_aux, x[j][4 * a + c], v[c]);
+          if constexpr (MODE != kLast) split_half(MODE == kStep ? v[c] * kScaleX : v[c], p.terms, hi[c], lo[c]);
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int m = mb + c;
-          float v = acc[i][j][4 * a + c] * p.s_acc;
-          hi[c] = lo[c] = 0;
-          if (m < p.M) {
-            if constexpr (MODE == kPoly) {
-              const int64_t at = (int64_t)m * p.ldo + n;
-              float x = (float)__builtin_bit_cast(_Float16, aux[at]);
-              if (p.terms > 1) x += (float)__builtin_bit_cast(_Float16, aux[at + p.term_o]);
-              v = fmaf(p.s_aux, x, v);
-            }
-            if constexpr (MODE == kStep || MODE == kLast) {
-              float* xf = p.xf + (bi * p.M + m) * (int64_t)p.N + n;
-              v = fmaf(p.s_aux, *xf, v);
-              if constexpr (MODE == kStep) *xf = v;
-            }
-            if constexpr (MODE == kLast) {
-              store1(p.y, p.y_bf16, bi * p.M * (int64_t)p.N + (p.y_t ? (int64_t)n * p.M + m : (int64_t)m * p.N + n), v + bad);
-            } else {
-              split_half(MODE == kStep ? v * kScaleX : v, p.terms, hi[c], lo[c]);
-              const int64_t at = (int64_t)m * p.ldo + n;
-              out[at] = hi[c];
-              if (p.terms > 1) out[at + p.term_o] = lo[c];
-            }
+          if (m >= p.M) continue;
+          if constexpr (MODE == kStep) p.xf[(bi * p.M + m) * (int64_t)p.N + n] = v[c];
+          if constexpr (MODE == kLast) {
+            store1(p.y, p.y_bf16, bi * p.M * (int64_t)p.N + (p.y_t ? (int64_t)n * p.M + m : (int64_t)m * p.N + n), v[c] + bad);
+          } else {
+            const int64_t at = (int64_t)m * p.ldo + n;
+            out[at] = hi[c];
+            if (p.terms > 1) out[at + p.term_o] = lo[c];
           }
         }
-        if ((MODE == kStep || mirror) && mb < p.M) {
-          uint16_t* d = (MODE == kStep ? outt : out) + (int64_t)n * (MODE == kStep ? p.ldt : p.ldo) + mb;
-          const int64_t term = MODE == kStep ? p.term_t : p.term_o;
-          if (mb + 4 <= p.M) {
-            *reinterpret_cast<u16x4*>(d) = u16x4{hi[0], hi[1], hi[2], hi[3]};
-            if (p.terms > 1) *reinterpret_cast<u16x4*>(d + term) = u16x4{lo[0], lo[1], lo[2], lo[3]};
-          } else {
-            for (int c = 0; c < p.M - mb; ++c) {
-              d[c] = hi[c];
-              if (p.terms > 1) d[term + c] = lo[c];
+        if constexpr (MODE != kLast) {
+          if ((MODE == kStep || mirror) && mb < p.M) {
+            uint16_t* d = (MODE == kStep ? outt : out) + (int64_t)n * (MODE == kStep ? p.ldt : p.ldo) + mb;
+            const int64_t term = MODE == kStep ? p.term_t : p.term_o;
+            if (mb + 4 <= p.M) {
+              *reinterpret_cast<u16x4*>(d) = u16x4{hi[0], hi[1], hi[2], hi[3]};
+              if (p.terms > 1) *reinterpret_cast<u16x4*>(d + term) = u16x4{lo[0], lo[1], lo[2], lo[3]};
+            } else {
+              for (int c = 0; c < p.M - mb; ++c) {
+                d[c] = hi[c];
+                if (p.terms > 1) d[term + c] = lo[c];
+              }
             }
           }
         }
       }
     }
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -589,7 +629,7 @@ struct OrthoLayout {
   bool small;
   int p, P, pp, qp, terms, spans;
   int64_t q, span;
-  size_t off_g, off_q, off_part, off_inv, off_xf, off_x16, off_xt[2], off_g16, off_b16, bytes;
+  size_t off_g, off_q, off_part, off_bad, off_xf, off_x16, off_xt[2], off_g16, off_b16, bytes;
 };
 
 OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd) {
@@ -615,7 +655,7 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
     L.pp = (int)round_up(L.p, kBK);
     L.qp = (int)round_up(L.q, kBK);
     L.off_part = take((size_t)batch * kSumBlocks * sizeof(double));
-    L.off_inv = take((size_t)batch * 2 * sizeof(float));
+    L.off_bad = take((size_t)batch * sizeof(float));
     L.off_xf = take((size_t)batch * L.p * L.q * sizeof(float));
     L.off_x16 = take((size_t)batch * L.terms * L.p * L.qp * 2);
     for (auto& o : L.off_xt) o = take((size_t)batch * L.terms * L.q * L.pp * 2);
@@ -724,7 +764,6 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
     return xd == NQ_BF16 ? launch_small_p<uint16_t>(a, batch, s) : launch_small_p<float>(a, batch, s);
   }
   double* part = reinterpret_cast<double*>(ws + L.off_part);
-  float* inv = reinterpret_cast<float*>(ws + L.off_inv);
   LargeArgs l;
   l.p = L.p;
   l.pp = L.pp;
@@ -736,7 +775,8 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   for (int i = 0; i < 2; ++i) l.xt16[i] = reinterpret_cast<uint16_t*>(ws + L.off_xt[i]);
   l.g16 = reinterpret_cast<uint16_t*>(ws + L.off_g16);
   l.b16 = reinterpret_cast<uint16_t*>(ws + L.off_b16);
-  l.inv = inv;
+  l.part = part;
+  l.bad = reinterpret_cast<float*>(ws + L.off_bad);
   // |x| <= 1.25, |G| <= 1.25^2 and the polynomial's bound, each times its scale
   // below 65504
   const float sx = kScaleX, sg = 16384.0f;
@@ -752,8 +792,6 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
                        static_cast<const float*>(x), rows, cols, ldx, stride_x, part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(ortho_norm_kernel, dim3((unsigned)batch), dim3(64), 0, s, part, kSumBlocks, inv);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   if (xd == NQ_BF16)
     hipLaunchKernelGGL((ortho_prepare_kernel<uint16_t>), pgrid, dim3(256), 0, s, l, static_cast<const uint16_t*>(x), ldx,
                        stride_x, tall);
@@ -803,7 +841,7 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   step.y = y;
   step.y_bf16 = yd == NQ_BF16;
   step.y_t = tall;
-  step.inv = inv;
+  step.bad = l.bad;
   for (int i = 0; i < steps; ++i) {
     if ((e = launch_ortho_gemm<kGram>(gram, batch, s)) != hipSuccess) return e;
     if ((e = launch_ortho_gemm<kPoly>(poly, batch, s)) != hipSuccess) return e;
