@@ -32,7 +32,6 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kGramMax = 64;  // shorter sides up to this take the fp64 form
 
@@ -286,7 +285,7 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
 }
 
 // ---------------------------------------------------------------- p > 64
-constexpr int kBK = 64;
+constexpr int kBK = 64;  // operand rows are padded to this: every tile shape is a multiple of it
 constexpr float kScaleX = 16384.0f;  // operand scale of x: |x| <= 1.25
 constexpr int kSumBlocks = 512;  // partial sums of ||X||_F^2 per matrix
 
@@ -334,21 +333,53 @@ __device__ inline void split_half(float v, int terms, uint16_t& hi, uint16_t& lo
   lo = terms > 1 ? half_bits(v - (float)h) : 0;
 }
 
+// 8 values as fp16 terms, times a power of two.
+__device__ inline void store_terms(uint16_t* out, int64_t term, int terms, const float (&v)[8], float scale) {
+  f16x8 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = v[e] * scale;
+    hi[e] = (_Float16)x;
+    lo[e] = (_Float16)(x - (float)hi[e]);
+  }
+  *reinterpret_cast<f16x8*>(out) = hi;
+  if (terms > 1) *reinterpret_cast<f16x8*>(out + term) = lo;
+}
+
+// The first `count` of 8 consecutive results.
+__device__ inline void store8(void* y, int bf16, int64_t at, const float (&v)[8], int count) {
+  if (count >= 8) {
+    if (bf16) {
+      typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+      u32x4u w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)bf16_bits(v[2 * e]) | ((uint32_t)bf16_bits(v[2 * e + 1]) << 16);
+      *reinterpret_cast<u32x4u*>(static_cast<uint16_t*>(y) + at) = w;
+    } else {
+      f32x4u* o = reinterpret_cast<f32x4u*>(static_cast<float*>(y) + at);
+      o[0] = f32x4{v[0], v[1], v[2], v[3]};
+      o[1] = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < count) store1(y, bf16, at + e, v[e]);
+  }
+}
+
 struct LargeArgs {
   int p, pp;           // shorter side, and rounded up to kBK
   int q, qp;           // longer side
   int terms;
-  float* xf;           // [batch][p][q] state
+  float* xf;           // [batch][p][qp] state
   uint16_t* x16;       // [batch][terms][p][qp]
-  uint16_t* xt16[2];   // [batch][terms][q][pp]
-  uint16_t* g16;       // [batch][terms][p][pp]
-  uint16_t* b16;       // [batch][terms][p][pp]
+  uint16_t* xt16;      // [batch][terms][q][pp]
   const double* part;  // [batch][kSumBlocks]
   float* bad;          // [batch]: 0, or NaN for a matrix that is not finite
   float sx;            // operand scale of x
 };
 
-// X0 in all its forms, and zeros in the padding of every operand.  A workgroup
+// X0 in all its forms, with zeros in the padding.  A workgroup
 // takes 64 x 64 elements (shorter side by longer side) through LDS.
 template <typename E>
 __global__ __launch_bounds__(256) void ortho_prepare_kernel(LargeArgs s, const E* __restrict__ x, int64_t ldx,
@@ -369,13 +400,13 @@ __global__ __launch_bounds__(256) void ortho_prepare_kernel(LargeArgs s, const E
     tile[tall ? tx : k][tall ? k : tx] = v;
   }
   __syncthreads();
-  const int64_t xs = (int64_t)s.p * s.qp, ts = (int64_t)s.q * s.pp, gs = (int64_t)s.p * s.pp;
+  const int64_t xs = (int64_t)s.p * s.qp, ts = (int64_t)s.q * s.pp;
   for (int k = ty; k < 64; k += 4) {
     {
       const int i = i0 + k, j = j0 + tx;
       if (i < s.p) {
         const float v = tile[k][tx];
-        if (j < s.q) s.xf[(bi * s.p + i) * s.q + j] = v;
+        s.xf[(bi * s.p + i) * s.qp + j] = v;
         uint16_t hi, lo;
         split_half(v * s.sx, s.terms, hi, lo);
         uint16_t* d = s.x16 + bi * s.terms * xs + (int64_t)i * s.qp + j;
@@ -388,19 +419,20 @@ __global__ __launch_bounds__(256) void ortho_prepare_kernel(LargeArgs s, const E
       if (j < s.q) {
         uint16_t hi, lo;
         split_half(tile[tx][k] * s.sx, s.terms, hi, lo);
-        for (int b = 0; b < (i < s.p ? 1 : 2); ++b) {
-          uint16_t* d = s.xt16[b] + bi * s.terms * ts + (int64_t)j * s.pp + i;
-          d[0] = hi;
-          if (s.terms > 1) d[ts] = lo;
-        }
+        uint16_t* d = s.xt16 + bi * s.terms * ts + (int64_t)j * s.pp + i;
+        d[0] = hi;
+        if (s.terms > 1) d[ts] = lo;
       }
     }
   }
-  if (blockIdx.x == 0 && i0 + 64 > s.p)  // the last rows' block: padding columns of G and B
-    for (int64_t e = threadIdx.x; e < (int64_t)s.p * (s.pp - s.p); e += 256) {
-      const int64_t at = bi * s.terms * gs + e / (s.pp - s.p) * s.pp + s.p + e % (s.pp - s.p);
-      for (int t = 0; t < s.terms; ++t) s.g16[at + t * gs] = s.b16[at + t * gs] = 0;
-    }
+}
+
+// Wait until at most N vector-memory operations of this wave are outstanding,
+// and none of its LDS reads.
+template <int N>
+__device__ inline void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
 }
 
 enum Mode { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
@@ -414,7 +446,7 @@ struct GemmArgs {
   float s_acc, s_aux;
   int terms;
   // kGram, kPoly: out16 [batch][terms][M][ldo]; kPoly: aux16 as out16
-  // kStep: xf, out16 (x16), outt16 (the transpose); kLast: y
+  // kStep: xf (rows of ldo), out16 (x16), outt16 (the transpose); kLast: xf, y
   uint16_t* out16;
   uint16_t* outt16;
   const uint16_t* aux16;
@@ -425,15 +457,21 @@ struct GemmArgs {
   const float* bad;
 };
 
-// C = A B^T, workgroup tile BM x BN x 64: WM x WN waves of 32x32x16 fp16
+// C = A B^T, workgroup tile BM x BN x BK: WM x WN waves of 32x32x16 fp16
 // instructions.  Both operands stream into a ring of S LDS stages by direct
-// global->LDS loads; rows of 128 bytes, 16-byte chunk c of row r stored at
-// chunk c ^ ((r >> 1) & 7), so that fragment reads (32 rows at one chunk) meet
-// no bank twice in a group of 8 lanes.
-template <int BM, int BN, int WM, int WN, int S, int MODE>
+// global->LDS loads; rows of 2 BK bytes, 16-byte chunk c of row r stored at
+// chunk c ^ swizzle(r), so that the 16 rows that a fragment read takes at once
+// meet 16 different bank groups.
+template <int BK>
+__device__ constexpr int swizzle(int r) {
+  return BK == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
+
+template <int BM, int BN, int BK, int WM, int WN, int S, bool SPREAD, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
   constexpr int NW = WM * WN, MB = BM / WM / 32, NB = BN / WN / 32;
-  constexpr int STAGE = (BM + BN) * 128, LOADS_A = BM / 8 / NW, LOADS_B = BN / 8 / NW;
+  constexpr int ROW = 2 * BK, RPL = 1024 / ROW, CH = BK / 8;  // row bytes, rows of a load, chunks of a row
+  constexpr int STAGE = (BM + BN) * ROW, LOADS_A = BM / RPL / NW, LOADS_B = BN / RPL / NW;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -458,35 +496,43 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
   const uint16_t* A = p.A + bi * p.stride_a + (int64_t)m0 * p.K;
   const uint16_t* B = p.B + bi * p.stride_b + (int64_t)n0 * p.K;
   // rows past the matrix load its last row; they are not stored
-  const int drow = lane / 8, dchunk = lane % 8;
-  uint32_t oa[LOADS_A], ob[LOADS_B];
+  const int drow = lane / CH, dchunk = lane % CH;
+  uint32_t oa[LOADS_A], ob[LOADS_B];  // bytes: a row of a tile lies below 2^25
 #pragma unroll
   for (int j = 0; j < LOADS_A; ++j) {
-    const int r = (wave * LOADS_A + j) * 8 + drow;
-    oa[j] = (uint32_t)min(r, p.M - 1 - m0) * p.K + ((dchunk ^ ((r >> 1) & 7)) * 8);
+    const int r = (wave * LOADS_A + j) * RPL + drow;
+    oa[j] = 2 * ((uint32_t)min(r, p.M - 1 - m0) * p.K + (dchunk ^ swizzle<BK>(r)) * 8);
   }
 #pragma unroll
   for (int j = 0; j < LOADS_B; ++j) {
-    const int r = (wave * LOADS_B + j) * 8 + drow;
-    ob[j] = (uint32_t)min(r, p.N - 1 - n0) * p.K + ((dchunk ^ ((r >> 1) & 7)) * 8);
+    const int r = (wave * LOADS_B + j) * RPL + drow;
+    ob[j] = 2 * ((uint32_t)min(r, p.N - 1 - n0) * p.K + (dchunk ^ swizzle<BK>(r)) * 8);
   }
-  const int nk = p.K / kBK, total = nk * p.nseg;
-  // product terms, the smallest first: hi lo, lo hi, hi hi
-  auto issue = [&](int kt, int st) {
+  const int nk = p.K / BK, total = nk * p.nseg;
+  // product terms, the smallest first: hi lo, lo hi, hi hi; a stage's loads in
+  // STEPS parts
+  constexpr int STEPS = BK / 16, PER = LOADS_A + LOADS_B, PART = (PER + STEPS - 1) / STEPS;
+  auto issue = [&](int k, int st, int part) {
+    const int kt = min(k, total - 1);
     const int seg = kt / nk, kk = kt - seg * nk;
     const int ta = p.nseg == 1 ? 0 : (seg == 1), tb = p.nseg == 1 ? 0 : (seg == 0);
-    const uint16_t* a = A + ta * p.term_a + (int64_t)kk * kBK;
-    const uint16_t* b = B + tb * p.term_b + (int64_t)kk * kBK;
+    const char* a = reinterpret_cast<const char*>(A + ta * p.term_a + (int64_t)kk * BK);
+    const char* b = reinterpret_cast<const char*>(B + tb * p.term_b + (int64_t)kk * BK);
     char* dst = lds + st * STAGE;
 #pragma unroll
-    for (int j = 0; j < LOADS_A; ++j)
-      __builtin_amdgcn_global_load_lds((const void*)(a + oa[j]),
-                                       (__attribute__((address_space(3))) void*)(dst + (wave * LOADS_A + j) * 1024), 16, 0, 0);
-#pragma unroll
-    for (int j = 0; j < LOADS_B; ++j)
-      __builtin_amdgcn_global_load_lds(
-          (const void*)(b + ob[j]), (__attribute__((address_space(3))) void*)(dst + BM * 128 + (wave * LOADS_B + j) * 1024),
-          16, 0, 0);
+    for (int l = part * PART; l < (part + 1) * PART && l < PER; ++l) {
+      const int j = l / 2;  // A and B in turn
+      const bool of_a = LOADS_A == LOADS_B ? l % 2 == 0 : l < LOADS_A;
+      const int i = LOADS_A == LOADS_B ? j : (of_a ? l : l - LOADS_A);
+      if (of_a)
+        __builtin_amdgcn_global_load_lds((const void*)(a + oa[i < LOADS_A ? i : 0]),
+                                         (__attribute__((address_space(3))) void*)(dst + (wave * LOADS_A + i) * 1024), 16, 0,
+                                         0);
+      else
+        __builtin_amdgcn_global_load_lds(
+            (const void*)(b + ob[i < LOADS_B ? i : 0]),
+            (__attribute__((address_space(3))) void*)(dst + BM * ROW + (wave * LOADS_B + i) * 1024), 16, 0, 0);
+    }
   };
   f32x16 acc[MB][NB];
 #pragma unroll
@@ -495,128 +541,246 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  uint32_t sw[4];  // chunk 2s + h of this lane's row, swizzled
+  uint32_t sw[STEPS];  // chunk 2s + h of this lane's row, swizzled
 #pragma unroll
-  for (int s = 0; s < 4; ++s) sw[s] = (uint32_t)l32 * 128 + (((2 * s + h) ^ ((l32 >> 1) & 7)) * 16);
-  const uint32_t fa = wm * (BM / WM) * 128, fb = BM * 128 + wn * (BN / WN) * 128;
+  for (int s = 0; s < STEPS; ++s) sw[s] = (uint32_t)l32 * ROW + (((2 * s + h) ^ swizzle<BK>(l32)) * 16);
+  const uint32_t fa = wm * (BM / WM) * ROW, fb = BM * ROW + wn * (BN / WN) * ROW;
+  // The fragments of a 16-deep step are read while the one before it is
+  // multiplied, across stages too: once a wave holds the last step's fragments
+  // it has no more use for the stage, so the barrier that frees it stands before
+  // that step's products.
+  f16x8 af[2][MB], bf[2][NB];
+  auto read = [&](const char* stage, int s) {
 #pragma unroll
-  for (int kt = 0; kt < S - 1; ++kt)
-    if (kt < total) issue(kt, kt);
-  for (int kt0 = 0; kt0 < total; kt0 += S) {
+    for (int i = 0; i < MB; ++i) af[s & 1][i] = *reinterpret_cast<const f16x8*>(stage + fa + i * 32 * ROW + sw[s]);
 #pragma unroll
-    for (int st = 0; st < S; ++st) {
-      const int kt = kt0 + st;
-      if (kt >= total) break;
-      // wait for stage kt; up to S - 2 later ones stay in flight
-      const int ahead = min(total - 1 - kt, S - 2);
-      constexpr int PER = LOADS_A + LOADS_B;
-      if (S > 2 && ahead == S - 2)
-        __builtin_amdgcn_s_waitcnt((((S - 2) * PER) & 15) | (7 << 4) | (15 << 8) | ((((S - 2) * PER) >> 4) << 14));
-      else
-        __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
+    for (int j = 0; j < NB; ++j) bf[s & 1][j] = *reinterpret_cast<const f16x8*>(stage + fb + j * 32 * ROW + sw[s]);
+  };
+  auto issue_all = [&](int kt, int st) {
+#pragma unroll
+    for (int part = 0; part < STEPS; ++part) issue(kt, st, part);
+  };
+  static_assert(STEPS % 2 == 0, "fragment buffers alternate across stages");
+  if constexpr (SPREAD) {
+    // the loads of stage kt + S follow in parts, one beside each step's products.
+    // There are no branches: past the end the last stage is loaded and read again
+    // (a branch would have the compiler wait for the reads on both its sides).
+    // 128 x 128 tiles of 2 x 1371 x 1371 x 2203: 59 us, at once 75.
+    // wait for the stage after this one (the S - 2 younger ones may stay in
+    // flight) and for this wave's fragment reads, then meet the other waves
+    auto landed = [&] {
+      wait_loads<(S - 2) * PER>();
       asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_barrier();  // every wave's loads of stage kt have landed, stage kt - 1 is consumed
+      __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      if (kt + S - 1 < total) issue(kt + S - 1, (st + S - 1) % S);
-      const char* stage = lds + st * STAGE;
-      f16x8 af[2][MB], bf[2][NB];
-      auto read = [&](int s) {
+    };
 #pragma unroll
-        for (int i = 0; i < MB; ++i) af[s & 1][i] = *reinterpret_cast<const f16x8*>(stage + fa + i * 32 * 128 + sw[s]);
+    for (int kt = 0; kt < S - 1; ++kt)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) bf[s & 1][j] = *reinterpret_cast<const f16x8*>(stage + fb + j * 32 * 128 + sw[s]);
-      };
-      read(0);
+      for (int part = 0; part < STEPS; ++part) issue(kt, kt, part);
+    landed();
+    issue(S - 1, S - 1, 0);
+    read(lds, 0);
+    for (int kt0 = 0; kt0 < total; kt0 += S) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        __builtin_amdgcn_sched_barrier(0);
-        if (s < 3) read(s + 1);
+      for (int st = 0; st < S; ++st) {
+        const int kt = kt0 + st;
+        if (kt >= total) break;
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+        for (int s = 0; s < STEPS; ++s) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (s + 1 < STEPS) {
+            read(lds + st * STAGE, s + 1);
+            issue(kt + S - 1, (st + S - 1) % S, s + 1);
+          } else {
+            landed();
+            __builtin_amdgcn_sched_barrier(0);
+            read(lds + (st + 1) % S * STAGE, 0);
+            issue(kt + S, st, 0);
+          }
 #pragma unroll
-          for (int j = 0; j < NB; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[s & 1][i], bf[s & 1][j], acc[i][j], 0, 0, 0);
-        // one matrix instruction, then a share of the next step's fragment reads
+          for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int i = 0; i < MB * NB; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          if (s < 3 && i < MB + NB) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            for (int j = 0; j < NB; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[s & 1][i], bf[s & 1][j], acc[i][j], 0, 0, 0);
+          // one matrix instruction, then a share of the next step's fragment reads
+          // and of the loads
+#pragma unroll
+          for (int i = 0; i < MB * NB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (i < MB + NB) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (i >= MB * NB - PART) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    wait_loads<0>();  // no load may land in LDS that the next workgroup owns
+  } else {
+    // the loads of stage kt + S at once behind the barrier: faster where two stages
+    // are all that LDS holds (256 x 256: 276 us, spread 308; 4096 x 4096 x 11008)
+    // wait for stage kt (later stages, S - 1 at most, may stay in flight) and for
+    // this wave's fragment reads, then meet the other waves
+    auto landed = [&](int later) {
+      if (later >= S - 2)
+        wait_loads<(S - 2) * PER>();
+      else if (S > 3 && later == 1)
+        wait_loads<PER>();
+      else
+        wait_loads<0>();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+#pragma unroll
+    for (int kt = 0; kt < S; ++kt)
+      if (kt < total) issue_all(kt, kt);
+    if (total > S - 1)
+      wait_loads<(S - 1) * PER>();
+    else
+      wait_loads<0>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(lds, 0);
+    for (int kt0 = 0; kt0 < total; kt0 += S) {
+#pragma unroll
+      for (int st = 0; st < S; ++st) {
+        const int kt = kt0 + st;
+        if (kt >= total) break;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const bool more = s + 1 < STEPS || kt + 1 < total;
+          __builtin_amdgcn_sched_barrier(0);
+          if (s + 1 < STEPS) {
+            read(lds + st * STAGE, s + 1);
+          } else if (kt + 1 < total) {
+            landed(total - 2 - kt);
+            if (kt + S < total) issue_all(kt + S, st);
+            __builtin_amdgcn_sched_barrier(0);
+            read(lds + (st + 1) % S * STAGE, 0);
+          } else {  // as on the other path, so that no wait for the reads above comes before the products
+            wait_loads<0>();
+          }
+#pragma unroll
+          for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[s & 1][i], bf[s & 1][j], acc[i][j], 0, 0, 0);
+          // one matrix instruction, then a share of the next step's fragment reads
+          if (more) {
+#pragma unroll
+            for (int i = 0; i < MB * NB; ++i) {
+              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+              if (i < MB + NB) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   }
-  // lane l, register 4a + c of a block: row 8a + 4(l / 32) + c, column l % 32
+  // Epilogue, 32 rows at a time through the wave's part of LDS: lane l, register
+  // 4a + c of a block holds row 8a + 4(l / 32) + c of column l % 32; read back, a
+  // lane holds 8 consecutive columns of a row, and for a transposed result 8
+  // consecutive rows of a column.  So everything moves 16 bytes a lane, in runs of
+  // 64 bytes or more (two bytes a lane, straight from the registers, took 75 us of
+  // the 150 us of a 256 x 256 tile with two terms).  Values past the matrix are
+  // zero: they are the padding of the next product's operands.
+  constexpr int CW = BN / WN, CS = CW + 4, CH8 = CW / 8, RPI = 64 / CH8;  // columns, LDS row, pieces, rows at once
+  static_assert(NW * 32 * CS * 4 <= S * STAGE, "the ring holds the waves' blocks");
+  float* blk = reinterpret_cast<float*>(lds) + wave * 32 * CS;
   uint16_t* out = p.out16 + bi * p.terms * p.term_o;
   uint16_t* outt = p.outt16 + bi * p.terms * p.term_t;
   const uint16_t* aux = p.aux16 + bi * p.terms * p.term_o;
+  float* xf = p.xf + bi * p.M * p.ldo;
+  const int64_t ybase = bi * p.M * (int64_t)p.N;
   const bool mirror = (MODE == kGram || MODE == kPoly) && p.sym && tm != tn;
+  const bool transposed = MODE == kStep || (MODE == kLast && p.y_t) || mirror;
   const float bad = MODE == kLast ? p.bad[bi] : 0.0f;
+  const int nb = n0 + wn * CW;
+  // a transposed operand has padding along this tile's rows, too
+  const int64_t rows_end = MODE == kStep ? p.ldt : (mirror ? p.ldo : p.M);
+  __syncthreads();  // every wave is done with the ring
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    const int mr = m0 + wm * (BM / WM) + i * 32 + 4 * h;
-    // what the block row reads, ahead of its stores (the compiler keeps their
-    // order: one load at a time cost 70 us a round of tiles); elements past the
-    // matrix repeat its last
-    float x[NB][16];
+    const int mr = m0 + wm * (BM / WM) + i * 32;
+    if (mr >= rows_end) break;
+    // what the block reads: 8 columns of rows lane / CH8 + RPI t
+    float x[32 / RPI][8];
+    const int n = nb + lane % CH8 * 8;
     if constexpr (MODE != kGram) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int n = min(n0 + wn * (BN / WN) + j * 32 + l32, p.N - 1);
+      for (int t = 0; t < 32 / RPI; ++t) {
+        const int64_t at = (int64_t)min(mr + lane / CH8 + RPI * t, p.M - 1) * p.ldo + min((int64_t)n, p.ldo - 8);
+        if constexpr (MODE == kPoly) {
+          const f16x8 g = *reinterpret_cast<const f16x8*>(aux + at);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int m = min(mr + 8 * (r / 4) + r % 4, p.M - 1);
-          if constexpr (MODE == kPoly) {
-            x[j][r] = (float)__builtin_bit_cast(_Float16, aux[(int64_t)m * p.ldo + n]);
-            if (p.terms > 1) x[j][r] += (float)__builtin_bit_cast(_Float16, aux[(int64_t)m * p.ldo + n + p.term_o]);
-          } else {
-            x[j][r] = p.xf[(bi * p.M + m) * (int64_t)p.N + n];
+          for (int e = 0; e < 8; ++e) x[t][e] = (float)g[e];
+          if (p.terms > 1) {
+            const f16x8 l = *reinterpret_cast<const f16x8*>(aux + at + p.term_o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[t][e] += (float)l[e];
           }
+        } else {
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(xf + at), hi = *reinterpret_cast<const f32x4*>(xf + at + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][e] = lo[e], x[t][4 + e] = hi[e];
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int n = n0 + wn * (BN / WN) + j * 32 + l32;
-      if (n >= p.N) continue;
+    for (int j = 0; j < NB; ++j)
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int mb = mr + 8 * a;
-        uint16_t hi[4], lo[4];
-        float v[4];
+      for (int r = 0; r < 16; ++r) blk[(8 * (r / 4) + 4 * h + r % 4) * CS + j * 32 + l32] = acc[i][j][r];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          v[c] = acc[i][j][4 * a + c] * p.s_acc;
-          if constexpr (MODE != kGram) v[c] = fmaf(p.s_aux, x[j][4 * a + c], v[c]);
-          if constexpr (MODE != kLast) split_half(MODE == kStep ? v[c] * kScaleX : v[c], p.terms, hi[c], lo[c]);
+    for (int t = 0; t < 32 / RPI; ++t) {
+      const int row = lane / CH8 + RPI * t, m = mr + row;
+      float* cell = blk + row * CS + lane % CH8 * 8;
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f32x4 c = *reinterpret_cast<const f32x4*>(cell + 4 * u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * u + e] = c[e] * p.s_acc;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (MODE != kGram) v[e] = fmaf(p.s_aux, x[t][e], v[e]);
+        if constexpr (MODE == kLast) v[e] += bad;
+        if (m >= p.M || n + e >= p.N) v[e] = 0.0f;
+      }
+      if (transposed) {
+        *reinterpret_cast<f32x4*>(cell) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(cell + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      }
+      if (m >= p.M) continue;
+      if constexpr (MODE == kLast) {
+        if (!p.y_t) store8(p.y, p.y_bf16, ybase + (int64_t)m * p.N + n, v, p.N - n);
+      } else if (n < p.ldo) {
+        if constexpr (MODE == kStep) {
+          float* at = xf + (int64_t)m * p.ldo + n;
+          *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+          *reinterpret_cast<f32x4*>(at + 4) = f32x4{v[4], v[5], v[6], v[7]};
         }
+        store_terms(out + (int64_t)m * p.ldo + n, p.term_o, p.terms, v, MODE == kStep ? kScaleX : 1.0f);
+      }
+    }
+    if (transposed) {  // 8 rows of column lane / 4 + 16 t
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int m = mb + c;
-          if (m >= p.M) continue;
-          if constexpr (MODE == kStep) p.xf[(bi * p.M + m) * (int64_t)p.N + n] = v[c];
-          if constexpr (MODE == kLast) {
-            store1(p.y, p.y_bf16, bi * p.M * (int64_t)p.N + (p.y_t ? (int64_t)n * p.M + m : (int64_t)m * p.N + n), v[c] + bad);
-          } else {
-            const int64_t at = (int64_t)m * p.ldo + n;
-            out[at] = hi[c];
-            if (p.terms > 1) out[at + p.term_o] = lo[c];
-          }
-        }
-        if constexpr (MODE != kLast) {
-          if ((MODE == kStep || mirror) && mb < p.M) {
-            uint16_t* d = (MODE == kStep ? outt : out) + (int64_t)n * (MODE == kStep ? p.ldt : p.ldo) + mb;
-            const int64_t term = MODE == kStep ? p.term_t : p.term_o;
-            if (mb + 4 <= p.M) {
-              *reinterpret_cast<u16x4*>(d) = u16x4{hi[0], hi[1], hi[2], hi[3]};
-              if (p.terms > 1) *reinterpret_cast<u16x4*>(d + term) = u16x4{lo[0], lo[1], lo[2], lo[3]};
-            } else {
-              for (int c = 0; c < p.M - mb; ++c) {
-                d[c] = hi[c];
-                if (p.terms > 1) d[term + c] = lo[c];
-              }
-            }
-          }
+      for (int t = 0; t < CW / 16; ++t) {
+        const int col = lane / 4 + 16 * t, nn = nb + col, m = mr + lane % 4 * 8;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = blk[(lane % 4 * 8 + e) * CS + col];
+        if (nn >= p.N) continue;
+        if constexpr (MODE == kLast) {
+          store8(p.y, p.y_bf16, ybase + (int64_t)nn * p.M + m, v, p.M - m);
+        } else {
+          const int64_t ld = MODE == kStep ? p.ldt : p.ldo;
+          if (m < ld)
+            store_terms((MODE == kStep ? outt : out) + (int64_t)nn * ld + m, MODE == kStep ? p.term_t : p.term_o, p.terms, v,
+                        MODE == kStep ? kScaleX : 1.0f);
         }
       }
     }
@@ -656,7 +820,7 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
     L.qp = (int)round_up(L.q, kBK);
     L.off_part = take((size_t)batch * kSumBlocks * sizeof(double));
     L.off_bad = take((size_t)batch * sizeof(float));
-    L.off_xf = take((size_t)batch * L.p * L.q * sizeof(float));
+    L.off_xf = take((size_t)batch * L.p * L.qp * sizeof(float));
     L.off_x16 = take((size_t)batch * L.terms * L.p * L.qp * 2);
     for (auto& o : L.off_xt) o = take((size_t)batch * L.terms * L.q * L.pp * 2);
     L.off_g16 = take((size_t)batch * L.terms * L.p * L.pp * 2);
@@ -692,10 +856,10 @@ hipError_t launch_small_p(const SmallArgs& a, int64_t batch, hipStream_t s) {
   }
 }
 
-template <int BM, int BN, int WM, int WN, int S, int MODE>
+template <int BM, int BN, int BK, int WM, int WN, int S, bool SPREAD, int MODE>
 hipError_t launch_gemm_tile(GemmArgs g, int64_t batch, hipStream_t s) {
-  constexpr size_t lds = (size_t)S * (BM + BN) * 128;
-  const auto kernel = ortho_gemm_kernel<BM, BN, WM, WN, S, MODE>;
+  constexpr size_t lds = (size_t)S * (BM + BN) * BK * 2;
+  const auto kernel = ortho_gemm_kernel<BM, BN, BK, WM, WN, S, SPREAD, MODE>;
   static std::atomic<uint64_t> done{0};
   hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), lds, done);
   if (e != hipSuccess) return e;
@@ -709,16 +873,23 @@ hipError_t launch_gemm_tile(GemmArgs g, int64_t batch, hipStream_t s) {
 template <int MODE>
 hipError_t launch_ortho_gemm(GemmArgs g, int64_t batch, hipStream_t s) {
   constexpr bool square = MODE == kGram || MODE == kPoly;
-  // 256 x 256 tiles (one workgroup per CU) once they fill the chip; symmetric
-  // results skip the tiles above the diagonal where that saves whole rounds
-  const int64_t t256 = cdiv(g.M, 256), big = t256 * cdiv(g.N, 256) * batch;
-  if (big >= 192) {
-    const int64_t half = t256 * (t256 + 1) / 2 * batch;
-    g.sym = square && cdiv(half, 256) < cdiv(big, 256);
-    return launch_gemm_tile<256, 256, 2, 4, 2, MODE>(g, batch, s);
-  }
-  g.sym = square;
-  return launch_gemm_tile<128, 128, 2, 2, 2, MODE>(g, batch, s);
+  // The largest tile that still occupies most of the chip: per product, smaller
+  // tiles move more operand bytes and take more of the power the matrix cores run
+  // on (4096 x 4096 x 11008, symmetric: 256 us with 256 x 256 tiles, 300 with
+  // 128 x 128), but a launch of few large tiles leaves CUs idle (2 x 1371 x 1371 x
+  // 2203, two terms: 108 tiles of 256 x 256 107 us, 198 of 128 x 256 75 us; 42 /
+  // 132 / 552 tiles of 256 / 128 / 64 in the symmetric product of p x p matrices
+  // 101 / 45 / 39 us).
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    const int64_t tm = cdiv(g.M, bm), tn = cdiv(g.N, bn);
+    return batch * (g.sym ? tm * (tm + 1) / 2 : tm * tn);
+  };
+  g.sym = square;  // a symmetric result: tiles on and below the diagonal, stored twice
+  if (tiles(256, 256) >= (square ? 128 : 224)) return launch_gemm_tile<256, 256, 64, 2, 4, 2, false, MODE>(g, batch, s);
+  if constexpr (!square)
+    if (tiles(128, 256) >= 128) return launch_gemm_tile<128, 256, 64, 2, 4, 3, true, MODE>(g, batch, s);
+  if (tiles(128, 128) >= 192) return launch_gemm_tile<128, 128, 64, 2, 2, 4, true, MODE>(g, batch, s);
+  return launch_gemm_tile<64, 64, 64, 2, 2, 4, true, MODE>(g, batch, s);
 }
 
 // The largest |b l + c l^2| for l in [0, top].
@@ -772,9 +943,10 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   l.terms = L.terms;
   l.xf = reinterpret_cast<float*>(ws + L.off_xf);
   l.x16 = reinterpret_cast<uint16_t*>(ws + L.off_x16);
-  for (int i = 0; i < 2; ++i) l.xt16[i] = reinterpret_cast<uint16_t*>(ws + L.off_xt[i]);
-  l.g16 = reinterpret_cast<uint16_t*>(ws + L.off_g16);
-  l.b16 = reinterpret_cast<uint16_t*>(ws + L.off_b16);
+  uint16_t* const xt16[2] = {reinterpret_cast<uint16_t*>(ws + L.off_xt[0]), reinterpret_cast<uint16_t*>(ws + L.off_xt[1])};
+  uint16_t* const g16 = reinterpret_cast<uint16_t*>(ws + L.off_g16);
+  uint16_t* const b16 = reinterpret_cast<uint16_t*>(ws + L.off_b16);
+  l.xt16 = xt16[0];
   l.part = part;
   l.bad = reinterpret_cast<float*>(ws + L.off_bad);
   // |x| <= 1.25, |G| <= 1.25^2 and the polynomial's bound, each times its scale
@@ -809,20 +981,20 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   gram.term_a = gram.term_b = xs;
   gram.M = gram.N = L.p;
   gram.K = L.qp;
-  gram.out16 = l.g16;
+  gram.out16 = g16;
   gram.ldo = L.pp;
   gram.term_o = gs;
   gram.s_acc = sg / (sx * sx);
   poly = gram;
-  poly.A = poly.B = l.g16;
+  poly.A = poly.B = g16;
   poly.stride_a = poly.stride_b = L.terms * gs;
   poly.term_a = poly.term_b = gs;
   poly.K = L.pp;
-  poly.out16 = l.b16;
-  poly.aux16 = l.g16;
+  poly.out16 = b16;
+  poly.aux16 = g16;
   poly.s_acc = (float)(cc * sb / ((double)sg * sg));
   poly.s_aux = (float)(cb * sb / sg);
-  step.A = l.b16;
+  step.A = b16;
   step.stride_a = L.terms * gs;
   step.term_a = gs;
   step.stride_b = L.terms * ts;
@@ -845,8 +1017,8 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   for (int i = 0; i < steps; ++i) {
     if ((e = launch_ortho_gemm<kGram>(gram, batch, s)) != hipSuccess) return e;
     if ((e = launch_ortho_gemm<kPoly>(poly, batch, s)) != hipSuccess) return e;
-    step.B = l.xt16[i % 2];
-    step.outt16 = l.xt16[1 - i % 2];
+    step.B = xt16[i % 2];
+    step.outt16 = xt16[1 - i % 2];
     e = i + 1 < steps ? launch_ortho_gemm<kStep>(step, batch, s) : launch_ortho_gemm<kLast>(step, batch, s);
     if (e != hipSuccess) return e;
   }
