@@ -70,6 +70,20 @@ __device__ inline void store1(void* y, int bf16, int64_t i, float v) {
     static_cast<float*>(y)[i] = v;
 }
 
+// The first `count` of 4 consecutive results.
+__device__ inline void store4(void* y, int bf16, int64_t at, const float (&v)[4], int64_t count) {
+  if (count >= 4 && bf16) {
+    *reinterpret_cast<u16x4u*>(static_cast<uint16_t*>(y) + at) =
+        u16x4u{bf16_bits(v[0]), bf16_bits(v[1]), bf16_bits(v[2]), bf16_bits(v[3])};
+  } else if (count >= 4) {
+    *reinterpret_cast<f32x4u*>(static_cast<float*>(y) + at) = f32x4{v[0], v[1], v[2], v[3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < count) store1(y, bf16, at + e, v[e]);
+  }
+}
+
 // ---------------------------------------------------------------- p <= 64
 // One 16x16x4 fp64 instruction: lane l holds row l % 16, reduction l / 16 of
 // each operand and rows 4 i + l / 16 (i = 0..3) of column l % 16 of the result.
@@ -93,6 +107,34 @@ __device__ inline const E* elem(const SmallArgs& s, const E* x, int64_t i, int64
   return s.tall ? x + j * s.ldx + i : x + i * s.ldx + j;
 }
 
+// A lane's operands of a 32-deep step of the longer side from j: rows 16t + c,
+// elements j + 8q + e (e-th instruction), zero from j1 on.
+template <typename E, int PT>
+__device__ inline void load_step(const SmallArgs& s, const E* x, int64_t j, int64_t j1, int q, int c, float (&v)[PT][8]) {
+  const bool full = j + 32 <= j1;
+#pragma unroll
+  for (int t = 0; t < PT; ++t) {
+    const int64_t i = min(16 * t + c, s.p - 1);
+    const E* at = elem(s, x, i, j + 8 * q);
+    if (full && !s.tall) {
+      float lo[4], hi[4];
+      load4(at, lo);
+      load4(at + 4, hi);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[t][e] = lo[e], v[t][4 + e] = hi[e];
+    } else if (full) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[t][e] = load1(at + e * s.ldx);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t jj = j + 8 * q + e;
+        v[t][e] = jj < j1 ? load1(elem(s, x, i, jj)) : 0.0f;
+      }
+    }
+  }
+}
+
 template <typename E, int PT>
 __global__ __launch_bounds__(256) void ortho_gram_kernel(SmallArgs s) {
   __shared__ double part[4][4][64];
@@ -103,18 +145,16 @@ __global__ __launch_bounds__(256) void ortho_gram_kernel(SmallArgs s) {
 #pragma unroll
   for (int k = 0; k < NPAIR; ++k) acc[k] = f64x4{0, 0, 0, 0};
   const int64_t j0 = (int64_t)blockIdx.x * s.span, j1 = imin(s.q, j0 + s.span);
-  for (int64_t j = j0 + 32 * wave; j < j1; j += 128) {
-    // lane group q takes elements j + 8q .. of the longer side, step e the e-th
+  float next[PT][8];
+  int64_t j = j0 + 32 * wave;
+  if (j < j1) load_step<E, PT>(s, x, j, j1, q, c, next);
+  for (; j < j1; j += 128) {
     float v[PT][8];
 #pragma unroll
-    for (int t = 0; t < PT; ++t) {
-      const int64_t i = min(16 * t + c, s.p - 1);
+    for (int t = 0; t < PT; ++t)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t jj = j + 8 * q + e;
-        v[t][e] = jj < j1 ? load1(elem(s, x, i, jj)) : 0.0f;
-      }
-    }
+      for (int e = 0; e < 8; ++e) v[t][e] = next[t][e];
+    if (j + 128 < j1) load_step<E, PT>(s, x, j + 128, j1, q, c, next);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       int k = 0;
@@ -144,6 +184,13 @@ __global__ __launch_bounds__(256) void ortho_gram_kernel(SmallArgs s) {
     }
 }
 
+// 1 / ||X||_F^2 and 1 / ||X||_F from the trace of the Gram matrix.  A zero matrix
+// stays zero; one that is not finite gives NaN.
+__device__ inline void inverse_trace(double t, double& inv, double& root) {
+  inv = t > 0.0 && isfinite(t) ? 1.0 / t : (t == 0.0 ? 0.0 : __builtin_nan(""));
+  root = t > 0.0 && isfinite(t) ? 1.0 / sqrt(t) : inv;
+}
+
 // The iteration on p x p matrices, one workgroup per matrix.  A (the Gram
 // matrix of the iterate), P = a I + b A + c A^2 and Q (the product of the P so
 // far) commute and are symmetric: every product reads both operands by rows.
@@ -156,19 +203,16 @@ __global__ __launch_bounds__(256) void ortho_solve_kernel(SmallArgs s) {
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, q = lane / 16, c = lane % 16;
   const double* g = s.gpart + (int64_t)blockIdx.x * s.spans * P * P;
   for (int i = tid; i < P * P; i += 256) {
-    double v = g[i];
-    for (int k = 1; k < s.spans; ++k) v += g[(int64_t)k * P * P + i];
+    double v = 0.0;
+#pragma unroll 8
+    for (int k = 0; k < s.spans; ++k) v += g[(int64_t)k * P * P + i];
     A[i / P * S + i % P] = v;
   }
   __syncthreads();
   if (wave == 0) {  // ||X||_F^2 is the trace
     double t = lane < P ? A[lane * S + lane] : 0.0;
     for (int off = 32; off > 0; off >>= 1) t += __shfl_xor(t, off);
-    if (lane == 0) {
-      // a zero matrix stays zero; a matrix that is not finite gives NaN
-      inv_sh[0] = t > 0.0 && isfinite(t) ? 1.0 / t : (t == 0.0 ? 0.0 : __builtin_nan(""));
-      inv_sh[1] = t > 0.0 && isfinite(t) ? 1.0 / sqrt(t) : inv_sh[0];
-    }
+    if (lane == 0) inverse_trace(t, inv_sh[0], inv_sh[1]);
   }
   __syncthreads();
   const double inv = inv_sh[0];
@@ -223,40 +267,124 @@ __global__ __launch_bounds__(256) void ortho_solve_kernel(SmallArgs s) {
   for (int i = tid; i < P * P; i += 256) out[i] = Q[i / P * S + i % P] * inv_sh[1];
 }
 
-// Y = Q X: a wave takes 64 elements of the longer side.
+// The same for p <= 16 in the registers of a wave: its lanes hold a symmetric
+// matrix M as M[c][4i + q], which is both how the instruction takes either operand
+// (step i) and how it returns M[4i + q][c].
+__device__ inline void solve16(const SmallArgs& s, double (&A)[4], double (&Q)[4], int q, int c) {
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t += c == 4 * i + q ? A[i] : 0.0;
+  for (int off = 32; off > 0; off >>= 1) t += __shfl_xor(t, off);
+  double inv, root;
+  inverse_trace(t, inv, root);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] *= inv;
+  auto product = [&](const double (&L)[4], const double (&R)[4], double (&D)[4]) {
+    f64x4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(L[i], R[i], acc, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) D[i] = acc[i];
+  };
+  for (int step = 0; step < s.steps; ++step) {
+    double B[4];
+    product(A, A, B);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) B[i] = s.c * B[i] + s.b * A[i] + (c == 4 * i + q ? s.a : 0.0);
+    if (step == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) Q[i] = B[i];
+    } else {
+      product(Q, B, Q);
+    }
+    if (step + 1 < s.steps) {
+      product(A, B, A);
+      product(A, B, A);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) Q[i] *= root;
+}
+
+// Y = Q X: a wave takes 64 elements of the longer side.  For p <= 16 every
+// workgroup computes Q itself, from the spans' Gram matrices (a launch of its own
+// for a few thousand operations would cost more).
 template <typename E, int PT>
 __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
   constexpr int P = 16 * PT, S = P + 4;
   extern __shared__ double lds64[];
   const int tid = threadIdx.x, lane = tid % 64, q = lane / 16, c = lane % 16;
-  const double* qm = s.qmat + (int64_t)blockIdx.y * P * P;
-  for (int i = tid; i < P * P; i += 256) lds64[i / P * S + i % P] = qm[i];
-  __syncthreads();
   const int64_t j0 = ((int64_t)blockIdx.x * 4 + tid / 64) * 64;
-  if (j0 >= s.q) return;
   const E* x = static_cast<const E*>(s.x) + (int64_t)blockIdx.y * s.stride_x;
+  // block v of the four holds longer-side elements j0 + 4c + v (wide: 16 bytes
+  // of a row) or j0 + 16v + c (tall); e-th reduction step: shorter-side index
+  // 16u + 4e + q (wide), 16u + 4q + e (tall)
+  const bool full = j0 + 64 <= s.q;
+  auto load = [&](int u, float (&v)[4][4]) {
+    if (full && !s.tall) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a[4];
+        load4(x + (int64_t)min(16 * u + 4 * e + q, s.p - 1) * s.ldx + j0 + 4 * c, a);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) v[b][e] = 16 * u + 4 * e + q < s.p ? a[b] : 0.0f;
+      }
+    } else if (full && 16 * u + 16 <= s.p) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) load4(x + (j0 + 16 * b + c) * s.ldx + 16 * u + 4 * q, v[b]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 16 * u + (s.tall ? 4 * q + e : 4 * e + q);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int64_t j = imin(s.tall ? j0 + 16 * b + c : j0 + 4 * c + b, s.q - 1);
+          v[b][e] = k < s.p ? load1(elem(s, x, k, j)) : 0.0f;
+        }
+      }
+    }
+  };
+  float first[4][4];
+  if (j0 < s.q) load(0, first);
+  if constexpr (PT == 1) {
+    const double* g = s.gpart + (int64_t)blockIdx.y * s.spans * P * P;
+    double v = 0.0;
+#pragma unroll 8
+    for (int k = 0; k < s.spans; ++k) v += g[(int64_t)k * P * P + tid];
+    lds64[tid / P * S + tid % P] = v;
+    __syncthreads();
+    if (tid < 64) {
+      double A[4], Q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) A[i] = lds64[c * S + 4 * i + q];
+      solve16(s, A, Q, q, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds64[c * S + 4 * i + q] = Q[i];
+    }
+  } else {
+    const double* qm = s.qmat + (int64_t)blockIdx.y * P * P;
+    for (int i = tid; i < P * P; i += 256) lds64[i / P * S + i % P] = qm[i];
+  }
+  __syncthreads();
+  if (j0 >= s.q) return;
   f64x4 acc[PT][4];
 #pragma unroll
   for (int t = 0; t < PT; ++t)
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[t][v] = f64x4{0, 0, 0, 0};
-  // block v of the four holds longer-side elements j0 + 4c + v (wide: 16 bytes
-  // of a row) or j0 + 16v + c (tall)
-  int64_t j[4];
-#pragma unroll
-  for (int v = 0; v < 4; ++v) j[v] = imin(s.tall ? j0 + 16 * v + c : j0 + 4 * c + v, s.q - 1);
   // tall: result row 4i + q of a block is stored as shorter-side index 4q + i, so
   // that a lane ends with 4 consecutive ones
   const int row = s.tall ? 4 * (c % 4) + c / 4 : c;
 #pragma unroll
   for (int u = 0; u < PT; ++u) {
     float v[4][4];
+    if (u == 0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // reduction order: wide 16u + 4e + q, tall 16u + 4q + e
-      const int k = 16 * u + (s.tall ? 4 * q + e : 4 * e + q);
+      for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) v[b][e] = k < s.p ? load1(elem(s, x, k, j[b])) : 0.0f;
+        for (int e = 0; e < 4; ++e) v[b][e] = first[b][e];
+    } else {
+      load(u, v);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -273,14 +401,17 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
 #pragma unroll
   for (int t = 0; t < PT; ++t)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int64_t jj = s.tall ? j0 + 16 * b + c : j0 + 4 * c + b;
-      if (jj >= s.q) continue;
+    for (int a = 0; a < 4; ++a) {  // four results side by side: of block a (tall), of register a (wide)
+      float v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ii = 16 * t + (s.tall ? 4 * q + i : 4 * i + q);
-        if (ii < s.p) store1(s.y, s.y_bf16, base + (s.tall ? jj * s.p + ii : ii * s.q + jj), (float)acc[t][b][i]);
-      }
+      for (int e = 0; e < 4; ++e) v[e] = (float)(s.tall ? acc[t][a][e] : acc[t][e][a]);
+      const int64_t j = s.tall ? j0 + 16 * a + c : j0 + 4 * c;
+      const int i = 16 * t + (s.tall ? 4 * q : 4 * a + q);
+      if (j >= s.q || i >= s.p) continue;
+      if (s.tall)
+        store4(s.y, s.y_bf16, base + j * s.p + i, v, s.p - i);
+      else
+        store4(s.y, s.y_bf16, base + (int64_t)i * s.q + j, v, s.q - j);
     }
 }
 
@@ -809,7 +940,7 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
   };
   if (L.small) {
     L.P = (int)round_up(L.p, 16);
-    L.spans = (int)imax(1, imin(imin(cdiv(512, batch), cdiv(L.q, 512)), 64));
+    L.spans = (int)imax(1, imin(imin(cdiv(1024, batch), cdiv(L.q, 256)), 32));
     L.span = round_up(cdiv(L.q, L.spans), 128);
     L.spans = (int)cdiv(L.q, L.span);
     L.off_g = take((size_t)batch * L.spans * L.P * L.P * sizeof(double));
@@ -835,12 +966,15 @@ hipError_t launch_small(const SmallArgs& a, int64_t batch, hipStream_t s) {
   constexpr int P = 16 * PT, S = P + 4;
   hipLaunchKernelGGL((ortho_gram_kernel<E, PT>), dim3((unsigned)a.spans, (unsigned)batch), dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
-  static std::atomic<uint64_t> done{0};
-  if (e == hipSuccess)
-    e = allow_lds(reinterpret_cast<const void*>(ortho_solve_kernel<PT>), 3 * P * S * sizeof(double), done);
+  if constexpr (PT > 1) {
+    static std::atomic<uint64_t> done{0};
+    if (e == hipSuccess)
+      e = allow_lds(reinterpret_cast<const void*>(ortho_solve_kernel<PT>), 3 * P * S * sizeof(double), done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ortho_solve_kernel<PT>), dim3((unsigned)batch), dim3(256), 3 * P * S * sizeof(double), s, a);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((ortho_solve_kernel<PT>), dim3((unsigned)batch), dim3(256), 3 * P * S * sizeof(double), s, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL((ortho_apply_kernel<E, PT>), dim3((unsigned)cdiv(a.q, 256), (unsigned)batch), dim3(256),
                      P * S * sizeof(double), s, a);
   return hipGetLastError();
