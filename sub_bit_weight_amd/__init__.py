@@ -182,6 +182,23 @@ def _on(stream):
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _device_and_stream(dev, stream):
+    with torch.cuda.device(dev), _on(stream):
+        yield
+
+
+def _call_on(dev: torch.device, stream):
+    """Allocation and launch context of a call whose tensors are on `dev`: that
+    device current, and `stream` (see _on)."""
+    if stream is None and dev.index == torch._C._cuda_getDevice():
+        return _NO_CONTEXT
+    return _device_and_stream(dev, stream)
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -500,6 +517,14 @@ class Lora:
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_struct", None)  # any field change re-validates
+        object.__setattr__(self, "_bytes", {})     # workspace sizes per call and token count
+
+    def _workspace_bytes(self, query, T: int) -> int:
+        key = (query, T)
+        size = self._bytes.get(key)
+        if size is None:
+            size = self._bytes[key] = int(getattr(lib(), query)(ctypes.byref(self.struct()), T))
+        return size
 
     @property
     def n(self) -> int:
@@ -583,11 +608,11 @@ def lora_linear(pool: Lora, x: torch.Tensor, ids: torch.Tensor, base: torch.Tens
         _f32_rows(base, "base", (T, pool.d_out), dev)
     if y is not None:
         _f32_rows(y, "y", (T, pool.d_out), dev)
-    with torch.cuda.device(dev), _on(stream):
+    with _call_on(dev, stream):
         if y is None:
             y = torch.empty((T, pool.d_out), dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = torch.empty(max(int(lib().nq_lora_workspace_bytes(ctypes.byref(s), T)), 1), dtype=torch.uint8,
+            workspace = torch.empty(max(pool._workspace_bytes("nq_lora_workspace_bytes", T), 1), dtype=torch.uint8,
                                     device=dev)
         _check(lib().nq_lora_linear(ctypes.byref(s), _ptr(x), _x_dtype(x), _ptr(ids), T, _ptr(base), _ptr(y),
                                     _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -607,7 +632,7 @@ def lrb_lora_linear(layer: Lrb, pool: Lora, x: torch.Tensor, ids: torch.Tensor, 
     dev = x.device
     if y is not None:
         _f32_rows(y, "y", (T, layer.d_out), dev)
-    with torch.cuda.device(dev), _on(stream):
+    with _call_on(dev, stream):
         if y is None:
             y = torch.empty((T, layer.d_out), dtype=torch.float32, device=dev)
         if workspace is None:
@@ -636,14 +661,14 @@ def lora_grads(pool: Lora, x: torch.Tensor, g: torch.Tensor, ids: torch.Tensor, 
     for t, name in ((dx_base, "dx_base"), (dx, "dx")):
         if t is not None:
             _f32_rows(t, name, (T, pool.d_in), dev)
-    with torch.cuda.device(dev), _on(stream):
+    with _call_on(dev, stream):
         if dx is None:
             dx = torch.empty((T, pool.d_in), dtype=torch.float32, device=dev)
         da = torch.empty((pool.n, pool.r, pool.d_in), dtype=torch.float32, device=dev)
         db = torch.empty((pool.n, pool.d_out, pool.r), dtype=torch.float32, device=dev)
         if workspace is None:
-            need = int(lib().nq_lora_grads_workspace_bytes(ctypes.byref(s), T))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(max(pool._workspace_bytes("nq_lora_grads_workspace_bytes", T), 1),
+                                    dtype=torch.uint8, device=dev)
         _check(lib().nq_lora_grads(ctypes.byref(s), _ptr(x), _x_dtype(x), _ptr(g), _x_dtype(g), _ptr(ids), T,
                                    _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(), _stream(stream, dev.index)))
@@ -688,7 +713,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coeffs=NEWTON_SCHULZ, out_dty
     stride = x.stride(0) if x.dim() == 3 and batch > 1 else 0
     a, b, c = (float(v) for v in coeffs)
     dev = x.device
-    with torch.cuda.device(dev), _on(stream):
+    with _call_on(dev, stream):
         if y is None:
             y = torch.empty(x.shape, dtype=out_dtype, device=dev)
         if workspace is None:

@@ -886,18 +886,18 @@ __device__ inline void store_rows(const ExpandArgs& p, int row, int64_t n0, int 
   }
 }
 
+// Workgroup bx of the groups of tiles, by of the columns (512 each).
 template <typename EW, bool TW, int KB>
-__global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kernel(ExpandArgs p) {
-  __shared__ __attribute__((aligned(16))) float out[4][16 * kOutRow];
+__device__ inline void expand(const ExpandArgs& p, int bx, int by, float (*out)[16 * kOutRow]) {
   const int lane = threadIdx.x % 64, q = lane / 16, c = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int64_t n0 = ((int64_t)blockIdx.y * 4 + wave) * 128;
+  const int64_t n0 = ((int64_t)by * 4 + wave) * 128;
   if (n0 >= p.d) return;
   const int kbs = p.rp / 32;
   Frag<EW> w[KB][8];
   f32x4 acc[8], bcur[8], bnext[8];
   constexpr int SUB = kTile / 16;
-  const int begin = (int)blockIdx.x * p.tiles_per_wg;
+  const int begin = bx * p.tiles_per_wg;
   const int end = min(p.tile_off[p.n + 2], begin + p.tiles_per_wg);
   if (begin >= end) return;
   int have = -1;  // adapter whose factors w holds
@@ -933,6 +933,12 @@ __global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kern
     for (int t = 0; t < 8; ++t) bcur[t] = bnext[t];
     row = next;
   }
+}
+
+template <typename EW, int KB>
+__global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kernel(ExpandArgs p) {
+  __shared__ __attribute__((aligned(16))) float out[4][16 * kOutRow];
+  expand<EW, false, KB>(p, (int)blockIdx.x, (int)blockIdx.y, out);
 }
 
 // Calls of up to 64 tokens: most groups hold a token or two, where 16-wide
@@ -1038,7 +1044,7 @@ struct WgradArgs {
   const int* slot_row;
   int64_t d, nslots;
   int n, r, rp;
-  int chunks;        // token chunks (blockIdx.z / rank blocks)
+  int chunks;        // token chunks
   float* out;        // [chunks][n][r][d] or [chunks][n][d][r]
   int64_t chunk_stride;
 };
@@ -1046,13 +1052,12 @@ struct WgradArgs {
 constexpr int kWgradWaves = 4;
 
 template <typename EX, int NT, int RW, bool DB>
-__device__ inline void wgrad(const WgradArgs& p, int64_t block, float (*part)[8][4][64]) {
+__device__ inline void wgrad(const WgradArgs& p, int64_t block, int ad, int z, float (*part)[8][4][64]) {
   constexpr int TWN = kWgradWaves / RW;
   const int lane = threadIdx.x % 64, q = lane / 16, c = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), tw = wave / RW;
   const int64_t n0 = block * 128;
-  const int ad = (int)blockIdx.y;
-  const int chunk = (int)blockIdx.z % p.chunks, kb = (int)blockIdx.z / p.chunks * 16 * NT * RW;
+  const int chunk = z % p.chunks, kb = z / p.chunks * 16 * NT * RW;
   const int k0 = kb + wave % RW * 16 * NT;
   const int a0 = p.tile_off[ad], a1 = p.tile_off[ad + 1];
   const int per = (a1 - a0 + p.chunks - 1) / p.chunks;
@@ -1146,15 +1151,37 @@ __device__ inline void wgrad(const WgradArgs& p, int64_t block, float (*part)[8]
   }
 }
 
-// dB (g and h) and dA (x and dh) in one launch.
-template <typename EX, typename EG, int NT, int RW>
-__global__ __launch_bounds__(64 * kWgradWaves, 2) void lora_wgrad_kernel(WgradArgs pa, WgradArgs pb) {
-  __shared__ float part[kWgradWaves][8][4][64];
-  const int64_t blocks = cdiv(pb.d, 128), b = blockIdx.x;
-  if (b < blocks)
-    wgrad<EG, NT, RW, true>(pb, b, part);
-  else
-    wgrad<EX, NT, RW, false>(pa, b - blocks, part);
+// What follows the hidden vectors of the gradients, in one launch, so that the
+// parts fill each other's tails: dB (g and h), dA (x and dh), then dx (dh and A).
+// Grid: z below `parts` the factor gradients (x: 128-column blocks of both, y:
+// adapters), z = parts the output product (x * y: its workgroups).
+struct BackArgs {
+  WgradArgs a, b;
+  ExpandArgs dx;
+  int parts, groups, cols;  // dx: groups of tiles and 512-column blocks
+};
+
+template <typename EX, typename EG, typename EW, int NT, int RW, int KB>
+__global__ __launch_bounds__(64 * kWgradWaves, sizeof(EW) == 2 ? 2 : 1) void lora_back_kernel(BackArgs p) {
+  static_assert(kWgradWaves == 4, "the output product takes four waves");
+  union Shared {
+    float part[kWgradWaves][8][4][64];
+    float out[4][16 * kOutRow];
+  };
+  __shared__ __attribute__((aligned(16))) Shared lds;
+  const int z = (int)blockIdx.z, y = (int)blockIdx.y;
+  if (z == p.parts) {
+    const int64_t i = (int64_t)y * gridDim.x + blockIdx.x;
+    if (i < (int64_t)p.groups * p.cols)
+      expand<EW, true, KB>(p.dx, (int)(i % p.groups), (int)(i / p.groups), lds.out);
+    return;
+  }
+  const int64_t blocks_b = cdiv(p.b.d, 128), b = blockIdx.x;
+  if (y >= p.a.n) return;
+  if (b < blocks_b)
+    wgrad<EG, NT, RW, true>(p.b, b, y, z, lds.part);
+  else if (b < blocks_b + cdiv(p.a.d, 128))
+    wgrad<EX, NT, RW, false>(p.a, b - blocks_b, y, z, lds.part);
 }
 
 // da and db: the sums over chunks, in order (both lie one after the other in a chunk)
@@ -1322,14 +1349,17 @@ hipError_t launch_shrink2(const ShrinkArgs& x, const ShrinkArgs& g, const LoraLa
   return hipGetLastError();
 }
 
-template <bool TW>
+// Groups of tiles of an output product: more tiles keep the factors in registers
+// for longer, fewer fill the chip.
+int expand_groups(ExpandArgs* a, const LoraLayout& L) {
+  a->tiles_per_wg = (int)imax(1, imin(8, L.tiles * cdiv(a->d, 512) / 1024));
+  return (int)cdiv(L.tiles, a->tiles_per_wg);
+}
+
 hipError_t launch_expand(ExpandArgs a, const LoraLayout& L, nq_dtype wd, hipStream_t s) {
-  const int64_t cols = cdiv(a.d, 512);
-  // tiles of a workgroup: more keep the factors in registers for longer, fewer
-  // fill the chip
-  a.tiles_per_wg = (int)imax(1, imin(8, L.tiles * cols / 1024));
-  const dim3 grid((unsigned)cdiv(L.tiles, a.tiles_per_wg), (unsigned)cols);
-#define NQ_EXPAND(E, KB) hipLaunchKernelGGL((lora_expand_kernel<E, TW, KB>), grid, dim3(256), 0, s, a)
+  const int groups = expand_groups(&a, L);
+  const dim3 grid((unsigned)groups, (unsigned)cdiv(a.d, 512));
+#define NQ_EXPAND(E, KB) hipLaunchKernelGGL((lora_expand_kernel<E, KB>), grid, dim3(256), 0, s, a)
   if (wd == NQ_BF16) {
     if (a.r <= 32)
       NQ_EXPAND(Bf16, 1);
@@ -1345,18 +1375,29 @@ hipError_t launch_expand(ExpandArgs a, const LoraLayout& L, nq_dtype wd, hipStre
   return hipGetLastError();
 }
 
-template <typename EX, typename EG>
-hipError_t launch_wgrad(const WgradArgs& a, const WgradArgs& b, const LoraLayout& L, hipStream_t s) {
-  const dim3 grid((unsigned)(cdiv(a.d, 128) + cdiv(b.d, 128)), (unsigned)a.n, (unsigned)(L.kblocks * L.chunks));
-#define NQ_WGRAD(NT, RW) \
-  hipLaunchKernelGGL((lora_wgrad_kernel<EX, EG, NT, RW>), grid, dim3(64 * kWgradWaves), 0, s, a, b)
+template <typename EX, typename EG, typename EW>
+hipError_t launch_back(const WgradArgs& wa, const WgradArgs& wb, const ExpandArgs& ea, const LoraLayout& L, hipStream_t s) {
+  BackArgs a;
+  a.a = wa;
+  a.b = wb;
+  a.dx = ea;
+  a.parts = L.kblocks * L.chunks;
+  a.groups = expand_groups(&a.dx, L);
+  a.cols = (int)cdiv(ea.d, 512);
+  // x: the column blocks of both gradients; y: the adapters, or more where the
+  // output product needs them
+  const int64_t gx = cdiv(wa.d, 128) + cdiv(wb.d, 128), gy = imax(wa.n, cdiv((int64_t)a.groups * a.cols, gx));
+  if (gy > 65535) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)(a.parts + 1));
+#define NQ_BACK(NT, RW, KB) \
+  hipLaunchKernelGGL((lora_back_kernel<EX, EG, EW, NT, RW, KB>), grid, dim3(64 * kWgradWaves), 0, s, a)
   if (L.nt == 1)
-    NQ_WGRAD(1, 1);
+    NQ_BACK(1, 1, 1);
   else if (L.nt == 2)
-    NQ_WGRAD(2, 1);
+    NQ_BACK(2, 1, 1);
   else
-    NQ_WGRAD(2, 2);
-#undef NQ_WGRAD
+    NQ_BACK(2, 2, 2);
+#undef NQ_BACK
   return hipGetLastError();
 }
 
@@ -1391,8 +1432,8 @@ hipError_t launch_lora_grads_types(const nq_lora& P, const LoraLayout& L, const 
                                    const ExpandArgs& ea, const WgradArgs& wa, const WgradArgs& wb, float* da, float* db,
                                    hipStream_t s) {
   hipError_t e = P.dtype == NQ_BF16 ? launch_shrink2<EX, EG, Bf16>(sx, sg, L, s) : launch_shrink2<EX, EG, float>(sx, sg, L, s);
-  if (e == hipSuccess) e = launch_expand<true>(ea, L, P.dtype, s);
-  if (e == hipSuccess) e = launch_wgrad<EX, EG>(wa, wb, L, s);
+  if (e == hipSuccess)
+    e = P.dtype == NQ_BF16 ? launch_back<EX, EG, Bf16>(wa, wb, ea, L, s) : launch_back<EX, EG, float>(wa, wb, ea, L, s);
   if (e != hipSuccess || L.chunks == 1) return e;
   const int64_t count_a = P.n * P.r * P.d_in, count = count_a + P.n * P.r * P.d_out;
   hipLaunchKernelGGL(lora_sum_kernel, dim3((unsigned)imin(cdiv(count, 256), 2048)), dim3(256), 0, s, wa.out, L.chunks,
@@ -1421,7 +1462,7 @@ hipError_t launch_lora_linear(const nq_lora& P, const void* x, nq_dtype xd, cons
   if (e != hipSuccess) return e;
   const ExpandArgs ea =
       expand_args(P, L, ws, false, L.direct ? static_cast<const void*>(sa.hpart) : sa.h, ids, T, base, y);
-  if (!L.direct) return launch_expand<false>(ea, L, P.dtype, s);
+  if (!L.direct) return launch_expand(ea, L, P.dtype, s);
   const dim3 grid((unsigned)T, (unsigned)cdiv(P.d_out, 512));
   if (P.dtype == NQ_BF16)
     hipLaunchKernelGGL((lora_expand_direct_kernel<Bf16>), grid, dim3(256), 0, s, ea);
