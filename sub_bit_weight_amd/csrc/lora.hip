@@ -186,21 +186,9 @@ __device__ inline Frag<float> load8<float, Bf16>(const Bf16* p, int64_t nv) {
   return f;
 }
 
-// The same from 8 elements `stride` apart.
-template <typename F, typename E>
-__device__ inline Frag<F> load8s(const E* p, int64_t stride, int64_t nv) {
-  Frag<F> f;
-  if constexpr (sizeof(F) == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < nv ? p[2 * i * stride].u : 0, hi = 2 * i + 1 < nv ? p[(2 * i + 1) * stride].u : 0;
-      f.d[i] = lo | (hi << 16);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = e < nv ? to_f32(p[e * stride]) : 0.0f;
-  }
-  return f;
+__device__ inline float element(const Frag<float>& f, int e) { return f.v[e]; }
+__device__ inline float element(const Frag<Bf16>& f, int e) {
+  return __uint_as_float(e % 2 ? f.d[e / 2] & 0xFFFF0000u : f.d[e / 2] << 16);
 }
 
 // in[e] holds elements 0..7 of row e: out[v] takes element v of each row.
@@ -300,21 +288,22 @@ struct Rows {
 };
 
 // Calls of up to 64 tokens: token t stands for its group when its place among
-// the tokens of the same adapter is a multiple of 16; the group's rows are that
-// token and the next 15 of them.  False: another token stands for t's group.
+// the tokens of the same adapter is a multiple of G; the group's rows are that
+// token and the next G - 1 of them.  False: another token stands for t's group.
+template <int G>
 __device__ inline bool direct_rows(const int32_t* __restrict__ ids, int T, int n, int t, Rows& g) {
   const int lane = threadIdx.x % 64;
   const int id = lane < T ? ids[lane] : 0;
   const int key = lane >= T ? -3 : (id < 0 ? -1 : (id >= n ? -2 : id));
   const int mykey = __builtin_amdgcn_readlane(key, t);
   unsigned long long m = __ballot(key == mykey);
-  if (__popcll(m & ((1ull << t) - 1)) % 16 != 0) return false;
+  if (__popcll(m & ((1ull << t) - 1)) % G != 0) return false;
   m &= ~0ull << t;
   g.ad = mykey;
   g.row = -1;
   const int c = lane % 16;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
+  for (int k = 0; k < G; ++k) {
     const int b = m ? (int)__ffsll(m) - 1 : -1;
     if (k == c) g.row = b;
     m &= m - 1;
@@ -584,7 +573,7 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
   int64_t slot0 = 0;
   int tile = 0;
   if (MT == 1) {  // direct: slots are the tokens themselves
-    if (!direct_rows(p.ids, p.T, p.n, (int)blockIdx.x, g[0]) || g[0].ad < 0) return;
+    if (!direct_rows<16>(p.ids, p.T, p.n, (int)blockIdx.x, g[0]) || g[0].ad < 0) return;
   } else {
     tile = (int)blockIdx.x;
     if (tile >= p.tile_off[p.n]) return;  // tiles without an adapter have no h
@@ -765,7 +754,7 @@ struct ExpandArgs {
   const int* slot_row;
   int T, n, r, rp, spans;
   int64_t nslots;
-  int tiles_per_wg;
+  int per_wg;           // 16-slot groups of a workgroup
   const float* base;    // [T][d] or null
   float* y;             // [T][d]
 };
@@ -886,7 +875,8 @@ __device__ inline void store_rows(const ExpandArgs& p, int row, int64_t n0, int 
   }
 }
 
-// Workgroup bx of the groups of tiles, by of the columns (512 each).
+// Workgroup bx along the slots (per_wg 16-slot groups each), by along the columns
+// (512 each).
 template <typename EW, bool TW, int KB>
 __device__ inline void expand(const ExpandArgs& p, int bx, int by, float (*out)[16 * kOutRow]) {
   const int lane = threadIdx.x % 64, q = lane / 16, c = lane % 16;
@@ -897,15 +887,15 @@ __device__ inline void expand(const ExpandArgs& p, int bx, int by, float (*out)[
   Frag<EW> w[KB][8];
   f32x4 acc[8], bcur[8], bnext[8];
   constexpr int SUB = kTile / 16;
-  const int begin = bx * p.tiles_per_wg;
-  const int end = min(p.tile_off[p.n + 2], begin + p.tiles_per_wg);
+  const int begin = bx * p.per_wg;
+  const int end = min(p.tile_off[p.n + 2] * SUB, begin + p.per_wg);
   if (begin >= end) return;
   int have = -1;  // adapter whose factors w holds
-  int row = p.slot_row[(int64_t)begin * kTile + c];
+  int row = p.slot_row[(int64_t)begin * 16 + c];
   load_base(p, row, n0, lane, bcur);
-  for (int it = begin * SUB; it < end * SUB; ++it) {
+  for (int it = begin; it < end; ++it) {
     const int ad = __builtin_amdgcn_readfirstlane(p.tile_ad[it / SUB]);
-    const int next = it + 1 < end * SUB ? p.slot_row[(int64_t)it * 16 + 16 + c] : -1;
+    const int next = it + 1 < end ? p.slot_row[(int64_t)it * 16 + 16 + c] : -1;
     const bool any = __ballot(row >= 0) != 0;
 #pragma unroll
     for (int v = 0; v < 8; ++v) acc[v] = zero4();
@@ -943,21 +933,38 @@ __global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kern
 
 // Calls of up to 64 tokens: most groups hold a token or two, where 16-wide
 // tiles would leave the matrix cores and the lanes that load rows mostly idle.
-// One thread per column j of W instead, whose rank row it reads whole, and
-// fp32 products with the group's hidden vectors, which lie in LDS.
-constexpr int kDirectRanks = 64;  // ranks held in LDS at a time
+// Two columns of W per thread instead, whose rank rows it reads whole, and fp32
+// products with the hidden vectors of up to four tokens, which lie in LDS.  Bound
+// by the factors' bytes where tokens have adapters of their own (48 mixed tokens,
+// rank 16, 8192 -> 28672: 40 MB).
+//
+// FUSED: the workgroup computes the hidden vectors itself, four ranks a wave at a
+// time, in one launch; for factors small enough that reading them again in every
+// column block costs less than a launch.
+constexpr int kDirectTokens = 4, kDirectRanks = 64;  // tokens of a group, ranks held in LDS at a time
+constexpr int64_t kFusedElements = 65536, kFusedColumns = 4096;  // r * d_in and d_out of a fused call, at most
 
-template <typename EW>
-__global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
-  constexpr int NC = 2;  // columns of a thread, 256 apart
-  __shared__ float hs[16][kDirectRanks];
-  __shared__ int rows[16];
+struct DirectArgs {
+  ExpandArgs e;
+  const void* x;  // fused
+  const void* a;
+  int64_t d_in, lda, stride_a;
+};
+
+template <typename EX, typename EW, bool FUSED>
+__global__ __launch_bounds__(256) void lora_direct_kernel(DirectArgs f) {
+  constexpr int NC = 2, G = kDirectTokens;  // columns of a thread, 256 apart
+  const ExpandArgs& p = f.e;
+  __shared__ float hs[G][kDirectRanks];
+  __shared__ int rows[G];
   const int tid = threadIdx.x;
   Rows g;
-  if (!direct_rows(p.ids, p.T, p.n, (int)blockIdx.x, g)) return;
+  if (!direct_rows<G>(p.ids, p.T, p.n, (int)blockIdx.x, g)) return;
   const int ad = __builtin_amdgcn_readfirstlane(g.ad);
-  if (tid < 16) rows[tid] = g.row;
   const int count = __popcll(__ballot(g.row >= 0) & 0xFFFF);
+  int row[G];
+#pragma unroll
+  for (int t = 0; t < G; ++t) row[t] = __builtin_amdgcn_readlane(g.row, t);
   int64_t j[NC], jc[NC];  // columns past the last are not stored
   const EW* w[NC];
 #pragma unroll
@@ -966,63 +973,103 @@ __global__ __launch_bounds__(256) void lora_expand_direct_kernel(ExpandArgs p) {
     jc[u] = imin(j[u], p.d - 1);
     w[u] = static_cast<const EW*>(p.w) + imax(ad, 0) * p.stride_w + jc[u] * p.ldw;
   }
-  Frag<float> wf[NC][2];
+  Frag<EW> wf[NC][2];
   auto load = [&](int k, int left) {
 #pragma unroll
     for (int u = 0; u < NC; ++u) {
-      wf[u][0] = load8<float, EW>(w[u] + k, left);
-      wf[u][1] = load8<float, EW>(w[u] + k + 8, left - 8);
+      wf[u][0] = load8<EW, EW>(w[u] + k, left);
+      wf[u][1] = load8<EW, EW>(w[u] + k + 8, left - 8);
     }
   };
-  float acc[16][NC];
+  float acc[G][NC], b[G][NC];
 #pragma unroll
-  for (int t = 0; t < 16; ++t)
+  for (int t = 0; t < G; ++t)
 #pragma unroll
-    for (int u = 0; u < NC; ++u) acc[t][u] = 0.0f;
-  if (ad >= 0) load(0, p.r);
-  __syncthreads();
+    for (int u = 0; u < NC; ++u) {
+      acc[t][u] = 0.0f;
+      b[t][u] = p.base && t < count ? p.base[(int64_t)row[t] * p.d + jc[u]] : 0.0f;
+    }
   if (ad >= 0) {
+    load(0, p.r);
     const float sc = p.scale[ad];
+#pragma unroll 1
     for (int k0 = 0; k0 < p.r; k0 += kDirectRanks) {
       const int kn = min(p.r - k0, kDirectRanks);
       if (k0 > 0) __syncthreads();
-      for (int i = tid; i < count * kDirectRanks; i += 256) {
-        const int t = i / kDirectRanks, k = i % kDirectRanks;
-        float v = 0.0f;
-        if (k < kn) {
-          const float* hp = static_cast<const float*>(p.h) + (int64_t)rows[t] * p.rp + k0 + k;
-#pragma unroll 8
-          for (int s = 0; s < p.spans; ++s) v += hp[(int64_t)s * p.nslots * p.rp];
+      if constexpr (FUSED) {
+        const int lane = tid % 64, wave = tid / 64;
+        const EW* A = static_cast<const EW*>(f.a) + ad * f.stride_a;
+        for (int kb = 4 * wave; kb < (kn + 15) / 16 * 16; kb += 16) {
+          float h[4][G];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int t = 0; t < G; ++t) h[v][t] = 0.0f;
+          if (kb < kn)
+#pragma unroll 1
+            for (int64_t i = 8 * lane; i < f.d_in; i += 512) {
+              Frag<float> af[4], xf[G];
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                af[v] = load8<float, EW>(A + (int64_t)min(k0 + kb + v, p.r - 1) * f.lda + i, f.d_in - i);
+#pragma unroll
+              for (int t = 0; t < G; ++t)
+                if (t < count) xf[t] = load8<float, EX>(static_cast<const EX*>(f.x) + (int64_t)row[t] * f.d_in + i, f.d_in - i);
+#pragma unroll
+              for (int t = 0; t < G; ++t)
+                if (t < count)
+#pragma unroll
+                  for (int v = 0; v < 4; ++v)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h[v][t] = fmaf(af[v].v[e], xf[t].v[e], h[v][t]);
+            }
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int t = 0; t < G; ++t) {
+              if (t >= count) break;
+              for (int off = 32; off > 0; off >>= 1) h[v][t] += __shfl_xor(h[v][t], off);
+              if (lane == 0) hs[t][kb + v] = kb + v < kn ? h[v][t] * sc : 0.0f;
+            }
         }
-        hs[t][k] = v * sc;  // ranks past r: zero, beside a zero factor
+      } else {
+        if (tid < G) rows[tid] = g.row;
+        __syncthreads();
+        for (int i = tid; i < count * kDirectRanks; i += 256) {
+          const int t = i / kDirectRanks, k = i % kDirectRanks;
+          float v = 0.0f;
+          if (k < kn) {
+            const float* hp = static_cast<const float*>(p.h) + (int64_t)rows[t] * p.rp + k0 + k;
+#pragma unroll 8
+            for (int s = 0; s < p.spans; ++s) v += hp[(int64_t)s * p.nslots * p.rp];
+          }
+          hs[t][k] = v * sc;  // ranks past r: zero, beside a zero factor
+        }
       }
       __syncthreads();
+#pragma unroll 1
       for (int kk = 0; kk < kn; kk += 16) {
-        Frag<float> cur[NC][2];
+        Frag<EW> cur[NC][2];
 #pragma unroll
         for (int u = 0; u < NC; ++u) cur[u][0] = wf[u][0], cur[u][1] = wf[u][1];
         if (k0 + kk + 16 < p.r) load(k0 + kk + 16, p.r - k0 - kk - 16);
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
+        for (int t = 0; t < G; ++t) {
           if (t >= count) break;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
 #pragma unroll
-            for (int u = 0; u < NC; ++u) acc[t][u] = fmaf(cur[u][e / 8].v[e % 8], hs[t][kk + e], acc[t][u]);
+            for (int u = 0; u < NC; ++u) acc[t][u] = fmaf(element(cur[u][e / 8], e % 8), hs[t][kk + e], acc[t][u]);
         }
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
+  for (int t = 0; t < G; ++t) {
     if (t >= count) break;
-    const int64_t at = (int64_t)rows[t] * p.d;
 #pragma unroll
-    for (int u = 0; u < NC; ++u) {
-      if (j[u] >= p.d) continue;
-      const float b = p.base ? p.base[at + j[u]] : 0.0f;
-      p.y[at + j[u]] = ad == -2 ? __builtin_nanf("") : b + acc[t][u];
-    }
+    for (int u = 0; u < NC; ++u)
+      if (j[u] < p.d) p.y[(int64_t)row[t] * p.d + j[u]] = ad == -2 ? __builtin_nanf("") : b[t][u] + acc[t][u];
   }
 }
 
@@ -1158,7 +1205,7 @@ __device__ inline void wgrad(const WgradArgs& p, int64_t block, int ad, int z, f
 struct BackArgs {
   WgradArgs a, b;
   ExpandArgs dx;
-  int parts, groups, cols;  // dx: groups of tiles and 512-column blocks
+  int parts, groups, cols;  // dx: workgroups along the slots and the columns
 };
 
 template <typename EX, typename EG, typename EW, int NT, int RW, int KB>
@@ -1205,7 +1252,7 @@ int shrink_spans(int64_t groups, int64_t d) { return (int)imax(1, imin(imin(kWan
 int64_t span_len(int64_t d, int spans) { return round_up(cdiv(d, spans), 64); }
 
 struct LoraLayout {
-  bool direct;
+  bool direct, fused;
   int64_t tiles, nslots;
   int rp, nt, kblocks, spans_x, spans_g, chunks;
   int64_t span_x, span_g;
@@ -1215,6 +1262,7 @@ struct LoraLayout {
 LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
   LoraLayout L{};
   L.direct = !grads && T <= 64;
+  L.fused = L.direct && P.r <= kDirectRanks && P.r * P.d_in <= kFusedElements && P.d_out <= kFusedColumns;
   L.tiles = max_tiles(P.n, T);
   L.nslots = L.direct ? T : L.tiles * kTile;
   L.rp = (int)round_up(P.r, 32);
@@ -1236,7 +1284,9 @@ LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
     return at;
   };
   const size_t hb = (size_t)L.nslots * L.rp * sizeof(float);
-  if (L.direct) {
+  if (L.fused) {
+    take(1);  // no workspace, but a call is given one all the same
+  } else if (L.direct) {
     L.off_hp = take(L.spans_x * hb);
   } else {
     L.off_toff = take((size_t)(P.n + 3) * sizeof(int));
@@ -1349,11 +1399,12 @@ hipError_t launch_shrink2(const ShrinkArgs& x, const ShrinkArgs& g, const LoraLa
   return hipGetLastError();
 }
 
-// Groups of tiles of an output product: more tiles keep the factors in registers
-// for longer, fewer fill the chip.
+// Workgroups along the slots of an output product: more 16-slot groups each keep
+// the factors in registers for longer, fewer fill the chip.
 int expand_groups(ExpandArgs* a, const LoraLayout& L) {
-  a->tiles_per_wg = (int)imax(1, imin(8, L.tiles * cdiv(a->d, 512) / 1024));
-  return (int)cdiv(L.tiles, a->tiles_per_wg);
+  const int64_t groups = L.tiles * (kTile / 16);
+  a->per_wg = (int)imax(1, imin(16, groups * cdiv(a->d, 512) / 1024));
+  return (int)cdiv(groups, a->per_wg);
 }
 
 hipError_t launch_expand(ExpandArgs a, const LoraLayout& L, nq_dtype wd, hipStream_t s) {
@@ -1366,10 +1417,7 @@ hipError_t launch_expand(ExpandArgs a, const LoraLayout& L, nq_dtype wd, hipStre
     else
       NQ_EXPAND(Bf16, 2);
   } else {
-    if (a.r <= 32)
-      NQ_EXPAND(float, 1);
-    else
-      NQ_EXPAND(float, 2);
+    NQ_EXPAND(float, 1);  // factors of 64 ranks would leave registers for one wave a SIMD
   }
 #undef NQ_EXPAND
   return hipGetLastError();
@@ -1396,7 +1444,7 @@ hipError_t launch_back(const WgradArgs& wa, const WgradArgs& wb, const ExpandArg
   else if (L.nt == 2)
     NQ_BACK(2, 1, 1);
   else
-    NQ_BACK(2, 2, 2);
+    NQ_BACK(2, 2, (sizeof(EW) == 2 ? 2 : 1));
 #undef NQ_BACK
   return hipGetLastError();
 }
@@ -1455,19 +1503,36 @@ hipError_t launch_lora_linear(const nq_lora& P, const void* x, nq_dtype xd, cons
   ShrinkArgs sa = shrink_args(P, L, ws, 0, x, ids, T);
   sa.h = ws + L.off_h;
   sa.h_bf16 = P.dtype == NQ_BF16;
-  if (xd == NQ_BF16)
-    e = P.dtype == NQ_BF16 ? launch_shrink<Bf16, Bf16>(sa, L, s) : launch_shrink<Bf16, float>(sa, L, s);
-  else
-    e = P.dtype == NQ_BF16 ? launch_shrink<float, Bf16>(sa, L, s) : launch_shrink<float, float>(sa, L, s);
-  if (e != hipSuccess) return e;
+  if (!L.fused) {
+    if (xd == NQ_BF16)
+      e = P.dtype == NQ_BF16 ? launch_shrink<Bf16, Bf16>(sa, L, s) : launch_shrink<Bf16, float>(sa, L, s);
+    else
+      e = P.dtype == NQ_BF16 ? launch_shrink<float, Bf16>(sa, L, s) : launch_shrink<float, float>(sa, L, s);
+    if (e != hipSuccess) return e;
+  }
   const ExpandArgs ea =
       expand_args(P, L, ws, false, L.direct ? static_cast<const void*>(sa.hpart) : sa.h, ids, T, base, y);
   if (!L.direct) return launch_expand(ea, L, P.dtype, s);
+  const DirectArgs da{ea, x, P.a, P.d_in, P.lda, P.stride_a};
   const dim3 grid((unsigned)T, (unsigned)cdiv(P.d_out, 512));
-  if (P.dtype == NQ_BF16)
-    hipLaunchKernelGGL((lora_expand_direct_kernel<Bf16>), grid, dim3(256), 0, s, ea);
-  else
-    hipLaunchKernelGGL((lora_expand_direct_kernel<float>), grid, dim3(256), 0, s, ea);
+#define NQ_DIRECT(EX, EW, FUSED) hipLaunchKernelGGL((lora_direct_kernel<EX, EW, FUSED>), grid, dim3(256), 0, s, da)
+  const bool xb = xd == NQ_BF16, wb = P.dtype == NQ_BF16;
+  if (!L.fused) {  // x is not read
+    if (wb)
+      NQ_DIRECT(float, Bf16, false);
+    else
+      NQ_DIRECT(float, float, false);
+  } else if (xb) {
+    if (wb)
+      NQ_DIRECT(Bf16, Bf16, true);
+    else
+      NQ_DIRECT(Bf16, float, true);
+  } else if (wb) {
+    NQ_DIRECT(float, Bf16, true);
+  } else {
+    NQ_DIRECT(float, float, true);
+  }
+#undef NQ_DIRECT
   return hipGetLastError();
 }
 
