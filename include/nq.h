@@ -346,7 +346,10 @@ typedef struct {
  *   base: [T][d_out] fp32, the shared projection's output, or null (zeros);
  *   y: [T][d_out] fp32, fully overwritten; y may be base (in place).
  *   ids[t] < 0: no adapter, y[t] = base[t].  ids[t] >= n: row t of y is NaN
- *   (ids is device data, which a call cannot check on the host).
+ *   (ids is device data, which a call cannot check on the host).  A call reads
+ *   ids more than once: they must be final when it starts on `stream` (work of
+ *   another stream that writes them must be waited for) and must not change while
+ *   it runs.
  * The hidden vectors A_a x[t] and all sums are fp32: nothing is rounded to
  * fewer bits, whatever the types of x and of the factors.  Values that are not
  * finite stay within the rows whose x, base or adapter holds them.  Summation
@@ -358,9 +361,9 @@ typedef struct {
  * Errors: NQ_ERR_ARG for null pointers, sizes < 1, lda < d_in, ldb < r, a
  * negative adapter stride, T < 1, an unknown dtype or a pointer not aligned to
  * its elements; NQ_ERR_UNSUPPORTED for n > NQ_LORA_MAX_ADAPTERS,
- * r > NQ_LORA_MAX_RANK, d_out or d_in > 2^24 or T > 2^24; NQ_ERR_WORKSPACE when workspace_bytes
- * is too small; NQ_ERR_HIP when a launch fails.  The size query returns 0 for
- * invalid arguments.
+ * r > NQ_LORA_MAX_RANK, d_out or d_in > 2^24 or T > 2^24; NQ_ERR_WORKSPACE when
+ * workspace_bytes is too small; NQ_ERR_HIP when a launch fails.  The size query
+ * returns 0 for invalid arguments.
  */
 size_t nq_lora_workspace_bytes(const nq_lora* P, int64_t T);
 nq_status nq_lora_linear(const nq_lora* P, const void* x, nq_dtype x_dtype, const int32_t* ids, int64_t T,

@@ -938,11 +938,13 @@ __global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kern
 // by the factors' bytes where tokens have adapters of their own (48 mixed tokens,
 // rank 16, 8192 -> 28672: 40 MB).
 //
-// FUSED: the workgroup computes the hidden vectors itself, four ranks a wave at a
-// time, in one launch; for factors small enough that reading them again in every
-// column block costs less than a launch.
+// FUSED: the workgroup computes the hidden vectors itself, four ranks a wave, in
+// one launch; for calls so small that a second launch costs more than the longer
+// chain of one workgroup (rank 16 in us, one launch / two: 1 token 512 wide 5.2 /
+// 6.5, 2048 wide 7.3 / 7.8, 4096 wide 9.7 / 7.3; 4 tokens 1024 wide 6.2 / 7.5; 16
+// tokens 256 wide 8.8 / 7.1; rank 64, 1 token 256 wide 11.2 / 8.1).
 constexpr int kDirectTokens = 4, kDirectRanks = 64;  // tokens of a group, ranks held in LDS at a time
-constexpr int64_t kFusedElements = 65536, kFusedColumns = 4096;  // r * d_in and d_out of a fused call, at most
+constexpr int64_t kFusedTokens = 4, kFusedRanks = 16, kFusedWidth = 2048;  // of a fused call, at most
 
 struct DirectArgs {
   ExpandArgs e;
@@ -999,39 +1001,39 @@ __global__ __launch_bounds__(256) void lora_direct_kernel(DirectArgs f) {
       if constexpr (FUSED) {
         const int lane = tid % 64, wave = tid / 64;
         const EW* A = static_cast<const EW*>(f.a) + ad * f.stride_a;
-        for (int kb = 4 * wave; kb < (kn + 15) / 16 * 16; kb += 16) {
-          float h[4][G];
+        const int kb = 4 * wave;
+        static_assert(kFusedRanks == 16 && kFusedTokens <= G, "four waves of four ranks");
+        float h[4][G];
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
+        for (int v = 0; v < 4; ++v)
 #pragma unroll
-            for (int t = 0; t < G; ++t) h[v][t] = 0.0f;
-          if (kb < kn)
+          for (int t = 0; t < G; ++t) h[v][t] = 0.0f;
+        if (kb < kn)
 #pragma unroll 1
-            for (int64_t i = 8 * lane; i < f.d_in; i += 512) {
-              Frag<float> af[4], xf[G];
+          for (int64_t i = 8 * lane; i < f.d_in; i += 512) {
+            Frag<float> af[4], xf[G];
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                af[v] = load8<float, EW>(A + (int64_t)min(k0 + kb + v, p.r - 1) * f.lda + i, f.d_in - i);
+            for (int v = 0; v < 4; ++v)
+              af[v] = load8<float, EW>(A + (int64_t)min(kb + v, p.r - 1) * f.lda + i, f.d_in - i);
 #pragma unroll
-              for (int t = 0; t < G; ++t)
-                if (t < count) xf[t] = load8<float, EX>(static_cast<const EX*>(f.x) + (int64_t)row[t] * f.d_in + i, f.d_in - i);
+            for (int t = 0; t < G; ++t)
+              if (t < count) xf[t] = load8<float, EX>(static_cast<const EX*>(f.x) + (int64_t)row[t] * f.d_in + i, f.d_in - i);
 #pragma unroll
-              for (int t = 0; t < G; ++t)
-                if (t < count)
+            for (int t = 0; t < G; ++t)
+              if (t < count)
 #pragma unroll
-                  for (int v = 0; v < 4; ++v)
+                for (int v = 0; v < 4; ++v)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[v][t] = fmaf(af[v].v[e], xf[t].v[e], h[v][t]);
-            }
+                  for (int e = 0; e < 8; ++e) h[v][t] = fmaf(af[v].v[e], xf[t].v[e], h[v][t]);
+          }
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
+        for (int v = 0; v < 4; ++v)
 #pragma unroll
-            for (int t = 0; t < G; ++t) {
-              if (t >= count) break;
-              for (int off = 32; off > 0; off >>= 1) h[v][t] += __shfl_xor(h[v][t], off);
-              if (lane == 0) hs[t][kb + v] = kb + v < kn ? h[v][t] * sc : 0.0f;
-            }
-        }
+          for (int t = 0; t < G; ++t) {
+            if (t >= count) break;
+            for (int off = 32; off > 0; off >>= 1) h[v][t] += __shfl_xor(h[v][t], off);
+            if (lane == 0) hs[t][kb + v] = kb + v < kn ? h[v][t] * sc : 0.0f;
+          }
       } else {
         if (tid < G) rows[tid] = g.row;
         __syncthreads();
@@ -1245,10 +1247,16 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const float* __restrict__
 
 int64_t max_tiles(int64_t n, int64_t T) { return T / kTile + imin(n + 2, T); }
 
-// Spans of a shrink's reduction: enough workgroups of eight waves for the chip,
-// 512 elements (one 64-deep step a wave) or more each.
-constexpr int64_t kWantGroups = 384;
-int shrink_spans(int64_t groups, int64_t d) { return (int)imax(1, imin(imin(kWantGroups / groups, d / 512), 16)); }
+// Spans of a shrink's reduction, 512 elements (one 64-deep step a wave) or more
+// each, until the launch has `want` workgroups.  bf16 factors: 128, since a
+// workgroup streams its rows and every span adds partial sums to write and read
+// back (in us for 64 / 128 / 192 / 384: 512 tokens of 8192, rank 64 30.8 / 30.8 /
+// 32.7 / 36.6; 2048 tokens, rank 16 49.5 / 46.2 / 47.5 / 50.4).  fp32 factors: 384,
+// since their matrix instructions and scattered loads need more waves (777 tokens
+// of 4099, rank 41 50.5 / 37.7 / 36.5 / 34.2).
+int shrink_spans(int64_t groups, int64_t d, int64_t want) {
+  return (int)imax(1, imin(imin(want / groups, d / 512), 16));
+}
 int64_t span_len(int64_t d, int spans) { return round_up(cdiv(d, spans), 64); }
 
 struct LoraLayout {
@@ -1262,7 +1270,7 @@ struct LoraLayout {
 LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
   LoraLayout L{};
   L.direct = !grads && T <= 64;
-  L.fused = L.direct && P.r <= kDirectRanks && P.r * P.d_in <= kFusedElements && P.d_out <= kFusedColumns;
+  L.fused = L.direct && T <= kFusedTokens && P.r <= kFusedRanks && P.d_in <= kFusedWidth;
   L.tiles = max_tiles(P.n, T);
   L.nslots = L.direct ? T : L.tiles * kTile;
   L.rp = (int)round_up(P.r, 32);
@@ -1271,7 +1279,8 @@ LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
   // tiles in use lie between T / 32 and the maximum: the spans go by the former
   const int64_t groups = (L.direct ? cdiv(T, 4) : cdiv(T, kTile)) * L.kblocks;
   auto spans = [&](int64_t d, int64_t* len) {
-    const int s = (int)imin(shrink_spans(groups, d), L.direct ? 8 : 16);
+    const int s = L.direct ? (int)imin(shrink_spans(groups, d, 384), 8)
+                           : shrink_spans(groups, d, P.dtype == NQ_BF16 ? 128 : 384);
     *len = span_len(d, s);
     return (int)cdiv(d, *len);
   };
@@ -1301,7 +1310,12 @@ LoraLayout lora_layout(const nq_lora& P, int64_t T, bool grads) {
     L.off_dh = take(hb / 4 * 6);
     L.off_dht = take(hb / 4 * 6);
     const int64_t wgs = P.n * (cdiv(P.d_in, 128) + cdiv(P.d_out, 128)) * L.kblocks;
-    L.chunks = (int)imax(1, imin(imin(512 / wgs, T / (P.n * 8 * kTile)), 16));
+    // Few adapters leave CUs idle: their tokens are then split, 16 tiles or more of
+    // an adapter each, and the parts added by a launch of their own (one adapter of
+    // rank 64, 2048 x 2048 in us, split / whole: 8192 tokens 87 / 201, 2048 tokens
+    // 49 / 72, 1024 tokens 35 / 41; two adapters of rank 16, 4096 x 4096, 1024
+    // tokens: 31 split by 8 tiles, 28 whole).
+    L.chunks = (int)imax(1, imin(imin(256 / wgs, T / (P.n * 16 * kTile)), 16));
     if (L.chunks > 1) L.off_part = take((size_t)L.chunks * P.n * P.r * (P.d_in + P.d_out) * sizeof(float));
   }
   L.bytes = off;
@@ -1400,10 +1414,15 @@ hipError_t launch_shrink2(const ShrinkArgs& x, const ShrinkArgs& g, const LoraLa
 }
 
 // Workgroups along the slots of an output product: more 16-slot groups each keep
-// the factors in registers for longer, fewer fill the chip.
+// an adapter's factors in registers for longer, fewer leave a shorter tail behind
+// the last round (two workgroups a CU).  2048 workgroups or 8 groups each (us for
+// 2 / 4 / 8 / 16 groups at most: 8192 tokens, 8192 -> 28672, 32 adapters of rank
+// 64 537 / 491 / 475 / 487; 8 adapters of rank 16, 8192 x 8192 164 / 160 / 179 /
+// 179, where 8 groups are 1056 workgroups).
 int expand_groups(ExpandArgs* a, const LoraLayout& L) {
   const int64_t groups = L.tiles * (kTile / 16);
-  a->per_wg = (int)imax(1, imin(16, groups * cdiv(a->d, 512) / 1024));
+  // never more than 65536 of them: the gradients' grid folds them into y
+  a->per_wg = (int)imax(cdiv(groups, 65536), imin(8, groups * cdiv(a->d, 512) / 2048));
   return (int)cdiv(groups, a->per_wg);
 }
 
@@ -1432,10 +1451,9 @@ hipError_t launch_back(const WgradArgs& wa, const WgradArgs& wb, const ExpandArg
   a.parts = L.kblocks * L.chunks;
   a.groups = expand_groups(&a.dx, L);
   a.cols = (int)cdiv(ea.d, 512);
-  // x: the column blocks of both gradients; y: the adapters, or more where the
-  // output product needs them
+  // x: the column blocks of both gradients (two or more for each of its own); y:
+  // the adapters, or more where the output product needs them
   const int64_t gx = cdiv(wa.d, 128) + cdiv(wb.d, 128), gy = imax(wa.n, cdiv((int64_t)a.groups * a.cols, gx));
-  if (gy > 65535) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)(a.parts + 1));
 #define NQ_BACK(NT, RW, KB) \
   hipLaunchKernelGGL((lora_back_kernel<EX, EG, EW, NT, RW, KB>), grid, dim3(64 * kWgradWaves), 0, s, a)

@@ -844,7 +844,9 @@ bool keeps_range(double ca, double cb, double cc) {
     return s * fabs(ca + cb * l + cc * l * l) <= top;
   };
   auto at = [&](double l) { return !(l > 0.0 && l < top * top) || inside(sqrt(l)); };
-  if (!inside(top)) return false;
+  // no polynomial that stays inside has a larger coefficient (those of the fifth
+  // Chebyshev polynomial, 5, 12.8 and 6.6, are the largest), and none overflows below
+  if (fabs(ca) > 16.0 || fabs(cb) > 16.0 || fabs(cc) > 16.0 || !inside(top)) return false;
   // ca + 3 cb l + 5 cc l^2 = 0
   const double p = 3.0 * cb, q = 5.0 * cc;
   if (q == 0.0) return p == 0.0 || at(-ca / p);

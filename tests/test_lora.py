@@ -191,6 +191,7 @@ SHAPES = [  # T, n, r, d_in, d_out
     (1, 1, 1, 1, 1), (1, 3, 16, 256, 128), (2, 1, 8, 64, 64), (5, 4, 17, 100, 33), (17, 1, 4, 37, 129),
     (64, 5, 16, 520, 260), (64, 64, 7, 65, 513), (65, 3, 16, 256, 256), (33, 2, 64, 130, 1030), (100, 7, 33, 1031, 77),
     (130, 40, 65, 300, 520), (200, 2, 130, 64, 100), (257, 1, 48, 2100, 640), (96, 300, 2, 16, 9),
+    (4, 2, 16, 2048, 600), (3, 3, 5, 2047, 1030), (4, 1, 16, 2049, 70), (4, 2, 17, 300, 70), (5, 5, 16, 256, 64),
 ]
 
 
@@ -311,6 +312,38 @@ def test_grads_of_few_adapters_with_many_tokens():
     """One adapter's tokens cut into chunks whose sums are joined."""
     _run_grads(_case("chunks", 2100, 1, 16, 40, 24))
     _run_grads(_case("chunks2", 1500, 2, 24, 200, 130, "f32", "f32"))
+
+
+@gpu
+@pytest.mark.parametrize("T,n,r,d_in,d_out,kind", [
+    (1 << 24, 3, 2, 3, 5, "f32"),        # the largest call: offsets past 32 bits, a grid at its limit
+    (4200, 3, 20, 8192, 8200, "bf16"),   # several 16-slot groups a workgroup
+    (1 << 16, 8192, 33, 40, 24, "f32"),  # the most adapters
+])
+def test_exact_on_integers_at_large_sizes(T, n, r, d_in, d_out, kind):
+    """Small integers and scales of 1/2: every sum is exact, so results are equal bit for bit."""
+    gen = torch.Generator(DEV).manual_seed(T + n)
+
+    def ints(shape, top, t=torch.float32):
+        return torch.randint(-top, top + 1, shape, generator=gen, device=DEV).to(t)
+    t = torch.bfloat16 if kind == "bf16" else torch.float32
+    a, b, x, g = ints((n, r, d_in), 1, t), ints((n, d_out, r), 1, t), ints((T, d_in), 1, t), ints((T, d_out), 1, t)
+    base, dxb = ints((T, d_out), 9), ints((T, d_in), 9)
+    ids = torch.randint(-1, n + 1, (T,), generator=gen, device=DEV, dtype=torch.int32)
+    scale = torch.full((n,), 0.5, device=DEV)
+    pool = nq.Lora(a, b, scale)
+    y = nq.lora_linear(pool, x, ids, base)
+    dx, da, db = nq.lora_grads(pool, x, g, ids, dxb)
+    none, bad = ids < 0, ids >= n
+    assert torch.equal(y[none], base[none]) and torch.equal(dx[none], dxb[none])
+    assert torch.isnan(y[bad]).all() and torch.isnan(dx[bad]).all()
+    for i in range(n) if n < 10 else (0, 1, 4095, n - 2, n - 1):
+        rows = (ids == i).nonzero()[:, 0]
+        xi, gi, ai, bi = x[rows].double(), g[rows].double(), a[i].double(), b[i].double()
+        h, dh = xi @ ai.T, 0.5 * (gi @ bi)
+        assert torch.equal(y[rows].double(), base[rows] + 0.5 * (h @ bi.T)), i
+        assert torch.equal(dx[rows].double(), dxb[rows] + dh @ ai), i
+        assert torch.equal(da[i].double(), dh.T @ xi) and torch.equal(db[i].double(), 0.5 * (gi.T @ h)), i
 
 
 @gpu

@@ -83,7 +83,7 @@ def _call(x=DUMMY, xd=nq.NQ_F32, batch=2, rows=8, cols=12, ldx=12, stride=96, st
     (dict(ldx=11), nq.NQ_ERR_ARG), (dict(stride=-96), nq.NQ_ERR_ARG), (dict(steps=0), nq.NQ_ERR_ARG),
     (dict(steps=65), nq.NQ_ERR_ARG), (dict(co=(4.0, -4.775, 2.0315)), nq.NQ_ERR_ARG),
     (dict(co=(float("nan"), 0.0, 0.0)), nq.NQ_ERR_ARG), (dict(co=(2.0, 0.0, 0.0)), nq.NQ_ERR_ARG),
-    (dict(co=(-3.0, 2.0, 0.0)), nq.NQ_ERR_ARG), (dict(ws=None), nq.NQ_ERR_WORKSPACE), (dict(wsb=64), nq.NQ_ERR_WORKSPACE),
+    (dict(co=(-3.0, 2.0, 0.0)), nq.NQ_ERR_ARG), (dict(co=(1.5625 * 2.0 ** 600, -2.0 ** 600, 2.0 ** -10), ws=None), nq.NQ_ERR_ARG), (dict(ws=None), nq.NQ_ERR_WORKSPACE), (dict(wsb=64), nq.NQ_ERR_WORKSPACE),
     (dict(ws=DUMMY + 4), nq.NQ_ERR_ARG),
 ])
 def test_rejects_bad_args(kw, status):
