@@ -1415,14 +1415,16 @@ hipError_t launch_shrink2(const ShrinkArgs& x, const ShrinkArgs& g, const LoraLa
 
 // Workgroups along the slots of an output product: more 16-slot groups each keep
 // an adapter's factors in registers for longer, fewer leave a shorter tail behind
-// the last round (two workgroups a CU).  2048 workgroups or 8 groups each (us for
-// 2 / 4 / 8 / 16 groups at most: 8192 tokens, 8192 -> 28672, 32 adapters of rank
-// 64 537 / 491 / 475 / 487; 8 adapters of rank 16, 8192 x 8192 164 / 160 / 179 /
-// 179, where 8 groups are 1056 workgroups).
+// the last round (two workgroups a CU), and an odd number splits tiles.  2 or 4
+// groups while 1024 workgroups are left, 8 while 2048 are (us for 1 / 2 / 4 / 8
+// groups: 2048 tokens of rank 64, 8192 x 8192 72 / 66 / - / -; 8192 tokens of rank
+// 16, 8192 x 8192 - / 164 / 160 / 179; 8192 tokens of rank 64, 8192 -> 28672 - /
+// 537 / 491 / 475).
 int expand_groups(ExpandArgs* a, const LoraLayout& L) {
-  const int64_t groups = L.tiles * (kTile / 16);
+  const int64_t groups = L.tiles * (kTile / 16), all = groups * cdiv(a->d, 512);
   // never more than 65536 of them: the gradients' grid folds them into y
-  a->per_wg = (int)imax(cdiv(groups, 65536), imin(8, groups * cdiv(a->d, 512) / 2048));
+  const int64_t want = all >= 16384 ? 8 : (all >= 4096 ? 4 : (all >= 2048 ? 2 : 1));
+  a->per_wg = (int)imax(want, cdiv(groups, 65536));
   return (int)cdiv(groups, a->per_wg);
 }
 
