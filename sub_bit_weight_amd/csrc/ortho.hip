@@ -508,6 +508,8 @@ struct LargeArgs {
   const double* part;  // [batch][kSumBlocks]
   float* bad;          // [batch]: 0, or NaN for a matrix that is not finite
   float sx;            // operand scale of x
+  int* arrived;        // counters of the split products, cleared here
+  int64_t counters;
 };
 
 // X0 in all its forms, with zeros in the padding.  A workgroup
@@ -523,7 +525,10 @@ __global__ __launch_bounds__(256) void ortho_prepare_kernel(LargeArgs s, const E
   const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
   int ex;
   const float f = inverse_norm(s.part + bi * kSumBlocks, red, ex);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) s.bad[bi] = f * 0.0f;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (threadIdx.x == 0) s.bad[bi] = f * 0.0f;
+    for (int64_t i = threadIdx.x + 256 * bi; i < s.counters; i += 256 * (int64_t)gridDim.z) s.arrived[i] = 0;
+  }
   for (int k = ty; k < 64; k += 4) {
     const int i = i0 + (tall ? tx : k), j = j0 + (tall ? k : tx);
     float v = 0.0f;
@@ -586,7 +591,32 @@ struct GemmArgs {
   void* y;
   int y_bf16, y_t;         // y_t: store transposed
   const float* bad;
+  int per;                 // reduction tiles of a split (gridDim.z of them)
+  float* part;             // [batch][tiles][splits][registers][threads]
+  int* arrived;            // [batch][tiles], zero before and after
 };
+
+// A split's partial sums: agent-scope stores, which write through by themselves (a
+// release fence would write back the XCD's whole L2), then, once every thread's
+// have completed, a relaxed count; the last workgroup acquires before it reads.
+__device__ inline void store_agent(float* p, float v) {
+  typedef __attribute__((address_space(1))) float* gptr;
+  __hip_atomic_store((gptr)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline bool last_to_arrive(int* ctr, int n, int* s_last) {
+  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));  // vmcnt(0)
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    typedef __attribute__((address_space(1))) int* gptr;
+    *s_last = __hip_atomic_fetch_add((gptr)ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+    if (*s_last) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      __hip_atomic_store((gptr)ctr, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next product
+    }
+  }
+  __syncthreads();
+  return *s_last != 0;
+}
 
 // C = A B^T, workgroup tile BM x BN x BK: WM x WN waves of 32x32x16 fp16
 // instructions.  Both operands stream into a ring of S LDS stages by direct
@@ -639,12 +669,12 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
     const int r = (wave * LOADS_B + j) * RPL + drow;
     ob[j] = 2 * ((uint32_t)min(r, p.N - 1 - n0) * p.K + (dchunk ^ swizzle<BK>(r)) * 8);
   }
-  const int nk = p.K / BK, total = nk * p.nseg;
+  const int nk = p.K / BK, kbase = (int)blockIdx.z * p.per, total = min(p.per, nk * p.nseg - kbase);
   // product terms, the smallest first: hi lo, lo hi, hi hi; a stage's loads in
   // STEPS parts
   constexpr int STEPS = BK / 16, PER = LOADS_A + LOADS_B, PART = (PER + STEPS - 1) / STEPS;
   auto issue = [&](int k, int st, int part) {
-    const int kt = min(k, total - 1);
+    const int kt = kbase + min(k, total - 1);
     const int seg = kt / nk, kk = kt - seg * nk;
     const int ta = p.nseg == 1 ? 0 : (seg == 1), tb = p.nseg == 1 ? 0 : (seg == 0);
     const char* a = reinterpret_cast<const char*>(A + ta * p.term_a + (int64_t)kk * BK);
@@ -811,6 +841,32 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
       }
     }
   }
+  if constexpr (MODE == kGram || MODE == kPoly) {
+    // few tiles over a long axis: the splits' sums are added in their order by the
+    // workgroup that comes last (nobody waits)
+    if (gridDim.z > 1) {
+      constexpr int NT = 64 * NW, REGS = MB * NB * 16;
+      __shared__ int last;
+      float* part = p.part + (bi * ntiles + t) * gridDim.z * (REGS * NT) + threadIdx.x;
+      float* mine = part + (int64_t)blockIdx.z * (REGS * NT);
+#pragma unroll
+      for (int b = 0; b < MB * NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) store_agent(mine + (b * 16 + r) * NT, acc[b / NB][b % NB][r]);
+      if (!last_to_arrive(p.arrived + bi * ntiles + t, (int)gridDim.z, &last)) return;
+#pragma unroll
+      for (int b = 0; b < MB * NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[b / NB][b % NB][r] = part[(b * 16 + r) * NT];
+      for (int z = 1; z < (int)gridDim.z; ++z) {
+        part += REGS * NT;
+#pragma unroll
+        for (int b = 0; b < MB * NB; ++b)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[b / NB][b % NB][r] += part[(b * 16 + r) * NT];
+      }
+    }
+  }
   // Epilogue, 32 rows at a time through the wave's part of LDS: lane l, register
   // 4a + c of a block holds row 8a + 4(l / 32) + c of column l % 32; read back, a
   // lane holds 8 consecutive columns of a row, and for a transposed result 8
@@ -924,8 +980,20 @@ struct OrthoLayout {
   bool small;
   int p, P, pp, qp, terms, spans;
   int64_t q, span;
-  size_t off_g, off_q, off_part, off_bad, off_xf, off_x16, off_xt[2], off_g16, off_b16, bytes;
+  size_t off_g, off_q, off_part, off_bad, off_xf, off_x16, off_xt[2], off_g16, off_b16, off_sums, off_arr, bytes;
+  int64_t counters;
 };
+
+// Symmetric products of few tiles: the reduction is split, 16 tiles of it or more
+// each, until a workgroup runs on every CU.  One matrix of 128 x 16384 has 3 tiles
+// of 64 x 64: 229 us a call in fp32, unsplit 989; 128 x 4096 156 (splits of 8 tiles
+// or more, two workgroups a CU: 171), unsplit 323.  64 matrices of 128 x 1024 to
+// bf16 have 192: 378 us whole, 415 in two splits.
+int square_splits(int64_t batch, int64_t p, int64_t k, int terms) {
+  const int64_t t = cdiv(p, 64), tiles = batch * t * (t + 1) / 2, all = k / kBK * (terms > 1 ? 3 : 1);
+  const int64_t n = imax(1, imin(imin(256 / tiles, all / 16), 32));
+  return (int)cdiv(all, cdiv(all, n));
+}
 
 OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd) {
   OrthoLayout L{};
@@ -956,6 +1024,12 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
     for (auto& o : L.off_xt) o = take((size_t)batch * L.terms * L.q * L.pp * 2);
     L.off_g16 = take((size_t)batch * L.terms * L.p * L.pp * 2);
     L.off_b16 = take((size_t)batch * L.terms * L.p * L.pp * 2);
+    const int splits = (int)imax(square_splits(batch, L.p, L.qp, L.terms), square_splits(batch, L.p, L.pp, L.terms));
+    if (splits > 1) {
+      L.counters = batch * cdiv(L.p, 64) * (cdiv(L.p, 64) + 1) / 2;
+      L.off_sums = take((size_t)L.counters * splits * 64 * 64 * sizeof(float));
+      L.off_arr = take((size_t)L.counters * sizeof(int));
+    }
   }
   L.bytes = off;
   return L;
@@ -991,7 +1065,7 @@ hipError_t launch_small_p(const SmallArgs& a, int64_t batch, hipStream_t s) {
 }
 
 template <int BM, int BN, int BK, int WM, int WN, int S, bool SPREAD, int MODE>
-hipError_t launch_gemm_tile(GemmArgs g, int64_t batch, hipStream_t s) {
+hipError_t launch_gemm_tile(GemmArgs g, int64_t batch, hipStream_t s, int splits = 1) {
   constexpr size_t lds = (size_t)S * (BM + BN) * BK * 2;
   const auto kernel = ortho_gemm_kernel<BM, BN, BK, WM, WN, S, SPREAD, MODE>;
   static std::atomic<uint64_t> done{0};
@@ -999,8 +1073,9 @@ hipError_t launch_gemm_tile(GemmArgs g, int64_t batch, hipStream_t s) {
   if (e != hipSuccess) return e;
   g.tiles_m = (int)cdiv(g.M, BM);
   g.tiles_n = (int)cdiv(g.N, BN);
+  g.per = (int)cdiv(g.K / BK * g.nseg, splits);
   const int64_t tiles = g.sym ? (int64_t)g.tiles_m * (g.tiles_m + 1) / 2 : (int64_t)g.tiles_m * g.tiles_n;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(8 * cdiv(tiles, 8)), (unsigned)batch), dim3(64 * WM * WN), lds, s, g);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(8 * cdiv(tiles, 8)), (unsigned)batch, (unsigned)splits), dim3(64 * WM * WN), lds, s, g);
   return hipGetLastError();
 }
 
@@ -1023,7 +1098,8 @@ hipError_t launch_ortho_gemm(GemmArgs g, int64_t batch, hipStream_t s) {
   if constexpr (!square)
     if (tiles(128, 256) >= 128) return launch_gemm_tile<128, 256, 64, 2, 4, 3, true, MODE>(g, batch, s);
   if (tiles(128, 128) >= 192) return launch_gemm_tile<128, 128, 64, 2, 2, 4, true, MODE>(g, batch, s);
-  return launch_gemm_tile<64, 64, 64, 2, 2, 4, true, MODE>(g, batch, s);
+  const int splits = square ? square_splits(batch, g.M, g.K, g.terms) : 1;
+  return launch_gemm_tile<64, 64, 64, 2, 2, 4, true, MODE>(g, batch, s, splits);
 }
 
 // The largest |b l + c l^2| for l in [0, top].
@@ -1083,6 +1159,8 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   l.xt16 = xt16[0];
   l.part = part;
   l.bad = reinterpret_cast<float*>(ws + L.off_bad);
+  l.arrived = reinterpret_cast<int*>(ws + L.off_arr);
+  l.counters = L.counters;
   // |x| <= 1.25, |G| <= 1.25^2 and the polynomial's bound, each times its scale
   // below 65504
   const float sx = kScaleX, sg = 16384.0f;
@@ -1119,6 +1197,8 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   gram.ldo = L.pp;
   gram.term_o = gs;
   gram.s_acc = sg / (sx * sx);
+  gram.part = reinterpret_cast<float*>(ws + L.off_sums);
+  gram.arrived = l.arrived;
   poly = gram;
   poly.A = poly.B = g16;
   poly.stride_a = poly.stride_b = L.terms * gs;

@@ -116,7 +116,7 @@ def test_binding_refuses_host_tensors_and_shapes():
 
 
 SMALL = [(1, 1), (1, 9), (5, 3), (16, 256), (17, 300), (33, 1025), (64, 64), (64, 129), (500, 33), (2050, 48), (130, 2), (63, 640)]
-LARGE = [(65, 65), (65, 200), (130, 100), (257, 300), (300, 257), (128, 1030), (700, 400)]
+LARGE = [(65, 65), (65, 200), (130, 100), (257, 300), (300, 257), (128, 1030), (700, 400), (65, 9000), (4100, 190)]
 
 
 @gpu
