@@ -191,18 +191,21 @@ __device__ inline void inverse_trace(double t, double& inv, double& root) {
   root = t > 0.0 && isfinite(t) ? 1.0 / sqrt(t) : inv;
 }
 
-// The iteration on p x p matrices, one workgroup per matrix.  A (the Gram
-// matrix of the iterate), P = a I + b A + c A^2 and Q (the product of the P so
-// far) commute and are symmetric: every product reads both operands by rows.
+// The iteration on p x p matrices, one workgroup per matrix and a wave per 16x16
+// block of them.  A (the Gram matrix of the iterate), P = a I + b A + c A^2 and Q
+// (the product of the P so far) commute and are symmetric: every product reads both
+// operands by rows, and P and the last Q are made in the registers of the products
+// they come from.  Bound by the chain of 19 products of five steps, about half of it
+// the fp64 rate of one CU (a call of 64 x 1024: 96 us, with four waves 107).
 template <int PT>
-__global__ __launch_bounds__(256) void ortho_solve_kernel(SmallArgs s) {
-  constexpr int P = 16 * PT, S = P + 4, NT = (PT * PT + 3) / 4;
+__global__ __launch_bounds__(64 * PT * PT) void ortho_solve_kernel(SmallArgs s) {
+  constexpr int P = 16 * PT, S = P + 4, NTH = 64 * PT * PT;
   extern __shared__ double lds64[];
   double *A = lds64, *B = lds64 + P * S, *Q = lds64 + 2 * P * S;
   __shared__ double inv_sh[2];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, q = lane / 16, c = lane % 16;
   const double* g = s.gpart + (int64_t)blockIdx.x * s.spans * P * P;
-  for (int i = tid; i < P * P; i += 256) {
+  for (int i = tid; i < P * P; i += NTH) {
     double v = 0.0;
 #pragma unroll 8
     for (int k = 0; k < s.spans; ++k) v += g[(int64_t)k * P * P + i];
@@ -216,55 +219,45 @@ __global__ __launch_bounds__(256) void ortho_solve_kernel(SmallArgs s) {
   }
   __syncthreads();
   const double inv = inv_sh[0];
-  for (int i = tid; i < P * P; i += 256) A[i / P * S + i % P] *= inv;
+  for (int i = tid; i < P * P; i += NTH) A[i / P * S + i % P] *= inv;
   __syncthreads();
-  f64x4 acc[NT];
-  auto product = [&](const double* L, const double* R) {  // acc = this wave's blocks of L R
+  const int row = wave / PT * 16, col = wave % PT * 16;
+  const int at = (row + q) * S + col + c;  // this lane's values: rows row + q + 4 i of column col + c
+  auto product = [&](const double* L, const double* R) {  // this wave's block of L R
+    f64x4 acc = {0, 0, 0, 0};
+    const double* l = L + (row + c) * S + q;
+    const double* r = R + (col + c) * S + q;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      acc[n] = f64x4{0, 0, 0, 0};
-      const int blk = wave + 4 * n;
-      if (blk >= PT * PT) continue;
-      const double* l = L + (blk / PT * 16 + c) * S + q;
-      const double* r = R + (blk % PT * 16 + c) * S + q;
-#pragma unroll
-      for (int k = 0; k < P; k += 4) acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64(l[k], r[k], acc[n], 0, 0, 0);
-    }
+    for (int k = 0; k < P; k += 4) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(l[k], r[k], acc, 0, 0, 0);
+    return acc;
   };
-  auto store = [&](double* D) {
-    __syncthreads();  // every wave has read its operands
+  auto store = [&](double* D, const f64x4& v) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int blk = wave + 4 * n;
-      if (blk >= PT * PT) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) D[(blk / PT * 16 + 4 * i + q) * S + blk % PT * 16 + c] = acc[n][i];
-    }
-    __syncthreads();
+    for (int i = 0; i < 4; ++i) D[at + 4 * i * S] = v[i];
   };
   for (int step = 0; step < s.steps; ++step) {
-    product(A, A);
-    store(B);
-    for (int i = tid; i < P * P; i += 256) {
-      const int at = i / P * S + i % P;
-      const double v = s.c * B[at] + s.b * A[at] + (i / P == i % P ? s.a : 0.0);
-      B[at] = v;
-      if (step == 0) Q[at] = v;
+    f64x4 v = product(A, A);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = s.c * v[i] + s.b * A[at + 4 * i * S] + (row + q + 4 * i == col + c ? s.a : 0.0);
+    store(B, v);
+    __syncthreads();
+    const bool more = step + 1 < s.steps;
+    f64x4 w = v;
+    if (step > 0) w = product(Q, B);
+    if (more) v = product(A, B);
+    __syncthreads();  // every wave has read its operands
+    store(Q, w);
+    if (more) {
+      store(A, v);
+      __syncthreads();
+      v = product(A, B);
+      __syncthreads();
+      store(A, v);
     }
     __syncthreads();
-    if (step > 0) {
-      product(Q, B);
-      store(Q);
-    }
-    if (step + 1 < s.steps) {
-      product(A, B);
-      store(A);
-      product(A, B);
-      store(A);
-    }
   }
   double* out = s.qmat + (int64_t)blockIdx.x * P * P;
-  for (int i = tid; i < P * P; i += 256) out[i] = Q[i / P * S + i % P] * inv_sh[1];
+  for (int i = tid; i < P * P; i += NTH) out[i] = Q[i / P * S + i % P] * inv_sh[1];
 }
 
 // The same for p <= 16 in the registers of a wave: its lanes hold a symmetric
@@ -1045,7 +1038,7 @@ hipError_t launch_small(const SmallArgs& a, int64_t batch, hipStream_t s) {
     if (e == hipSuccess)
       e = allow_lds(reinterpret_cast<const void*>(ortho_solve_kernel<PT>), 3 * P * S * sizeof(double), done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ortho_solve_kernel<PT>), dim3((unsigned)batch), dim3(256), 3 * P * S * sizeof(double), s, a);
+    hipLaunchKernelGGL((ortho_solve_kernel<PT>), dim3((unsigned)batch), dim3(64 * PT * PT), 3 * P * S * sizeof(double), s, a);
     e = hipGetLastError();
   }
   if (e != hipSuccess) return e;
