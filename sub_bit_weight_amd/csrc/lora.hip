@@ -214,6 +214,7 @@ __device__ inline f32x4 zero4() { return f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
 // (integer counters in LDS), which gives its first tile, and then lists its own
 // tokens in order.  A wave owns a stretch of tokens, whose groups stay in
 // registers between the two passes (up to 16384 tokens; the rest is read again).
+// A chain of round trips: 5 us for 2048 tokens, 10 us for 8192.
 __global__ __launch_bounds__(kRouteThreads) void lora_route_kernel(const int32_t* __restrict__ ids, int T, int n,
                                                                    int* __restrict__ tile_off, int* __restrict__ tile_ad,
                                                                    int* __restrict__ slot_row, int* __restrict__ arrived,
@@ -316,9 +317,14 @@ __device__ inline bool direct_rows(const int32_t* __restrict__ ids, int T, int n
 // A workgroup takes MT groups of 16 slots of one adapter, 16 NT rank rows and a
 // span of the reduction.  bf16 operands stream through LDS (staged_steps);
 // otherwise its eight waves take 64-deep steps of the span in turn, straight
-// from memory.  The waves' sums are added through LDS in wave order.  With several spans, each
-// writes its sum and counts itself in; the workgroup that comes last adds them
-// in span order (nobody waits).  Direct calls leave that sum to the reader.
+// from memory.  The waves' sums are added through LDS in wave order.  With several
+// spans, each writes its sum and counts itself in; the workgroup that comes last
+// adds them in span order (nobody waits).  Direct calls leave that sum to the reader.
+// Bound by the rows' bytes and, for few tokens, by the chain load - multiply - sum:
+// 2048 tokens of 8192, bf16, rank 16 13 us (2.6 TB/s); 8192 tokens, rank 64 53 us
+// (2.5 TB/s, one workgroup of 147 KB LDS a CU); 777 tokens of 4099, fp32, rank 41
+// 18 us (loads of 4 bytes and the fp32 matrix rate; fp32 rows through LDS by loads
+// of 4 bytes a lane: 22 us).
 //
 // Rank rows of the NT tiles: 16n + row, or (TW) NT * row + n, so that a lane's
 // NT ranks are consecutive in a row of W.
@@ -350,7 +356,7 @@ constexpr int kShrinkWaves = 8;
 
 // Partial sums that another workgroup of the launch reads: agent-scope stores
 // (they write through by themselves, where a release fence would write back
-// the XCD's whole L2: 90 us instead of 12 for 2048 tokens of 8192), then, once
+// the XCD's whole L2: 90 us instead of 13 for 2048 tokens of 8192), then, once
 // every thread's stores have completed and the workgroup has met, a relaxed
 // count; the last workgroup acquires before it reads.
 __device__ inline void store_agent(float* p, float v) {
@@ -472,7 +478,8 @@ __device__ inline void shrink_step(const EX* (&xp)[MT], const EW* w, const int (
 // two chunks ahead, and wave w multiplies 32-deep step w of each chunk.  A row of
 // 512 bytes keeps its 16-byte piece i at i ^ (row % 16), so that the 16 rows of a
 // fragment read meet 16 different bank groups.  Straight from memory the same
-// loads took 68 us instead of the figure above (8192 tokens of 8192, rank 64).
+// loads took 68 us, this way 53 (8192 tokens of 8192, rank 64); chunks of 128 for
+// the wider rank tiles, so that two workgroups share a CU, 55.
 constexpr int kChunk = 256, kStages = 3;
 
 template <bool TW, int NT>
@@ -742,6 +749,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink2_kernel(ShrinkA
 // Columns: tile v, row p holds 16v + p, or (TW) tile 2u + b holds 32u + 2p + b,
 // so that a lane loads two consecutive columns of a row of W; either way a
 // lane's results are eight float4 pieces.
+// Bound by the bytes of base and y: 2048 x 8192, rank 16 27 us (4.9 TB/s), 8192 x
+// 28672, rank 64 415 us (4.5 TB/s); a large copy runs at 5.2.
 struct ExpandArgs {
   const void* h;        // fragments as shrink stores them; direct calls: fp32 [spans][nslots][rp] unscaled sums
   int64_t h_term;
@@ -936,7 +945,9 @@ __global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kern
 // Two columns of W per thread instead, whose rank rows it reads whole, and fp32
 // products with the hidden vectors of up to four tokens, which lie in LDS.  Bound
 // by the factors' bytes where tokens have adapters of their own (48 mixed tokens,
-// rank 16, 8192 -> 28672: 40 MB).
+// rank 16, 8192 -> 28672: 14 us for 42 MB, 3.0 TB/s).  As tiles: 34 us against 26
+// for 64 tokens, 15 against 10 for 16 of 4096 x 4096; only 64 tokens of one adapter
+// are faster as tiles, 16 against 18.
 //
 // FUSED: the workgroup computes the hidden vectors itself, four ranks a wave, in
 // one launch; for calls so small that a second launch costs more than the longer
@@ -1080,10 +1091,10 @@ __global__ __launch_bounds__(256) void lora_direct_kernel(DirectArgs f) {
 // ht (16 NT RW rank rows).  Lane (q, c) loads 8 consecutive columns 8c .. of the
 // rows of slots 8q .. 8q+7 of a tile and transposes them in registers, so tile v
 // of the eight holds columns 8c + v.  The four waves are 4 / RW that take tiles
-// in turn times RW that take 16 NT ranks each (RW = 2 for more than 32 ranks:
-// four rank tiles a wave leave no registers for the next tile's rows, 222 us
-// instead of the figure below); each loads the next tile's rows before it
-// multiplies.  Their sums are added through LDS in wave order.
+// in turn times RW that take 16 NT ranks each (RW = 2 for more than 32 ranks: four
+// rank tiles a wave leave no registers for the next tile's rows, 222 us against 129
+// for both gradients of 8192 tokens, rank 64, 8192 x 8192); each loads the next
+// tile's rows before it multiplies.  Their sums are added through LDS in wave order.
 // DB false: out[k][j] (dA: x and dh), true: out[j][k] (dB: g and h).
 struct WgradArgs {
   const void* x;     // [T][d]
@@ -1202,6 +1213,9 @@ __device__ inline void wgrad(const WgradArgs& p, int64_t block, int ad, int z, f
 
 // What follows the hidden vectors of the gradients, in one launch, so that the
 // parts fill each other's tails: dB (g and h), dA (x and dh), then dx (dh and A).
+// Bound by the rows' bytes: 196 us for 8192 tokens, 16 adapters of rank 64, 8192 x
+// 8192 (838 MB, 4.3 TB/s; as two launches 34 us more), 27 us for 2048 tokens, 4 adapters
+// of rank 16, 4096 -> 11008.
 // Grid: z below `parts` the factor gradients (x: 128-column blocks of both, y:
 // adapters), z = parts the output product (x * y: its workgroups).
 struct BackArgs {

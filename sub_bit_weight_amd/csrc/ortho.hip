@@ -10,9 +10,11 @@
 //    on p x p matrices and X is read twice and written once, instead of 3 passes
 //    a step.  G squares the singular values and Q multiplies the small ones by
 //    up to a^steps, so this form needs twice the digits: everything is fp64
-//    (X0 enters exactly, one rounding at the end).  HBM-bound for small p,
-//    bound by the fp64 matrix rate (60 TFLOP/s measured on a large product)
-//    as p nears 64.
+//    (X0 enters exactly, one rounding at the end).  Bound by the launches and by
+//    the bytes of X for p <= 16 (64 matrices of 16 x 4096: 8 + 14 us, 33 MB), by
+//    the small products' chain as p nears 64 (one of 64 x 1024: 96 us) and then by
+//    the fp64 matrix rate (60 TFLOP/s measured on a large product).  p = 65 takes
+//    125 us for 1024 columns the other way, so the boundary costs nothing.
 //  * p > 64: the iteration as written, on the fp16 matrix cores with fp32
 //    accumulation, all three products as C = P Q^T of row-major operands.  The
 //    state X is fp32 and a X is added in fp32; only the operands of products are
@@ -20,8 +22,11 @@
 //    the iteration does not blow them up as it does a rounding of X itself.  For
 //    an fp32 result each operand is two fp16 terms (hi + lo, 22 bits) and a
 //    product three fp16 products.  Operands are scaled by powers of two into
-//    fp16's range: |x| <= |G| bounds are known because the host checks that the
-//    polynomial maps [0, 1.25] into [-1.25, 1.25].
+//    fp16's range: bounds on x and G are known because the host checks that the
+//    polynomial maps [0, 1.25] into [-1.25, 1.25].  Bound by the matrix cores, whose
+//    clock such products hold near 1.7 GHz: 4096 x 11008 in one term 4.1 ms (gram
+//    260, polynomial 106, step 435 us; 3.1 TFLOP by symmetric halves, 0.76 PFLOP/s
+//    over the call), two of 1371 x 2203 in two terms 0.84 ms.
 #include "nq_internal.h"
 
 namespace nq {
