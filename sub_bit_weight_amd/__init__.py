@@ -593,6 +593,13 @@ def _f32_rows(t: torch.Tensor, name: str, shape: tuple, device) -> None:
         raise ValueError(f"{name} must be float32 {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _workspace_on(workspace: torch.Tensor | None, device) -> None:
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        if workspace.device != device:
+            raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+
+
 def lora_workspace_bytes(pool: Lora, T: int) -> int:
     return int(lib().nq_lora_workspace_bytes(ctypes.byref(pool.struct()), T))
 
@@ -608,6 +615,7 @@ def lora_linear(pool: Lora, x: torch.Tensor, ids: torch.Tensor, base: torch.Tens
         _f32_rows(base, "base", (T, pool.d_out), dev)
     if y is not None:
         _f32_rows(y, "y", (T, pool.d_out), dev)
+    _workspace_on(workspace, dev)
     with _call_on(dev, stream):
         if y is None:
             y = torch.empty((T, pool.d_out), dtype=torch.float32, device=dev)
@@ -632,6 +640,9 @@ def lrb_lora_linear(layer: Lrb, pool: Lora, x: torch.Tensor, ids: torch.Tensor, 
     dev = x.device
     if y is not None:
         _f32_rows(y, "y", (T, layer.d_out), dev)
+    if layer.s1.device != dev:
+        raise ValueError(f"the layer and x must share a device: {layer.s1.device}, {dev}")
+    _workspace_on(workspace, dev)
     with _call_on(dev, stream):
         if y is None:
             y = torch.empty((T, layer.d_out), dtype=torch.float32, device=dev)
@@ -661,6 +672,7 @@ def lora_grads(pool: Lora, x: torch.Tensor, g: torch.Tensor, ids: torch.Tensor, 
     for t, name in ((dx_base, "dx_base"), (dx, "dx")):
         if t is not None:
             _f32_rows(t, name, (T, pool.d_in), dev)
+    _workspace_on(workspace, dev)
     with _call_on(dev, stream):
         if dx is None:
             dx = torch.empty((T, pool.d_in), dtype=torch.float32, device=dev)
@@ -713,6 +725,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coeffs=NEWTON_SCHULZ, out_dty
     stride = x.stride(0) if x.dim() == 3 and batch > 1 else 0
     a, b, c = (float(v) for v in coeffs)
     dev = x.device
+    _workspace_on(workspace, dev)
     with _call_on(dev, stream):
         if y is None:
             y = torch.empty(x.shape, dtype=out_dtype, device=dev)

@@ -455,12 +455,16 @@ def test_binding_refuses_wrong_tensors():
     pool, x, ids = _gpu_pool(c), _dev(c["x"], "bf16"), _dev(c["ids"])
     bad = [dict(x=x[:, :8].contiguous()), dict(ids=ids.long()), dict(ids=ids[:4].contiguous()), dict(ids=ids.cpu()),
            dict(base=torch.zeros(5, 9, device=DEV)), dict(base=torch.zeros(5, 8, device=DEV, dtype=torch.bfloat16)),
-           dict(y=torch.zeros(4, 8, device=DEV)), dict(x=x.half()), dict(x=x.t().contiguous().t())]
+           dict(y=torch.zeros(4, 8, device=DEV)), dict(x=x.half()), dict(x=x.t().contiguous().t()),
+           dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)),
+           dict(workspace=torch.empty(1 << 20, 2, dtype=torch.uint8, device=DEV)[:, 0])]
     for kw in bad:
         with pytest.raises(ValueError):
             nq.lora_linear(**{**dict(pool=pool, x=x, ids=ids), **kw})
     with pytest.raises(ValueError):
         nq.lora_grads(pool, x, torch.zeros(5, 9, device=DEV), ids)
+    with pytest.raises(ValueError):
+        nq.lora_grads(pool, x, torch.zeros(5, 8, device=DEV), ids, workspace=torch.empty(1 << 20, dtype=torch.uint8))
     with pytest.raises(ValueError):
         nq.lora_grads(pool, x, torch.zeros(5, 8, device=DEV), ids, dx_base=torch.zeros(5, 15, device=DEV))
     with pytest.raises(nq.NqError):

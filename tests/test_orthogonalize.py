@@ -205,6 +205,8 @@ def test_views_workspace_and_streams(shape):
     with pytest.raises(nq.NqError):
         nq.orthogonalize(x, workspace=ws[:128])
     with pytest.raises(ValueError):
+        nq.orthogonalize(x, workspace=ws.cpu())
+    with pytest.raises(ValueError):
         nq.orthogonalize(x.transpose(1, 2))
     with pytest.raises(ValueError):
         nq.orthogonalize(x, out_dtype=torch.float16)
