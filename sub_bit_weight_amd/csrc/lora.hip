@@ -186,6 +186,25 @@ __device__ inline Frag<float> load8<float, Bf16>(const Bf16* p, int64_t nv) {
   return f;
 }
 
+// Elements k .. k + 7 of a row of r, zero past its end.  bf16 whose end lies among
+// them (and r > 8): the row's last eight, shifted into place, one load instead of
+// one per element (2048 tokens, rank 12, 4096 x 4096: 36 us, by elements 41).  fp32
+// by elements: shifting its eight words costs more (133 tokens, rank 18, 64 ->
+// 5616: 25 us, shifted 28).
+__device__ inline Frag<float> load8_row(const float* row, int k, int r) { return load8<float, float>(row + k, r - k); }
+__device__ inline Frag<Bf16> load8_row(const Bf16* row, int k, int r) {
+  if (r % 8 == 0 || r < 8) return load8<Bf16, Bf16>(row + k, r - k);
+  if (k >= r) return load8<Bf16, Bf16>(row, 0);
+  const int at = min(k, r - 8), n = k - at;
+  Frag<Bf16> f = load8<Bf16, Bf16>(row + at, 8);
+  uint64_t lo = (uint64_t)f.d[1] << 32 | f.d[0], hi = (uint64_t)f.d[3] << 32 | f.d[2];
+  if (n & 1) lo = lo >> 16 | hi << 48, hi >>= 16;
+  if (n & 2) lo = lo >> 32 | hi << 32, hi >>= 32;
+  if (n & 4) lo = hi, hi = 0;
+  f.d = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  return f;
+}
+
 __device__ inline float element(const Frag<float>& f, int e) { return f.v[e]; }
 __device__ inline float element(const Frag<Bf16>& f, int e) {
   return __uint_as_float(e % 2 ? f.d[e / 2] & 0xFFFF0000u : f.d[e / 2] << 16);
@@ -805,8 +824,8 @@ __device__ inline void expand_weights(const ExpandArgs& p, int ad, int64_t n0, i
   } else {
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-      const int64_t j = n0 + 16 * v + c;
-      w[v] = load8<EW, EW>(base + j * p.ldw + k, j < p.d ? p.r - k : 0);
+      const EW* row = base + imin(n0 + 16 * v + c, p.d - 1) * p.ldw;  // columns past the last are not stored
+      w[v] = load8_row(row, k, p.r);
     }
   }
 }
@@ -935,7 +954,7 @@ __device__ inline void expand(const ExpandArgs& p, int bx, int by, float (*out)[
 }
 
 template <typename EW, int KB>
-__global__ __launch_bounds__(256, sizeof(EW) == 2 ? 2 : 1) void lora_expand_kernel(ExpandArgs p) {
+__global__ __launch_bounds__(256, sizeof(EW) == 4 ? 1 : (KB == 1 ? 3 : 2)) void lora_expand_kernel(ExpandArgs p) {
   __shared__ __attribute__((aligned(16))) float out[4][16 * kOutRow];
   expand<EW, false, KB>(p, (int)blockIdx.x, (int)blockIdx.y, out);
 }
@@ -987,12 +1006,11 @@ __global__ __launch_bounds__(256) void lora_direct_kernel(DirectArgs f) {
     w[u] = static_cast<const EW*>(p.w) + imax(ad, 0) * p.stride_w + jc[u] * p.ldw;
   }
   Frag<EW> wf[NC][2];
-  auto load = [&](int k, int left) {
+  auto load = [&](int k) {
 #pragma unroll
-    for (int u = 0; u < NC; ++u) {
-      wf[u][0] = load8<EW, EW>(w[u] + k, left);
-      wf[u][1] = load8<EW, EW>(w[u] + k + 8, left - 8);
-    }
+    for (int u = 0; u < NC; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) wf[u][i] = load8_row(w[u], k + 8 * i, p.r);
   };
   float acc[G][NC], b[G][NC];
 #pragma unroll
@@ -1003,7 +1021,7 @@ __global__ __launch_bounds__(256) void lora_direct_kernel(DirectArgs f) {
       b[t][u] = p.base && t < count ? p.base[(int64_t)row[t] * p.d + jc[u]] : 0.0f;
     }
   if (ad >= 0) {
-    load(0, p.r);
+    load(0);
     const float sc = p.scale[ad];
 #pragma unroll 1
     for (int k0 = 0; k0 < p.r; k0 += kDirectRanks) {
@@ -1065,7 +1083,7 @@ __global__ __launch_bounds__(256) void lora_direct_kernel(DirectArgs f) {
         Frag<EW> cur[NC][2];
 #pragma unroll
         for (int u = 0; u < NC; ++u) cur[u][0] = wf[u][0], cur[u][1] = wf[u][1];
-        if (k0 + kk + 16 < p.r) load(k0 + kk + 16, p.r - k0 - kk - 16);
+        if (k0 + kk + 16 < p.r) load(k0 + kk + 16);
 #pragma unroll
         for (int t = 0; t < G; ++t) {
           if (t >= count) break;
@@ -1369,7 +1387,7 @@ ShrinkArgs shrink_args(const nq_lora& P, const LoraLayout& L, char* ws, int side
   a.arrived = reinterpret_cast<int*>(ws + L.off_arr) + side;
   a.h_term = a.ht_term = L.nslots * L.rp;
   a.staged = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.d % 8 == 0 &&
-             a.ldw % 8 == 0 && a.stride_w % 8 == 0 && P.r % 8 == 0;
+             a.ldw % 8 == 0 && a.stride_w % 8 == 0 && (side == 0 || P.r % 8 == 0);
   return a;
 }
 

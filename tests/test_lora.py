@@ -191,6 +191,7 @@ SHAPES = [  # T, n, r, d_in, d_out
     (1, 1, 1, 1, 1), (1, 3, 16, 256, 128), (2, 1, 8, 64, 64), (5, 4, 17, 100, 33), (17, 1, 4, 37, 129),
     (64, 5, 16, 520, 260), (64, 64, 7, 65, 513), (65, 3, 16, 256, 256), (33, 2, 64, 130, 1030), (100, 7, 33, 1031, 77),
     (130, 40, 65, 300, 520), (200, 2, 130, 64, 100), (257, 1, 48, 2100, 640), (96, 300, 2, 16, 9),
+    (90, 3, 12, 512, 300), (150, 2, 20, 768, 264), (70, 40, 41, 1032, 520),  # ranks that are no multiple of 8
     (4, 2, 16, 2048, 600), (3, 3, 5, 2047, 1030), (4, 1, 16, 2049, 70), (4, 2, 17, 300, 70), (5, 5, 16, 256, 64),
 ]
 
