@@ -847,11 +847,13 @@ bool keeps_range(double ca, double cb, double cc) {
   // no polynomial that stays inside has a larger coefficient (those of the fifth
   // Chebyshev polynomial, 5, 12.8 and 6.6, are the largest), and none overflows below
   if (fabs(ca) > 16.0 || fabs(cb) > 16.0 || fabs(cc) > 16.0 || !inside(top)) return false;
-  // ca + 3 cb l + 5 cc l^2 = 0
-  const double p = 3.0 * cb, q = 5.0 * cc;
-  if (q == 0.0) return p == 0.0 || at(-ca / p);
-  const double disc = p * p - 4.0 * q * ca;
-  return disc < 0.0 || (at((-p + sqrt(disc)) / (2.0 * q)) && at((-p - sqrt(disc)) / (2.0 * q)));
+  // ca + 3 cb l + 5 cc l^2 = 0: one zero from the sum of like signs, the other from
+  // the zeros' product, so that neither is lost to cancellation beside a tiny cc (a
+  // zero that does not exist comes out infinite or NaN, which `at` passes)
+  const double p = 3.0 * cb, q = 5.0 * cc, disc = p * p - 4.0 * q * ca;
+  if (disc < 0.0) return true;
+  const double t = -0.5 * (p + copysign(sqrt(disc), p));
+  return at(t / q) && at(ca / t);
 }
 
 }  // namespace

@@ -96,6 +96,14 @@ def test_usual_coefficients_pass_the_range_check(co):
     assert _call(co=co, ws=None) == nq.NQ_ERR_WORKSPACE  # the next check
 
 
+@pytest.mark.parametrize("cc", [0.0, 1e-16, -1e-17, 1e-20, -1e-300, 5e-324])
+@pytest.mark.parametrize("ca,cb", [(15.625, -10.0), (4.0, -3.2), (-4.0, 3.2)])
+def test_rejects_an_interior_maximum_beside_a_tiny_quintic_term(ca, cb, cc):
+    """All three leave 1.25 inside (at s = 0.72 or 0.65) although their ends do not."""
+    assert _call(co=(ca, cb, cc), ws=None) == nq.NQ_ERR_ARG
+    assert _call(co=(1.5, -0.5, cc), ws=None) == nq.NQ_ERR_WORKSPACE  # the next check
+
+
 def test_workspace_query():
     lib = nq.lib()
     assert lib.nq_orthogonalize_workspace_bytes(1, 16, 4096, nq.NQ_F32) > 0
