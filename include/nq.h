@@ -415,7 +415,10 @@ nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const
  * A zero matrix gives zeros; one with a value that is not finite gives NaN
  * throughout and leaves the other matrices of the batch alone.  Entries of any
  * size are fine (the norm is fp64).
- * Arithmetic: a shorter side up to 64 is computed in fp64 and rounded once.  A
+ * Arithmetic: a shorter side up to 64 is computed in fp64 and rounded once.  (Where
+ * X has no singular value, in a matrix of fewer independent rows than rows, what
+ * rounding leaves there grows by |ca| a step, as in any evaluation: 2^-53 |ca|^steps
+ * of the result, below its own rounding up to 15 steps of 3.4445.)  A
  * longer one keeps the iterate in fp32 and multiplies fp16 operands with fp32
  * accumulation: one fp16 term each for y in bf16, two (22 bits) for y in fp32.
  * Deterministic.

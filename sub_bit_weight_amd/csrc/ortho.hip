@@ -10,7 +10,11 @@
 //    on p x p matrices and X is read twice and written once, instead of 3 passes
 //    a step.  G squares the singular values and Q multiplies the small ones by
 //    up to a^steps, so this form needs twice the digits: everything is fp64
-//    (X0 enters exactly, one rounding at the end).  Bound by the launches and by
+//    (X0 enters exactly, one rounding at the end).  Rounding errors of the Gram
+//    matrix, negative eigenvalues among them, grow by a^2 a step, since nothing
+//    ties it to X again: after as many steps as that growth allows (five of the
+//    default quintic) Q is applied, the iterate kept in fp64, and its Gram matrix
+//    formed anew (segment_steps).  Bound by the launches and by
 //    the bytes of X for p <= 16 (64 matrices of 16 x 4096: 8 + 14 us, 33 MB), by
 //    the small products' chain as p nears 64 (one of 64 x 1024: 96 us) and then by
 //    the fp64 matrix rate (60 TFLOP/s measured on a large product).  p = 65 takes
@@ -27,6 +31,8 @@
 //    clock such products hold near 1.7 GHz: 4096 x 11008 in one term 4.1 ms (gram
 //    260, polynomial 106, step 435 us; 3.1 TFLOP by symmetric halves, 0.76 PFLOP/s
 //    over the call), two of 1371 x 2203 in two terms 0.84 ms.
+#include <type_traits>
+
 #include "nq_internal.h"
 
 namespace nq {
@@ -40,10 +46,27 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kGramMax = 64;  // shorter sides up to this take the fp64 form
 
+// Element types are fp32, bf16 bits and, of iterates between segments, fp64.
+template <typename E>
+struct ValueOf {
+  typedef float type;
+};
+template <>
+struct ValueOf<double> {
+  typedef double type;
+};
+
+__device__ inline double load1(const double* p) { return *p; }
 __device__ inline float load1(const float* p) { return *p; }
 __device__ inline float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
 typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef double f64x4u __attribute__((ext_vector_type(4), aligned(8)));
+__device__ inline void load4(const double* p, double (&v)[4]) {
+  const f64x4u a = *reinterpret_cast<const f64x4u*>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = a[e];
+}
 __device__ inline void load4(const float* p, float (&v)[4]) {
   const f32x4 a = *reinterpret_cast<const f32x4u*>(p);
 #pragma unroll
@@ -89,6 +112,16 @@ __device__ inline void store4(void* y, int bf16, int64_t at, const float (&v)[4]
   }
 }
 
+__device__ inline void store4(double* y, int64_t at, const double (&v)[4], int64_t count) {
+  if (count >= 4) {
+    *reinterpret_cast<f64x4u*>(y + at) = f64x4u{v[0], v[1], v[2], v[3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < count) y[at + e] = v[e];
+  }
+}
+
 // ---------------------------------------------------------------- p <= 64
 // One 16x16x4 fp64 instruction: lane l holds row l % 16, reduction l / 16 of
 // each operand and rows 4 i + l / 16 (i = 0..3) of column l % 16 of the result.
@@ -102,7 +135,9 @@ struct SmallArgs {
   double* qmat;      // [batch][P][P]
   void* y;
   int y_bf16;
-  int spans, steps;
+  double* it;        // [batch][rows][cols] the iterate between segments; may be x
+  int spans, steps;  // steps: of this segment
+  int normed;        // x is an iterate, not to be divided by its norm
   double a, b, c;
 };
 
@@ -115,14 +150,16 @@ __device__ inline const E* elem(const SmallArgs& s, const E* x, int64_t i, int64
 // A lane's operands of a 32-deep step of the longer side from j: rows 16t + c,
 // elements j + 8q + e (e-th instruction), zero from j1 on.
 template <typename E, int PT>
-__device__ inline void load_step(const SmallArgs& s, const E* x, int64_t j, int64_t j1, int q, int c, float (&v)[PT][8]) {
+__device__ inline void load_step(const SmallArgs& s, const E* x, int64_t j, int64_t j1, int q, int c,
+                                 typename ValueOf<E>::type (&v)[PT][8]) {
+  typedef typename ValueOf<E>::type V;
   const bool full = j + 32 <= j1;
 #pragma unroll
   for (int t = 0; t < PT; ++t) {
     const int64_t i = min(16 * t + c, s.p - 1);
     const E* at = elem(s, x, i, j + 8 * q);
     if (full && !s.tall) {
-      float lo[4], hi[4];
+      V lo[4], hi[4];
       load4(at, lo);
       load4(at + 4, hi);
 #pragma unroll
@@ -134,7 +171,7 @@ __device__ inline void load_step(const SmallArgs& s, const E* x, int64_t j, int6
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int64_t jj = j + 8 * q + e;
-        v[t][e] = jj < j1 ? load1(elem(s, x, i, jj)) : 0.0f;
+        v[t][e] = jj < j1 ? load1(elem(s, x, i, jj)) : V(0);
       }
     }
   }
@@ -150,11 +187,12 @@ __global__ __launch_bounds__(256) void ortho_gram_kernel(SmallArgs s) {
 #pragma unroll
   for (int k = 0; k < NPAIR; ++k) acc[k] = f64x4{0, 0, 0, 0};
   const int64_t j0 = (int64_t)blockIdx.x * s.span, j1 = imin(s.q, j0 + s.span);
-  float next[PT][8];
+  typedef typename ValueOf<E>::type V;
+  V next[PT][8];
   int64_t j = j0 + 32 * wave;
   if (j < j1) load_step<E, PT>(s, x, j, j1, q, c, next);
   for (; j < j1; j += 128) {
-    float v[PT][8];
+    V v[PT][8];
 #pragma unroll
     for (int t = 0; t < PT; ++t)
 #pragma unroll
@@ -190,8 +228,12 @@ __global__ __launch_bounds__(256) void ortho_gram_kernel(SmallArgs s) {
 }
 
 // 1 / ||X||_F^2 and 1 / ||X||_F from the trace of the Gram matrix.  A zero matrix
-// stays zero; one that is not finite gives NaN.
-__device__ inline void inverse_trace(double t, double& inv, double& root) {
+// stays zero; one that is not finite gives NaN.  An iterate is taken as it is.
+__device__ inline void inverse_trace(double t, int normed, double& inv, double& root) {
+  if (normed) {
+    inv = root = 1.0;
+    return;
+  }
   inv = t > 0.0 && isfinite(t) ? 1.0 / t : (t == 0.0 ? 0.0 : __builtin_nan(""));
   root = t > 0.0 && isfinite(t) ? 1.0 / sqrt(t) : inv;
 }
@@ -200,7 +242,8 @@ __device__ inline void inverse_trace(double t, double& inv, double& root) {
 // block of them.  A (the Gram matrix of the iterate), P = a I + b A + c A^2 and Q
 // (the product of the P so far) commute and are symmetric: every product reads both
 // operands by rows, and P and the last Q are made in the registers of the products
-// they come from.  Bound by the chain of 19 products of five steps, about half of it
+// they come from.  A becomes P A^T P^T: with P on one side twice, A P^T P^T, what
+// rounding leaves beside the diagonal grows by a^2 a step instead of a.  Bound by the chain of 19 products of five steps, about half of it
 // the fp64 rate of one CU (a call of 64 x 1024: 96 us, with four waves 107).
 template <int PT>
 __global__ __launch_bounds__(64 * PT * PT) void ortho_solve_kernel(SmallArgs s) {
@@ -220,7 +263,7 @@ __global__ __launch_bounds__(64 * PT * PT) void ortho_solve_kernel(SmallArgs s) 
   if (wave == 0) {  // ||X||_F^2 is the trace
     double t = lane < P ? A[lane * S + lane] : 0.0;
     for (int off = 32; off > 0; off >>= 1) t += __shfl_xor(t, off);
-    if (lane == 0) inverse_trace(t, inv_sh[0], inv_sh[1]);
+    if (lane == 0) inverse_trace(t, s.normed, inv_sh[0], inv_sh[1]);
   }
   __syncthreads();
   const double inv = inv_sh[0];
@@ -228,7 +271,7 @@ __global__ __launch_bounds__(64 * PT * PT) void ortho_solve_kernel(SmallArgs s) 
   __syncthreads();
   const int row = wave / PT * 16, col = wave % PT * 16;
   const int at = (row + q) * S + col + c;  // this lane's values: rows row + q + 4 i of column col + c
-  auto product = [&](const double* L, const double* R) {  // this wave's block of L R
+  auto product = [&](const double* L, const double* R) {  // this wave's block of L R^T
     f64x4 acc = {0, 0, 0, 0};
     const double* l = L + (row + c) * S + q;
     const double* r = R + (col + c) * S + q;
@@ -249,7 +292,7 @@ __global__ __launch_bounds__(64 * PT * PT) void ortho_solve_kernel(SmallArgs s) 
     const bool more = step + 1 < s.steps;
     f64x4 w = v;
     if (step > 0) w = product(Q, B);
-    if (more) v = product(A, B);
+    if (more) v = product(B, A);
     __syncthreads();  // every wave has read its operands
     store(Q, w);
     if (more) {
@@ -274,7 +317,7 @@ __device__ inline void solve16(const SmallArgs& s, double (&A)[4], double (&Q)[4
   for (int i = 0; i < 4; ++i) t += c == 4 * i + q ? A[i] : 0.0;
   for (int off = 32; off > 0; off >>= 1) t += __shfl_xor(t, off);
   double inv, root;
-  inverse_trace(t, inv, root);
+  inverse_trace(t, s.normed, inv, root);
 #pragma unroll
   for (int i = 0; i < 4; ++i) A[i] *= inv;
   auto product = [&](const double (&L)[4], const double (&R)[4], double (&D)[4]) {
@@ -306,8 +349,9 @@ __device__ inline void solve16(const SmallArgs& s, double (&A)[4], double (&Q)[4
 
 // Y = Q X: a wave takes 64 elements of the longer side.  For p <= 16 every
 // workgroup computes Q itself, from the spans' Gram matrices (a launch of its own
-// for a few thousand operations would cost more).
-template <typename E, int PT>
+// for a few thousand operations would cost more).  IT: Y is the iterate in fp64; X
+// may be the same one, since a wave stores only what it alone has loaded.
+template <typename E, int PT, bool IT>
 __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
   constexpr int P = 16 * PT, S = P + 4;
   extern __shared__ double lds64[];
@@ -318,14 +362,15 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
   // of a row) or j0 + 16v + c (tall); e-th reduction step: shorter-side index
   // 16u + 4e + q (wide), 16u + 4q + e (tall)
   const bool full = j0 + 64 <= s.q;
-  auto load = [&](int u, float (&v)[4][4]) {
+  typedef typename ValueOf<E>::type V;
+  auto load = [&](int u, V (&v)[4][4]) {
     if (full && !s.tall) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float a[4];
+        V a[4];
         load4(x + (int64_t)min(16 * u + 4 * e + q, s.p - 1) * s.ldx + j0 + 4 * c, a);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) v[b][e] = 16 * u + 4 * e + q < s.p ? a[b] : 0.0f;
+        for (int b = 0; b < 4; ++b) v[b][e] = 16 * u + 4 * e + q < s.p ? a[b] : V(0);
       }
     } else if (full && 16 * u + 16 <= s.p) {
 #pragma unroll
@@ -337,12 +382,12 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const int64_t j = imin(s.tall ? j0 + 16 * b + c : j0 + 4 * c + b, s.q - 1);
-          v[b][e] = k < s.p ? load1(elem(s, x, k, j)) : 0.0f;
+          v[b][e] = k < s.p ? load1(elem(s, x, k, j)) : V(0);
         }
       }
     }
   };
-  float first[4][4];
+  V first[4][4];
   if (j0 < s.q) load(0, first);
   if constexpr (PT == 1) {
     const double* g = s.gpart + (int64_t)blockIdx.y * s.spans * P * P;
@@ -375,7 +420,7 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
   const int row = s.tall ? 4 * (c % 4) + c / 4 : c;
 #pragma unroll
   for (int u = 0; u < PT; ++u) {
-    float v[4][4];
+    V v[4][4];
     if (u == 0) {
 #pragma unroll
       for (int b = 0; b < 4; ++b)
@@ -400,16 +445,17 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
   for (int t = 0; t < PT; ++t)
 #pragma unroll
     for (int a = 0; a < 4; ++a) {  // four results side by side: of block a (tall), of register a (wide)
-      float v[4];
+      typename std::conditional<IT, double, float>::type v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (float)(s.tall ? acc[t][a][e] : acc[t][e][a]);
+      for (int e = 0; e < 4; ++e) v[e] = s.tall ? acc[t][a][e] : acc[t][e][a];
       const int64_t j = s.tall ? j0 + 16 * a + c : j0 + 4 * c;
       const int i = 16 * t + (s.tall ? 4 * q : 4 * a + q);
       if (j >= s.q || i >= s.p) continue;
-      if (s.tall)
-        store4(s.y, s.y_bf16, base + j * s.p + i, v, s.p - i);
+      const int64_t at = base + (s.tall ? j * s.p + i : (int64_t)i * s.q + j), count = s.tall ? s.p - i : s.q - j;
+      if constexpr (IT)
+        store4(s.it, at, v, count);
       else
-        store4(s.y, s.y_bf16, base + (int64_t)i * s.q + j, v, s.q - j);
+        store4(s.y, s.y_bf16, at, v, count);
     }
 }
 
@@ -978,7 +1024,7 @@ struct OrthoLayout {
   bool small;
   int p, P, pp, qp, terms, spans;
   int64_t q, span;
-  size_t off_g, off_q, off_part, off_bad, off_xf, off_x16, off_xt[2], off_g16, off_b16, off_sums, off_arr, bytes;
+  size_t off_g, off_q, off_it, off_part, off_bad, off_xf, off_x16, off_xt[2], off_g16, off_b16, off_sums, off_arr, bytes;
   int64_t counters;
 };
 
@@ -1011,6 +1057,7 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
     L.spans = (int)cdiv(L.q, L.span);
     L.off_g = take((size_t)batch * L.spans * L.P * L.P * sizeof(double));
     L.off_q = take((size_t)batch * L.P * L.P * sizeof(double));
+    L.off_it = take((size_t)batch * rows * cols * sizeof(double));  // the query does not know the steps: always
   } else {
     L.terms = yd == NQ_F32 ? 2 : 1;
     L.pp = (int)round_up(L.p, kBK);
@@ -1033,8 +1080,22 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
   return L;
 }
 
+// Steps on one Gram matrix.  Its rounding errors, 2^-53 n of the largest value,
+// grow by at most the polynomial's largest square a step: by 2^20 in all, 2^-33 n,
+// far below the result's rounding (five steps of the default quintic, 17 of 1.5,
+// -0.5).  With more, a gradient of rank 4 (fewer tokens than rows) loses every digit
+// from 20 steps on and is NaN at 30; in segments it stays as near the definition as
+// the iteration as written in fp64 (2e-6 at 20 steps, 6e-6 as written).
+int segment_steps(double ca, double cb, double cc) {
+  const double top = 1.25 * 1.25;
+  double m = fmax(fabs(ca), fabs(ca + cb * top + cc * top * top));
+  const double v = cc != 0.0 ? -cb / (2.0 * cc) : 0.0;
+  if (v > 0.0 && v < top) m = fmax(m, fabs(ca + cb * v + cc * v * v));
+  return m * m <= 1.25 ? 64 : (int)imax(1, (int64_t)floor(20.0 / log2(m * m)));
+}
+
 template <typename E, int PT>
-hipError_t launch_small(const SmallArgs& a, int64_t batch, hipStream_t s) {
+hipError_t launch_small(const SmallArgs& a, int64_t batch, bool last, hipStream_t s) {
   constexpr int P = 16 * PT, S = P + 4;
   hipLaunchKernelGGL((ortho_gram_kernel<E, PT>), dim3((unsigned)a.spans, (unsigned)batch), dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
@@ -1047,18 +1108,21 @@ hipError_t launch_small(const SmallArgs& a, int64_t batch, hipStream_t s) {
     e = hipGetLastError();
   }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((ortho_apply_kernel<E, PT>), dim3((unsigned)cdiv(a.q, 256), (unsigned)batch), dim3(256),
-                     P * S * sizeof(double), s, a);
+  const dim3 grid((unsigned)cdiv(a.q, 256), (unsigned)batch);
+  if (last)
+    hipLaunchKernelGGL((ortho_apply_kernel<E, PT, false>), grid, dim3(256), P * S * sizeof(double), s, a);
+  else
+    hipLaunchKernelGGL((ortho_apply_kernel<E, PT, true>), grid, dim3(256), P * S * sizeof(double), s, a);
   return hipGetLastError();
 }
 
 template <typename E>
-hipError_t launch_small_p(const SmallArgs& a, int64_t batch, hipStream_t s) {
+hipError_t launch_small_p(const SmallArgs& a, int64_t batch, bool last, hipStream_t s) {
   switch (cdiv(a.p, 16)) {
-    case 1: return launch_small<E, 1>(a, batch, s);
-    case 2: return launch_small<E, 2>(a, batch, s);
-    case 3: return launch_small<E, 3>(a, batch, s);
-    default: return launch_small<E, 4>(a, batch, s);
+    case 1: return launch_small<E, 1>(a, batch, last, s);
+    case 2: return launch_small<E, 2>(a, batch, last, s);
+    case 3: return launch_small<E, 3>(a, batch, last, s);
+    default: return launch_small<E, 4>(a, batch, last, s);
   }
 }
 
@@ -1136,11 +1200,26 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
     a.y = y;
     a.y_bf16 = yd == NQ_BF16;
     a.spans = L.spans;
-    a.steps = steps;
+    a.it = reinterpret_cast<double*>(ws + L.off_it);
     a.a = ca;
     a.b = cb;
     a.c = cc;
-    return xd == NQ_BF16 ? launch_small_p<uint16_t>(a, batch, s) : launch_small_p<float>(a, batch, s);
+    const int most = segment_steps(ca, cb, cc);
+    for (int done = 0; done < steps; done += a.steps) {
+      a.steps = (int)imin(most, steps - done);
+      a.normed = done > 0;
+      const bool last = done + a.steps == steps;
+      hipError_t e;
+      if (done > 0)
+        e = launch_small_p<double>(a, batch, last, s);
+      else
+        e = xd == NQ_BF16 ? launch_small_p<uint16_t>(a, batch, last, s) : launch_small_p<float>(a, batch, last, s);
+      if (e != hipSuccess) return e;
+      a.x = a.it;
+      a.ldx = cols;
+      a.stride_x = rows * cols;
+    }
+    return hipSuccess;
   }
   double* part = reinterpret_cast<double*>(ws + L.off_part);
   LargeArgs l;

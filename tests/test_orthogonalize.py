@@ -270,3 +270,115 @@ def test_captured_training_step_of_adapters():
         nq.orthogonalize(x)  # eager work of the program's own between replays
         torch.cuda.synchronize()
         assert torch.equal(y, yw) and torch.equal(pool.a, aw) and torch.equal(pool.b, bw)
+
+
+# ---------------------------------------------------------------- many steps, short sides
+
+
+def _definition(x, steps, co):
+    """The iteration as written, in 80 bits."""
+    x = x.astype(np.longdouble)
+    x = x.T if x.shape[0] > x.shape[1] else x
+    x = x / np.sqrt((x * x).sum())
+    for _ in range(steps):
+        g = x @ x.T
+        gx = g @ x
+        x = co[0] * x + co[1] * gx + co[2] * (g @ gx)
+    return x
+
+
+def _deficient(kind, p, q):
+    """p x q of a known rank or spectrum, exact in bf16 (but for the spectrum)."""
+    g = synth.rng(f"ortho/deficient/{kind}/{p}/{q}")
+    if kind == "six decades":
+        u, v = np.linalg.qr(g.standard_normal((p, p)))[0], np.linalg.qr(g.standard_normal((q, p)))[0]
+        return ((u * 10.0 ** (-6.0 * np.arange(p) / (p - 1))) @ v.T).astype(np.float32)
+    if kind == "duplicated row":
+        x = g.integers(-8, 9, (p, q))
+        x[p - 1] = x[p // 2]
+    else:
+        r = {"rank 1": 1, "a quarter": max(1, p // 4), "three quarters": 3 * p // 4}[kind]
+        u = np.zeros((p, r), dtype=int)
+        u[np.arange(p), g.integers(0, r, p)] = 1  # each row one of r, times a sign: small integers
+        x = (u * g.choice([-1, 1], (p, 1))) @ g.integers(-8, 9, (r, q))
+    return x.astype(np.float32)
+
+
+KINDS = ["rank 1", "a quarter", "three quarters", "duplicated row", "six decades"]
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", [(5, 40), (16, 600), (200, 16), (33, 500), (130, 48), (64, 300)], ids=str)
+@pytest.mark.parametrize("steps,co", [(s, NS) for s in (5, 6, 8, 10, 12, 20)] + [(17, (1.5, -0.5, 0.0)), (40, (1.5, -0.5, 0.0))])
+def test_many_steps_of_deficient_matrices(kind, shape, steps, co):
+    """Gradients of fewer tokens than rows.  An fp64 evaluation of the definition rounds values of size one
+    to 2^-53, in sums of p products (4 sqrt(p) of them); a direction without a singular value of its own
+    multiplies what it gets of that by ca a step, a geometric sum of ca^steps * ca / (ca - 1) at most, while
+    the result's norm is 0.7 or more.  1e-8 and the last rounding as at five steps."""
+    p, q = min(shape), max(shape)
+    x = _deficient(kind, p, q)
+    x = x.T.copy() if shape[0] > shape[1] else x
+    y = nq.orthogonalize(torch.from_numpy(x).to(DEV), steps=steps, coeffs=co).double().cpu().numpy()
+    want = _definition(x, steps, co)
+    want = np.asarray(want.T if shape[0] > shape[1] else want, dtype=np.float64)
+    noise = 4 * np.sqrt(p) * 2.0 ** -53 * co[0] ** steps * co[0] / (co[0] - 1) / 0.7
+    assert np.linalg.norm(y - want) <= (2.0 ** -24 + 1e-8 + noise) * np.linalg.norm(want)
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", [(16, 600), (200, 16), (64, 300)], ids=str)
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_the_most_steps_stay_in_range(kind, shape, out):
+    """64 steps: no singular value leaves [0, 1.25], which the coefficients promise, beyond the result's rounding."""
+    p, q = min(shape), max(shape)
+    x = _deficient(kind, p, q)
+    x = x.T.copy() if shape[0] > shape[1] else x
+    y = nq.orthogonalize(torch.from_numpy(x).to(DEV), steps=64, out_dtype=out).double().cpu().numpy()
+    last = 2.0 ** -24 if out == torch.float32 else 2.0 ** -8
+    assert np.isfinite(y).all()
+    assert np.linalg.norm(y, 2) <= 1.25 * (1 + last * np.sqrt(p))
+    if kind == "six decades":  # no direction without a singular value: rounding errors grow by 1e6 at most, then stay
+        want = _definition(x, 64, NS)
+        want = np.asarray(want.T if shape[0] > shape[1] else want, dtype=np.float64)
+        assert np.linalg.norm(y - want) <= (last + 1e-8) * np.linalg.norm(want)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(16, 100), (90, 40)], ids=str)
+def test_many_steps_of_a_batch(shape):
+    """Zero and non-finite matrices, views, a dirty workspace, bf16 and a captured call at more steps than one Gram matrix serves."""
+    rows, cols = shape
+    x = _gradient(f"batch/{shape}", 5, rows, cols)
+    steps = 13
+    want = nq.orthogonalize(torch.from_numpy(x).to(DEV), steps=steps)
+    for i in range(5):
+        w = _definition(x[i], steps, NS)
+        w = np.asarray(w.T if rows > cols else w, dtype=np.float64)
+        # the smallest singular value is 1e-2 or more of the largest
+        assert np.linalg.norm(want[i].double().cpu().numpy() - w) <= (2.0 ** -24 + 1e-8) * np.linalg.norm(w)
+    x[1] = 0
+    x[2, 3, 5] = np.inf
+    x[3, 0, 0] = np.nan
+    big = torch.full((rows, 5, cols + 7), float("nan"), device=DEV)
+    view = big.permute(1, 0, 2)[:, :, 2:2 + cols]
+    view.copy_(torch.from_numpy(x))
+    ws = torch.full((nq.orthogonalize_workspace_bytes(5, rows, cols),), 255, dtype=torch.uint8, device=DEV)
+    y = nq.orthogonalize(view, steps=steps, workspace=ws)
+    assert torch.equal(y[0], want[0]) and torch.equal(y[4], want[4])
+    assert not y[1].any() and torch.isnan(y[2]).all() and torch.isnan(y[3]).all()
+    half = torch.from_numpy(x[4]).to(DEV).to(torch.bfloat16)
+    assert torch.equal(nq.orthogonalize(half, steps=steps), nq.orthogonalize(half.float(), steps=steps).to(torch.bfloat16))
+    src = torch.from_numpy(x[0]).to(DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = nq.orthogonalize(src, steps=steps)
+    for i in (0, 4, 0):
+        src.copy_(torch.from_numpy(x[i]))
+        eager = nq.orthogonalize(src, steps=steps)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager) and torch.equal(y, want[i])
