@@ -419,9 +419,14 @@ nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const
  * X has no singular value, in a matrix of fewer independent rows than rows, what
  * rounding leaves there grows by |ca| a step, as in any evaluation: 2^-53 |ca|^steps
  * of the result, below its own rounding up to 15 steps of 3.4445.)  A
- * longer one keeps the iterate in fp32 and multiplies fp16 operands with fp32
- * accumulation: one fp16 term each for y in bf16, two (22 bits) for y in fp32.
- * Deterministic.
+ * longer one keeps the iterate in fp32 (what rounding leaves without a singular
+ * value: 2^-24 |ca|^steps) and multiplies fp16 operands with fp32 accumulation:
+ * two terms each (22 bits), or one (11 bits) for y in bf16 and a shorter side of
+ * 512 or more.  One term costs a third of the products; its error is below the
+ * rounding of y to bf16 at five steps of the default coefficients (1.3e-3 of the
+ * norm beside 1.7e-3 at 512 x 700, 1.1e-3 at 2000 x 8000), grows with the square
+ * root of the steps, and passes that rounding for matrices of rank one (up to
+ * 7e-3).  Take y in fp32 and round it where that matters.  Deterministic.
  *   steps: 1 .. 64; the coefficients must be finite and must map [0, 1.25] into
  *   [-1.25, 1.25], so that no iterate leaves the operands' range (3.4445,
  *   -4.7750, 2.0315 and 1.5, -0.5, 0 do).

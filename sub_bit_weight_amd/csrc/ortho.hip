@@ -23,9 +23,10 @@
 //    accumulation, all three products as C = P Q^T of row-major operands.  The
 //    state X is fp32 and a X is added in fp32; only the operands of products are
 //    fp16.  Their rounding errors sit in the spaces that G spans with weight, so
-//    the iteration does not blow them up as it does a rounding of X itself.  For
-//    an fp32 result each operand is two fp16 terms (hi + lo, 22 bits) and a
-//    product three fp16 products.  Operands are scaled by powers of two into
+//    the iteration does not blow them up as it does a rounding of X itself.  An
+//    operand is two fp16 terms (hi + lo, 22 bits) and a product three fp16
+//    products; one term and one product for a bf16 result of kOneTerm rows or more.
+//    Operands are scaled by powers of two into
 //    fp16's range: bounds on x and G are known because the host checks that the
 //    polynomial maps [0, 1.25] into [-1.25, 1.25].  Bound by the matrix cores, whose
 //    clock such products hold near 1.7 GHz: 4096 x 11008 in one term 4.1 ms (gram
@@ -45,6 +46,16 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kGramMax = 64;  // shorter sides up to this take the fp64 form
+
+// Shorter sides from this on take one fp16 term for a bf16 result.  One term moves a
+// result by 2e-4 of its norm (a rounding to 11 bits) times what B multiplies it by,
+// 2.7, once per step whose singular values have grown to one.  At five default steps,
+// beside a rounding to bf16 of 1.7e-3: 1.9e-3 for 65 x 300, 1.6e-3 for 256 x 256,
+// 1.3e-3 for 512 x 700, 1.1e-3 for 2000 x 8000; in all 1.5, 1.4, 1.27 and 1.2 times the
+// rounding alone, with two terms 1.00.  Two terms cost 1.2 to 1.8 times the call below
+// the bound (us, one / two terms: 65 x 300 90 / 109, 256 x 1024 110 / 146, 500 x 700
+// 117 / 184) and up to three times above it (4 of 768 x 4096 527 / 1193).
+constexpr int kOneTerm = 512;
 
 // Element types are fp32, bf16 bits and, of iterates between segments, fp64.
 template <typename E>
@@ -1031,8 +1042,8 @@ struct OrthoLayout {
 // Symmetric products of few tiles: the reduction is split, 16 tiles of it or more
 // each, until a workgroup runs on every CU.  One matrix of 128 x 16384 has 3 tiles
 // of 64 x 64: 229 us a call in fp32, unsplit 989; 128 x 4096 156 (splits of 8 tiles
-// or more, two workgroups a CU: 171), unsplit 323.  64 matrices of 128 x 1024 to
-// bf16 have 192: 378 us whole, 415 in two splits.
+// or more, two workgroups a CU: 171), unsplit 323.  64 matrices of 128 x 1024
+// have 192: in one term 378 us whole, 415 in two splits.
 int square_splits(int64_t batch, int64_t p, int64_t k, int terms) {
   const int64_t t = cdiv(p, 64), tiles = batch * t * (t + 1) / 2, all = k / kBK * (terms > 1 ? 3 : 1);
   const int64_t n = imax(1, imin(imin(256 / tiles, all / 16), 32));
@@ -1059,7 +1070,7 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
     L.off_q = take((size_t)batch * L.P * L.P * sizeof(double));
     L.off_it = take((size_t)batch * rows * cols * sizeof(double));  // the query does not know the steps: always
   } else {
-    L.terms = yd == NQ_F32 ? 2 : 1;
+    L.terms = yd == NQ_F32 || L.p < kOneTerm ? 2 : 1;
     L.pp = (int)round_up(L.p, kBK);
     L.qp = (int)round_up(L.q, kBK);
     L.off_part = take((size_t)batch * kSumBlocks * sizeof(double));

@@ -382,3 +382,23 @@ def test_many_steps_of_a_batch(shape):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, eager) and torch.equal(y, want[i])
+
+
+# ---------------------------------------------------------------- bf16 results
+
+
+@gpu
+@pytest.mark.parametrize("steps", [5, 12])
+@pytest.mark.parametrize("shape", [(65, 300), (66, 4096), (300, 130), (256, 600), (900, 511)], ids=str)
+def test_bf16_results_of_smaller_matrices_lose_their_rounding_alone(shape, steps):
+    """A result z rounded to bf16 is off by at most half a step of it and |z - z*|.  So what is left of each
+    value's error beyond half a step of z* is at most |z - z*| and the step's growth, whose norm is that
+    of an fp32 result: two-term products as above (twice, for values that cross a power of two)."""
+    p, q = min(shape), max(shape)
+    x = synth.normal_f32(f"ortho/bf16/{shape}", shape) * np.exp(0.3 * synth.normal_f32(f"ortho/bf16r/{shape}", (shape[0], 1)))
+    y = nq.orthogonalize(torch.from_numpy(x.astype(np.float32)).to(DEV), steps=steps, out_dtype=torch.bfloat16)
+    want = A.orthogonalize_ref(x.astype(np.float32), steps, NS)
+    tol = (5 * 2.0 ** -21 + 4 * np.sqrt(3 * q) * 2.0 ** -24) * np.sqrt(4 * steps)
+    half = 2.0 ** (np.floor(np.log2(np.abs(want) + 1e-30)) - 8)
+    beyond = np.maximum(np.abs(y.double().cpu().numpy() - want) - half, 0)
+    assert np.linalg.norm(beyond) <= 2 * tol * np.linalg.norm(want)
