@@ -428,8 +428,11 @@ nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const
  * root of the steps, and passes that rounding for matrices of rank one (up to
  * 7e-3).  Take y in fp32 and round it where that matters.  Deterministic.
  *   steps: 1 .. 64; the coefficients must be finite and must map [0, 1.25] into
- *   [-1.25, 1.25], so that no iterate leaves the operands' range (3.4445,
- *   -4.7750, 2.0315 and 1.5, -0.5, 0 do).
+ *   [-1.25, 1.25], and the largest singular value, one at first, must stay below
+ *   1.3125 when every step adds its operands' roundings (up to 0.02 with one term
+ *   and 3.4445, -4.7750, 2.0315; 2e-5 with two), so that no iterate leaves the
+ *   operands' range.  3.4445, -4.7750, 2.0315 and 1.5, -0.5, 0 do in any form; a
+ *   polynomial that touches 1.25 and rises steeply behind it does not.
  *   workspace: at least nq_orthogonalize_workspace_bytes(batch, rows, cols,
  *   y_dtype) bytes, 256-byte aligned (the query returns 0 for invalid
  *   arguments).

@@ -835,25 +835,52 @@ nq_status check_ortho_sizes(const char* who, int64_t batch, int64_t rows, int64_
   return NQ_OK;
 }
 
-// Whether s -> ca s + cb s^3 + cc s^5 maps [0, 1.25] into [-1.25, 1.25] (its
-// ends and the zeros of its derivative, a quadratic in s^2).
-bool keeps_range(double ca, double cb, double cc) {
-  const double top = 1.25;
-  auto inside = [&](double s) {
+// The largest |ca s + cb s^3 + cc s^5| for s in [0, top]: at its end or where the
+// derivative, a quadratic in s^2, is zero.
+double largest_value(double ca, double cb, double cc, double top) {
+  auto value = [&](double s) {
     const double l = s * s;
-    return s * fabs(ca + cb * l + cc * l * l) <= top;
+    return s * fabs(ca + cb * l + cc * l * l);
   };
-  auto at = [&](double l) { return !(l > 0.0 && l < top * top) || inside(sqrt(l)); };
-  // no polynomial that stays inside has a larger coefficient (those of the fifth
-  // Chebyshev polynomial, 5, 12.8 and 6.6, are the largest), and none overflows below
-  if (fabs(ca) > 16.0 || fabs(cb) > 16.0 || fabs(cc) > 16.0 || !inside(top)) return false;
+  double m = value(top);
   // ca + 3 cb l + 5 cc l^2 = 0: one zero from the sum of like signs, the other from
   // the zeros' product, so that neither is lost to cancellation beside a tiny cc (a
-  // zero that does not exist comes out infinite or NaN, which `at` passes)
+  // zero that does not exist comes out infinite or NaN)
   const double p = 3.0 * cb, q = 5.0 * cc, disc = p * p - 4.0 * q * ca;
-  if (disc < 0.0) return true;
+  if (disc < 0.0) return m;
   const double t = -0.5 * (p + copysign(sqrt(disc), p));
-  return at(t / q) && at(ca / t);
+  for (const double l : {t / q, ca / t})
+    if (l > 0.0 && l < top * top) m = std::max(m, value(sqrt(l)));
+  return m;
+}
+
+// Whether the polynomial maps [0, 1.25] into [-1.25, 1.25] ...
+bool keeps_range(double ca, double cb, double cc) {
+  // no polynomial that stays inside has a larger coefficient (those of the fifth
+  // Chebyshev polynomial, 5, 12.8 and 6.6, are the largest), and none overflows below
+  if (fabs(ca) > 16.0 || fabs(cb) > 16.0 || fabs(cc) > 16.0) return false;
+  return largest_value(ca, cb, cc, 1.25) <= 1.25;
+}
+
+// ... and whether singular values that begin at one at most stay below the operands'
+// limit when each step adds its roundings (u each, relative, root mean square): one
+// that touches 1.25 and is steep beyond runs away from there (with 11 bits the fifth
+// Chebyshev polynomial of s / 1.25 is at 1.8 after five steps and infinite after twelve).
+// An error of x (of spectral norm 2.5 u, a random matrix's) enters G twice and the last
+// product, G and B are rounded themselves: with |x| <= 1.25, |b + 2 c l| <= slope and
+// |b l + c l^2| <= bound, u (11.7 slope + 5 bound) in all.
+bool stays_in_range(double ca, double cb, double cc, int steps, double u) {
+  const double top = 1.25 * 1.25, v = cc != 0.0 ? -cb / (2.0 * cc) : 0.0;
+  const double slope = std::max(fabs(cb), fabs(cb + 2.0 * cc * top));
+  double bound = fabs(cb * top + cc * top * top);
+  if (v > 0.0 && v < top) bound = std::max(bound, fabs(cb * v + cc * v * v));
+  const double e = u * (11.7 * slope + 5.0 * bound);
+  double reach = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    reach = largest_value(ca, cb, cc, reach) + e;
+    if (reach > kOrthoRange) return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -881,6 +908,10 @@ nq_status nq_orthogonalize(const void* x, nq_dtype x_dtype, int64_t batch, int64
   if (steps < 1 || steps > 64) return set_error("%s: steps=%d outside 1..64", who, (int)steps), NQ_ERR_ARG;
   if (!std::isfinite(ca) || !std::isfinite(cb) || !std::isfinite(cc) || !keeps_range(ca, cb, cc))
     return set_error("%s: coefficients %g, %g, %g do not map [0, 1.25] into [-1.25, 1.25]", who, ca, cb, cc), NQ_ERR_ARG;
+  if (!stays_in_range(ca, cb, cc, steps, ortho_rounding(rows, cols, y_dtype)))
+    return set_error("%s: coefficients %g, %g, %g leave the operands' range in %d steps with their roundings", who, ca, cb,
+                     cc, (int)steps),
+           NQ_ERR_ARG;
   if ((st = check_workspace(who, workspace, workspace_bytes, ortho_workspace(batch, rows, cols, y_dtype))) != NQ_OK)
     return st;
   return hip_status(launch_ortho(x, x_dtype, batch, rows, cols, ldx, stride_x, steps, ca, cb, cc, y, y_dtype, workspace,

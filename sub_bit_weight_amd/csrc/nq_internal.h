@@ -195,7 +195,11 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
                              const int32_t* ids, int64_t T, const float* dx_base, float* dx, float* da, float* db,
                              void* workspace, hipStream_t s);
 
-// Orthogonalised updates (ortho.hip).
+// Orthogonalised updates (ortho.hip).  Singular values of iterates stay below
+// kOrthoRange, for which the operands are scaled; ortho_rounding: the relative
+// rounding of an operand (root mean square).
+constexpr double kOrthoRange = 1.3125;
+double ortho_rounding(int64_t rows, int64_t cols, nq_dtype yd);
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd);
 hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows, int64_t cols, int64_t ldx,
                         int64_t stride_x, int steps, double ca, double cb, double cc, void* y, nq_dtype yd, void* workspace,

@@ -28,7 +28,7 @@
 //    products; one term and one product for a bf16 result of kOneTerm rows or more.
 //    Operands are scaled by powers of two into
 //    fp16's range: bounds on x and G are known because the host checks that the
-//    polynomial maps [0, 1.25] into [-1.25, 1.25].  Bound by the matrix cores, whose
+//    polynomial keeps singular values there, roundings included.  Bound by the matrix cores, whose
 //    clock such products hold near 1.7 GHz: 4096 x 11008 in one term 4.1 ms (gram
 //    260, polynomial 106, step 435 us; 3.1 TFLOP by symmetric halves, 0.76 PFLOP/s
 //    over the call), two of 1371 x 2203 in two terms 0.84 ms.
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(256) void ortho_apply_kernel(SmallArgs s) {
 
 // ---------------------------------------------------------------- p > 64
 constexpr int kBK = 64;  // operand rows are padded to this: every tile shape is a multiple of it
-constexpr float kScaleX = 16384.0f;  // operand scale of x: |x| <= 1.25
+constexpr float kScaleX = 16384.0f;  // operand scale of x: |x| <= kOrthoRange
 constexpr int kSumBlocks = 512;  // partial sums of ||X||_F^2 per matrix
 
 template <typename E>
@@ -1187,6 +1187,11 @@ double poly_bound(double b, double c, double top) {
 
 }  // namespace
 
+double ortho_rounding(int64_t rows, int64_t cols, nq_dtype yd) {
+  const OrthoLayout L = ortho_layout(1, rows, cols, yd);
+  return L.small ? 0x1p-33 : (L.terms == 2 ? 0x1p-21 : 0x1p-11 / sqrt(3.0));  // small: what a segment may grow to
+}
+
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd) {
   return ortho_layout(batch, rows, cols, yd).bytes;
 }
@@ -1249,11 +1254,11 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   l.bad = reinterpret_cast<float*>(ws + L.off_bad);
   l.arrived = reinterpret_cast<int*>(ws + L.off_arr);
   l.counters = L.counters;
-  // |x| <= 1.25, |G| <= 1.25^2 and the polynomial's bound, each times its scale
-  // below 65504
+  // |x| <= kOrthoRange, |G| <= its square and the polynomial's bound, each times its
+  // scale below 65504
   const float sx = kScaleX, sg = 16384.0f;
   l.sx = sx;
-  const double bound = poly_bound(cb, cc, 1.25 * 1.25);
+  const double bound = poly_bound(cb, cc, kOrthoRange * kOrthoRange);
   const float sb = ldexpf(1.0f, bound > 0.0 ? (int)imax(-40, imin(14, (int64_t)floor(log2(60000.0 / bound)))) : 0);
   const dim3 pgrid((unsigned)(L.qp / 64), (unsigned)(L.pp / 64), (unsigned)batch);
   if (xd == NQ_BF16)

@@ -104,6 +104,27 @@ def test_rejects_an_interior_maximum_beside_a_tiny_quintic_term(ca, cb, cc):
     assert _call(co=(1.5, -0.5, cc), ws=None) == nq.NQ_ERR_WORKSPACE  # the next check
 
 
+FORMS = [dict(rows=60, cols=100, ldx=100), dict(rows=100, cols=200, ldx=200), dict(rows=600, cols=700, ldx=700),
+         dict(rows=600, cols=700, ldx=700, yd=nq.NQ_BF16)]  # fp64, two terms twice, one term
+
+
+def _chebyshev(f):
+    """f * 1.25 * T5(s / 1.25): touches +-1.25 f five times, with a slope of 25 f at 1.25."""
+    return (5.0 * f, -12.8 * f, 6.5536 * f)
+
+
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_coefficients_leave_room_for_roundings(form):
+    def call(co, steps=64):
+        return _call(co=co, steps=steps, ws=None, **form)
+    for co in (NS, (1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (1.0, 0.0, 0.0), (3.7418, -5.5913, 2.3037), _chebyshev(0.9)):
+        assert call(co) == nq.NQ_ERR_WORKSPACE, co  # the next check
+    # 1.25 (1 - 1e-15) in exact arithmetic; roundings leave it, and grow 25 times a step from there
+    assert call(_chebyshev(1 - 1e-15)) == nq.NQ_ERR_ARG and "roundings" in nq.last_error()
+    assert call(_chebyshev(0.999)) == (nq.NQ_ERR_ARG if "yd" in form else nq.NQ_ERR_WORKSPACE)
+    assert call(_chebyshev(0.999), steps=1) == nq.NQ_ERR_WORKSPACE
+
+
 def test_workspace_query():
     lib = nq.lib()
     assert lib.nq_orthogonalize_workspace_bytes(1, 16, 4096, nq.NQ_F32) > 0
@@ -402,3 +423,13 @@ def test_bf16_results_of_smaller_matrices_lose_their_rounding_alone(shape, steps
     half = 2.0 ** (np.floor(np.log2(np.abs(want) + 1e-30)) - 8)
     beyond = np.maximum(np.abs(y.double().cpu().numpy() - want) - half, 0)
     assert np.linalg.norm(beyond) <= 2 * tol * np.linalg.norm(want)
+
+
+@gpu
+@pytest.mark.parametrize("shape,out,f", [((48, 200), torch.float32, 0.999999), ((130, 200), torch.float32, 0.999),
+                                         ((300, 200), torch.bfloat16, 0.999), ((520, 600), torch.bfloat16, 0.95)])
+def test_coefficients_near_the_edge_stay_in_range(shape, out, f):
+    """The steepest polynomials that are accepted, for the most steps."""
+    x = torch.from_numpy(synth.normal_f32(f"ortho/edge/{shape}", shape)).to(DEV)
+    y = nq.orthogonalize(x, steps=64, coeffs=_chebyshev(f), out_dtype=out).double().cpu().numpy()
+    assert np.isfinite(y).all() and np.linalg.norm(y, 2) <= 1.3125
