@@ -510,7 +510,7 @@ template <bool TW, int NT>
 __device__ inline void staged_steps(const ShrinkArgs& p, const Bf16* x, const int* rows, const Bf16* w, int k0, int64_t j0,
                                     int chunks, char* lds, f32x4 (&acc)[2][NT]) {
   constexpr int R = 16 * NT, NW = kShrinkWaves, XL = kTile / 2 / NW, WL = R / 2 / NW, STAGE = stage_bytes<TW, NT>();
-  static_assert(XL >= 1 && WL >= 1, "a load per wave and operand");
+  static_assert(XL >= 1 && WL >= 1 && XL + WL < 16, "a load per wave and operand, and the wait's range");
   const int tid = threadIdx.x, lane = tid % 64, q = lane / 16, c = lane % 16;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const Bf16 *xa[XL], *wa[WL];
@@ -545,12 +545,14 @@ __device__ inline void staged_steps(const ShrinkArgs& p, const Bf16* x, const in
   for (int ch = 0; ch < kStages - 1 && ch < chunks; ++ch) issue(ch, ch);
   int st = 0;
   for (int ch = 0; ch < chunks; ++ch) {
+    // vmcnt: this chunk has landed, the next may stay in flight; lgkmcnt(0): this
+    // wave's reads of the last chunk have returned, whose stage is loaded anew below
     if (ch + 1 < chunks)
-      __builtin_amdgcn_s_waitcnt((XL + WL) | (7 << 4) | (15 << 8));  // the next chunk may stay in flight
+      __builtin_amdgcn_s_waitcnt((XL + WL) | (7 << 4));
     else
-      __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
+      __builtin_amdgcn_s_waitcnt(7 << 4);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // every wave's loads of this chunk have landed, the last one is consumed
+    __builtin_amdgcn_s_barrier();  // the same of every wave
     asm volatile("" ::: "memory");
     if (ch + kStages - 1 < chunks) issue(ch + kStages - 1, st + kStages - 1 < kStages ? st + kStages - 1 : st - 1);
     const char* stage = lds + st * STAGE;
