@@ -351,8 +351,11 @@ typedef struct {
  *   another stream that writes them must be waited for) and must not change while
  *   it runs.
  * The hidden vectors A_a x[t] and all sums are fp32: nothing is rounded to
- * fewer bits, whatever the types of x and of the factors.  Values that are not
- * finite stay within the rows whose x, base or adapter holds them.  Summation
+ * fewer bits, whatever the types of x and of the factors (beside bf16 factors
+ * hidden values below 2^-110 lose what lies under 2^-133).  Values that are not
+ * finite stay within the rows whose x, base or adapter holds them, and are
+ * infinite or NaN as the products and sums of the formula are (NaN beside a hidden
+ * value below 2^-100).  Summation
  * order is fixed: results are run-to-run deterministic, but the order depends
  * on T and n.
  *   workspace: at least nq_lora_workspace_bytes(P, T) bytes, 256-byte aligned;

@@ -27,7 +27,8 @@
 //
 // h and dh are kept in fp32.  Beside bf16 factors they enter the matrix cores
 // as three bf16 terms that carry all 24 bits (split3), so nothing is rounded to
-// fewer bits than fp32 anywhere.  Sums have a fixed order; there are no
+// fewer bits than fp32 (but for values below 2^-110, whose bits under bf16's
+// smallest, 2^-133, are lost).  Sums have a fixed order; there are no
 // atomics on floating data.
 //
 // A load of 16 bytes per lane costs a cache access per line that 16 neighbouring
@@ -99,15 +100,27 @@ __device__ inline uint32_t high_halves(uint32_t lo, uint32_t hi) {  // (hi's upp
   return __builtin_amdgcn_perm(hi, lo, 0x07060302);
 }
 
-// v = t0 + t1 + t2 exactly: each term takes the next 8 bits of the significand
-// (truncated, so no term rounds).  An infinity is its own first term; a NaN that
-// arithmetic made has its quiet bit in the upper half and stays one.
+// v = t0 + t1 + t2 exactly for |v| >= 2^-110: each term takes the next 8 bits of the
+// significand (truncated, so no term rounds and all have v's sign).  From 2^-100 on
+// no term is zero, which an infinite factor would turn into NaN where the product is
+// infinite: a value of fewer bits is cut into halves.  An infinity is three; a NaN
+// that arithmetic made has its quiet bit in the upper half and stays one.
 __device__ inline void split3(float v, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
-  t0 = __float_as_uint(v) & 0xFFFF0000u;
-  float rest = v - __uint_as_float(t0);
-  if (__builtin_isinf(v)) rest = 0.0f;
-  t1 = __float_as_uint(rest) & 0xFFFF0000u;
-  t2 = __float_as_uint(rest - __uint_as_float(t1));
+  float a = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), rest = v - a;
+  float b = __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u), c = rest - b;
+  if (__builtin_isinf(v)) {
+    b = c = v;
+  } else if (__builtin_fabsf(v) >= 0x1p-100f) {
+    if (rest == 0.0f) {
+      a = 0.5f * v;
+      b = c = 0.25f * v;
+    } else if (c == 0.0f) {
+      b = c = 0.5f * b;
+    }
+  }
+  t0 = __float_as_uint(a);
+  t1 = __float_as_uint(b);
+  t2 = __float_as_uint(c);
 }
 
 __device__ inline void widen(const float (&v)[8], Wide<float>& w) {

@@ -470,3 +470,55 @@ def test_binding_refuses_wrong_tensors():
         nq.lora_grads(pool, x, torch.zeros(5, 8, device=DEV), ids, dx_base=torch.zeros(5, 15, device=DEV))
     with pytest.raises(nq.NqError):
         nq.lora_linear(pool, x, ids, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+def _non_finite(tag, T, n, r, d_in, d_out, xd, wd):
+    """Small integers (hidden values of few bits) with infinities and NaN in factors, activations, g and base."""
+    g = synth.rng(f"lora/inf/{tag}")
+    ids = np.arange(T) % n
+    few = [-2, -1, 1, 2]  # no zeros, beside which an infinity is NaN
+    c = dict(a=g.integers(-2, 3, (n, r, d_in)), b=g.choice(few, (n, d_out, r)), scale=np.full(n, 0.5),
+             x=g.choice(few, (T, d_in)), base=g.integers(-9, 10, (T, d_out)), g=g.choice(few, (T, d_out)),
+             dx_base=g.integers(-9, 10, (T, d_in)))
+    c = {k: v.astype(np.float32) for k, v in c.items()}
+    c.update(ids=ids.astype(np.int32), xd=xd, wd=wd)
+    c["b"][1, 7, 2] = np.inf          # one column of adapter 1's rows
+    c["b"][2, :3, 0] = [-np.inf, np.nan, np.inf]
+    c["a"][3, r - 1, 5] = -np.inf     # one hidden value of adapter 3's tokens
+    c["x"][0, 4] = np.inf             # adapter 0
+    c["g"][0, 3] = -np.inf
+    c["g"][T // 2, 1] = np.nan
+    c["base"][T - 1, 1] = c["dx_base"][T - 1, 2] = np.inf
+    return c
+
+
+def _same_class(got, want):
+    got = got.cpu().numpy().astype(np.float64)
+    for f in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(f(got), f(want)), (f.__name__, np.argwhere(f(got) != f(want))[:5])
+    fine = np.isfinite(want)
+    assert np.array_equal(got[fine], want[fine])  # integers and halves: exact
+
+
+@gpu
+@pytest.mark.parametrize("xd,wd", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("T,d_in", [(4, 90), (20, 90), (96, 90), (96, 520)])
+def test_non_finite_values_are_those_of_the_formula(T, d_in, xd, wd):
+    """Element by element: infinite where the formula's products and sums are, NaN where they are not a number,
+    the same at any number of tokens."""
+    c = _non_finite(f"{T}/{d_in}", T, 4, 12, d_in, 60, xd, wd)
+    with np.errstate(invalid="ignore"):
+        want = A.lora_linear_ref(c["a"], c["b"], c["scale"], c["x"], c["ids"], c["base"])
+    _same_class(nq.lora_linear(_gpu_pool(c), _dev(c["x"], xd), _dev(c["ids"]), _dev(c["base"])), want)
+
+
+@gpu
+@pytest.mark.parametrize("xd,wd", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("T,d_in,d_out", [(20, 90, 60), (96, 520, 600)])
+def test_non_finite_gradients_are_those_of_the_formula(T, d_in, d_out, xd, wd):
+    c = _non_finite(f"g/{T}/{d_in}", T, 4, 12, d_in, d_out, xd, wd)
+    with np.errstate(invalid="ignore"):
+        want = A.lora_grads_ref(c["a"], c["b"], c["scale"], c["x"], c["g"], c["ids"], c["dx_base"])
+    got = nq.lora_grads(_gpu_pool(c), _dev(c["x"], xd), _dev(c["g"], xd), _dev(c["ids"]), _dev(c["dx_base"]))
+    for v, w in zip(got, want):
+        _same_class(v, w)
