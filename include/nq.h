@@ -349,7 +349,7 @@ typedef struct {
  *   (ids is device data, which a call cannot check on the host).  A call reads
  *   ids more than once: they must be final when it starts on `stream` (work of
  *   another stream that writes them must be waited for) and must not change while
- *   it runs.
+ *   it runs (results are undefined then; no address is made of them).
  * The hidden vectors A_a x[t] and all sums are fp32: nothing is rounded to
  * fewer bits, whatever the types of x and of the factors (beside bf16 factors
  * hidden values below 2^-110 lose what lies under 2^-133).  Values that are not

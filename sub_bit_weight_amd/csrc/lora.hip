@@ -305,7 +305,8 @@ __global__ __launch_bounds__(kRouteThreads) void lora_route_kernel(const int32_t
   for (int w = 0; w < wave; ++w) at += red[w];
   auto list = [&](int g, int t) {
     const unsigned long long m = __ballot(g == me);
-    if (g == me) rows[at + __popcll(m & ((1ull << lane) - 1))] = t;
+    const int place = at + __popcll(m & ((1ull << lane) - 1));
+    if (g == me && place < tiles * kTile) rows[place] = t;  // ids read again: see routed_row
     at += __popcll(m);
   };
 #pragma unroll
@@ -313,6 +314,13 @@ __global__ __launch_bounds__(kRouteThreads) void lora_route_kernel(const int32_t
     if (t0 + 64 * i < t1) list(held[i], t0 + 64 * i + lane);
   for (int t = t0 + 64 * HELD; t < t1; t += 64) list(t + lane < t1 ? group(ids[t + lane]) : -1, t + lane);
 }
+
+// Every routing workgroup reads ids for itself.  If a caller changes them meanwhile
+// (which it must not), workgroups disagree, tiles overlap and slots or adapters of
+// others are never written: whatever stands there must not become an address.  The
+// number of tiles is in range all the same, since each workgroup counts T tokens.
+__device__ inline int routed_row(int row, int T) { return (unsigned)row < (unsigned)T ? row : -1; }
+__device__ inline bool routed_adapter(int ad, int n) { return (unsigned)ad < (unsigned)n; }
 
 // The rows of a tile as a workgroup sees them.
 struct Rows {
@@ -622,11 +630,12 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       g[m].ad = p.tile_ad[tile];
-      g[m].row = p.slot_row[slot0 + 16 * m + c];
+      g[m].row = routed_row(p.slot_row[slot0 + 16 * m + c], p.T);
     }
   }
   const int ad = __builtin_amdgcn_readfirstlane(g[0].ad);
-  const int first = __builtin_amdgcn_readfirstlane(g[0].row);  // slot 0 always has a row
+  if (MT == 2 && !routed_adapter(ad, p.n)) return;
+  const int first = max(__builtin_amdgcn_readfirstlane(g[0].row), 0);  // slot 0 always has a row
   const int k0 = (int)blockIdx.z * R;
   const EX* xp[MT];
 #pragma unroll
@@ -652,9 +661,10 @@ __device__ inline void shrink(const ShrinkArgs& p, int span, float* lds) {
   if constexpr (MT == 2 && sizeof(F) == 2) {
     const int chunks = p.staged ? (int)((j1 - j0) / kChunk) : 0;
     if (chunks > 0) {  // slots without a row load the tile's first one
-      if (tid < 16 * MT) rows[tid] = p.slot_row[slot0 + tid];
-      __syncthreads();
-      if (tid < 16 * MT && rows[tid] < 0) rows[tid] = rows[0];
+      if (tid < 16 * MT) {
+        const int row = routed_row(p.slot_row[slot0 + tid], p.T);
+        rows[tid] = row < 0 ? first : row;
+      }
       __syncthreads();
       staged_steps<TW, NT>(p, static_cast<const Bf16*>(p.x), rows, w, k0, j0, chunks, reinterpret_cast<char*>(lds), acc);
       js += (int64_t)chunks * kChunk;
@@ -937,15 +947,15 @@ __device__ inline void expand(const ExpandArgs& p, int bx, int by, float (*out)[
   const int end = min(p.tile_off[p.n + 2] * SUB, begin + p.per_wg);
   if (begin >= end) return;
   int have = -1;  // adapter whose factors w holds
-  int row = p.slot_row[(int64_t)begin * 16 + c];
+  int row = routed_row(p.slot_row[(int64_t)begin * 16 + c], p.T);
   load_base(p, row, n0, lane, bcur);
   for (int it = begin; it < end; ++it) {
     const int ad = __builtin_amdgcn_readfirstlane(p.tile_ad[it / SUB]);
-    const int next = it + 1 < end ? p.slot_row[(int64_t)it * 16 + 16 + c] : -1;
+    const int next = it + 1 < end ? routed_row(p.slot_row[(int64_t)it * 16 + 16 + c], p.T) : -1;
     const bool any = __ballot(row >= 0) != 0;
 #pragma unroll
     for (int v = 0; v < 8; ++v) acc[v] = zero4();
-    if (any && ad >= 0) {
+    if (any && routed_adapter(ad, p.n)) {
       for (int kb0 = 0; kb0 < kbs; kb0 += KB) {
         Wide<EW> hw[KB];
 #pragma unroll
@@ -1139,7 +1149,7 @@ struct WgradArgs {
   const int* tile_off;
   const int* slot_row;
   int64_t d, nslots;
-  int n, r, rp;
+  int T, n, r, rp;
   int chunks;        // token chunks
   float* out;        // [chunks][n][r][d] or [chunks][n][d][r]
   int64_t chunk_stride;
@@ -1168,11 +1178,14 @@ __device__ inline void wgrad(const WgradArgs& p, int64_t block, int ad, int z, f
   Frag<EX> in[8];
   auto load = [&](int tile) {
     const int* rows = p.slot_row + (int64_t)tile * kTile + 8 * q;
-    int row[8];
+    int row[8], all = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) row[e] = rows[e];
+    for (int e = 0; e < 8; ++e) {
+      row[e] = routed_row(rows[e], p.T);
+      all |= row[e];
+    }
     const EX* x = static_cast<const EX*>(p.x) + j;
-    if (full && __ballot(row[7] < 0) == 0) {  // rows fill a tile from its front
+    if (full && __ballot(all < 0) == 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) in[e] = load8<EX, EX>(x + (int64_t)row[e] * p.d, 8);
     } else {
@@ -1631,6 +1644,7 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
   wa.slot_row = sx.slot_row;
   wa.d = P.d_in;
   wa.nslots = L.nslots;
+  wa.T = (int)T;
   wa.n = (int)P.n;
   wa.r = (int)P.r;
   wa.rp = L.rp;
