@@ -504,6 +504,8 @@ def lrb_scale_grads_batch(layers, adjs, xs, gs, workspace: torch.Tensor | None =
 
 # ---------------------------------------------------------------- adapters
 
+_SIZES_KEPT = 256  # workspace sizes that a pool remembers
+
 
 @dataclass
 class Lora:
@@ -523,6 +525,8 @@ class Lora:
         key = (query, T)
         size = self._bytes.get(key)
         if size is None:
+            if len(self._bytes) >= _SIZES_KEPT:  # token counts of a long-lived pool are without end
+                self._bytes.clear()
             size = self._bytes[key] = int(getattr(lib(), query)(ctypes.byref(self.struct()), T))
         return size
 

@@ -155,6 +155,17 @@ def test_binding_refuses_what_the_library_cannot_see():
         nq.Lora(a[:0], b[:0], s[:0]).struct()
 
 
+def test_a_pool_keeps_a_bounded_number_of_workspace_sizes():
+    pool = nq.Lora(torch.zeros(2, 4, 8), torch.zeros(2, 6, 4), torch.ones(2))
+    st = _pool(n=2, d_in=8, d_out=6, r=4)
+    object.__setattr__(pool, "_struct", st)
+    for T in range(1, 5000):
+        want = nq.lib().nq_lora_workspace_bytes(ctypes.byref(st), T)
+        assert pool._workspace_bytes("nq_lora_workspace_bytes", T) == want
+        assert pool._workspace_bytes("nq_lora_workspace_bytes", T) == want
+        assert len(pool._bytes) <= 256
+
+
 # ---------------------------------------------------------------- GPU
 
 
