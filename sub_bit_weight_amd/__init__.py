@@ -194,7 +194,7 @@ def _device_and_stream(dev, stream):
 def _call_on(dev: torch.device, stream):
     """Allocation and launch context of a call whose tensors are on `dev`: that
     device current, and `stream` (see _on)."""
-    if stream is None and dev.index == torch._C._cuda_getDevice():
+    if stream is None and dev.index == torch.cuda.current_device():
         return _NO_CONTEXT
     return _device_and_stream(dev, stream)
 
