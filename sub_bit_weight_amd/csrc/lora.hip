@@ -363,8 +363,9 @@ __device__ inline bool direct_rows(const int32_t* __restrict__ ids, int T, int n
 // Bound by the rows' bytes and, for few tokens, by the chain load - multiply - sum:
 // 2048 tokens of 8192, bf16, rank 16 13 us (2.6 TB/s); 8192 tokens, rank 64 53 us
 // (2.5 TB/s, one workgroup of 147 KB LDS a CU); 777 tokens of 4099, fp32, rank 41
-// 18 us (loads of 4 bytes and the fp32 matrix rate; fp32 rows through LDS by loads
-// of 4 bytes a lane: 22 us).
+// 18 us (loads straight from rows of odd length in eight dependent steps a wave; the
+// matrix cores of its 248 CUs are busy 29 % of the time, and its waves wait half of
+// it; fp32 rows through LDS by loads of 4 bytes a lane: 22 us).
 //
 // Rank rows of the NT tiles: 16n + row, or (TW) NT * row + n, so that a lane's
 // NT ranks are consecutive in a row of W.

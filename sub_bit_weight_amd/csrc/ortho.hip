@@ -26,12 +26,14 @@
 //    the iteration does not blow them up as it does a rounding of X itself.  An
 //    operand is two fp16 terms (hi + lo, 22 bits) and a product three fp16
 //    products; one term and one product for a bf16 result of kOneTerm rows or more.
-//    Operands are scaled by powers of two into
-//    fp16's range: bounds on x and G are known because the host checks that the
-//    polynomial keeps singular values there, roundings included.  Bound by the matrix cores, whose
-//    clock such products hold near 1.7 GHz: 4096 x 11008 in one term 4.1 ms (gram
-//    260, polynomial 106, step 435 us; 3.1 TFLOP by symmetric halves, 0.76 PFLOP/s
-//    over the call), two of 1371 x 2203 in two terms 0.84 ms.
+//    Operands are scaled by powers of two into fp16's range: bounds on x and G are
+//    known because the host checks that the polynomial keeps singular values there,
+//    roundings included.  Bound by how the tiles fill the chip and by the epilogues
+//    behind the products: 4096 x 11008 in one term 4.1 ms (3.1 TFLOP by symmetric
+//    halves, 0.76 PFLOP/s over the call).  Its symmetric products (gram 260,
+//    polynomial 106 us) are 136 tiles on 256 CUs, whose matrix cores are busy 60 %
+//    of the time; the step (435 us) is 688 tiles in three rounds, busy 46 %, with
+//    540 MB of epilogue.  Two of 1371 x 2203 in two terms 0.84 ms.
 #include <type_traits>
 
 #include "nq_internal.h"
