@@ -424,12 +424,13 @@ nq_status nq_lora_grads(const nq_lora* P, const void* x, nq_dtype x_dtype, const
  * of the result, below its own rounding up to 15 steps of 3.4445.)  A
  * longer one keeps the iterate in fp32 (what rounding leaves without a singular
  * value: 2^-24 |ca|^steps) and multiplies fp16 operands with fp32 accumulation:
- * two terms each (22 bits), or one (11 bits) for y in bf16 and a shorter side of
- * 512 or more.  One term costs a third of the products; its error is below the
- * rounding of y to bf16 at five steps of the default coefficients (1.3e-3 of the
- * norm beside 1.7e-3 at 512 x 700, 1.1e-3 at 2000 x 8000), grows with the square
- * root of the steps, and passes that rounding for matrices of rank one (up to
- * 7e-3).  Take y in fp32 and round it where that matters.  Deterministic.
+ * two terms each (22 bits), or one (11 bits) for y in bf16, a shorter side of 512
+ * or more and few steps: while the square of the largest |cb l + cc l^2|, l in [0,
+ * 1.25^2], times the steps is at most 40 (five steps of 3.4445, -4.7750, 2.0315; 64
+ * of 1.5, -0.5, 0).  One term costs a third of the products.  Its error is below the
+ * rounding of y to bf16 (at five steps 1.3e-3 of the norm beside 1.7e-3 at 512 x 700,
+ * 1.1e-3 at 2000 x 8000) but passes it for matrices of rank one (up to 1e-2): take y
+ * in fp32 and round it where that matters.  Deterministic.
  *   steps: 1 .. 64; the coefficients must be finite and must map [0, 1.25] into
  *   [-1.25, 1.25], and the largest singular value, one at first, must stay below
  *   1.3125 when every step adds its operands' roundings (up to 0.02 with one term

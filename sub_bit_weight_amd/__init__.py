@@ -708,7 +708,8 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coeffs=NEWTON_SCHULZ, out_dty
     """Newton-Schulz orthogonalisation of x [rows][cols] or [batch][rows][cols] (fp32 or bf16; strided
     views with a contiguous last dimension are fine): `steps` times X <- a X + (b G + c G^2) X with
     G = X X^T, from X / ||X||_F.  The result is fp32 or bf16 (out_dtype, default x's); bf16 takes a
-    third of the products of fp32 when the shorter side is 512 or more, in 11 bits instead of 22."""
+    third of the products of fp32, in 11 bits instead of 22, when the shorter side is 512 or more and
+    the steps are few (five of the default coefficients)."""
     if x.dim() not in (2, 3) or x.numel() == 0:
         raise ValueError(f"x must be [rows][cols] or [batch][rows][cols], got {tuple(x.shape)}")
     if not x.is_cuda:

@@ -908,7 +908,7 @@ nq_status nq_orthogonalize(const void* x, nq_dtype x_dtype, int64_t batch, int64
   if (steps < 1 || steps > 64) return set_error("%s: steps=%d outside 1..64", who, (int)steps), NQ_ERR_ARG;
   if (!std::isfinite(ca) || !std::isfinite(cb) || !std::isfinite(cc) || !keeps_range(ca, cb, cc))
     return set_error("%s: coefficients %g, %g, %g do not map [0, 1.25] into [-1.25, 1.25]", who, ca, cb, cc), NQ_ERR_ARG;
-  if (!stays_in_range(ca, cb, cc, steps, ortho_rounding(rows, cols, y_dtype)))
+  if (!stays_in_range(ca, cb, cc, steps, ortho_rounding(rows, cols, y_dtype, steps, cb, cc)))
     return set_error("%s: coefficients %g, %g, %g leave the operands' range in %d steps with their roundings", who, ca, cb,
                      cc, (int)steps),
            NQ_ERR_ARG;

@@ -199,7 +199,7 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
 // kOrthoRange, for which the operands are scaled; ortho_rounding: the relative
 // rounding of an operand (root mean square).
 constexpr double kOrthoRange = 1.3125;
-double ortho_rounding(int64_t rows, int64_t cols, nq_dtype yd);
+double ortho_rounding(int64_t rows, int64_t cols, nq_dtype yd, int steps, double cb, double cc);
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd);
 hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows, int64_t cols, int64_t ldx,
                         int64_t stride_x, int steps, double ca, double cb, double cc, void* y, nq_dtype yd, void* workspace,

@@ -25,7 +25,8 @@
 //    fp16.  Their rounding errors sit in the spaces that G spans with weight, so
 //    the iteration does not blow them up as it does a rounding of X itself.  An
 //    operand is two fp16 terms (hi + lo, 22 bits) and a product three fp16
-//    products; one term and one product for a bf16 result of kOneTerm rows or more.
+//    products; one term and one product for a bf16 result of kOneTerm rows or more
+//    in few steps (ortho_terms).
 //    Operands are scaled by powers of two into fp16's range: bounds on x and G are
 //    known because the host checks that the polynomial keeps singular values there,
 //    roundings included.  Bound by how the tiles fill the chip and by the epilogues
@@ -49,15 +50,20 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kGramMax = 64;  // shorter sides up to this take the fp64 form
 
-// Shorter sides from this on take one fp16 term for a bf16 result.  One term moves a
-// result by 2e-4 of its norm (a rounding to 11 bits) times what B multiplies it by,
-// 2.7, once per step whose singular values have grown to one.  At five default steps,
-// beside a rounding to bf16 of 1.7e-3: 1.9e-3 for 65 x 300, 1.6e-3 for 256 x 256,
-// 1.3e-3 for 512 x 700, 1.1e-3 for 2000 x 8000; in all 1.5, 1.4, 1.27 and 1.2 times the
-// rounding alone, with two terms 1.00.  Two terms cost 1.2 to 1.8 times the call below
-// the bound (us, one / two terms: 65 x 300 90 / 109, 256 x 1024 110 / 146, 500 x 700
-// 117 / 184) and up to three times above it (4 of 768 x 4096 527 / 1193).
+// Shorter sides from kOneTerm on take one fp16 term for a bf16 result, in as many
+// steps as kOneTermGain allows.  One term moves a result by 2e-4 of its norm (a
+// rounding to 11 bits) times what B multiplies it by, its largest eigenvalue (2.8 of
+// the default quintic), once per step whose singular values have grown to one.  At five
+// default steps, beside a rounding to bf16 of 1.7e-3: 1.9e-3 for 65 x 300, 1.6e-3 for
+// 256 x 256, 1.3e-3 for 512 x 700, 1.1e-3 for 2000 x 8000; in all 1.5, 1.4, 1.3 and
+// 1.2 times the rounding alone.  At 512 x 700 twelve steps are off by 2.7 times the
+// rounding and twenty by 5, so the square of that factor times the steps is bounded:
+// 40, five default steps, 64 of 1.5, -0.5.  Two terms are off by 1.00 times the
+// rounding.  They cost 1.2 to 1.8 times the call below 512 (us, one / two terms: 65 x
+// 300 90 / 109, 256 x 1024 110 / 146, 500 x 700 117 / 184) and up to three times above
+// it (4 of 768 x 4096 527 / 1193).
 constexpr int kOneTerm = 512;
+constexpr double kOneTermGain = 40.0;  // 512 x 700, twelve steps: 511 us; 4096 x 11008, five 4.1 ms, six 13.3
 
 // Element types are fp32, bf16 bits and, of iterates between segments, fp64.
 template <typename E>
@@ -569,6 +575,22 @@ struct LargeArgs {
   int64_t counters;
 };
 
+// Rows j0 .. of the transposed operand, columns i0 .., from a tile [i][j] of x.
+__device__ inline void store_transposed(const LargeArgs& s, int64_t bi, int i0, int j0, const float (&tile)[64][65]) {
+  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+  const int64_t ts = (int64_t)s.q * s.pp;
+  for (int k = ty; k < 64; k += 4) {
+    const int j = j0 + k, i = i0 + tx;
+    if (j < s.q) {
+      uint16_t hi, lo;
+      split_half(tile[tx][k] * s.sx, s.terms, hi, lo);
+      uint16_t* d = s.xt16 + bi * s.terms * ts + (int64_t)j * s.pp + i;
+      d[0] = hi;
+      if (s.terms > 1) d[ts] = lo;
+    }
+  }
+}
+
 // X0 in all its forms, with zeros in the padding.  A workgroup
 // takes 64 x 64 elements (shorter side by longer side) through LDS.
 template <typename E>
@@ -593,31 +615,36 @@ __global__ __launch_bounds__(256) void ortho_prepare_kernel(LargeArgs s, const E
     tile[tall ? tx : k][tall ? k : tx] = v;
   }
   __syncthreads();
-  const int64_t xs = (int64_t)s.p * s.qp, ts = (int64_t)s.q * s.pp;
+  const int64_t xs = (int64_t)s.p * s.qp;
   for (int k = ty; k < 64; k += 4) {
-    {
-      const int i = i0 + k, j = j0 + tx;
-      if (i < s.p) {
-        const float v = tile[k][tx];
-        s.xf[(bi * s.p + i) * s.qp + j] = v;
-        uint16_t hi, lo;
-        split_half(v * s.sx, s.terms, hi, lo);
-        uint16_t* d = s.x16 + bi * s.terms * xs + (int64_t)i * s.qp + j;
-        d[0] = hi;
-        if (s.terms > 1) d[xs] = lo;
-      }
-    }
-    {
-      const int j = j0 + k, i = i0 + tx;
-      if (j < s.q) {
-        uint16_t hi, lo;
-        split_half(tile[tx][k] * s.sx, s.terms, hi, lo);
-        uint16_t* d = s.xt16 + bi * s.terms * ts + (int64_t)j * s.pp + i;
-        d[0] = hi;
-        if (s.terms > 1) d[ts] = lo;
-      }
+    const int i = i0 + k, j = j0 + tx;
+    if (i < s.p) {
+      const float v = tile[k][tx];
+      s.xf[(bi * s.p + i) * s.qp + j] = v;
+      uint16_t hi, lo;
+      split_half(v * s.sx, s.terms, hi, lo);
+      uint16_t* d = s.x16 + bi * s.terms * xs + (int64_t)i * s.qp + j;
+      d[0] = hi;
+      if (s.terms > 1) d[xs] = lo;
     }
   }
+  store_transposed(s, bi, i0, j0, tile);
+}
+
+// The transposed operand of an iterate, where there is room for one copy of it only: a
+// step reads it whole and cannot write the next one beside.  Bound by its bytes (8 for
+// each value; 512 x 700 to bf16, twelve steps: 511 us, to fp32 with two copies 421).
+__global__ __launch_bounds__(256) void ortho_transpose_kernel(LargeArgs s) {
+  __shared__ float tile[64][65];
+  const int64_t bi = blockIdx.z;
+  const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;  // i < pp, j < qp
+  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+  for (int k = ty; k < 64; k += 4) {
+    const int i = i0 + k;
+    tile[k][tx] = i < s.p ? s.xf[(bi * s.p + i) * s.qp + j0 + tx] : 0.0f;
+  }
+  __syncthreads();
+  store_transposed(s, bi, i0, j0, tile);
 }
 
 // Wait until at most N vector-memory operations of this wave are outstanding,
@@ -628,7 +655,7 @@ __device__ inline void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
 }
 
-enum Mode { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
+enum Mode { kGram = 0, kPoly = 1, kStep = 2, kLast = 3, kStepRows = 4 };
 
 struct GemmArgs {
   const uint16_t *A, *B;   // [batch][terms][rows][K] fp16
@@ -639,7 +666,8 @@ struct GemmArgs {
   float s_acc, s_aux;
   int terms;
   // kGram, kPoly: out16 [batch][terms][M][ldo]; kPoly: aux16 as out16
-  // kStep: xf (rows of ldo), out16 (x16), outt16 (the transpose); kLast: xf, y
+  // kStep: xf (rows of ldo), out16 (x16), outt16 (the transpose); kStepRows: without
+  // the transpose; kLast: xf, y
   uint16_t* out16;
   uint16_t* outt16;
   const uint16_t* aux16;
@@ -689,6 +717,7 @@ template <int BM, int BN, int BK, int WM, int WN, int S, bool SPREAD, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
   constexpr int NW = WM * WN, MB = BM / WM / 32, NB = BN / WN / 32;
   constexpr int ROW = 2 * BK, RPL = 1024 / ROW, CH = BK / 8;  // row bytes, rows of a load, chunks of a row
+  constexpr bool STEP = MODE == kStep || MODE == kStepRows;
   constexpr int STAGE = (BM + BN) * ROW, LOADS_A = BM / RPL / NW, LOADS_B = BN / RPL / NW;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x % 64;
@@ -1002,12 +1031,12 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
       if constexpr (MODE == kLast) {
         if (!p.y_t) store8(p.y, p.y_bf16, ybase + (int64_t)m * p.N + n, v, p.N - n);
       } else if (n < p.ldo) {
-        if constexpr (MODE == kStep) {
+        if constexpr (STEP) {
           float* at = xf + (int64_t)m * p.ldo + n;
           *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
           *reinterpret_cast<f32x4*>(at + 4) = f32x4{v[4], v[5], v[6], v[7]};
         }
-        store_terms(out + (int64_t)m * p.ldo + n, p.term_o, p.terms, v, MODE == kStep ? kScaleX : 1.0f);
+        store_terms(out + (int64_t)m * p.ldo + n, p.term_o, p.terms, v, STEP ? kScaleX : 1.0f);
       }
     }
     if (transposed) {  // 8 rows of column lane / 4 + 16 t
@@ -1035,7 +1064,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_gemm_kernel(GemmArgs p) {
 
 struct OrthoLayout {
   bool small;
-  int p, P, pp, qp, terms, spans;
+  int p, P, pp, qp, terms, copies, spans;  // copies: of the transposed operand
   int64_t q, span;
   size_t off_g, off_q, off_it, off_part, off_bad, off_xf, off_x16, off_xt[2], off_g16, off_b16, off_sums, off_arr, bytes;
   int64_t counters;
@@ -1052,7 +1081,8 @@ int square_splits(int64_t batch, int64_t p, int64_t k, int terms) {
   return (int)cdiv(all, cdiv(all, n));
 }
 
-OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd) {
+// terms: of the operands (of a shorter side past kGramMax)
+OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd, int terms) {
   OrthoLayout L{};
   L.p = (int)imin(rows, cols);
   L.q = imax(rows, cols);
@@ -1072,14 +1102,15 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd)
     L.off_q = take((size_t)batch * L.P * L.P * sizeof(double));
     L.off_it = take((size_t)batch * rows * cols * sizeof(double));  // the query does not know the steps: always
   } else {
-    L.terms = yd == NQ_F32 || L.p < kOneTerm ? 2 : 1;
+    L.terms = terms;
+    L.copies = yd == NQ_BF16 && L.p >= kOneTerm && terms == 2 ? 1 : 2;  // no more than a quarter over one term
     L.pp = (int)round_up(L.p, kBK);
     L.qp = (int)round_up(L.q, kBK);
     L.off_part = take((size_t)batch * kSumBlocks * sizeof(double));
     L.off_bad = take((size_t)batch * sizeof(float));
     L.off_xf = take((size_t)batch * L.p * L.qp * sizeof(float));
     L.off_x16 = take((size_t)batch * L.terms * L.p * L.qp * 2);
-    for (auto& o : L.off_xt) o = take((size_t)batch * L.terms * L.q * L.pp * 2);
+    for (int i = 0; i < L.copies; ++i) L.off_xt[i] = take((size_t)batch * L.terms * L.q * L.pp * 2);
     L.off_g16 = take((size_t)batch * L.terms * L.p * L.pp * 2);
     L.off_b16 = take((size_t)batch * L.terms * L.p * L.pp * 2);
     const int splits = (int)imax(square_splits(batch, L.p, L.qp, L.terms), square_splits(batch, L.p, L.pp, L.terms));
@@ -1187,21 +1218,31 @@ double poly_bound(double b, double c, double top) {
   return m;
 }
 
+// The operands' terms (of a shorter side past kGramMax): see kOneTerm.
+int ortho_terms(int64_t rows, int64_t cols, nq_dtype yd, int steps, double cb, double cc) {
+  if (yd == NQ_F32 || imin(rows, cols) < kOneTerm) return 2;
+  const double gain = poly_bound(cb, cc, 1.25 * 1.25);
+  return gain * gain * steps <= kOneTermGain ? 1 : 2;
+}
+
 }  // namespace
 
-double ortho_rounding(int64_t rows, int64_t cols, nq_dtype yd) {
-  const OrthoLayout L = ortho_layout(1, rows, cols, yd);
-  return L.small ? 0x1p-33 : (L.terms == 2 ? 0x1p-21 : 0x1p-11 / sqrt(3.0));  // small: what a segment may grow to
+double ortho_rounding(int64_t rows, int64_t cols, nq_dtype yd, int steps, double cb, double cc) {
+  if (imin(rows, cols) <= kGramMax) return 0x1p-33;  // what a segment may grow to
+  return ortho_terms(rows, cols, yd, steps, cb, cc) == 2 ? 0x1p-21 : 0x1p-11 / sqrt(3.0);
 }
 
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols, nq_dtype yd) {
-  return ortho_layout(batch, rows, cols, yd).bytes;
+  const size_t two = ortho_layout(batch, rows, cols, yd, 2).bytes;
+  if (yd == NQ_F32 || imin(rows, cols) < kOneTerm) return two;
+  const size_t one = ortho_layout(batch, rows, cols, yd, 1).bytes;  // the steps are not known here
+  return one > two ? one : two;
 }
 
 hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows, int64_t cols, int64_t ldx,
                         int64_t stride_x, int steps, double ca, double cb, double cc, void* y, nq_dtype yd, void* workspace,
                         hipStream_t s) {
-  const OrthoLayout L = ortho_layout(batch, rows, cols, yd);
+  const OrthoLayout L = ortho_layout(batch, rows, cols, yd, ortho_terms(rows, cols, yd, steps, cb, cc));
   char* ws = static_cast<char*>(workspace);
   const int tall = rows > cols;
   if (L.small) {
@@ -1248,7 +1289,8 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
   l.terms = L.terms;
   l.xf = reinterpret_cast<float*>(ws + L.off_xf);
   l.x16 = reinterpret_cast<uint16_t*>(ws + L.off_x16);
-  uint16_t* const xt16[2] = {reinterpret_cast<uint16_t*>(ws + L.off_xt[0]), reinterpret_cast<uint16_t*>(ws + L.off_xt[1])};
+  uint16_t* const xt16[2] = {reinterpret_cast<uint16_t*>(ws + L.off_xt[0]),
+                             reinterpret_cast<uint16_t*>(ws + L.off_xt[L.copies - 1])};
   uint16_t* const g16 = reinterpret_cast<uint16_t*>(ws + L.off_g16);
   uint16_t* const b16 = reinterpret_cast<uint16_t*>(ws + L.off_b16);
   l.xt16 = xt16[0];
@@ -1328,7 +1370,15 @@ hipError_t launch_ortho(const void* x, nq_dtype xd, int64_t batch, int64_t rows,
     if ((e = launch_ortho_gemm<kPoly>(poly, batch, s)) != hipSuccess) return e;
     step.B = xt16[i % 2];
     step.outt16 = xt16[1 - i % 2];
-    e = i + 1 < steps ? launch_ortho_gemm<kStep>(step, batch, s) : launch_ortho_gemm<kLast>(step, batch, s);
+    if (i + 1 == steps) {
+      e = launch_ortho_gemm<kLast>(step, batch, s);
+    } else if (L.copies == 2) {
+      e = launch_ortho_gemm<kStep>(step, batch, s);
+    } else {
+      if ((e = launch_ortho_gemm<kStepRows>(step, batch, s)) != hipSuccess) return e;
+      hipLaunchKernelGGL(ortho_transpose_kernel, pgrid, dim3(256), 0, s, l);
+      e = hipGetLastError();
+    }
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
