@@ -262,8 +262,9 @@ __device__ inline void inverse_trace(double t, int normed, double& inv, double& 
 // (the product of the P so far) commute and are symmetric: every product reads both
 // operands by rows, and P and the last Q are made in the registers of the products
 // they come from.  A becomes P A^T P^T: with P on one side twice, A P^T P^T, what
-// rounding leaves beside the diagonal grows by a^2 a step instead of a.  Bound by the chain of 19 products of five steps, about half of it
-// the fp64 rate of one CU (a call of 64 x 1024: 96 us, with four waves 107).
+// rounding leaves beside the diagonal grows by a^2 a step instead of a.  Bound by the
+// chain of 19 products of five steps, about half of it the fp64 rate of one CU (a call
+// of 64 x 1024: 96 us, with four waves 107).
 template <int PT>
 __global__ __launch_bounds__(64 * PT * PT) void ortho_solve_kernel(SmallArgs s) {
   constexpr int P = 16 * PT, S = P + 4, NTH = 64 * PT * PT;
