@@ -451,6 +451,133 @@ nq_status nq_orthogonalize(const void* x, nq_dtype x_dtype, int64_t batch, int64
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The packed layer inside a block: bias, activation, gate and residual in the
+ * epilogue of the product, and the gradients of that epilogue.
+ */
+typedef int32_t nq_act;
+enum {
+  NQ_ACT_NONE = 0,      /* z */
+  NQ_ACT_RELU = 1,      /* max(z, 0) */
+  NQ_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution's cdf */
+  NQ_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  NQ_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+};
+typedef struct {
+  nq_act act;
+  const float* bias;    /* [d_out] fp32, or null */
+  const void* mul;      /* [T][d_out], or null: what act(z) is multiplied by (a gated layer's other projection) */
+  nq_dtype mul_dtype;   /* read only with mul; likewise below */
+  const void* residual; /* [T][d_out], or null */
+  nq_dtype residual_dtype;
+  void* z;              /* [T][d_out], or null: receives z, for the backward pass */
+  nq_dtype z_dtype;
+} nq_epilogue;
+
+/*
+ * nq_lrb_linear_act -- nq_lrb_linear with an epilogue:
+ *     z[t] = W x[t] + bias,   y[t] = act(z[t]) (.) mul[t] + residual[t]
+ *   (a factor or term that is null is left out).  x, T: as in nq_lrb_linear;
+ *   y: [T][d_out], fp32 or bf16 (y_dtype).  W x is computed as by nq_lrb_linear
+ *   (the same regimes and arithmetic); the epilogue is fp32 and rounds once, to
+ *   y's type (and z to its own).  y may be mul or residual where the types are
+ *   equal (in place); z may not be any of them.  silu and gelu of -inf are NaN,
+ *   the products -inf * 0 of their formulas.
+ *   workspace: at least nq_lrb_act_workspace_bytes(L, T) bytes, 256-byte aligned.
+ *   Streams, graphs and determinism: as for nq_lrb_linear.
+ * Errors: as for nq_lrb_linear; NQ_ERR_ARG for a null epilogue, an unknown
+ * activation or dtype, or a pointer not aligned to its elements.
+ */
+size_t nq_lrb_act_workspace_bytes(const nq_lrb* L, int64_t T);
+nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, int64_t T, const nq_epilogue* E, void* y,
+                            nq_dtype y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * nq_act_grads -- the gradients of that epilogue for dy = dL/dy:
+ *     dz = dy (.) mul (.) act'(z),   dmul = dy (.) act(z),   dbias[i] = sum_t dz[t][i]
+ *   (the residual's gradient is dy itself; dz is the g of nq_lrb_scale_grads).
+ *   z, mul, dy, dz, dmul: [T][d] contiguous, fp32 or bf16 each; mul null: ones, and
+ *   dmul must be null; dmul and dbias may be null (not computed); z may be null
+ *   where neither act' nor dmul needs it (NQ_ACT_NONE without dmul).  dz may be dy
+ *   or z and dmul may be mul where the types are equal (in place).  fp32
+ *   arithmetic, each result rounded once; relu'(0) = 0; dbias sums the unrounded dz
+ *   in fp32 in a fixed order (deterministic).
+ *   workspace: at least nq_act_grads_workspace_bytes(T, d) bytes, 256-byte aligned
+ *   (null with dbias null); calls that may overlap need one each.
+ * Errors: NQ_ERR_ARG for null or misaligned pointers, sizes < 1, unknown
+ * activations or dtypes; NQ_ERR_UNSUPPORTED for T or d > 2^24; NQ_ERR_WORKSPACE;
+ * NQ_ERR_HIP.  The size query returns 0 for invalid arguments.
+ */
+size_t nq_act_grads_workspace_bytes(int64_t T, int64_t d);
+nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* mul, nq_dtype mul_dtype, const void* dy,
+                       nq_dtype dy_dtype, int64_t T, int64_t d, void* dz, nq_dtype dz_dtype, void* dmul,
+                       nq_dtype dmul_dtype, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits: the objective of scale-only
+ * reconstruction (section 3 "Phase 3: Scale-Only Model Reconstruction": the
+ * divergence KL of the quantized model's outputs from the full-precision
+ * model's), with the teacher kept as its k most likely tokens per position.
+ *
+ * nq_logits_top -- a teacher's record: of each row's V logits, at a temperature,
+ *   the k largest (largest first; equal ones by index) with their log-probabilities
+ *   and the log-probability of all the others together:
+ *     l = log sum_v exp(z[v] / temperature)
+ *     logp[t][e] = z[ids[t][e]] / temperature - l
+ *     rest[t] = log sum over the v not in ids[t] of exp(z[v] / temperature) - l
+ *   logits: [T] rows of V, row stride ld >= V elements, fp32 or bf16; ids: [T][k]
+ *   int32, logp: [T][k] fp32, rest: [T] fp32 (may be null).  Logits of -inf (masked
+ *   tokens) are not listed: where fewer than k remain, ids is -1 and logp -inf from
+ *   there on, and rest is -inf where nothing else is left (a row of -inf alone: an
+ *   empty record).  A row with NaN or +inf has NaN logp and rest (NaN counts as the
+ *   largest logit).
+ *
+ * nq_distill_loss -- the divergence of a student from the record, row by row.  With
+ *   q = softmax(s[t] / temperature), p_e = exp(logp[t][e]), r = exp(rest[t]) and
+ *   q_rest = the sum of q over the tokens not listed:
+ *     loss[t] = weight[t] * ( sum_e p_e (logp[t][e] - log q[ids[t][e]]) + r (rest[t] - log q_rest) )
+ *   rest null: r = 0 and the p_e are divided by their sum.  Entries with ids < 0
+ *   are not there, those of probability 0 add nothing to the sum (but are listed); a
+ *   token listed more than once counts once in q_rest and each of its entries in the
+ *   sum.  An id >= V: NaN for that row.  Nothing listed and r = 0: 0 for that row.
+ *   weight[t] = 0: the row's logits are not read, its loss and gradient are 0; weight
+ *   null: ones.
+ *   logits: [T] rows of V, row stride ld >= V elements, fp32 or bf16; weight, loss:
+ *   [T] fp32.
+ *
+ * nq_distill_grads -- the same and its gradient, dlogits[t][v] = d loss[t] / d s[t][v]:
+ *     v listed:      weight/temperature * ( (P + r) q_v - sum of p_e over ids[t][e] = v ),  P = sum_e p_e
+ *     v not listed:  weight/temperature * ( (P + r) q_v - r q_v / q_rest )
+ *   dlogits: [T] rows of V, row stride ldd >= V elements, fp32 or bf16
+ *   (dlogits_dtype); columns past V are not written; it may be logits itself with
+ *   the same type and stride (in place).  loss may be null.
+ * Both read the logits from memory once for V up to 131072 (bf16) or 65536 (fp32);
+ * exponentials are fp32, the sums over a row fp32 per thread and fp64 across, the
+ * loss is formed in fp64 and rounded once, each gradient rounded once.  Deterministic.
+ * Logits that are not finite stay within their row, infinite or NaN as the formulas
+ * are (a row of -inf alone has no softmax: NaN; a token of logit -inf has q = 0).
+ * No workspace.
+ * Errors: NQ_ERR_ARG for null or misaligned pointers, T < 1, V < 1, k < 1, ld < V,
+ * ldd < V, unknown dtypes, a temperature outside [2^-20, 2^20], or dlogits
+ * equal to logits with another type or stride; NQ_ERR_UNSUPPORTED for k >
+ * NQ_TOP_MAX, V > 2^20 or T > 2^21; NQ_ERR_HIP.
+ */
+#define NQ_TOP_MAX 1024
+typedef struct {
+  int64_t k;            /* entries per row, 1 .. NQ_TOP_MAX */
+  const int32_t* ids;   /* [T][k] device */
+  const float* logp;    /* [T][k] device: log-probabilities at `temperature` */
+  const float* rest;    /* [T] device, or null */
+  float temperature;    /* 2^-20 .. 2^20 */
+} nq_teacher;
+nq_status nq_logits_top(const void* logits, nq_dtype logits_dtype, int64_t T, int64_t V, int64_t ld, int64_t k,
+                        float temperature, int32_t* ids, float* logp, float* rest, void* stream);
+nq_status nq_distill_loss(const nq_teacher* P, const void* logits, nq_dtype logits_dtype, int64_t T, int64_t V,
+                          int64_t ld, const float* weight, float* loss, void* stream);
+nq_status nq_distill_grads(const nq_teacher* P, const void* logits, nq_dtype logits_dtype, int64_t T, int64_t V,
+                           int64_t ld, const float* weight, float* loss, void* dlogits, nq_dtype dlogits_dtype,
+                           int64_t ldd, void* stream);
+
+/*
  * nq_fill_random_words -- synthetic sign words for large benchmark matrices:
  *   dst[i] = low 32 bits of SplitMix64(seed, i), i < n, where SplitMix64(seed,
  *   i) is output number i+1 of the SplitMix64 stream started at `seed`

@@ -9,7 +9,8 @@ Names follow the C ABI in include/nq.h:
   storage_bits, fill_random_words, Seq (nq_seq_*), transpose_signs,
   lrb_scale_grads (nq_lrb_scale_grads*), lrb_scale_grads_batch
   (nq_lrb_scale_grads_batch*), Lora (nq_lora), lora_linear, lora_grads,
-  lrb_lora_linear, orthogonalize, last_error.
+  lrb_lora_linear, orthogonalize, lrb_linear_act, act_grads, Teacher
+  (nq_teacher), logits_top, distill_loss, distill_grads, last_error.
 """
 from __future__ import annotations
 
@@ -37,6 +38,8 @@ EXPORTED = [
     "nq_balance_factors", "nq_lrb_latent_workspace_bytes", "nq_lrb_linear_latent", "nq_lrb_linear_noalloc",
     "nq_lora_workspace_bytes", "nq_lora_linear", "nq_lrb_lora_workspace_bytes", "nq_lrb_lora_linear",
     "nq_lora_grads_workspace_bytes", "nq_lora_grads", "nq_orthogonalize_workspace_bytes", "nq_orthogonalize",
+    "nq_lrb_act_workspace_bytes", "nq_lrb_linear_act", "nq_act_grads_workspace_bytes", "nq_act_grads",
+    "nq_logits_top", "nq_distill_loss", "nq_distill_grads",
 ]
 
 # Size of the library's fixed per-GPU workspace array (NQ_NOALLOC_SCRATCH_BYTES in nq.h).
@@ -65,6 +68,22 @@ class nq_lora(ctypes.Structure):
         ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("stride_a", ctypes.c_int64),
         ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("stride_b", ctypes.c_int64),
         ("scale", ctypes.c_void_p),
+    ]
+
+
+class nq_epilogue(ctypes.Structure):
+    _fields_ = [
+        ("act", ctypes.c_int32), ("bias", ctypes.c_void_p),
+        ("mul", ctypes.c_void_p), ("mul_dtype", ctypes.c_int32),
+        ("residual", ctypes.c_void_p), ("residual_dtype", ctypes.c_int32),
+        ("z", ctypes.c_void_p), ("z_dtype", ctypes.c_int32),
+    ]
+
+
+class nq_teacher(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_int64), ("ids", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("rest", ctypes.c_void_p),
+        ("temperature", ctypes.c_float),
     ]
 
 
@@ -144,6 +163,21 @@ def lib() -> ctypes.CDLL:
     L.nq_orthogonalize.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, ctypes.c_int32, f64, f64, f64, vp,
                                    ctypes.c_int, vp, sz, vp]
     L.nq_orthogonalize.restype = st
+    i32, f32 = ctypes.c_int32, ctypes.c_float
+    L.nq_lrb_act_workspace_bytes.argtypes = [P(nq_lrb), i64]
+    L.nq_lrb_act_workspace_bytes.restype = sz
+    L.nq_lrb_linear_act.argtypes = [P(nq_lrb), vp, i32, i64, P(nq_epilogue), vp, i32, vp, sz, vp]
+    L.nq_lrb_linear_act.restype = st
+    L.nq_act_grads_workspace_bytes.argtypes = [i64, i64]
+    L.nq_act_grads_workspace_bytes.restype = sz
+    L.nq_act_grads.argtypes = [i32, vp, i32, vp, i32, vp, i32, i64, i64, vp, i32, vp, i32, vp, vp, sz, vp]
+    L.nq_act_grads.restype = st
+    L.nq_logits_top.argtypes = [vp, i32, i64, i64, i64, i64, f32, vp, vp, vp, vp]
+    L.nq_logits_top.restype = st
+    L.nq_distill_loss.argtypes = [P(nq_teacher), vp, i32, i64, i64, i64, vp, vp, vp]
+    L.nq_distill_loss.restype = st
+    L.nq_distill_grads.argtypes = [P(nq_teacher), vp, i32, i64, i64, i64, vp, vp, vp, i32, i64, vp]
+    L.nq_distill_grads.restype = st
     L.nq_last_error.argtypes = []
     L.nq_last_error.restype = ctypes.c_char_p
     L.nq_version.argtypes = []
@@ -741,6 +775,226 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coeffs=NEWTON_SCHULZ, out_dty
                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
                                       _stream(stream, dev.index)))
     return y
+
+
+# ---------------------------------------------------------------- epilogues
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _act_code(act: str) -> int:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})")
+    return code
+
+
+def _rows(t: torch.Tensor | None, name: str, shape: tuple, device) -> int:
+    """The dtype code of an optional operand [T][d] (NQ_F32 where there is none)."""
+    if t is None:
+        return NQ_F32
+    _dev(t, name)
+    if tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} dtype {t.dtype} not supported (float32 or bfloat16)")
+    return NQ_BF16 if t.dtype == torch.bfloat16 else NQ_F32
+
+
+def lrb_act_workspace_bytes(layer: Lrb, T: int) -> int:
+    return int(lib().nq_lrb_act_workspace_bytes(ctypes.byref(layer.struct()), T))
+
+
+def lrb_linear_act(layer: Lrb, x: torch.Tensor, act: str = "none", bias: torch.Tensor | None = None,
+                   mul: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                   out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None, z: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = act(W x + bias) * mul + residual for the packed layer W, in one pass: x [T][d_in], bias
+    [d_out] fp32, mul, residual and y [T][d_out], each fp32 or bf16 (y: out_dtype, default x's).  act is
+    one of ACTIVATIONS.  z, when given, receives W x + bias (for act_grads).  y may be mul or residual."""
+    _dev(x, "x")
+    if x.dim() != 2 or x.shape[1] != layer.d_in:
+        raise ValueError(f"x must be [T][{layer.d_in}], got {tuple(x.shape)}")
+    code, xd, dev = _act_code(act), _x_dtype(x), x.device
+    s = layer.struct()
+    if layer.s1.device != dev:
+        raise ValueError(f"the layer and x must share a device: {layer.s1.device}, {dev}")
+    T, shape = x.shape[0], (x.shape[0], layer.d_out)
+    if bias is not None:
+        _f32_rows(bias, "bias", (layer.d_out,), dev)
+    md, rd, zd = _rows(mul, "mul", shape, dev), _rows(residual, "residual", shape, dev), _rows(z, "z", shape, dev)
+    if y is not None:
+        yd = _rows(y, "y", shape, dev)
+        if out_dtype is not None and y.dtype != out_dtype:
+            raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
+    else:
+        out_dtype = x.dtype if out_dtype is None else out_dtype
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"output dtype {out_dtype} not supported (float32 or bfloat16)")
+        yd = NQ_BF16 if out_dtype == torch.bfloat16 else NQ_F32
+    _workspace_on(workspace, dev)
+    with _call_on(dev, stream):
+        if y is None:
+            y = torch.empty(shape, dtype=out_dtype, device=dev)
+        if workspace is None:
+            need = int(lib().nq_lrb_act_workspace_bytes(ctypes.byref(s), T))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        epi = nq_epilogue(code, _ptr(bias), _ptr(mul), md, _ptr(residual), rd, _ptr(z), zd)
+        _check(lib().nq_lrb_linear_act(ctypes.byref(s), _ptr(x), xd, T, ctypes.byref(epi), _ptr(y), yd, _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream(stream, dev.index)))
+    return y
+
+
+def act_grads(act: str, z: torch.Tensor | None, dy: torch.Tensor, mul: torch.Tensor | None = None, bias: bool = True,
+              dz: torch.Tensor | None = None, dmul: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              stream=None):
+    """(dz, dmul, dbias) of y = act(z) * mul + residual for dy = dL/dy [T][d]: dz in dy's dtype (or the given
+    tensor's), dmul in mul's (None without mul), dbias [d] fp32 (None unless bias).  z is what lrb_linear_act
+    stored (None will do for act "none" without mul); dz may be dy or z and dmul may be mul (in place)."""
+    _dev(dy, "dy")
+    if dy.dim() != 2 or dy.numel() == 0:
+        raise ValueError(f"dy must be [T][d], got {tuple(dy.shape)}")
+    code, shape, dev = _act_code(act), tuple(dy.shape), dy.device
+    dyd = _rows(dy, "dy", shape, dev)
+    zd, md = _rows(z, "z", shape, dev), _rows(mul, "mul", shape, dev)
+    if z is None and (act != "none" or mul is not None):
+        raise ValueError("z is needed but for act 'none' without mul")
+    if dmul is not None and mul is None:
+        raise ValueError("dmul without mul")
+    for t, name in ((dz, "dz"), (dmul, "dmul")):
+        _rows(t, name, shape, dev)
+    _workspace_on(workspace, dev)
+    with _call_on(dev, stream):
+        if dz is None:
+            dz = torch.empty_like(dy)
+        if dmul is None and mul is not None:
+            dmul = torch.empty_like(mul)
+        dbias = torch.empty(shape[1], dtype=torch.float32, device=dev) if bias else None
+        size = 0
+        if bias:
+            if workspace is None:
+                need = int(lib().nq_act_grads_workspace_bytes(*shape))
+                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            size = workspace.numel() * workspace.element_size()
+        _check(lib().nq_act_grads(code, _ptr(z), zd, _ptr(mul), md, _ptr(dy), dyd, shape[0], shape[1], _ptr(dz),
+                                  _rows(dz, "dz", shape, dev), _ptr(dmul), _rows(dmul, "dmul", shape, dev), _ptr(dbias),
+                                  _ptr(workspace), size, _stream(stream, dev.index)))
+    return dz, dmul, dbias
+
+
+# ---------------------------------------------------------------- distillation
+
+
+@dataclass
+class Teacher:
+    """A teacher's record on the device: per row the ids and log-probabilities (at `temperature`) of its
+    likeliest tokens, and the log-probability of all the others together (rest; None: the listed
+    probabilities are divided by their sum).  ids < 0: no entry.  Made by logits_top or loaded."""
+    ids: torch.Tensor          # [T][k] int32
+    logp: torch.Tensor         # [T][k] float32
+    rest: torch.Tensor | None = None  # [T] float32
+    temperature: float = 1.0
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_struct", None)  # any field change re-validates
+
+    def struct(self) -> nq_teacher:
+        """The C struct, after checking what the C ABI cannot see.  Built once and kept until a field is
+        assigned again; tensors must not be resized in place while the record is in use."""
+        cached = self.__dict__.get("_struct")
+        if cached is not None:
+            return cached
+        ids, logp, rest = self.ids, self.logp, self.rest
+        _dev(ids, "ids")
+        if ids.dtype != torch.int32 or ids.dim() != 2 or ids.numel() == 0:
+            raise ValueError(f"ids must be int32 [T][k], got {ids.dtype} {tuple(ids.shape)}")
+        _f32_rows(logp, "logp", tuple(ids.shape), ids.device)
+        if rest is not None:
+            _f32_rows(rest, "rest", (ids.shape[0],), ids.device)
+        st = nq_teacher(ids.shape[1], ids.data_ptr(), logp.data_ptr(), _ptr(rest), float(self.temperature))
+        object.__setattr__(self, "_struct", st)
+        return st
+
+
+def _logits(t: torch.Tensor, name: str) -> int:
+    """Checks rows of logits [T][V] (a view whose rows are contiguous will do); the row stride."""
+    if t.dim() != 2 or t.numel() == 0:
+        raise ValueError(f"{name} must be [T][V], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] == 1:  # one row may carry any stride
+        return max(t.stride(0), t.shape[1])
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap, got strides {t.stride()}")
+    return t.stride(0)
+
+
+def logits_top(logits: torch.Tensor, k: int, temperature: float = 1.0, stream=None) -> Teacher:
+    """The record of a teacher's logits [T][V] (fp32 or bf16; rows may be strided): its k likeliest tokens per
+    row, largest first and equal ones by index, and the mass of the rest."""
+    ld, dev = _logits(logits, "logits"), logits.device
+    T, V = logits.shape
+    if k < 1:
+        raise ValueError(f"k must be >= 1, got {k}")
+    xd = _x_dtype(logits)
+    with _call_on(dev, stream):
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        logp = torch.empty((T, k), dtype=torch.float32, device=dev)
+        rest = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(lib().nq_logits_top(_ptr(logits), xd, T, V, ld, k, temperature, _ptr(ids), _ptr(logp), _ptr(rest),
+                                   _stream(stream, dev.index)))
+    return Teacher(ids, logp, rest, temperature)
+
+
+def _distill_args(teacher: Teacher, logits: torch.Tensor, weight: torch.Tensor | None):
+    s, ld = teacher.struct(), _logits(logits, "logits")
+    T = logits.shape[0]
+    if teacher.ids.shape[0] != T or teacher.ids.device != logits.device:
+        raise ValueError(f"the teacher has {teacher.ids.shape[0]} rows on {teacher.ids.device}, "
+                         f"logits {T} on {logits.device}")
+    if weight is not None:
+        _f32_rows(weight, "weight", (T,), logits.device)
+    return s, ld
+
+
+def distill_loss(teacher: Teacher, logits: torch.Tensor, weight: torch.Tensor | None = None,
+                 loss: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """loss[t] = weight[t] * KL(teacher || softmax(logits[t] / teacher.temperature)), fp32 [T]; logits [T][V] fp32
+    or bf16 (rows may be strided), weight [T] fp32 (0: the row is not read) or None (ones)."""
+    s, ld = _distill_args(teacher, logits, weight)
+    (T, V), dev, xd = logits.shape, logits.device, _x_dtype(logits)
+    if loss is not None:
+        _f32_rows(loss, "loss", (T,), dev)
+    with _call_on(dev, stream):
+        if loss is None:
+            loss = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(lib().nq_distill_loss(ctypes.byref(s), _ptr(logits), xd, T, V, ld, _ptr(weight), _ptr(loss),
+                                     _stream(stream, dev.index)))
+    return loss
+
+
+def distill_grads(teacher: Teacher, logits: torch.Tensor, weight: torch.Tensor | None = None,
+                  dlogits: torch.Tensor | None = None, stream=None):
+    """(loss, dlogits): distill_loss and the gradient of its sum over rows, [T][V] in the logits' dtype or the
+    given tensor's (fp32 or bf16; it may be logits itself, in place)."""
+    s, ld = _distill_args(teacher, logits, weight)
+    (T, V), dev, xd = logits.shape, logits.device, _x_dtype(logits)
+    if dlogits is not None:
+        ldd = _logits(dlogits, "dlogits")
+        if dlogits.shape != logits.shape or dlogits.device != dev:
+            raise ValueError(f"dlogits must be {tuple(logits.shape)} on {dev}, got {tuple(dlogits.shape)} on {dlogits.device}")
+        dd = _x_dtype(dlogits)
+    with _call_on(dev, stream):
+        if dlogits is None:
+            dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev)
+            ldd, dd = V, xd
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(lib().nq_distill_grads(ctypes.byref(s), _ptr(logits), xd, T, V, ld, _ptr(weight), _ptr(loss),
+                                      _ptr(dlogits), dd, ldd, _stream(stream, dev.index)))
+    return loss, dlogits
 
 
 def balance_factors(u_hat: torch.Tensor, v_hat: torch.Tensor, r: int | None = None, balanced: bool = True,

@@ -13,6 +13,7 @@
 #include <array>
 #include <vector>
 
+#include "epilogue.h"
 #include "nq_internal.h"
 
 namespace nq {
@@ -917,6 +918,191 @@ nq_status nq_orthogonalize(const void* x, nq_dtype x_dtype, int64_t batch, int64
   return hip_status(launch_ortho(x, x_dtype, batch, rows, cols, ldx, stride_x, steps, ca, cb, cc, y, y_dtype, workspace,
                                  (hipStream_t)stream),
                     "nq_orthogonalize launch");
+}
+
+namespace {
+
+bool dtype_ok(nq_dtype d) { return d == NQ_F32 || d == NQ_BF16; }
+size_t dtype_size(nq_dtype d) { return d == NQ_F32 ? 4 : 2; }
+
+// An operand of an epilogue or of its gradients: p may be null, and its dtype is then not read.
+nq_status check_operand(const char* who, const char* name, const void* p, nq_dtype d) {
+  if (!p) return NQ_OK;
+  if (!dtype_ok(d)) return set_error("%s: unknown %s dtype %d", who, name, (int)d), NQ_ERR_ARG;
+  if (!aligned(p, dtype_size(d))) return set_error("%s: %s misaligned", who, name), NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+nq_status check_act(const char* who, nq_act act) {
+  if (act < NQ_ACT_NONE || act > NQ_ACT_SILU) return set_error("%s: unknown activation %d", who, (int)act), NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+size_t linear_act_workspace(const nq_lrb& L, int64_t T) {
+  return align_up(linear_workspace(L, T)) + (size_t)T * L.d_out * sizeof(float);
+}
+
+}  // namespace
+
+size_t nq_lrb_act_workspace_bytes(const nq_lrb* L, int64_t T) {
+  if (check_lrb("nq_lrb_act_workspace_bytes", L) != NQ_OK || T < 1 || T > (int64_t(1) << 24)) return 0;
+  return linear_act_workspace(*L, T);
+}
+
+nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, int64_t T, const nq_epilogue* E, void* y,
+                            nq_dtype y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "nq_lrb_linear_act";
+  nq_status st = check_lrb(who, L);
+  if (st != NQ_OK) return st;
+  if (!E) return set_error("%s: null epilogue", who), NQ_ERR_ARG;
+  if (!dtype_ok(y_dtype)) return set_error("%s: unknown y dtype %d", who, (int)y_dtype), NQ_ERR_ARG;
+  if (!y || !aligned(y, dtype_size(y_dtype))) return set_error("%s: y null or misaligned", who), NQ_ERR_ARG;
+  // y's own checks are above: any aligned pointer stands in for an fp32 y
+  if ((st = check_io(who, L, x, x_dtype, T, L->s1)) != NQ_OK) return st;
+  if ((st = check_act(who, E->act)) != NQ_OK || (st = check_operand(who, "bias", E->bias, NQ_F32)) != NQ_OK ||
+      (st = check_operand(who, "mul", E->mul, E->mul_dtype)) != NQ_OK ||
+      (st = check_operand(who, "residual", E->residual, E->residual_dtype)) != NQ_OK ||
+      (st = check_operand(who, "z", E->z, E->z_dtype)) != NQ_OK)
+    return st;
+  if ((E->mul == y && E->mul_dtype != y_dtype) || (E->residual == y && E->residual_dtype != y_dtype))
+    return set_error("%s: y in place of an operand of another dtype", who), NQ_ERR_ARG;
+  if (E->z && (E->z == y || E->z == E->mul || E->z == E->residual))
+    return set_error("%s: z in place of y or an operand", who), NQ_ERR_ARG;
+  if ((st = check_workspace(who, workspace, workspace_bytes, linear_act_workspace(*L, T))) != NQ_OK) return st;
+  const Epilogue epi{E->bias,
+                     E->mul,
+                     E->residual,
+                     E->z,
+                     y,
+                     E->act,
+                     E->mul_dtype == NQ_BF16,
+                     E->residual_dtype == NQ_BF16,
+                     E->z_dtype == NQ_BF16,
+                     y_dtype == NQ_BF16};
+  float* v = reinterpret_cast<float*>(static_cast<char*>(workspace) + align_up(linear_workspace(*L, T)));
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = launch_linear(*L, x, x_dtype, T, v, workspace, s);
+  if (e == hipSuccess) e = launch_epilogue(v, T, L->d_out, epi, s);
+  return hip_status(e, "nq_lrb_linear_act launch");
+}
+
+size_t nq_act_grads_workspace_bytes(int64_t T, int64_t d) {
+  const int64_t most = int64_t(1) << 24;
+  return T < 1 || d < 1 || T > most || d > most ? 0 : std::max<size_t>(act_grads_workspace(T, d), kAlign);
+}
+
+nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* mul, nq_dtype mul_dtype, const void* dy,
+                       nq_dtype dy_dtype, int64_t T, int64_t d, void* dz, nq_dtype dz_dtype, void* dmul,
+                       nq_dtype dmul_dtype, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "nq_act_grads";
+  nq_status st = check_act(who, act);
+  if (st != NQ_OK) return st;
+  if (T < 1 || d < 1) return set_error("%s: T=%lld d=%lld must be >= 1", who, (long long)T, (long long)d), NQ_ERR_ARG;
+  if (T > (int64_t(1) << 24) || d > (int64_t(1) << 24)) return set_error("%s: T or d exceeds 2^24", who), NQ_ERR_UNSUPPORTED;
+  if (!dy || !dz) return set_error("%s: null dy or dz", who), NQ_ERR_ARG;
+  if (dmul && !mul) return set_error("%s: dmul without mul", who), NQ_ERR_ARG;
+  const bool needs_z = act != NQ_ACT_NONE || dmul;
+  if (needs_z && !z) return set_error("%s: null z", who), NQ_ERR_ARG;
+  if (!needs_z) z = nullptr;
+  if ((st = check_operand(who, "z", z, z_dtype)) != NQ_OK || (st = check_operand(who, "mul", mul, mul_dtype)) != NQ_OK ||
+      (st = check_operand(who, "dy", dy, dy_dtype)) != NQ_OK || (st = check_operand(who, "dz", dz, dz_dtype)) != NQ_OK ||
+      (st = check_operand(who, "dmul", dmul, dmul_dtype)) != NQ_OK ||
+      (st = check_operand(who, "dbias", dbias, NQ_F32)) != NQ_OK)
+    return st;
+  if (dmul && dmul == dz) return set_error("%s: dmul in place of dz", who), NQ_ERR_ARG;
+  // in place: an element's operands are read before its results are written
+  const struct {
+    const void* out;
+    nq_dtype od;
+    const void* in;
+    nq_dtype id;
+  } pairs[] = {{dz, dz_dtype, dy, dy_dtype},       {dz, dz_dtype, z, z_dtype},       {dz, dz_dtype, mul, mul_dtype},
+               {dmul, dmul_dtype, dy, dy_dtype}, {dmul, dmul_dtype, z, z_dtype}, {dmul, dmul_dtype, mul, mul_dtype}};
+  for (const auto& p : pairs)
+    if (p.out && p.out == p.in && p.od != p.id)
+      return set_error("%s: a result in place of an operand of another dtype", who), NQ_ERR_ARG;
+  if (dbias && (st = check_workspace(who, workspace, workspace_bytes, nq_act_grads_workspace_bytes(T, d))) != NQ_OK)
+    return st;
+  return hip_status(launch_act_grads(act, z, z_dtype, mul, mul_dtype, dy, dy_dtype, T, d, dz, dz_dtype, dmul, dmul_dtype,
+                                     dbias, workspace, (hipStream_t)stream),
+                    "nq_act_grads launch");
+}
+
+namespace {
+
+nq_status check_logits(const char* who, const void* logits, nq_dtype dt, int64_t T, int64_t V, int64_t ld, int64_t k,
+                       float temperature) {
+  if (T < 1 || V < 1 || k < 1)
+    return set_error("%s: T=%lld V=%lld k=%lld must be >= 1", who, (long long)T, (long long)V, (long long)k), NQ_ERR_ARG;
+  if (ld < V) return set_error("%s: row stride %lld < V=%lld", who, (long long)ld, (long long)V), NQ_ERR_ARG;
+  // a workgroup of up to 1024 threads per row, and fewer than 2^32 threads in all
+  if (T > (int64_t(1) << 21) || V > (int64_t(1) << 20) || k > NQ_TOP_MAX)
+    return set_error("%s: T=%lld V=%lld k=%lld exceed 2^21, 2^20, %d", who, (long long)T, (long long)V, (long long)k,
+                     NQ_TOP_MAX),
+           NQ_ERR_UNSUPPORTED;
+  if (!dtype_ok(dt)) return set_error("%s: unknown logits dtype %d", who, (int)dt), NQ_ERR_ARG;
+  if (!logits || !aligned(logits, dtype_size(dt))) return set_error("%s: logits null or misaligned", who), NQ_ERR_ARG;
+  if (!(temperature >= 0x1p-20f && temperature <= 0x1p20f))
+    return set_error("%s: temperature %g outside [2^-20, 2^20]", who, (double)temperature), NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+nq_status check_distill(const char* who, const nq_teacher* P, const void* logits, nq_dtype dt, int64_t T, int64_t V,
+                        int64_t ld, const float* weight, const float* loss) {
+  if (!P) return set_error("%s: null teacher", who), NQ_ERR_ARG;
+  const nq_status st = check_logits(who, logits, dt, T, V, ld, P->k, P->temperature);
+  if (st != NQ_OK) return st;
+  if (!P->ids || !P->logp) return set_error("%s: null teacher ids or logp", who), NQ_ERR_ARG;
+  if (!aligned(P->ids, 4) || !aligned(P->logp, 4) || !aligned(P->rest, 4) || !aligned(weight, 4) || !aligned(loss, 4))
+    return set_error("%s: a teacher's array, weight or loss misaligned", who), NQ_ERR_ARG;
+  return NQ_OK;
+}
+
+}  // namespace
+
+nq_status nq_logits_top(const void* logits, nq_dtype logits_dtype, int64_t T, int64_t V, int64_t ld, int64_t k,
+                        float temperature, int32_t* ids, float* logp, float* rest, void* stream) {
+  clear_error();
+  const char* who = "nq_logits_top";
+  const nq_status st = check_logits(who, logits, logits_dtype, T, V, ld, k, temperature);
+  if (st != NQ_OK) return st;
+  if (!ids || !logp || !aligned(ids, 4) || !aligned(logp, 4) || !aligned(rest, 4))
+    return set_error("%s: ids or logp null, or a result misaligned", who), NQ_ERR_ARG;
+  return hip_status(launch_logits_top(logits, logits_dtype, T, V, ld, (int)k, temperature, ids, logp, rest,
+                                      (hipStream_t)stream),
+                    "nq_logits_top launch");
+}
+
+nq_status nq_distill_loss(const nq_teacher* P, const void* logits, nq_dtype logits_dtype, int64_t T, int64_t V,
+                          int64_t ld, const float* weight, float* loss, void* stream) {
+  clear_error();
+  const char* who = "nq_distill_loss";
+  const nq_status st = check_distill(who, P, logits, logits_dtype, T, V, ld, weight, loss);
+  if (st != NQ_OK) return st;
+  if (!loss) return set_error("%s: null loss", who), NQ_ERR_ARG;
+  return hip_status(launch_distill(*P, logits, logits_dtype, T, V, ld, weight, loss, nullptr, NQ_F32, V,
+                                   (hipStream_t)stream),
+                    "nq_distill_loss launch");
+}
+
+nq_status nq_distill_grads(const nq_teacher* P, const void* logits, nq_dtype logits_dtype, int64_t T, int64_t V,
+                           int64_t ld, const float* weight, float* loss, void* dlogits, nq_dtype dlogits_dtype,
+                           int64_t ldd, void* stream) {
+  clear_error();
+  const char* who = "nq_distill_grads";
+  const nq_status st = check_distill(who, P, logits, logits_dtype, T, V, ld, weight, loss);
+  if (st != NQ_OK) return st;
+  if (!dtype_ok(dlogits_dtype)) return set_error("%s: unknown dlogits dtype %d", who, (int)dlogits_dtype), NQ_ERR_ARG;
+  if (!dlogits || !aligned(dlogits, dtype_size(dlogits_dtype)))
+    return set_error("%s: dlogits null or misaligned", who), NQ_ERR_ARG;
+  if (ldd < V) return set_error("%s: row stride %lld < V=%lld", who, (long long)ldd, (long long)V), NQ_ERR_ARG;
+  if (dlogits == logits && (dlogits_dtype != logits_dtype || ldd != ld))
+    return set_error("%s: dlogits in place of logits of another dtype or stride", who), NQ_ERR_ARG;
+  return hip_status(launch_distill(*P, logits, logits_dtype, T, V, ld, weight, loss, dlogits, dlogits_dtype, ldd,
+                                   (hipStream_t)stream),
+                    "nq_distill_grads launch");
 }
 
 size_t nq_balance_workspace_bytes(int64_t d_out, int64_t d_in) {

@@ -195,6 +195,20 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
                              const int32_t* ids, int64_t T, const float* dx_base, float* dx, float* da, float* db,
                              void* workspace, hipStream_t s);
 
+// Epilogue of a packed linear and its gradients (act.hip; epilogue.h has the element).
+struct Epilogue;
+hipError_t launch_epilogue(const float* v, int64_t T, int64_t d, const Epilogue& E, hipStream_t s);
+size_t act_grads_workspace(int64_t T, int64_t d);
+hipError_t launch_act_grads(int act, const void* z, nq_dtype zd, const void* mul, nq_dtype md, const void* dy,
+                            nq_dtype dyd, int64_t T, int64_t d, void* dz, nq_dtype dzd, void* dmul, nq_dtype dmd,
+                            float* dbias, void* ws, hipStream_t s);
+
+// A teacher's top logits, the divergence of a student's from them and its gradient (distill.hip).
+hipError_t launch_logits_top(const void* logits, nq_dtype dt, int64_t T, int64_t V, int64_t ld, int k, float temperature,
+                             int32_t* ids, float* logp, float* rest, hipStream_t s);
+hipError_t launch_distill(const nq_teacher& P, const void* logits, nq_dtype dt, int64_t T, int64_t V, int64_t ld,
+                          const float* weight, float* loss, void* dlogits, nq_dtype dd, int64_t ldd, hipStream_t s);
+
 // Orthogonalised updates (ortho.hip).  Singular values of iterates stay below
 // kOrthoRange, for which the operands are scaled; ortho_rounding: the relative
 // rounding of an operand (root mean square).

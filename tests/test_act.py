@@ -1,0 +1,363 @@
+"""The packed linear's epilogue and its gradients, against the fp64 reference.
+
+The epilogue's tolerance takes the layer's own output as given (nq_lrb_linear's, fp32: the same products and sums)
+and counts the epilogue's roundings (oracle.distill.epilogue_ref, act_grads_ref) and that of the result, half a step
+of its type.  Against the layer's fp64 oracle the bars are the layer's own (tests/gpu_cases.py), plus the rounding of
+the result and the roundings of the epilogue."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import distill as D
+from oracle import nq_oracle as O
+from tests import gpu_cases as G
+
+nq = pytest.importorskip("sub_bit_weight_amd")
+
+DEV = "cuda:0"
+DUMMY = 0x100000
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+gpu = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- the reference
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_reference_derivative_matches_differences(act):
+    z = np.linspace(-6, 6, 241) + 0.013
+    num = (D.act_ref(act, z + 1e-5)[0] - D.act_ref(act, z - 1e-5)[0]) / 2e-5
+    assert np.allclose(D.act_ref(act, z)[1], num, atol=1e-9)
+
+
+def test_reference_activations_are_torchs():
+    z = torch.linspace(-7, 7, 301, dtype=torch.float64)
+    f = torch.nn.functional
+    for act, want in (("relu", f.relu(z)), ("gelu", f.gelu(z)), ("gelu_tanh", f.gelu(z, approximate="tanh")),
+                      ("silu", f.silu(z))):
+        assert np.allclose(D.act_ref(act, z.numpy())[0], want.numpy(), rtol=1e-12, atol=1e-14), act
+
+
+# ---------------------------------------------------------------- refusals (no GPU)
+
+
+def _layer(**kw):
+    d = dict(d_out=64, d_in=64, r=32, u_bits=DUMMY, ldu=64, vt_bits=DUMMY, ldv=32, s1=DUMMY, s2=DUMMY)
+    d.update(kw)
+    return nq.nq_lrb(**d)
+
+
+def _linear(L=None, x=DUMMY, xd=nq.NQ_BF16, T=3, y=2 * DUMMY, yd=nq.NQ_BF16, ws=DUMMY, wsb=1 << 40, null=False, **kw):
+    e = nq.nq_epilogue(**{**dict(act=0), **kw})
+    L = L or _layer()
+    return nq.lib().nq_lrb_linear_act(ctypes.byref(L), x, xd, T, None if null else ctypes.byref(e), y, yd, ws, wsb, None)
+
+
+def _grads(act=4, z=DUMMY, zd=1, mul=3 * DUMMY, md=1, dy=5 * DUMMY, dyd=1, T=3, d=64, dz=7 * DUMMY, dzd=1, dmul=9 * DUMMY,
+           dmd=1, db=DUMMY, ws=DUMMY, wsb=1 << 30):
+    return nq.lib().nq_act_grads(act, z, zd, mul, md, dy, dyd, T, d, dz, dzd, dmul, dmd, db, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(null=True), dict(act=-1), dict(act=5), dict(T=0), dict(x=None), dict(xd=4), dict(y=None), dict(yd=2),
+    dict(y=DUMMY + 1), dict(yd=0, y=DUMMY + 2), dict(bias=DUMMY + 2), dict(mul=DUMMY + 1, mul_dtype=1),
+    dict(mul=DUMMY, mul_dtype=3), dict(residual=DUMMY + 2, residual_dtype=0), dict(residual=DUMMY, residual_dtype=-1),
+    dict(z=DUMMY, z_dtype=9), dict(z=DUMMY + 1, z_dtype=1), dict(z=2 * DUMMY, z_dtype=1),
+    dict(z=DUMMY, z_dtype=1, mul=DUMMY, mul_dtype=1), dict(mul=2 * DUMMY, mul_dtype=0),
+    dict(residual=2 * DUMMY, residual_dtype=0), dict(ws=DUMMY + 4), dict(L=_layer(d_in=0)), dict(L=_layer(ldu=1))])
+def test_linear_rejects(kw):
+    assert _linear(**kw) == nq.NQ_ERR_ARG and nq.last_error() != ""
+
+
+def test_linear_rejects_workspace_and_sizes():
+    assert _linear(ws=None) == nq.NQ_ERR_WORKSPACE
+    assert _linear(wsb=4) == nq.NQ_ERR_WORKSPACE
+    assert _linear(T=(1 << 24) + 1) == nq.NQ_ERR_UNSUPPORTED
+    q = nq.lib().nq_lrb_act_workspace_bytes
+    assert q(ctypes.byref(_layer(r=0)), 3) == 0 and q(ctypes.byref(_layer()), 0) == 0
+    for T in (1, 8, 9, 1000):
+        assert q(ctypes.byref(_layer()), T) >= nq.lib().nq_lrb_workspace_bytes(ctypes.byref(_layer()), T)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=9), 1), (dict(T=0), 1), (dict(d=0), 1), (dict(T=(1 << 24) + 1), 2), (dict(d=(1 << 24) + 1), 2),
+    (dict(dy=None), 1), (dict(dz=None), 1), (dict(z=None), 1), (dict(act=0, z=None), 1), (dict(mul=None), 1),
+    (dict(zd=2), 1), (dict(md=-1), 1), (dict(dyd=7), 1), (dict(dzd=5), 1), (dict(dmd=3), 1), (dict(db=DUMMY + 2), 1),
+    (dict(dy=DUMMY + 1), 1), (dict(dzd=0, dz=DUMMY + 2), 1), (dict(dmul=7 * DUMMY), 1), (dict(dz=5 * DUMMY, dzd=0), 1),
+    (dict(dmul=3 * DUMMY, dmd=0), 1), (dict(dz=DUMMY, dzd=0), 1), (dict(ws=None), 3), (dict(wsb=1), 3), (dict(ws=DUMMY + 8), 1)])
+def test_grads_reject(kw, status):
+    assert _grads(**kw) == status and nq.last_error() != ""
+
+
+def test_grads_workspace_query():
+    q = nq.lib().nq_act_grads_workspace_bytes
+    assert q(0, 4) == 0 and q(4, 0) == 0 and q(1 << 25, 1) == 0 and q(1, 1) >= 1 and q(4096, 1000) >= 1
+
+
+# ---------------------------------------------------------------- GPU
+
+
+def _act_layer(d_out, d_in, r):
+    """A layer whose outputs are around one, and its oracle."""
+    dev, ref, _ = G.latent_layer(G.tiny_config(f"act/{d_out}/{d_in}/{r}"), synth.LayerShape("act", d_out, d_in, r))
+    for t, a, n in ((dev.s1, ref.s1, r), (dev.s2, ref.s2, d_in)):
+        t.mul_(50.0 / np.sqrt(n))
+        a[:] = t.cpu().numpy()
+    return dev, ref
+
+
+def _np(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def _rand(tag, shape, dtype):
+    return torch.from_numpy(synth.normal_f32(f"act/{tag}", shape)).to(DEV).to(dtype)
+
+
+def _close(got, want, err, what):
+    got, tol = _np(got), err + HALF[got.dtype] * np.abs(want)
+    with np.errstate(invalid="ignore"):
+        bad = ~((np.abs(got - want) <= tol) | (got == want) | (np.isnan(got) & np.isnan(want)))
+    assert not bad.any(), (what, np.argwhere(bad)[:4], got[bad][:4], want[bad][:4], tol[bad][:4])
+
+
+SHAPES = [(1, 1, 1), (200, 130, 70), (256, 256, 64), (1100, 130, 70), (1111, 1030, 517), (3000, 700, 520)]
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 40, 200])
+@pytest.mark.parametrize("d_out,d_in,r", SHAPES)
+def test_linear_act(d_out, d_in, r, T):
+    layer, ref = _act_layer(d_out, d_in, r)
+    bias = _rand("bias", (d_out,), torch.float32)
+    for i, act in enumerate(ACTS):
+        for xd in ("bf16", "f32"):
+            dt = TYPES[xd]
+            x = _rand(f"x/{d_in}", (T, d_in), dt)
+            mul, res = _rand("mul", (T, d_out), dt), _rand("res", (T, d_out), TYPES["f32" if i % 2 else xd])
+            z = torch.empty(T, d_out, dtype=dt, device=DEV)
+            v = nq.lrb_linear(layer, x)
+            for kw in (dict(), dict(bias=bias, mul=mul, residual=res), dict(bias=bias, z=z), dict(mul=mul, z=z),
+                       dict(residual=res, out_dtype=torch.bfloat16), dict(bias=bias, mul=mul, out_dtype=torch.float32)):
+                y = nq.lrb_linear_act(layer, x, act=act, **kw)
+                assert y.dtype == kw.get("out_dtype", dt)
+                want, wz, err = D.epilogue_ref(_np(v), act, *[None if kw.get(n) is None else _np(kw[n])
+                                                              for n in ("bias", "mul", "residual")])
+                _close(y, want, err, (act, xd, list(kw)))
+                if "z" in kw:
+                    _close(z, wz, np.abs(wz) * D.EPS32, (act, "z"))
+            # against the oracle of the whole layer: the layer's bar, a gated activation being at most 1.13-Lipschitz
+            if T <= 40 or d_out < 300:
+                y0 = O.linear_ref(ref, _np(x).astype(np.float32))
+                want, _, err = D.epilogue_ref(y0, act, _np(bias), None, _np(res))
+                y = nq.lrb_linear_act(layer, x, act=act, bias=bias, residual=res, out_dtype=torch.float32)
+                bar = 1.2 * G.tol_for(T, xd) * np.linalg.norm(y0) + np.linalg.norm(err + D.EPS32 * np.abs(want))
+                assert np.linalg.norm(_np(y) - want) <= bar, (act, xd)
+
+
+@gpu
+@pytest.mark.parametrize("T", [2, 30, 130])
+def test_linear_act_in_place_and_given_outputs(T):
+    layer, _ = _act_layer(1100, 600, 530)
+    for dt in (torch.float32, torch.bfloat16):
+        x, mul, res = _rand("ip/x", (T, 600), dt), _rand("ip/mul", (T, 1100), dt), _rand("ip/res", (T, 1100), dt)
+        want = nq.lrb_linear_act(layer, x, "silu", mul=mul, residual=res)
+        a, b = mul.clone(), res.clone()
+        assert nq.lrb_linear_act(layer, x, "silu", mul=a, residual=res, y=a) is a and torch.equal(a, want)
+        assert torch.equal(nq.lrb_linear_act(layer, x, "silu", mul=mul, residual=b, y=b), want)
+        ws = torch.full((nq.lrb_act_workspace_bytes(layer, T) + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+        y = torch.full((T + 2, 1100), 3.0, dtype=dt, device=DEV)
+        nq.lrb_linear_act(layer, x, "silu", mul=mul, residual=res, y=y[1:T + 1], workspace=ws[:-512])
+        assert torch.equal(y[1:T + 1], want) and (y[0] == 3).all() and (y[T + 1] == 3).all() and (ws[-512:] == 0x5A).all()
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 5, 20])
+def test_linear_act_of_infinite_and_extreme_values(T):
+    """Large arguments of either sign reach the activations' limits; NaN in an operand stays at its element."""
+    layer, _ = _act_layer(300, 40, 33)
+    x = _rand("inf/x", (T, 40), torch.float32)
+    bias = torch.zeros(300, device=DEV)
+    bias[:12] = torch.tensor([1e4, -1e4, 1e30, -1e30, float("inf"), float("-inf"), float("nan"), 88.0, -88.0, -104.0, 30.0,
+                              -30.0], device=DEV)
+    mul, res = _rand("inf/mul", (T, 300), torch.float32), _rand("inf/res", (T, 300), torch.float32)
+    mul[0, 20], res[T - 1, 30] = float("nan"), float("inf")
+    v = _np(nq.lrb_linear(layer, x))
+    for act in ACTS:
+        got = _np(nq.lrb_linear_act(layer, x, act, bias=bias, mul=mul, residual=res))
+        with np.errstate(all="ignore"):
+            want, _, err = D.epilogue_ref(v, act, _np(bias), _np(mul), _np(res))
+        ok = np.isfinite(want) & np.isfinite(err)
+        assert (np.abs(got - want)[ok] <= (err + D.EPS32 * np.abs(want))[ok]).all(), act
+        assert np.array_equal(np.isnan(got), np.isnan(want)), act
+
+
+GRADS = [(1, 1), (3, 7), (5, 64), (64, 300), (65, 1117), (200, 257), (777, 1000), (2100, 96), (300, 4104)]
+
+
+@gpu
+@pytest.mark.parametrize("T,d", GRADS)
+def test_act_grads(T, d):
+    for act in ACTS:
+        for dt in (torch.float32, torch.bfloat16):
+            z, dy = 2 * _rand("g/z", (T, d), dt), _rand("g/dy", (T, d), dt)
+            for mul in (None, _rand("g/mul", (T, d), dt)):
+                dz, dmul, dbias = nq.act_grads(act, z, dy, mul=mul)
+                wz, wm, wb, (ez, em, eb) = D.act_grads_ref(act, _np(z), _np(dy), None if mul is None else _np(mul))
+                _close(dz, wz, ez, (act, "dz"))
+                _close(dbias, wb, eb, (act, "dbias"))
+                assert (dmul is None) == (mul is None)
+                if mul is not None:
+                    _close(dmul, wm, em, (act, "dmul"))
+                again = nq.act_grads(act, z, dy, mul=mul)
+                assert torch.equal(again[2], dbias) and torch.equal(again[0], dz)
+                assert nq.act_grads(act, z, dy, mul=mul, bias=False)[2] is None
+
+
+@gpu
+def test_act_grads_mixed_types_in_place_and_strange_operands():
+    T, d = 90, 513
+    z, dy, mul = _rand("m/z", (T, d), torch.float32), _rand("m/dy", (T, d), torch.bfloat16), _rand("m/mul", (T, d), torch.float32)
+    dz = torch.empty(T, d, device=DEV)
+    dmul = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+    got = nq.act_grads("gelu", z, dy, mul=mul, dz=dz, dmul=dmul)
+    wz, wm, wb, (ez, em, eb) = D.act_grads_ref("gelu", _np(z), _np(dy), _np(mul))
+    assert got[0] is dz and got[1] is dmul
+    _close(dz, wz, ez, "dz"), _close(dmul, wm, em, "dmul"), _close(got[2], wb, eb, "dbias")
+    a, b = dy.float(), mul.clone()
+    dz2, dmul2, _ = nq.act_grads("gelu", z, a, mul=b, dz=a, dmul=b)
+    assert dz2 is a and dmul2 is b and torch.equal(a, dz)
+    _close(b, wm, em, "dmul")
+    c = z.clone()
+    assert torch.equal(nq.act_grads("gelu", c, dy.float(), mul=mul, dz=c)[0], dz)
+    # without z: act none and no gate
+    dz3, none, db3 = nq.act_grads("none", None, dy)
+    assert none is None and torch.equal(dz3, dy)
+    _close(db3, _np(dy).sum(0), T * D.EPS32 * np.abs(_np(dy)).sum(0), "dbias")
+    # a misaligned view, rows of padding that hold nothing
+    flat = torch.zeros(T * d + 3, dtype=torch.bfloat16, device=DEV)
+    flat[1:1 + T * d].copy_(dy.flatten())
+    assert torch.equal(nq.act_grads("relu", z, flat[1:1 + T * d].view(T, d))[0], nq.act_grads("relu", z, dy)[0])
+    z[3], dy[5] = float("nan"), 0.0
+    dz4, _, db4 = nq.act_grads("silu", z, dy)
+    assert torch.isnan(dz4[3]).all() and torch.isnan(db4).all() and (dz4[5] == 0).all() and torch.isfinite(dz4[6]).all()
+
+
+@gpu
+def test_streams_and_captured_calls():
+    layer, _ = _act_layer(1100, 600, 530)
+    ws = {}
+    side = torch.cuda.Stream()
+    for T in (4, 50):
+        xs = [_rand(f"cap/{T}/{i}", (T, 600), torch.bfloat16) for i in range(3)]
+        dys = [_rand(f"cap/{T}/dy/{i}", (T, 1100), torch.bfloat16) for i in range(3)]
+        mul = _rand(f"cap/{T}/mul", (T, 1100), torch.bfloat16)
+        z = torch.empty(T, 1100, dtype=torch.bfloat16, device=DEV)
+
+        def run(x, dy, z, **kw):
+            y = nq.lrb_linear_act(layer, x, "silu", mul=mul, z=z, **kw)
+            return (y, *nq.act_grads("silu", z, dy, mul=mul, **({"stream": kw["stream"]} if "stream" in kw else {})))
+        want = [[t.clone() for t in run(x, dy, z)] for x, dy in zip(xs, dys)]
+        side.wait_stream(torch.cuda.current_stream())
+        got = run(xs[0], dys[0], z, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
+        x, dy, z2 = xs[0].clone(), dys[0].clone(), torch.empty_like(z)
+        ws[T] = torch.empty(nq.lrb_act_workspace_bytes(layer, T), dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run(x, dy, z2, workspace=ws[T])
+        for i in (0, 1, 2, 1):
+            x.copy_(xs[i]), dy.copy_(dys[i])
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i])), (T, i)
+            run(xs[0], dys[0], z)  # eager work between the replays
+
+
+@gpu
+def test_binding_refuses_wrong_tensors():
+    layer, _ = _act_layer(200, 130, 70)
+    x = torch.zeros(4, 130, device=DEV)
+    row = torch.zeros(4, 200, device=DEV)
+    for kw in (dict(x=x[:, :60].contiguous()), dict(x=x.half()), dict(x=x.cpu()), dict(act="tanh"), dict(bias=row[0].bfloat16()),
+               dict(bias=row[0, :5]), dict(mul=row[:3]), dict(mul=row.half()), dict(residual=row.cpu()),
+               dict(residual=torch.zeros(4, 400, device=DEV)[:, ::2]), dict(z=row.double()), dict(y=row[:2]),
+               dict(y=row, out_dtype=torch.bfloat16), dict(out_dtype=torch.float16),
+               dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            nq.lrb_linear_act(**{**dict(layer=layer, x=x), **kw})
+    for kw in (dict(y=row, z=row), dict(mul=row.bfloat16(), y=row.bfloat16(), workspace=torch.empty(16, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(nq.NqError):
+            nq.lrb_linear_act(layer, x, **kw)
+    for kw in (dict(z=None), dict(z=row[:2]), dict(dy=row.half()), dict(mul=row[:, :9]), dict(dmul=row), dict(dz=row[:1]),
+               dict(act="x"), dict(dy=row[0]), dict(dz=row.cpu())):
+        with pytest.raises(ValueError):
+            nq.act_grads(**{**dict(act="silu", z=row, dy=row), **kw})
+
+
+# ---------------------------------------------------------------- a step of scale-only reconstruction
+
+
+
+
+@gpu
+@pytest.mark.parametrize("T", [6, 40])
+def test_a_step_of_scale_only_reconstruction(T):
+    """A packed gated block (up, gate with silu and the up's output, down with a residual) and a packed head, its
+    logits against a teacher's record: the loss and every gradient of the scales against fp64 automatic
+    differentiation of the same formulas.  Bars: every product of the chain is within the layer's own bar of
+    its exact value (G.tol_for, fp32 activations), and a gradient passes through at most eight of them."""
+    d, f, V, k = 96, 260, 1000, 30
+    names = dict(up=(f, d, 60), gate=(f, d, 60), down=(d, f, 60), head=(V, d, 70))
+    layers = {n: _act_layer(*shape) for n, shape in names.items()}
+    dev = {n: v[0] for n, v in layers.items()}
+    adj = {n: nq.Adjoint.of(v) for n, v in dev.items()}
+    x = _rand(f"step/{T}/x", (T, d), torch.float32)
+    bias = 0.1 * _rand("step/bias", (f,), torch.float32)
+    teacher = nq.logits_top(3 * _rand(f"step/{T}/teacher", (T, V), torch.float32), k)
+    w = torch.full((T,), 1.0 / T, device=DEV)
+
+    up = nq.lrb_linear_act(dev["up"], x)
+    z = torch.empty(T, f, device=DEV)
+    h = nq.lrb_linear_act(dev["gate"], x, "silu", bias=bias, mul=up, z=z)
+    hidden = nq.lrb_linear_act(dev["down"], h, residual=x)
+    logits = nq.lrb_linear_act(dev["head"], hidden)
+    loss, dlogits = nq.distill_grads(teacher, logits, weight=w)
+    dhidden, *head = nq.lrb_scale_grads(dev["head"], adj["head"], hidden, dlogits)
+    dh, *down = nq.lrb_scale_grads(dev["down"], adj["down"], h, dhidden)
+    dz, dup, dbias = nq.act_grads("silu", z, dh, mul=up)
+    dx_gate, *gate = nq.lrb_scale_grads(dev["gate"], adj["gate"], x, dz)
+    dx_up, *ups = nq.lrb_scale_grads(dev["up"], adj["up"], x, dup)
+    dx = dx_gate + dx_up + dhidden
+
+    p64 = {n: [torch.tensor(v[1].s1, dtype=torch.float64, requires_grad=True),
+               torch.tensor(v[1].s2, dtype=torch.float64, requires_grad=True),
+               torch.from_numpy(np.array(v[1].U(), dtype=np.float64)), torch.from_numpy(np.array(v[1].Vt().T, dtype=np.float64))]
+           for n, v in layers.items()}
+
+    def lin(n, a):
+        s1, s2, u, v = p64[n]
+        return ((a * s2) @ v @ u.T) * s1
+    x64 = x.double().cpu().requires_grad_()
+    b64 = bias.double().cpu().requires_grad_()
+    hid = lin("down", torch.nn.functional.silu(lin("gate", x64) + b64) * lin("up", x64)) + x64
+    logq = torch.log_softmax(lin("head", hid), 1)
+    ids, lp, rest = teacher.ids.long().cpu(), teacher.logp.double().cpu(), teacher.rest.double().cpu()
+    away = torch.logsumexp(logq.scatter(1, ids, -float("inf")), 1)
+    loss64 = (lp.exp() * (lp - logq.gather(1, ids))).sum(1) + rest.exp() * (rest - away)
+    (loss64 / T).sum().backward()
+    assert np.linalg.norm(_np(loss) - loss64.detach().numpy() / T) <= 8e-5 * np.linalg.norm(loss64.detach().numpy() / T)
+    got = dict(head=head, down=down, gate=gate, up=ups)
+    for n, g in got.items():
+        for a, b in zip(g, p64[n][:2]):
+            assert np.linalg.norm(_np(a) - b.grad.numpy()) <= 8e-5 * np.linalg.norm(b.grad.numpy()), n
+    for a, b in ((dx, x64), (dbias, b64)):
+        assert np.linalg.norm(_np(a) - b.grad.numpy()) <= 8e-5 * np.linalg.norm(b.grad.numpy())
