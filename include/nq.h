@@ -552,7 +552,9 @@ nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* 
  *   the same type and stride (in place).  loss may be null.
  * Both read the logits from memory once for V up to 131072 (bf16) or 65536 (fp32);
  * exponentials are fp32, the sums over a row fp32 per thread and fp64 across, the
- * loss is formed in fp64 and rounded once, each gradient rounded once.  Deterministic.
+ * loss is formed in fp64 and rounded once, each gradient rounded once.  Deterministic;
+ * the order of the sums depends on T, V and the call, so the two calls' losses agree
+ * to rounding.
  * Logits that are not finite stay within their row, infinite or NaN as the formulas
  * are (a row of -inf alone has no softmax: NaN; a token of logit -inf has q = 0).
  * No workspace.

@@ -34,7 +34,8 @@ __device__ inline void row_store(void* p, bool bf16, int64_t i, float v) {
 struct ExpScale {
   float hi, lo;
 };
-__device__ inline float exp_scaled(float d, ExpScale c) { return exp2f(fmaf(d, c.hi, d * c.lo)); }
+// The hardware's 2^x: one unit in the last place, and 0 below 2^-126.
+__device__ inline float exp_scaled(float d, ExpScale c) { return __builtin_amdgcn_exp2f(fmaf(d, c.hi, d * c.lo)); }
 ExpScale exp_scale(float tau) {
   const double c = kLog2e / (double)tau;
   float hi = (float)c;
@@ -83,152 +84,395 @@ struct MaxSum {
 
 // ------------------------------------------------------------------ the divergence and its gradient
 
-constexpr int kDistillThreads = 512;
-constexpr int kEntries = (NQ_TOP_MAX + kDistillThreads - 1) / kDistillThreads;  // per thread
+struct DistillArgs {
+  nq_teacher P;
+  ExpScale c;
+  const void* logits;
+  int64_t ld;
+  const float* weight;
+  float* loss;
+  void* dlogits;
+  int64_t ldd;
+  int V;
+};
 
 struct RowConsts {  // of one row, for every thread
-  double base, lse, total, scale;
+  double base, lse, total, scale, w;
   float ref, coef;
   int zero;
 };
 
-// LDS: [bitmap of the listed tokens, V bits][ids][logits][probabilities of the k entries].
+// LDS of a row: [bitmap of the listed tokens, whole words][ids][logits][probabilities of the k entries].
 // An entry's id is -1 where there is none, and -2 - id for a repetition of an earlier entry.
-template <bool GRADS>
-__global__ __launch_bounds__(kDistillThreads) void distill_kernel(const nq_teacher P, ExpScale c, const void* logits,
-                                                                  int bf16, int V, int64_t ld,
-                                                                  const float* __restrict__ weight,
-                                                                  float* __restrict__ loss, void* dlogits, int d_bf16,
-                                                                  int64_t ldd) {
-  constexpr int NT = kDistillThreads;
-  extern __shared__ uint32_t lds[];
-  __shared__ double red[NT / 64];
-  __shared__ RowConsts row;
-  __shared__ int s_bad, s_dup;
-  const int tid = threadIdx.x, k = (int)P.k, nw = (V + 31) / 32;
-  uint32_t* listed = lds;
-  int* ids = reinterpret_cast<int*>(lds + nw);
-  float* sv = reinterpret_cast<float*>(ids + k);
-  float* ps = sv + k;
-  const int64_t t = blockIdx.x;
-  const char* x = static_cast<const char*>(logits) + t * ld * (bf16 ? 2 : 4);
-  char* dx = GRADS ? static_cast<char*>(dlogits) + t * ldd * (d_bf16 ? 2 : 4) : nullptr;
-  const float w = weight ? weight[t] : 1.0f;
-  auto constant_row = [&](float v) {
-    if (tid == 0 && loss) loss[t] = v;
-    if (GRADS)
-      for (int i = tid; i < V; i += NT) row_store(dx, d_bf16, i, v);
-  };
-  if (w == 0.0f) return constant_row(0.0f);
+struct RowLds {
+  uint32_t* listed;
+  int* ids;
+  float *sv, *ps;
+  __device__ RowLds(uint32_t* lds, int V, int k) {
+    listed = lds;
+    ids = reinterpret_cast<int*>(lds + (V + 31) / 32);
+    sv = reinterpret_cast<float*>(ids + k);
+    ps = sv + k;
+  }
+};
+size_t row_lds_bytes(int64_t V, int64_t k) { return (size_t)cdiv(V, 32) * 4 + (size_t)k * 12; }
 
-  if (tid == 0) s_bad = s_dup = 0;
-  for (int i = tid; i < nw; i += NT) listed[i] = 0;
+template <int NT>
+struct RowShared {
+  double red[NT / 64][4];
+  RowConsts row;
+  int bad, dup;
+};
+
+template <bool BF16>
+__device__ inline const char* row_at(const void* p, int64_t t, int64_t ld) {
+  return static_cast<const char*>(p) + t * ld * (BF16 ? 2 : 4);
+}
+
+// The entries of row t into LDS and the bitmap.  False: an id is out of range.
+template <int NT, bool BF16>
+__device__ bool row_entries(const DistillArgs& A, int64_t t, const char* x, const RowLds& L, RowShared<NT>& S) {
+  const int tid = threadIdx.x, k = (int)A.P.k, V = A.V;
+  if (tid == 0) S.bad = S.dup = 0;
+  for (int i = tid; i < (V + 31) / 32; i += NT) L.listed[i] = 0;
   __syncthreads();
-  const int32_t* gid = P.ids + t * k;
-  const float* glp = P.logp + t * k;
   for (int e = tid; e < k; e += NT) {
-    const int id = gid[e];
+    const int id = A.P.ids[t * k + e];
     float s = -kInf, p = 0.0f;
     if (id >= V) {
-      s_bad = 1;
+      S.bad = 1;
     } else if (id >= 0) {
-      if (atomicOr(&listed[id / 32], 1u << (id % 32)) >> (id % 32) & 1u) s_dup = 1;
-      s = row_load(x, bf16, id);
-      p = expf(glp[e]);
+      if (atomicOr(&L.listed[id / 32], 1u << (id % 32)) >> (id % 32) & 1u) S.dup = 1;
+      s = row_load(x, BF16, id);
+      p = expf(A.P.logp[t * k + e]);
     }
-    ids[e] = id < 0 ? -1 : id;
-    sv[e] = s;
-    ps[e] = p;
+    L.ids[e] = id < 0 ? -1 : id;
+    L.sv[e] = s;
+    L.ps[e] = p;
   }
   __syncthreads();
-  if (s_bad) return constant_row(__builtin_nanf(""));
-  if (s_dup) {  // the first of equal entries takes the probabilities of all
+  if (S.bad) return false;
+  if (S.dup) {  // the first of equal entries takes the probabilities of all
+    constexpr int kEntries = (NQ_TOP_MAX + NT - 1) / NT;  // per thread
     float sum[kEntries];
     bool again[kEntries];
     for (int i = 0, e = tid; i < kEntries; ++i, e += NT) {
       sum[i] = 0.0f;
       again[i] = false;
-      if (e >= k || ids[e] < 0) continue;
+      if (e >= k || L.ids[e] < 0) continue;
       for (int f = 0; f < k; ++f)
-        if (ids[f] == ids[e]) {
+        if (L.ids[f] == L.ids[e]) {
           again[i] |= f < e;
-          sum[i] += ps[f];
+          sum[i] += L.ps[f];
         }
     }
     __syncthreads();
     for (int i = 0, e = tid; i < kEntries; ++i, e += NT)
-      if (e < k && ids[e] >= 0) {
-        ps[e] = sum[i];
-        if (again[i]) ids[e] = -2 - ids[e];
+      if (e < k && L.ids[e] >= 0) {
+        L.ps[e] = sum[i];
+        if (again[i]) L.ids[e] = -2 - L.ids[e];
       }
     __syncthreads();
   }
+  return true;
+}
 
-  MaxSum rest;
-  for (int i = tid; i < V; i += NT)
-    if (!(listed[i / 32] >> (i % 32) & 1u)) rest.add(row_load(x, bf16, i), c);
-  const float m_r = wg_max<NT>(rest.m, red);
-  const float ref = m_r == -kInf ? 0.0f : m_r;
-  const double s_r = wg_sum<NT>((double)rest.s * (double)exp_scaled(rest.m == -kInf ? 0.0f : rest.m - ref, c), red);
-
-  float m_k = -kInf;
+// The row's loss and the constants of its gradient, from each thread's maximum m and sum s (relative
+// to its maximum) over the tokens not listed that it has read.
+template <int NT>
+__device__ RowConsts row_finish(const DistillArgs& A, int64_t t, float w, float m, float s, const RowLds& L,
+                                RowShared<NT>& S) {
+  constexpr int W = NT / 64;  // waves, a power of two
+  const int tid = threadIdx.x, k = (int)A.P.k, lane = tid % 64, wave = tid / 64;
+  float m_k = -kInf, m_r = m;
   for (int e = tid; e < k; e += NT)
-    if (ids[e] != -1) m_k = fmaxf(m_k, sv[e]);
-  m_k = wg_max<NT>(m_k, red);
+    if (L.ids[e] != -1) m_k = fmaxf(m_k, L.sv[e]);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    m_r = fmaxf(m_r, __shfl_xor(m_r, o));
+    m_k = fmaxf(m_k, __shfl_xor(m_k, o));
+  }
+  if (lane == 0) {
+    S.red[wave][0] = (double)m_r;
+    S.red[wave][1] = (double)m_k;
+  }
+  __syncthreads();
+  m_r = (float)S.red[lane % W][0];
+  m_k = (float)S.red[lane % W][1];
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) {
+    m_r = fmaxf(m_r, __shfl_xor(m_r, o));
+    m_k = fmaxf(m_k, __shfl_xor(m_k, o));
+  }
   // everything relative to the row's largest logit, at which an fp64 number of its own size may not
   // hold the logarithms
-  const float top = fmaxf(m_r, m_k);
-  const double base = top == -kInf ? 0.0 : (double)top, rtau = 1.0 / (double)P.temperature;
-  double s_k = 0.0, mass = 0.0, cross = 0.0;  // sum p, sum p (log p - s / tau)
+  const float ref = m_r == -kInf ? 0.0f : m_r, top = fmaxf(m_r, m_k);
+  const double base = top == -kInf ? 0.0 : (double)top, rtau = 1.0 / (double)A.P.temperature;
+  // sums: of the rest, of the listed tokens' exponentials, of p and of p (log p - s / tau)
+  double sum[4] = {(double)s * (double)exp_scaled(m == -kInf ? 0.0f : m - ref, A.c), 0.0, 0.0, 0.0};
   for (int e = tid; e < k; e += NT) {
-    if (ids[e] == -1) continue;
-    const double sx = ((double)sv[e] - base) * rtau;
-    if (ids[e] >= 0) s_k += exp(sx);
-    const double lp = glp[e], p = exp(lp);
+    if (L.ids[e] == -1) continue;
+    const double sx = ((double)L.sv[e] - base) * rtau;
+    if (L.ids[e] >= 0) sum[1] += exp(sx);
+    const double lp = A.P.logp[t * k + e], p = exp(lp);
     if (p == 0.0) continue;
-    mass += p;
-    cross += p * (lp - sx);
+    sum[2] += p;
+    sum[3] += p * (lp - sx);
   }
-  s_k = wg_sum<NT>(s_k, red);
-  mass = wg_sum<NT>(mass, red);
-  cross = wg_sum<NT>(cross, red);
-
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], o);
+  __syncthreads();
+  if (lane == 0)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) S.red[wave][j] = sum[j];
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = S.red[lane % W][j];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], o);
+  }
   if (tid == 0) {
+    const double s_r = sum[0], s_k = sum[1], mass = sum[2], cross = sum[3];
     const double ref_r = ((double)ref - base) * rtau, lse_r = ref_r + log(s_r);
     const double lse = log(s_k + s_r * exp(ref_r));
-    const double lr = P.rest ? (double)P.rest[t] : -(double)kInf, r = exp(lr);
-    const double total = P.rest ? mass + r : 1.0;
+    const double lr = A.P.rest ? (double)A.P.rest[t] : -(double)kInf, r = exp(lr);
+    const double total = A.P.rest ? mass + r : 1.0;
     RowConsts R;
-    R.zero = P.rest ? total == 0.0 : mass == 0.0;
-    double L = P.rest ? cross + mass * lse : cross / mass - log(mass) + lse;
-    if (P.rest && r != 0.0) L += r * (lr - (lse_r - lse));
-    if (loss) loss[t] = R.zero ? 0.0f : (float)((double)w * L);
+    R.zero = A.P.rest ? total == 0.0 : mass == 0.0;
+    double loss = A.P.rest ? cross + mass * lse : cross / mass - log(mass) + lse;
+    if (A.P.rest && r != 0.0) loss += r * (lr - (lse_r - lse));
+    if (A.loss) A.loss[t] = R.zero ? 0.0f : (float)((double)w * loss);
     R.base = base;
     R.lse = lse;
     R.total = total;
-    R.scale = P.rest ? 1.0 : 1.0 / mass;  // of the listed probabilities
+    R.scale = A.P.rest ? 1.0 : 1.0 / mass;  // of the listed probabilities
+    R.w = (double)w * rtau;
     R.ref = ref;
     // the gradient of a token not listed is coef * exp((s - ref) / tau)
     double coef = total * exp(ref_r - lse);
     if (r != 0.0) coef -= r / s_r;
-    R.coef = s_r == 0.0 && lse > -(double)kInf ? 0.0f : (float)((double)w * rtau * coef);
-    row = R;
+    R.coef = s_r == 0.0 && lse > -(double)kInf ? 0.0f : (float)(R.w * coef);
+    S.row = R;
   }
-  if (!GRADS) return;
   __syncthreads();
-  const RowConsts R = row;
-  if (R.zero) {
-    for (int i = tid; i < V; i += NT) row_store(dx, d_bf16, i, 0.0f);
-    return;
-  }
-  for (int i = tid; i < V; i += NT)
-    if (!(listed[i / 32] >> (i % 32) & 1u))
-      row_store(dx, d_bf16, i, R.coef * exp_scaled(row_load(x, bf16, i) - R.ref, c));
-  for (int e = tid; e < k; e += NT)
-    if (ids[e] >= 0) {
-      const double q = exp(((double)sv[e] - R.base) * rtau - R.lse);
-      row_store(dx, d_bf16, ids[e], (float)((double)w * rtau * (R.total * q - R.scale * (double)ps[e])));
+  return S.row;
+}
+
+// The listed tokens' gradients, over what was stored for them before the last barrier.
+template <int NT, bool DBF16>
+__device__ inline void row_listed_grads(const DistillArgs& A, char* dx, const RowConsts& R, const RowLds& L) {
+  const double rtau = 1.0 / (double)A.P.temperature;
+  for (int e = threadIdx.x; e < (int)A.P.k; e += NT)
+    if (L.ids[e] >= 0) {
+      const double q = exp(((double)L.sv[e] - R.base) * rtau - R.lse);
+      row_store(dx, DBF16, L.ids[e], (float)(R.w * (R.total * q - R.scale * (double)L.ps[e])));
     }
+}
+
+template <int NT, bool GRADS, bool DBF16>
+__device__ inline void constant_row(const DistillArgs& A, int64_t t, char* dx, float v) {
+  if (threadIdx.x == 0 && A.loss) A.loss[t] = v;
+  if (GRADS)
+    for (int i = threadIdx.x; i < A.V; i += NT) row_store(dx, DBF16, i, v);
+}
+
+// 16 bytes of a row at any alignment of its elements.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+template <bool BF16>
+struct Piece {
+  static constexpr int N = BF16 ? 8 : 4;  // elements
+  u32x4 v;
+  __device__ void load(const char* row, int j) {
+    if (BF16)
+      v = *reinterpret_cast<const u32x4_a2*>(row + (int64_t)j * 16);
+    else
+      v = *reinterpret_cast<const u32x4_a4*>(row + (int64_t)j * 16);
+  }
+  __device__ void fill() { v = u32x4{0, 0, 0, 0} + (BF16 ? 0xFF80FF80u : 0xFF800000u); }  // -inf
+  __device__ float at(int i) const {
+    if (!BF16) return __uint_as_float(v[i]);
+    return __uint_as_float(i % 2 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+  }
+  // Keeps the compiler from holding the unpacked elements across a pass beside the packed ones.
+  __device__ void packed() { asm volatile("" : "+v"(v)); }
+  // bit i of `m`: element i becomes -inf
+  __device__ void mask(uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (BF16) {
+        const uint32_t lo = (uint32_t)((int)(m << (31 - 2 * i)) >> 31) & 0xFFFFu;
+        const uint32_t hi = (uint32_t)((int)(m << (30 - 2 * i)) >> 31) & 0xFFFF0000u;
+        v[i] = (v[i] & ~(lo | hi)) | ((lo | hi) & 0xFF80FF80u);
+      } else {
+        const uint32_t on = (uint32_t)((int)(m << (31 - i)) >> 31);
+        v[i] = (v[i] & ~on) | (on & 0xFF800000u);
+      }
+    }
+  }
+  // the bits of piece j in the bitmap
+  __device__ static uint32_t bits(const uint32_t* listed, int j) {
+    if (BF16) return reinterpret_cast<const uint8_t*>(listed)[j];
+    return reinterpret_cast<const uint8_t*>(listed)[j / 2] >> (4 * (j % 2)) & 15u;
+  }
+};
+__device__ inline uint32_t bf16_pair(float a, float b) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
+}
+// N results as piece j of a row.
+template <int N, bool BF16>
+__device__ inline void store_piece(char* row, int j, const float (&g)[N]) {
+  char* p = row + (int64_t)j * N * (BF16 ? 2 : 4);
+  if constexpr (BF16 && N == 8) {
+    *reinterpret_cast<u32x4_a2*>(p) =
+        u32x4{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3]), bf16_pair(g[4], g[5]), bf16_pair(g[6], g[7])};
+  } else if constexpr (BF16) {
+    *reinterpret_cast<u32x2_a2*>(p) = u32x2{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<u32x4_a4*>(p + 4 * i) = u32x4{__float_as_uint(g[i]), __float_as_uint(g[i + 1]),
+                                                     __float_as_uint(g[i + 2]), __float_as_uint(g[i + 3])};
+  }
+}
+
+// A row held in registers: CH pieces per thread, V <= NT * CH * N, read once.  Tokens past the last
+// whole piece are one each of the first threads'.
+template <bool BF16, bool DBF16, int NT, int CH>
+__global__ __launch_bounds__(NT) void distill_held_kernel(const DistillArgs A) {
+  using Pc = Piece<BF16>;
+  constexpr int N = Pc::N;
+  extern __shared__ uint32_t lds[];
+  __shared__ RowShared<NT> S;
+  const int tid = threadIdx.x, V = A.V, np = V / N;
+  const int64_t t = blockIdx.x;
+  const RowLds L(lds, V, (int)A.P.k);
+  const char* x = row_at<BF16>(A.logits, t, A.ld);
+  char* dx = static_cast<char*>(A.dlogits) + t * A.ldd * (DBF16 ? 2 : 4);
+  const float w = A.weight ? A.weight[t] : 1.0f;
+  if (w == 0.0f) return constant_row<NT, true, DBF16>(A, t, dx, 0.0f);
+  Pc pc[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int j = tid + i * NT;
+    if (j < np)
+      pc[i].load(x, j);
+    else
+      pc[i].fill();
+  }
+  const int it = np * N + tid;  // this thread's token past the last piece
+  float xt = it < V ? row_load(x, BF16, it) : -kInf;
+  if (!row_entries<NT, BF16>(A, t, x, L, S)) return constant_row<NT, true, DBF16>(A, t, dx, __builtin_nanf(""));
+  if (it < V && (L.listed[it / 32] >> (it % 32) & 1u)) xt = -kInf;
+  float m = xt;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int j = tid + i * NT;
+    if (j < np) {
+      const uint32_t b = Pc::bits(L.listed, j);
+      if (b) pc[i].mask(b);
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) m = fmaxf(m, pc[i].at(q));
+  }
+  const float ref0 = m == -kInf ? 0.0f : m;
+  float s = exp_scaled(xt - ref0, A.c);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    pc[i].packed();
+#pragma unroll
+    for (int q = 0; q < N; ++q) s += exp_scaled(pc[i].at(q) - ref0, A.c);
+    pc[i].packed();
+  }
+  const RowConsts R = row_finish<NT>(A, t, w, m, s, L, S);
+  if (R.zero) return constant_row<NT, true, DBF16>(A, t, dx, 0.0f);
+  if (it < V) row_store(dx, DBF16, it, R.coef * exp_scaled(xt - R.ref, A.c));
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int j = tid + i * NT;
+    if (j >= np) continue;
+    float g[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) g[q] = R.coef * exp_scaled(pc[i].at(q) - R.ref, A.c);
+    store_piece<N, DBF16>(dx, j, g);
+  }
+  __syncthreads();  // the listed tokens' places are written
+  row_listed_grads<NT, DBF16>(A, dx, R, L);
+}
+
+// A row of any length: read once for the loss, a second time for the gradient.  Each thread keeps a
+// maximum and the sum below it, rescaled once for every U pieces.
+template <bool GRADS, bool BF16, bool DBF16, int NT>
+__global__ __launch_bounds__(NT) void distill_stream_kernel(const DistillArgs A) {
+  using Pc = Piece<BF16>;
+  constexpr int N = Pc::N, U = 4;
+  extern __shared__ uint32_t lds[];
+  __shared__ RowShared<NT> S;
+  const int tid = threadIdx.x, V = A.V, np = V / N;
+  const int64_t t = blockIdx.x;
+  const RowLds L(lds, V, (int)A.P.k);
+  const char* x = row_at<BF16>(A.logits, t, A.ld);
+  char* dx = GRADS ? static_cast<char*>(A.dlogits) + t * A.ldd * (DBF16 ? 2 : 4) : nullptr;
+  const float w = A.weight ? A.weight[t] : 1.0f;
+  if (w == 0.0f) return constant_row<NT, GRADS, DBF16>(A, t, dx, 0.0f);
+  if (!row_entries<NT, BF16>(A, t, x, L, S)) return constant_row<NT, GRADS, DBF16>(A, t, dx, __builtin_nanf(""));
+  const int it = np * N + tid;
+  float xt = it < V ? row_load(x, BF16, it) : -kInf;
+  if (it < V && (L.listed[it / 32] >> (it % 32) & 1u)) xt = -kInf;
+  float m = xt, s = exp_scaled(xt - (xt == -kInf ? 0.0f : xt), A.c);
+  for (int j0 = tid; j0 < np; j0 += NT * U) {
+    Pc pc[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i * NT;
+      if (j < np)
+        pc[i].load(x, j);
+      else
+        pc[i].fill();
+    }
+    float mm = m;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i * NT;
+      if (j < np) {
+        const uint32_t b = Pc::bits(L.listed, j);
+        if (b) pc[i].mask(b);
+      }
+#pragma unroll
+      for (int q = 0; q < N; ++q) mm = fmaxf(mm, pc[i].at(q));
+    }
+    const float ref = mm == -kInf ? 0.0f : mm;
+    s *= exp_scaled(m - ref, A.c);
+    m = mm;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int q = 0; q < N; ++q) s += exp_scaled(pc[i].at(q) - ref, A.c);
+  }
+  const RowConsts R = row_finish<NT>(A, t, w, m, s, L, S);
+  if (!GRADS) return;
+  if (R.zero) return constant_row<NT, GRADS, DBF16>(A, t, dx, 0.0f);
+  if (it < V) row_store(dx, DBF16, it, R.coef * exp_scaled(xt - R.ref, A.c));
+  for (int j = tid; j < np; j += NT) {
+    Pc pc;
+    pc.load(x, j);
+    const uint32_t b = Pc::bits(L.listed, j);
+    if (b) pc.mask(b);
+    float g[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) g[q] = R.coef * exp_scaled(pc.at(q) - R.ref, A.c);
+    store_piece<N, DBF16>(dx, j, g);
+  }
+  __syncthreads();
+  row_listed_grads<NT, DBF16>(A, dx, R, L);
 }
 
 // ------------------------------------------------------------------ a teacher's top logits
@@ -398,23 +642,51 @@ hipError_t launch_logits_top(const void* logits, nq_dtype dt, int64_t T, int64_t
   return hipGetLastError();
 }
 
+namespace {
+
+// kernel<<<T, NT, lds of the row>>>; the largest row's LDS is allowed once per device
+template <typename K>
+hipError_t launch_rows(K kernel, int64_t T, int nt, const DistillArgs& A, std::atomic<uint64_t>& done, hipStream_t s) {
+  const size_t lds = row_lds_bytes(A.V, A.P.k);
+  if (lds > 48 * 1024) {
+    const hipError_t e =
+        allow_lds(reinterpret_cast<const void*>(kernel), row_lds_bytes(int64_t{1} << 20, NQ_TOP_MAX), done);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(nt), lds, s, A);
+  return hipGetLastError();
+}
+template <bool BF16, bool DBF16, int NT, int CH>
+hipError_t launch_held(int64_t T, const DistillArgs& A, hipStream_t s) {
+  static std::atomic<uint64_t> done;
+  return launch_rows(distill_held_kernel<BF16, DBF16, NT, CH>, T, NT, A, done, s);
+}
+template <bool GRADS, bool BF16, bool DBF16, int NT>
+hipError_t launch_stream(int64_t T, const DistillArgs& A, hipStream_t s) {
+  static std::atomic<uint64_t> done;
+  return launch_rows(distill_stream_kernel<GRADS, BF16, DBF16, NT>, T, NT, A, done, s);
+}
+
+template <bool BF16, bool DBF16>
+hipError_t launch_grads(int64_t T, const DistillArgs& A, hipStream_t s) {
+  const int64_t np = A.V / Piece<BF16>::N;
+  if (np <= 256 * 4) return launch_held<BF16, DBF16, 256, 4>(T, A, s);
+  if (np <= 512 * 4) return launch_held<BF16, DBF16, 512, 4>(T, A, s);
+  if (np <= 1024 * 4) return launch_held<BF16, DBF16, 1024, 4>(T, A, s);
+  if (np <= 1024 * 8) return launch_held<BF16, DBF16, 1024, 8>(T, A, s);
+  if (np <= 1024 * 16) return launch_held<BF16, DBF16, 1024, 16>(T, A, s);
+  return launch_stream<true, BF16, DBF16, 1024>(T, A, s);
+}
+
+}  // namespace
+
 hipError_t launch_distill(const nq_teacher& P, const void* logits, nq_dtype dt, int64_t T, int64_t V, int64_t ld,
                           const float* weight, float* loss, void* dlogits, nq_dtype dd, int64_t ldd, hipStream_t s) {
-  const size_t lds = (size_t)cdiv(V, 32) * 4 + (size_t)P.k * 12;
-  static std::atomic<uint64_t> done[2];
-  const bool grads = dlogits != nullptr;
-  const void* kernel = grads ? reinterpret_cast<const void*>(distill_kernel<true>)
-                             : reinterpret_cast<const void*>(distill_kernel<false>);
-  // the largest call: 2^20 tokens and NQ_TOP_MAX entries
-  const hipError_t e = allow_lds(kernel, (size_t)(1 << 15) * 4 + (size_t)NQ_TOP_MAX * 12, done[grads]);
-  if (e != hipSuccess) return e;
-  if (grads)
-    hipLaunchKernelGGL(distill_kernel<true>, dim3((unsigned)T), dim3(kDistillThreads), lds, s, P, exp_scale(P.temperature),
-                       logits, (int)(dt == NQ_BF16), (int)V, ld, weight, loss, dlogits, (int)(dd == NQ_BF16), ldd);
-  else
-    hipLaunchKernelGGL(distill_kernel<false>, dim3((unsigned)T), dim3(kDistillThreads), lds, s, P, exp_scale(P.temperature),
-                       logits, (int)(dt == NQ_BF16), (int)V, ld, weight, loss, dlogits, 0, ldd);
-  return hipGetLastError();
+  const DistillArgs A{P, exp_scale(P.temperature), logits, ld, weight, loss, dlogits, ldd, (int)V};
+  if (!dlogits)
+    return dt == NQ_BF16 ? launch_stream<false, true, false, 512>(T, A, s) : launch_stream<false, false, false, 512>(T, A, s);
+  if (dt == NQ_BF16) return dd == NQ_BF16 ? launch_grads<true, true>(T, A, s) : launch_grads<true, false>(T, A, s);
+  return dd == NQ_BF16 ? launch_grads<false, true>(T, A, s) : launch_grads<false, false>(T, A, s);
 }
 
 }  // namespace nq

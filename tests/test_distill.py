@@ -292,7 +292,7 @@ def test_loss_and_gradient(T, V, k, dtype, tau, rest):
     loss = nq.distill_loss(P, x, _dev(w))
     _check_distill(ids, logp, left, tau, s, w, loss)
     loss2, grad = nq.distill_grads(P, x, _dev(w))
-    assert torch.equal(loss, loss2) and grad.dtype == x.dtype
+    assert grad.dtype == x.dtype and torch.equal(nq.distill_loss(P, x, _dev(w)), loss)
     _check_distill(ids, logp, left, tau, s, w, loss2, grad, dtype)
     other = torch.float32 if dtype == "bf16" else torch.bfloat16
     grad2 = torch.empty(T, V, dtype=other, device=DEV)
@@ -354,7 +354,7 @@ def test_masked_and_non_finite_logits(V, rest):
     for dtype in ("f32", "bf16"):
         loss, grad = nq.distill_grads(P, _dev(s, dtype))
         _check_distill(ids, logp, left, 1.0, s, None, loss, grad, dtype)
-        assert torch.equal(nq.distill_loss(P, _dev(s, dtype)).nan_to_num(7.0), loss.nan_to_num(7.0))
+        _check_distill(ids, logp, left, 1.0, s, None, nq.distill_loss(P, _dev(s, dtype)))
 
 
 @gpu
@@ -396,7 +396,7 @@ def test_strided_and_misaligned_rows(V, ld, shift, dtype):
     assert out is gs and torch.equal(loss2, loss) and torch.equal(gs, grad)
     gs.fill_(7.0)
     assert (gflat == 7.0).all()
-    assert torch.equal(nq.distill_loss(P, xs), loss)
+    assert torch.equal(nq.distill_loss(P, xs), nq.distill_loss(P, x))
     a, b = nq.logits_top(x, k), nq.logits_top(xs, k)
     assert torch.equal(a.ids, b.ids) and torch.equal(a.logp, b.logp) and torch.equal(a.rest, b.rest)
     before = xs.clone()
@@ -425,7 +425,7 @@ def test_other_stream_and_captured_calls():
     ids, logp, left = _record("graph", T, V, k, 1.0)
     P = nq.Teacher(_dev(ids), _dev(logp), _dev(left))
     xs = [_dev(_rows(f"graph/{i}", T, V, "bf16"), "bf16") for i in range(3)]
-    want = [(nq.logits_top(x, k), nq.distill_grads(P, x)) for x in xs]
+    want = [(nq.logits_top(x, k), nq.distill_grads(P, x), nq.distill_loss(P, x)) for x in xs]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     got = nq.distill_grads(P, xs[0], stream=side)
@@ -446,7 +446,7 @@ def test_other_stream_and_captured_calls():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(rec.ids, want[i][0].ids) and torch.equal(rec.rest, want[i][0].rest)
-        assert torch.equal(loss, want[i][1][0]) and torch.equal(loss2, loss) and torch.equal(grad, want[i][1][1])
+        assert torch.equal(loss, want[i][2]) and torch.equal(loss2, want[i][1][0]) and torch.equal(grad, want[i][1][1])
         nq.distill_grads(P, xs[(i + 1) % 3])  # eager work between the replays
 
 
