@@ -29,18 +29,59 @@ __device__ inline void row_store(void* p, bool bf16, int64_t i, float v) {
     static_cast<float*>(p)[i] = v;
 }
 
-// exp(d / tau) for d <= 0 as 2^(d c), c = log2(e) / tau in two parts: one part's rounding
-// would grow with |d|.  Both parts are above zero, so that d = -inf gives 0.
-struct ExpScale {
-  float hi, lo;
-};
-// The hardware's 2^x: one unit in the last place, and 0 below 2^-126.
-__device__ inline float exp_scaled(float d, ExpScale c) { return __builtin_amdgcn_exp2f(fmaf(d, c.hi, d * c.lo)); }
-ExpScale exp_scale(float tau) {
-  const double c = kLog2e / (double)tau;
-  float hi = (float)c;
-  if ((double)hi > c) hi = nextafterf(hi, 0.0f);
-  return {hi, fmaxf((float)(c - (double)hi), __FLT_MIN__)};
+// exp(d / tau) for d <= 0, c = log2(e) / tau: the hardware's 2^x, one unit in the last place and 0 below
+// 2^-126.  c's rounding and the product's are felt |d / tau| times each, as is the difference's.
+__device__ inline float exp_scaled(float d, float c) { return __builtin_amdgcn_exp2f(d * c); }
+float exp_scale(float tau) { return (float)(kLog2e / (double)tau); }
+
+// The largest of three; a library maximum would quiet its operands first, an instruction each.
+__device__ inline float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// Reductions over a wave by lane moves within rows of 16 and four lane reads; over a workgroup's waves
+// in a row of 16.
+template <int CTRL>
+__device__ inline float lane_move(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ inline double lane_move(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+__device__ inline float lane_read(float x, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), l));
+}
+__device__ inline double lane_read(double x, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l) << 32 |
+                                        (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l));
+}
+__device__ inline float row_max(float x) {  // of 16 lanes, to all of them
+  x = fmaxf(x, lane_move<kXor1>(x));
+  x = fmaxf(x, lane_move<kXor2>(x));
+  x = fmaxf(x, lane_move<kHalfMirror>(x));
+  return fmaxf(x, lane_move<kMirror>(x));
+}
+__device__ inline double row_sum(double x) {
+  x += lane_move<kXor1>(x);
+  x += lane_move<kXor2>(x);
+  x += lane_move<kHalfMirror>(x);
+  return x + lane_move<kMirror>(x);
+}
+__device__ inline float wave_max(float x) {
+  x = row_max(x);
+  return fmaxf(fmaxf(lane_read(x, 0), lane_read(x, 16)), fmaxf(lane_read(x, 32), lane_read(x, 48)));
+}
+__device__ inline double wave_sum(double x) {
+  x = row_sum(x);
+  return (lane_read(x, 0) + lane_read(x, 16)) + (lane_read(x, 32) + lane_read(x, 48));
 }
 
 // Workgroup reductions in a fixed order; `red` holds one double per wave and is free again after
@@ -73,7 +114,7 @@ __device__ inline double wg_sum(double x, double* red) {
 // A running maximum and the sum of exponentials below it.
 struct MaxSum {
   float m = -kInf, s = 0.0f;
-  __device__ inline void add(float x, ExpScale c) {
+  __device__ inline void add(float x, float c) {
     if (x > m) {
       s *= exp_scaled(m == -kInf ? -kInf : m - x, c);
       m = x;
@@ -86,7 +127,7 @@ struct MaxSum {
 
 struct DistillArgs {
   nq_teacher P;
-  ExpScale c;
+  float c;
   const void* logits;
   int64_t ld;
   const float* weight;
@@ -97,29 +138,31 @@ struct DistillArgs {
 };
 
 struct RowConsts {  // of one row, for every thread
-  double base, lse, total, scale, w;
+  double base, inv, total, scale, w;
   float ref, coef;
   int zero;
 };
 
-// LDS of a row: [bitmap of the listed tokens, whole words][ids][logits][probabilities of the k entries].
+// LDS of a row: [probabilities][ids][logits of the k entries][bitmap of the listed tokens, whole words].
 // An entry's id is -1 where there is none, and -2 - id for a repetition of an earlier entry.
 struct RowLds {
-  uint32_t* listed;
+  double* ps;
   int* ids;
-  float *sv, *ps;
-  __device__ RowLds(uint32_t* lds, int V, int k) {
-    listed = lds;
-    ids = reinterpret_cast<int*>(lds + (V + 31) / 32);
+  float* sv;
+  uint32_t* listed;
+  __device__ RowLds(double* lds, int k) {
+    ps = lds;
+    ids = reinterpret_cast<int*>(lds + k);
     sv = reinterpret_cast<float*>(ids + k);
-    ps = sv + k;
+    listed = reinterpret_cast<uint32_t*>(sv + k);
   }
 };
-size_t row_lds_bytes(int64_t V, int64_t k) { return (size_t)cdiv(V, 32) * 4 + (size_t)k * 12; }
+size_t row_lds_bytes(int64_t V, int64_t k) { return (size_t)cdiv(V, 32) * 4 + (size_t)k * 16; }
 
 template <int NT>
 struct RowShared {
-  double red[NT / 64][4];
+  float max[NT / 64][2];
+  double sum[NT / 64][4];
   RowConsts row;
   int bad, dup;
 };
@@ -129,137 +172,149 @@ __device__ inline const char* row_at(const void* p, int64_t t, int64_t ld) {
   return static_cast<const char*>(p) + t * ld * (BF16 ? 2 : 4);
 }
 
-// The entries of row t into LDS and the bitmap.  False: an id is out of range.
+// The entries of row t into LDS and the bitmap; this thread's part of sum p and of sum p log p.  False:
+// an id is out of range.
 template <int NT, bool BF16>
-__device__ bool row_entries(const DistillArgs& A, int64_t t, const char* x, const RowLds& L, RowShared<NT>& S) {
+__device__ bool row_entries(const DistillArgs& A, int64_t t, const char* x, const RowLds& L, RowShared<NT>& S,
+                            double& mass, double& plogp) {
   const int tid = threadIdx.x, k = (int)A.P.k, V = A.V;
   if (tid == 0) S.bad = S.dup = 0;
+#pragma unroll 1
   for (int i = tid; i < (V + 31) / 32; i += NT) L.listed[i] = 0;
   __syncthreads();
+  mass = plogp = 0.0;
+#pragma unroll 1
   for (int e = tid; e < k; e += NT) {
     const int id = A.P.ids[t * k + e];
-    float s = -kInf, p = 0.0f;
+    float s = -kInf;
+    double p = 0.0;
     if (id >= V) {
       S.bad = 1;
     } else if (id >= 0) {
       if (atomicOr(&L.listed[id / 32], 1u << (id % 32)) >> (id % 32) & 1u) S.dup = 1;
       s = row_load(x, BF16, id);
-      p = expf(A.P.logp[t * k + e]);
+      const double lp = A.P.logp[t * k + e];
+      p = exp(lp);
+      mass += p;
+      if (p != 0.0) plogp += p * lp;
     }
     L.ids[e] = id < 0 ? -1 : id;
     L.sv[e] = s;
     L.ps[e] = p;
   }
   __syncthreads();
-  if (S.bad) return false;
-  if (S.dup) {  // the first of equal entries takes the probabilities of all
-    constexpr int kEntries = (NQ_TOP_MAX + NT - 1) / NT;  // per thread
-    float sum[kEntries];
-    bool again[kEntries];
-    for (int i = 0, e = tid; i < kEntries; ++i, e += NT) {
-      sum[i] = 0.0f;
-      again[i] = false;
-      if (e >= k || L.ids[e] < 0) continue;
+  return !S.bad;
+}
+
+// Where a token is listed more than once: the first of its entries takes the probabilities of all.
+// (NT entries at a time: the first of a token's entries keeps its id, so later ones find it.)
+template <int NT>
+__device__ void row_repetitions(const DistillArgs& A, const RowLds& L) {
+  const int k = (int)A.P.k;
+#pragma unroll 1
+  for (int e0 = 0; e0 < k; e0 += NT) {
+    const int e = e0 + (int)threadIdx.x, id = e < k ? L.ids[e] : -1;
+    double sum = 0.0;
+    bool again = false;
+    if (id >= 0)
+#pragma unroll 1
       for (int f = 0; f < k; ++f)
-        if (L.ids[f] == L.ids[e]) {
-          again[i] |= f < e;
-          sum[i] += L.ps[f];
+        if (L.ids[f] == id) {
+          again |= f < e;
+          sum += L.ps[f];
         }
+    __syncthreads();
+    if (id >= 0) {
+      L.ps[e] = again ? 0.0 : sum;
+      if (again) L.ids[e] = -2 - id;
     }
     __syncthreads();
-    for (int i = 0, e = tid; i < kEntries; ++i, e += NT)
-      if (e < k && L.ids[e] >= 0) {
-        L.ps[e] = sum[i];
-        if (again[i]) L.ids[e] = -2 - L.ids[e];
-      }
-    __syncthreads();
   }
-  return true;
 }
 
 // The row's loss and the constants of its gradient, from each thread's maximum m and sum s (relative
-// to its maximum) over the tokens not listed that it has read.
-template <int NT>
-__device__ RowConsts row_finish(const DistillArgs& A, int64_t t, float w, float m, float s, const RowLds& L,
-                                RowShared<NT>& S) {
-  constexpr int W = NT / 64;  // waves, a power of two
+// to its maximum) over the tokens not listed that it has read, and its parts of sum p and sum p log p.
+template <int NT, bool GRADS>
+__device__ RowConsts row_finish(const DistillArgs& A, int64_t t, float w, float m, float s, double mass, double plogp,
+                                const RowLds& L, RowShared<NT>& S) {
+  constexpr int W = NT / 64;  // waves, at most 16
   const int tid = threadIdx.x, k = (int)A.P.k, lane = tid % 64, wave = tid / 64;
-  float m_k = -kInf, m_r = m;
-  for (int e = tid; e < k; e += NT)
-    if (L.ids[e] != -1) m_k = fmaxf(m_k, L.sv[e]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    m_r = fmaxf(m_r, __shfl_xor(m_r, o));
-    m_k = fmaxf(m_k, __shfl_xor(m_k, o));
+  const bool entries = wave * 64 < k;  // the waves that have entries
+  float m_k = -kInf;
+  if (entries) {
+#pragma unroll 1
+    for (int e = tid; e < k; e += NT)
+      if (L.ids[e] != -1) m_k = fmaxf(m_k, L.sv[e]);
+    m_k = wave_max(m_k);
   }
+  float m_r = wave_max(m);
   if (lane == 0) {
-    S.red[wave][0] = (double)m_r;
-    S.red[wave][1] = (double)m_k;
+    S.max[wave][0] = m_r;
+    S.max[wave][1] = m_k;
   }
   __syncthreads();
-  m_r = (float)S.red[lane % W][0];
-  m_k = (float)S.red[lane % W][1];
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) {
-    m_r = fmaxf(m_r, __shfl_xor(m_r, o));
-    m_k = fmaxf(m_k, __shfl_xor(m_k, o));
-  }
+  m_r = row_max(S.max[lane % W][0]);
+  m_k = row_max(S.max[lane % W][1]);
   // everything relative to the row's largest logit, at which an fp64 number of its own size may not
   // hold the logarithms
   const float ref = m_r == -kInf ? 0.0f : m_r, top = fmaxf(m_r, m_k);
   const double base = top == -kInf ? 0.0 : (double)top, rtau = 1.0 / (double)A.P.temperature;
   // sums: of the rest, of the listed tokens' exponentials, of p and of p (log p - s / tau)
-  double sum[4] = {(double)s * (double)exp_scaled(m == -kInf ? 0.0f : m - ref, A.c), 0.0, 0.0, 0.0};
-  for (int e = tid; e < k; e += NT) {
-    if (L.ids[e] == -1) continue;
-    const double sx = ((double)L.sv[e] - base) * rtau;
-    if (L.ids[e] >= 0) sum[1] += exp(sx);
-    const double lp = A.P.logp[t * k + e], p = exp(lp);
-    if (p == 0.0) continue;
-    sum[2] += p;
-    sum[3] += p * (lp - sx);
+  double sum[4] = {(double)s * (double)exp_scaled(m == -kInf ? 0.0f : m - ref, A.c), 0.0, mass, plogp};
+  sum[0] = wave_sum(sum[0]);
+  if (entries) {
+#pragma unroll 1
+    for (int e = tid; e < k; e += NT) {
+      if (L.ids[e] < 0) continue;  // a repetition's probability is with the first
+      const double p = L.ps[e], sx = ((double)L.sv[e] - base) * rtau;
+      sum[1] += exp(sx);
+      if (p != 0.0) sum[3] -= p * sx;
+    }
+#pragma unroll
+    for (int j = 1; j < 4; ++j) sum[j] = wave_sum(sum[j]);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], o);
-  __syncthreads();
   if (lane == 0)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) S.red[wave][j] = sum[j];
+    for (int j = 0; j < 4; ++j) S.sum[wave][j] = sum[j];
   __syncthreads();
-  if (wave == 0) {
+  if (GRADS && wave == 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] = S.red[lane % W][j];
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], o);
+    for (int j = 0; j < 3; ++j) sum[j] = row_sum(lane % 16 < W ? S.sum[lane % 16][j] : 0.0);
+    if (tid == 0) {
+      const double e_r = exp(((double)ref - base) * rtau), all = sum[1] + sum[0] * e_r;
+      const double r = A.P.rest ? exp((double)A.P.rest[t]) : 0.0, total = A.P.rest ? sum[2] + r : 1.0;
+      RowConsts R;
+      R.zero = (A.P.rest ? total : sum[2]) == 0.0;
+      R.base = base;
+      R.inv = 1.0 / all;
+      R.total = total;
+      R.scale = A.P.rest ? 1.0 : 1.0 / sum[2];  // of the listed probabilities
+      R.w = (double)w * rtau;
+      R.ref = ref;
+      // the gradient of a token not listed is coef * exp((s - ref) / tau)
+      double coef = total * e_r * R.inv;
+      if (r != 0.0) coef -= r / sum[0];
+      R.coef = sum[0] == 0.0 && all > 0.0 ? 0.0f : (float)(R.w * coef);
+      S.row = R;
+    }
   }
-  if (tid == 0) {
-    const double s_r = sum[0], s_k = sum[1], mass = sum[2], cross = sum[3];
-    const double ref_r = ((double)ref - base) * rtau, lse_r = ref_r + log(s_r);
-    const double lse = log(s_k + s_r * exp(ref_r));
-    const double lr = A.P.rest ? (double)A.P.rest[t] : -(double)kInf, r = exp(lr);
-    const double total = A.P.rest ? mass + r : 1.0;
-    RowConsts R;
-    R.zero = A.P.rest ? total == 0.0 : mass == 0.0;
-    double loss = A.P.rest ? cross + mass * lse : cross / mass - log(mass) + lse;
-    if (A.P.rest && r != 0.0) loss += r * (lr - (lse_r - lse));
-    if (A.loss) A.loss[t] = R.zero ? 0.0f : (float)((double)w * loss);
-    R.base = base;
-    R.lse = lse;
-    R.total = total;
-    R.scale = A.P.rest ? 1.0 : 1.0 / mass;  // of the listed probabilities
-    R.w = (double)w * rtau;
-    R.ref = ref;
-    // the gradient of a token not listed is coef * exp((s - ref) / tau)
-    double coef = total * exp(ref_r - lse);
-    if (r != 0.0) coef -= r / s_r;
-    R.coef = s_r == 0.0 && lse > -(double)kInf ? 0.0f : (float)(R.w * coef);
-    S.row = R;
+  if (GRADS) __syncthreads();
+  if (A.loss && wave == W - 1) {  // its logarithms are not waited for by the gradient
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = row_sum(lane % 16 < W ? S.sum[lane % 16][j] : 0.0);
+    if (lane == 0) {
+      const double ref_r = ((double)ref - base) * rtau, lse = log(sum[1] + sum[0] * exp(ref_r));
+      double loss = A.P.rest ? sum[3] + sum[2] * lse : sum[3] / sum[2] - log(sum[2]) + lse;
+      double all = sum[2];
+      if (A.P.rest) {
+        const double lr = A.P.rest[t], r = exp(lr);
+        all += r;
+        if (r != 0.0) loss += r * (lr - (ref_r + log(sum[0]) - lse));
+      }
+      A.loss[t] = all == 0.0 ? 0.0f : (float)((double)w * loss);
+    }
   }
-  __syncthreads();
+  if (!GRADS) return {};
   return S.row;
 }
 
@@ -267,10 +322,11 @@ __device__ RowConsts row_finish(const DistillArgs& A, int64_t t, float w, float 
 template <int NT, bool DBF16>
 __device__ inline void row_listed_grads(const DistillArgs& A, char* dx, const RowConsts& R, const RowLds& L) {
   const double rtau = 1.0 / (double)A.P.temperature;
+#pragma unroll 1
   for (int e = threadIdx.x; e < (int)A.P.k; e += NT)
     if (L.ids[e] >= 0) {
-      const double q = exp(((double)L.sv[e] - R.base) * rtau - R.lse);
-      row_store(dx, DBF16, L.ids[e], (float)(R.w * (R.total * q - R.scale * (double)L.ps[e])));
+      const double q = exp(((double)L.sv[e] - R.base) * rtau) * R.inv;
+      row_store(dx, DBF16, L.ids[e], (float)(R.w * (R.total * q - R.scale * L.ps[e])));
     }
 }
 
@@ -278,6 +334,7 @@ template <int NT, bool GRADS, bool DBF16>
 __device__ inline void constant_row(const DistillArgs& A, int64_t t, char* dx, float v) {
   if (threadIdx.x == 0 && A.loss) A.loss[t] = v;
   if (GRADS)
+#pragma unroll 1
     for (int i = threadIdx.x; i < A.V; i += NT) row_store(dx, DBF16, i, v);
 }
 
@@ -290,30 +347,36 @@ typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 template <bool BF16>
 struct Piece {
   static constexpr int N = BF16 ? 8 : 4;  // elements
-  u32x4 v;
+  uint32_t v[4];
   __device__ void load(const char* row, int j) {
+    u32x4 d;
     if (BF16)
-      v = *reinterpret_cast<const u32x4_a2*>(row + (int64_t)j * 16);
+      d = *reinterpret_cast<const u32x4_a2*>(row + (uint32_t)j * 16u);
     else
-      v = *reinterpret_cast<const u32x4_a4*>(row + (int64_t)j * 16);
+      d = *reinterpret_cast<const u32x4_a4*>(row + (uint32_t)j * 16u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = d[i];
   }
-  __device__ void fill() { v = u32x4{0, 0, 0, 0} + (BF16 ? 0xFF80FF80u : 0xFF800000u); }  // -inf
+  __device__ void fill() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  }
   __device__ float at(int i) const {
     if (!BF16) return __uint_as_float(v[i]);
     return __uint_as_float(i % 2 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
   }
   // Keeps the compiler from holding the unpacked elements across a pass beside the packed ones.
-  __device__ void packed() { asm volatile("" : "+v"(v)); }
+  __device__ void packed() { asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3])); }
   // bit i of `m`: element i becomes -inf
   __device__ void mask(uint32_t m) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (BF16) {
-        const uint32_t lo = (uint32_t)((int)(m << (31 - 2 * i)) >> 31) & 0xFFFFu;
-        const uint32_t hi = (uint32_t)((int)(m << (30 - 2 * i)) >> 31) & 0xFFFF0000u;
-        v[i] = (v[i] & ~(lo | hi)) | ((lo | hi) & 0xFF80FF80u);
+        const uint32_t lo = __builtin_amdgcn_sbfe(m, 2 * i, 1), hi = __builtin_amdgcn_sbfe(m, 2 * i + 1, 1);
+        const uint32_t on = (lo & 0xFFFFu) | (hi & 0xFFFF0000u);
+        v[i] = (v[i] & ~on) | (on & 0xFF80FF80u);
       } else {
-        const uint32_t on = (uint32_t)((int)(m << (31 - i)) >> 31);
+        const uint32_t on = __builtin_amdgcn_sbfe(m, i, 1);
         v[i] = (v[i] & ~on) | (on & 0xFF800000u);
       }
     }
@@ -324,112 +387,59 @@ struct Piece {
     return reinterpret_cast<const uint8_t*>(listed)[j / 2] >> (4 * (j % 2)) & 15u;
   }
 };
-__device__ inline uint32_t bf16_pair(float a, float b) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t bf16_pair(float a, float b) {  // one conversion for both
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
-// N results as piece j of a row.
+// N results as piece j of a row, past the caches: a gradient's rows are not read again by the call, and
+// what they would push out of the caches is (4096 rows of 131072 bf16: 522 us with plain stores, 456).
 template <int N, bool BF16>
 __device__ inline void store_piece(char* row, int j, const float (&g)[N]) {
-  char* p = row + (int64_t)j * N * (BF16 ? 2 : 4);
+  char* p = row + (uint32_t)j * (uint32_t)(N * (BF16 ? 2 : 4));
   if constexpr (BF16 && N == 8) {
-    *reinterpret_cast<u32x4_a2*>(p) =
-        u32x4{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3]), bf16_pair(g[4], g[5]), bf16_pair(g[6], g[7])};
+    const u32x4_a2 d = u32x4{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3]), bf16_pair(g[4], g[5]), bf16_pair(g[6], g[7])};
+    __builtin_nontemporal_store(d, reinterpret_cast<u32x4_a2*>(p));
   } else if constexpr (BF16) {
-    *reinterpret_cast<u32x2_a2*>(p) = u32x2{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])};
+    const u32x2_a2 d = u32x2{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])};
+    __builtin_nontemporal_store(d, reinterpret_cast<u32x2_a2*>(p));
   } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 4)
-      *reinterpret_cast<u32x4_a4*>(p + 4 * i) = u32x4{__float_as_uint(g[i]), __float_as_uint(g[i + 1]),
-                                                     __float_as_uint(g[i + 2]), __float_as_uint(g[i + 3])};
-  }
-}
-
-// A row held in registers: CH pieces per thread, V <= NT * CH * N, read once.  Tokens past the last
-// whole piece are one each of the first threads'.
-template <bool BF16, bool DBF16, int NT, int CH>
-__global__ __launch_bounds__(NT) void distill_held_kernel(const DistillArgs A) {
-  using Pc = Piece<BF16>;
-  constexpr int N = Pc::N;
-  extern __shared__ uint32_t lds[];
-  __shared__ RowShared<NT> S;
-  const int tid = threadIdx.x, V = A.V, np = V / N;
-  const int64_t t = blockIdx.x;
-  const RowLds L(lds, V, (int)A.P.k);
-  const char* x = row_at<BF16>(A.logits, t, A.ld);
-  char* dx = static_cast<char*>(A.dlogits) + t * A.ldd * (DBF16 ? 2 : 4);
-  const float w = A.weight ? A.weight[t] : 1.0f;
-  if (w == 0.0f) return constant_row<NT, true, DBF16>(A, t, dx, 0.0f);
-  Pc pc[CH];
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int j = tid + i * NT;
-    if (j < np)
-      pc[i].load(x, j);
-    else
-      pc[i].fill();
-  }
-  const int it = np * N + tid;  // this thread's token past the last piece
-  float xt = it < V ? row_load(x, BF16, it) : -kInf;
-  if (!row_entries<NT, BF16>(A, t, x, L, S)) return constant_row<NT, true, DBF16>(A, t, dx, __builtin_nanf(""));
-  if (it < V && (L.listed[it / 32] >> (it % 32) & 1u)) xt = -kInf;
-  float m = xt;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int j = tid + i * NT;
-    if (j < np) {
-      const uint32_t b = Pc::bits(L.listed, j);
-      if (b) pc[i].mask(b);
+    for (int i = 0; i < N; i += 4) {
+      const u32x4_a4 d = u32x4{__float_as_uint(g[i]), __float_as_uint(g[i + 1]), __float_as_uint(g[i + 2]),
+                               __float_as_uint(g[i + 3])};
+      __builtin_nontemporal_store(d, reinterpret_cast<u32x4_a4*>(p + 4 * i));
     }
-#pragma unroll
-    for (int q = 0; q < N; ++q) m = fmaxf(m, pc[i].at(q));
   }
-  const float ref0 = m == -kInf ? 0.0f : m;
-  float s = exp_scaled(xt - ref0, A.c);
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    pc[i].packed();
-#pragma unroll
-    for (int q = 0; q < N; ++q) s += exp_scaled(pc[i].at(q) - ref0, A.c);
-    pc[i].packed();
-  }
-  const RowConsts R = row_finish<NT>(A, t, w, m, s, L, S);
-  if (R.zero) return constant_row<NT, true, DBF16>(A, t, dx, 0.0f);
-  if (it < V) row_store(dx, DBF16, it, R.coef * exp_scaled(xt - R.ref, A.c));
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int j = tid + i * NT;
-    if (j >= np) continue;
-    float g[N];
-#pragma unroll
-    for (int q = 0; q < N; ++q) g[q] = R.coef * exp_scaled(pc[i].at(q) - R.ref, A.c);
-    store_piece<N, DBF16>(dx, j, g);
-  }
-  __syncthreads();  // the listed tokens' places are written
-  row_listed_grads<NT, DBF16>(A, dx, R, L);
 }
 
-// A row of any length: read once for the loss, a second time for the gradient.  Each thread keeps a
-// maximum and the sum below it, rescaled once for every U pieces.
+// A workgroup reads its row once, U pieces per thread at a time, each thread with a maximum and the sum
+// below it (rescaled once for the U pieces).  For the gradient it goes over the row a second time,
+// backwards: the last pieces are still in registers and those before them in the caches.  Tokens past
+// the last whole piece are one each of the first threads'.
 template <bool GRADS, bool BF16, bool DBF16, int NT>
-__global__ __launch_bounds__(NT) void distill_stream_kernel(const DistillArgs A) {
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void distill_kernel(const DistillArgs A) {
   using Pc = Piece<BF16>;
   constexpr int N = Pc::N, U = 4;
-  extern __shared__ uint32_t lds[];
+  extern __shared__ double lds[];
   __shared__ RowShared<NT> S;
   const int tid = threadIdx.x, V = A.V, np = V / N;
   const int64_t t = blockIdx.x;
-  const RowLds L(lds, V, (int)A.P.k);
+  const RowLds L(lds, (int)A.P.k);
   const char* x = row_at<BF16>(A.logits, t, A.ld);
   char* dx = GRADS ? static_cast<char*>(A.dlogits) + t * A.ldd * (DBF16 ? 2 : 4) : nullptr;
   const float w = A.weight ? A.weight[t] : 1.0f;
   if (w == 0.0f) return constant_row<NT, GRADS, DBF16>(A, t, dx, 0.0f);
-  if (!row_entries<NT, BF16>(A, t, x, L, S)) return constant_row<NT, GRADS, DBF16>(A, t, dx, __builtin_nanf(""));
+  double mass, plogp;
+  if (!row_entries<NT, BF16>(A, t, x, L, S, mass, plogp))
+    return constant_row<NT, GRADS, DBF16>(A, t, dx, __builtin_nanf(""));
+  if (S.dup) row_repetitions<NT>(A, L);
   const int it = np * N + tid;
   float xt = it < V ? row_load(x, BF16, it) : -kInf;
   if (it < V && (L.listed[it / 32] >> (it % 32) & 1u)) xt = -kInf;
   float m = xt, s = exp_scaled(xt - (xt == -kInf ? 0.0f : xt), A.c);
-  for (int j0 = tid; j0 < np; j0 += NT * U) {
-    Pc pc[U];
+  Pc pc[U];
+  auto load = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int j = j0 + i * NT;
@@ -438,40 +448,52 @@ __global__ __launch_bounds__(NT) void distill_stream_kernel(const DistillArgs A)
       else
         pc[i].fill();
     }
-    float mm = m;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int j = j0 + i * NT;
-      if (j < np) {
-        const uint32_t b = Pc::bits(L.listed, j);
-        if (b) pc[i].mask(b);
-      }
-#pragma unroll
-      for (int q = 0; q < N; ++q) mm = fmaxf(mm, pc[i].at(q));
+      pc[i].packed();
+      const uint32_t b = j < np ? Pc::bits(L.listed, j) : 0;
+      if (b) pc[i].mask(b);
+      pc[i].packed();
     }
+  };
+  int j0 = tid;
+  for (;; j0 += NT * U) {
+    load(j0);
+    float mm = m;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int q = 0; q < N; q += 2) mm = max3(mm, pc[i].at(q), pc[i].at(q + 1));
     const float ref = mm == -kInf ? 0.0f : mm;
     s *= exp_scaled(m - ref, A.c);
     m = mm;
 #pragma unroll
-    for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i) {
 #pragma unroll
       for (int q = 0; q < N; ++q) s += exp_scaled(pc[i].at(q) - ref, A.c);
+      pc[i].packed();
+    }
+    if (j0 - tid + NT * U >= np) break;
   }
-  const RowConsts R = row_finish<NT>(A, t, w, m, s, L, S);
+  const RowConsts R = row_finish<NT, GRADS>(A, t, w, m, s, mass, plogp, L, S);
   if (!GRADS) return;
   if (R.zero) return constant_row<NT, GRADS, DBF16>(A, t, dx, 0.0f);
   if (it < V) row_store(dx, DBF16, it, R.coef * exp_scaled(xt - R.ref, A.c));
-  for (int j = tid; j < np; j += NT) {
-    Pc pc;
-    pc.load(x, j);
-    const uint32_t b = Pc::bits(L.listed, j);
-    if (b) pc.mask(b);
-    float g[N];
+  for (;; j0 -= NT * U) {
 #pragma unroll
-    for (int q = 0; q < N; ++q) g[q] = R.coef * exp_scaled(pc.at(q) - R.ref, A.c);
-    store_piece<N, DBF16>(dx, j, g);
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i * NT;
+      pc[i].packed();
+      float g[N];
+#pragma unroll
+      for (int q = 0; q < N; ++q) g[q] = R.coef * exp_scaled(pc[i].at(q) - R.ref, A.c);
+      if (j < np) store_piece<N, DBF16>(dx, j, g);
+    }
+    if (j0 == tid) break;
+    load(j0 - NT * U);
   }
-  __syncthreads();
+  __syncthreads();  // the listed tokens' places are written
   row_listed_grads<NT, DBF16>(A, dx, R, L);
 }
 
@@ -507,7 +529,7 @@ __device__ inline int wg_count(int n, int* red) {
 // whose candidates are too many (long runs of equal logits, or the largest in few threads'
 // elements) finds the k-th logit by its bits instead.
 __global__ __launch_bounds__(kTopThreads) void logits_top_kernel(const void* __restrict__ logits, int bf16, int V,
-                                                                 int64_t ld, int k, double rtau, ExpScale c,
+                                                                 int64_t ld, int k, double rtau, float c,
                                                                  int32_t* __restrict__ ids, float* __restrict__ logp,
                                                                  float* __restrict__ rest_out) {
   constexpr int NT = kTopThreads;
@@ -656,26 +678,21 @@ hipError_t launch_rows(K kernel, int64_t T, int nt, const DistillArgs& A, std::a
   hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(nt), lds, s, A);
   return hipGetLastError();
 }
-template <bool BF16, bool DBF16, int NT, int CH>
-hipError_t launch_held(int64_t T, const DistillArgs& A, hipStream_t s) {
-  static std::atomic<uint64_t> done;
-  return launch_rows(distill_held_kernel<BF16, DBF16, NT, CH>, T, NT, A, done, s);
-}
-template <bool GRADS, bool BF16, bool DBF16, int NT>
-hipError_t launch_stream(int64_t T, const DistillArgs& A, hipStream_t s) {
-  static std::atomic<uint64_t> done;
-  return launch_rows(distill_stream_kernel<GRADS, BF16, DBF16, NT>, T, NT, A, done, s);
-}
-
-template <bool BF16, bool DBF16>
-hipError_t launch_grads(int64_t T, const DistillArgs& A, hipStream_t s) {
+// Threads per row, by its 16-byte pieces and the number of rows (us with 256 / 512 / 1024 threads):
+//   up to 1024 pieces, one step of 256 threads: a row costs by its threads more than by its length
+//     (8192 rows of 8192 bf16: loss 39 / 63 / 105, gradient 60 / 83 / 138; 16 rows: 6.3 / 6.5 / 6.8);
+//   a loss of many rows needs no more than 256 either, the rows fill the chip (2048 rows of 32000: 28 /
+//     29 / 37, of 131072: 100 / 109 / 102), one of few needs them (16 of 131072: 22 / 14 / 13);
+//   a gradient reads back what its threads' registers do not hold, and the fewer rows are under way at
+//     once the more of that is still in the caches (2048 of 131072: 283 / 267 / 240; 16: 41 / 26 / 22);
+//     rows of up to 2048 pieces fit 512 threads' (512 rows of 16384: 12.9 / 12.0 / 14.4).
+template <bool GRADS, bool BF16, bool DBF16>
+hipError_t launch_distill_t(int64_t T, const DistillArgs& A, hipStream_t s) {
+  static std::atomic<uint64_t> done[3];
   const int64_t np = A.V / Piece<BF16>::N;
-  if (np <= 256 * 4) return launch_held<BF16, DBF16, 256, 4>(T, A, s);
-  if (np <= 512 * 4) return launch_held<BF16, DBF16, 512, 4>(T, A, s);
-  if (np <= 1024 * 4) return launch_held<BF16, DBF16, 1024, 4>(T, A, s);
-  if (np <= 1024 * 8) return launch_held<BF16, DBF16, 1024, 8>(T, A, s);
-  if (np <= 1024 * 16) return launch_held<BF16, DBF16, 1024, 16>(T, A, s);
-  return launch_stream<true, BF16, DBF16, 1024>(T, A, s);
+  if (np <= 1024 || (!GRADS && T > 1024)) return launch_rows(distill_kernel<GRADS, BF16, DBF16, 256>, T, 256, A, done[0], s);
+  if (np <= 2048) return launch_rows(distill_kernel<GRADS, BF16, DBF16, 512>, T, 512, A, done[1], s);
+  return launch_rows(distill_kernel<GRADS, BF16, DBF16, 1024>, T, 1024, A, done[2], s);
 }
 
 }  // namespace
@@ -683,10 +700,10 @@ hipError_t launch_grads(int64_t T, const DistillArgs& A, hipStream_t s) {
 hipError_t launch_distill(const nq_teacher& P, const void* logits, nq_dtype dt, int64_t T, int64_t V, int64_t ld,
                           const float* weight, float* loss, void* dlogits, nq_dtype dd, int64_t ldd, hipStream_t s) {
   const DistillArgs A{P, exp_scale(P.temperature), logits, ld, weight, loss, dlogits, ldd, (int)V};
-  if (!dlogits)
-    return dt == NQ_BF16 ? launch_stream<false, true, false, 512>(T, A, s) : launch_stream<false, false, false, 512>(T, A, s);
-  if (dt == NQ_BF16) return dd == NQ_BF16 ? launch_grads<true, true>(T, A, s) : launch_grads<true, false>(T, A, s);
-  return dd == NQ_BF16 ? launch_grads<false, true>(T, A, s) : launch_grads<false, false>(T, A, s);
+  if (!dlogits) return dt == NQ_BF16 ? launch_distill_t<false, true, true>(T, A, s) : launch_distill_t<false, false, false>(T, A, s);
+  if (dt == NQ_BF16)
+    return dd == NQ_BF16 ? launch_distill_t<true, true, true>(T, A, s) : launch_distill_t<true, true, false>(T, A, s);
+  return dd == NQ_BF16 ? launch_distill_t<true, false, true>(T, A, s) : launch_distill_t<true, false, false>(T, A, s);
 }
 
 }  // namespace nq
