@@ -84,33 +84,6 @@ __device__ inline double wave_sum(double x) {
   return (lane_read(x, 0) + lane_read(x, 16)) + (lane_read(x, 32) + lane_read(x, 48));
 }
 
-// Workgroup reductions in a fixed order; `red` holds one double per wave and is free again after
-// the second barrier of the next use.
-template <int NT>
-__device__ inline float wg_max(float x, double* red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = (double)x;
-  __syncthreads();
-  x = (float)red[0];
-#pragma unroll
-  for (int w = 1; w < NT / 64; ++w) x = fmaxf(x, (float)red[w]);
-  return x;
-}
-template <int NT>
-__device__ inline double wg_sum(double x, double* red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = x;
-  __syncthreads();
-  x = red[0];
-#pragma unroll
-  for (int w = 1; w < NT / 64; ++w) x += red[w];
-  return x;
-}
-
 // A running maximum and the sum of exponentials below it.
 struct MaxSum {
   float m = -kInf, s = 0.0f;
@@ -505,10 +478,39 @@ __device__ inline uint32_t logit_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
+__device__ inline float key_logit(uint32_t key) { return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
 constexpr uint32_t kFirstKey = 0x00800000u;  // the lowest above -inf's
 
-constexpr int kTopThreads = 1024;
-constexpr int kCandidates = 2 * NQ_TOP_MAX;
+// Candidates a row has room for (twice the k that a workgroup's size serves), and each wave of it.
+template <int NT>
+constexpr int kCandidates = 2 * NT;
+constexpr int kWaveCandidates = 256;
+
+struct TopArgs {
+  const void* logits;
+  int64_t ld;
+  int V, k;
+  float c;
+  double rtau;
+  int32_t* ids;
+  float *logp, *rest;
+};
+
+// A candidate: its key above its index's complement, so that the larger comes first and, of equal ones,
+// the lower index.
+__device__ inline uint64_t top_place_key(uint32_t key, int idx) { return (uint64_t)key << 32 | ~(uint32_t)idx; }
+
+template <int NT>
+struct TopShared {
+  uint64_t cand[kCandidates<NT>];
+  uint64_t own[NT / 64][kWaveCandidates];
+  float top_z[kCandidates<NT>];  // by place
+  int top_i[NT];
+  double sum[NT / 64][2];
+  float max[NT / 64];
+  int count[NT / 64], bound[NT / 64];
+  int n, over;
+};
 
 template <int NT>
 __device__ inline int wg_count(int n, int* red) {
@@ -518,149 +520,320 @@ __device__ inline int wg_count(int n, int* red) {
   if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = n;
   __syncthreads();
   n = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < NT / 64; ++w) n += red[w];
   return n;
 }
 
-// The k-th largest of the threads' maxima is a lower bound of the k-th largest logit, and nearly
-// equal to it where the largest are spread over the row: the logits from it on (candidates) are few
-// more than k and go to LDS, where each one's place is the number of candidates before it.  A row
-// whose candidates are too many (long runs of equal logits, or the largest in few threads'
-// elements) finds the k-th logit by its bits instead.
-__global__ __launch_bounds__(kTopThreads) void logits_top_kernel(const void* __restrict__ logits, int bf16, int V,
-                                                                 int64_t ld, int k, double rtau, float c,
-                                                                 int32_t* __restrict__ ids, float* __restrict__ logp,
-                                                                 float* __restrict__ rest_out) {
-  constexpr int NT = kTopThreads;
-  __shared__ uint32_t ckey[kCandidates];  // the threads' maxima at first
-  __shared__ int cidx[kCandidates];
-  __shared__ float top_z[NQ_TOP_MAX];
-  __shared__ int top_i[NQ_TOP_MAX];
-  __shared__ double red[NT / 64];
-  __shared__ int s_n, s_last_i;
-  __shared__ uint32_t s_last_key;
-  int* ired = reinterpret_cast<int*>(red);
-  const int tid = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const char* x = static_cast<const char*>(logits) + t * ld * (bf16 ? 2 : 4);
+// Places of the candidates (each one's is the number of those before it); the first k are listed, the
+// others belong to the rest.  (The candidates' own order changes from run to run, their places do not.)
+template <int NT>
+__device__ void top_places(const TopArgs& A, TopShared<NT>& S, int n, MaxSum& rest) {
+  for (int e = threadIdx.x; e < n; e += NT) {
+    const uint64_t mine = S.cand[e];
+    int place = 0;
+#pragma unroll 8
+    for (int f = 0; f < n; ++f) place += S.cand[f] > mine;
+    S.top_z[place] = key_logit((uint32_t)(mine >> 32));
+    if (place < A.k) S.top_i[place] = (int)~(uint32_t)mine;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += NT)
+    if (e >= A.k) rest.add(S.top_z[e], A.c);
+}
 
-  uint32_t mine = 0;
-  for (int i = tid; i < V; i += NT) mine = max(mine, logit_key(row_load(x, bf16, i)));
-  ckey[tid] = mine;
-  if (tid == 0) {
-    s_n = 0;
-    s_last_key = kFirstKey - 1;  // everything finite is listed
-    s_last_i = 0x7fffffff;
+// The record of row t from the m listed tokens and each thread's part of the rest.  False: there is NaN
+// in the rest (nothing is written then).
+template <int NT>
+__device__ bool top_record(const TopArgs& A, TopShared<NT>& S, int64_t t, int m, const MaxSum& rest, bool even_nan) {
+  constexpr int W = NT / 64;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  float m_r = wave_max(rest.m);
+  if (lane == 0) S.max[wave] = m_r;
+  __syncthreads();
+  m_r = row_max(S.max[lane % W]);
+  const float ref = m_r == -kInf ? 0.0f : m_r;
+  const double ref_k = m > 0 ? (double)S.top_z[0] : 0.0;
+  double s_r = wave_sum((double)rest.s * (double)exp_scaled(rest.m == -kInf ? 0.0f : rest.m - ref, A.c)), s_k = 0.0;
+  if (wave * 64 < m) {
+#pragma unroll 1
+    for (int e = tid; e < m; e += NT) s_k += exp(((double)S.top_z[e] - ref_k) * A.rtau);
+    s_k = wave_sum(s_k);
+  }
+  if (lane == 0) {
+    S.sum[wave][0] = s_r;
+    S.sum[wave][1] = s_k;
   }
   __syncthreads();
-  uint32_t bound = 0;
-  if (tid < 64) {  // one wave: the largest value that at least k of the maxima reach
-    uint32_t v[NT / 64];
-#pragma unroll
-    for (int j = 0; j < NT / 64; ++j) v[j] = ckey[tid + 64 * j];
-    for (int b = 31; b >= 0; --b) {
-      const uint32_t at = bound | 1u << b;
-      int n = 0;
-#pragma unroll
-      for (int j = 0; j < NT / 64; ++j) n += __popcll(__ballot(v[j] >= at));
-      if (n >= k) bound = at;
-    }
-    if (tid == 0) s_last_i = (int)max(bound, kFirstKey);
+  s_r = row_sum(lane % 16 < W ? S.sum[lane % 16][0] : 0.0);
+  if (s_r != s_r && !even_nan) return false;
+  if (wave * 64 >= A.k && tid != 0) return true;
+  s_k = row_sum(lane % 16 < W ? S.sum[lane % 16][1] : 0.0);
+  // relative to ref_k / tau; an empty row has nothing listed and rest -inf
+  const double ref_r = ((double)ref - ref_k) * A.rtau, lse = log(s_k + s_r * exp(ref_r));
+#pragma unroll 1
+  for (int e = tid; e < A.k; e += NT) {
+    A.ids[t * A.k + e] = e < m ? S.top_i[e] : -1;
+    A.logp[t * A.k + e] = e < m ? (float)(((double)S.top_z[e] - ref_k) * A.rtau - lse) : -kInf;
   }
-  __syncthreads();
-  bound = (uint32_t)s_last_i;
-  __syncthreads();
-  if (tid == 0) s_last_i = 0x7fffffff;
-  int last_i = 0x7fffffff;  // candidates equal to the bound: indices up to this
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int i = tid; i < V; i += NT) {
-      const uint32_t key = logit_key(row_load(x, bf16, i));
-      if (key > bound || (key == bound && i <= last_i)) {
-        const int n = atomicAdd(&s_n, 1);
-        if (n < kCandidates) {
-          ckey[n] = key;
-          cidx[n] = i;
-        }
-      }
-    }
-    __syncthreads();
-    if (s_n <= kCandidates) break;
-    // too many: the k-th largest key bit by bit (at least k keys reach the bound), then the last
-    // of the equal ones by index; exactly k candidates are left
-    uint32_t at = 0;
-    for (int b = 31; b >= 0; --b) {
-      const uint32_t key = at | 1u << b;
-      int n = 0;
-      for (int i = tid; i < V; i += NT) n += logit_key(row_load(x, bf16, i)) >= key;
-      if (wg_count<NT>(n, ired) >= k) at = key;
-    }
+  if (tid == 0 && A.rest) A.rest[t] = s_r == 0.0 && lse == lse ? -kInf : (float)(ref_r + log(s_r) - lse);
+  return true;
+}
+
+// Any row, NaN and long runs of equal logits among them: the k-th largest key bit by bit, then the last
+// of the equal ones by index, so that exactly the listed tokens are candidates.
+template <int NT>
+__device__ void top_by_bits(const TopArgs& A, TopShared<NT>& S, int64_t t, const char* x, bool bf16) {
+  const int tid = threadIdx.x, V = A.V, k = A.k;
+  int* red = S.count;
+  uint32_t at = 0;
+#pragma unroll 1
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t key = at | 1u << b;
+    int n = 0;
+#pragma unroll 1
+    for (int i = tid; i < V; i += NT) n += logit_key(row_load(x, bf16, i)) >= key;
+    if (wg_count<NT>(n, red) >= k) at = key;
+  }
+  int last = 0x7fffffff;
+  if (at < kFirstKey) {  // fewer than k above -inf: all of those
+    at = kFirstKey;
+  } else {
     int above = 0;
+#pragma unroll 1
     for (int i = tid; i < V; i += NT) above += logit_key(row_load(x, bf16, i)) > at;
-    const int need = k - wg_count<NT>(above, ired);
-    int lo = 0, hi = V - 1;  // the smallest index up to which `need` keys equal the bound
+    const int need = k - wg_count<NT>(above, red);
+    int lo = 0, hi = V - 1;  // the smallest index up to which `need` keys equal the k-th
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
       int n = 0;
+#pragma unroll 1
       for (int i = tid; i <= mid; i += NT) n += logit_key(row_load(x, bf16, i)) == at;
-      if (wg_count<NT>(n, ired) >= need)
+      if (wg_count<NT>(n, red) >= need)
         hi = mid;
       else
         lo = mid + 1;
     }
-    bound = at;
-    last_i = lo;
-    __syncthreads();
-    if (tid == 0) s_n = 0;
-    __syncthreads();
-  }
-  const int n = s_n;
-  for (int e = tid; e < n; e += NT) {
-    const uint32_t key = ckey[e];
-    const int idx = cidx[e];
-    int place = 0;
-    for (int f = 0; f < n; ++f) place += ckey[f] > key || (ckey[f] == key && cidx[f] < idx);
-    if (place < k) {
-      top_z[place] = row_load(x, bf16, idx);
-      top_i[place] = idx;
-      if (place == k - 1) {
-        s_last_key = key;
-        s_last_i = idx;
-      }
-    }
+    last = lo;
   }
   __syncthreads();
-  const int m = min(n, k);  // listed
-  const uint32_t lkey = s_last_key;
-  const int li = s_last_i;
+  if (tid == 0) S.n = 0;
+  __syncthreads();
   MaxSum rest;
+#pragma unroll 1
   for (int i = tid; i < V; i += NT) {
     const float v = row_load(x, bf16, i);
     const uint32_t key = logit_key(v);
-    if (key < lkey || (key == lkey && i > li)) rest.add(v, c);
+    if (key > at || (key == at && i <= last))
+      S.cand[atomicAdd(&S.n, 1)] = top_place_key(key, i);  // at most k
+    else
+      rest.add(v, A.c);
   }
-  const float m_r = wg_max<NT>(rest.m, red);
-  const float ref = m_r == -kInf ? 0.0f : m_r;
-  const double s_r = wg_sum<NT>((double)rest.s * (double)exp_scaled(rest.m == -kInf ? 0.0f : rest.m - ref, c), red);
-  const double ref_k = m > 0 ? (double)top_z[0] : 0.0;
-  double s_k = 0.0;
-  for (int e = tid; e < m; e += NT) s_k += exp(((double)top_z[e] - ref_k) * rtau);
-  s_k = wg_sum<NT>(s_k, red);
-  // relative to ref_k / tau; an empty row has nothing listed and rest -inf
-  const double lse = log(s_k + s_r * exp(((double)ref - ref_k) * rtau));
-  for (int e = tid; e < k; e += NT) {
-    ids[t * k + e] = e < m ? top_i[e] : -1;
-    logp[t * k + e] = e < m ? (float)(((double)top_z[e] - ref_k) * rtau - lse) : -kInf;
+  __syncthreads();
+  const int n = S.n;
+  top_places<NT>(A, S, n, rest);
+  top_record<NT>(A, S, t, n, rest, true);
+}
+
+// Order of floats as integers (-0 below 0; a bound of 0 takes both).
+__device__ inline int float_order(float v) {
+  const int i = __float_as_int(v);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ inline float order_float(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+// A value that at least k logits reach, and few more where the largest are spread over the row: each of
+// the `waves` waves that have logits finds one that `quota` of its groups' maxima reach (each thread has
+// G), quota * waves >= k, and the lowest of them is taken.  The lowest finite value where a wave has too
+// few finite groups.
+template <int NT, int G>
+__device__ float top_bound(TopShared<NT>& S, const float (&gm)[G], int quota, int waves) {
+  constexpr int W = NT / 64;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  int lo = 0x7fffffff;
+  if (wave < waves) {
+    // between lo, which at least quota reach (the least of the lanes' largest, or of all groups, or the
+    // lowest finite value), and hi, which fewer do
+    float most = gm[0], least = gm[0];
+#pragma unroll
+    for (int i = 1; i < G; ++i) {
+      most = fmaxf(most, gm[i]);
+      least = fminf(least, gm[i]);
+    }
+    lo = max(float_order(-wave_max(-(quota <= 64 ? most : least))), float_order(-__FLT_MAX__));
+    int hi = float_order(wave_max(most)) + 1, g[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) g[i] = float_order(gm[i]);
+    while (hi > lo && (uint32_t)hi - (uint32_t)lo > 1) {
+      const int mid = (int)((uint32_t)lo + ((uint32_t)hi - (uint32_t)lo) / 2);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < G; ++i) n += __popcll(__ballot(g[i] >= mid));
+      if (n >= quota) {
+        lo = mid;
+        if (n <= quota + quota / 8 + 1) break;
+      } else {
+        hi = mid;
+      }
+    }
   }
-  if (tid == 0 && rest_out) rest_out[t] = s_r == 0.0 && lse == lse ? -kInf : (float)(((double)ref - ref_k) * rtau + log(s_r) - lse);
+  __syncthreads();  // an earlier call's values have been read
+  if (lane == 0) S.bound[wave] = lo;
+  __syncthreads();
+  int b = S.bound[lane % W];
+  b = min(b, __builtin_amdgcn_mov_dpp(b, kXor1, 0xF, 0xF, true));
+  b = min(b, __builtin_amdgcn_mov_dpp(b, kXor2, 0xF, 0xF, true));
+  b = min(b, __builtin_amdgcn_mov_dpp(b, kHalfMirror, 0xF, 0xF, true));
+  b = min(b, __builtin_amdgcn_mov_dpp(b, kMirror, 0xF, 0xF, true));
+  return order_float(b);
+}
+
+// One pass over the row.  The maxima of the first step's groups give a bound that at least k logits
+// reach; from there on logits that reach it are candidates, which each wave keeps in LDS in the order it
+// meets them, and the others are the rest, whose sum is taken as in distill_kernel.  The bound is taken
+// anew where the steps double and at the end, and what no longer reaches it joins the rest.  Rows with too
+// many candidates (long runs of equal logits, the largest in few groups) or with NaN are done by bits
+// instead.
+template <bool BF16, int NT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void logits_top_kernel(const TopArgs A) {
+  using Pc = Piece<BF16>;
+  constexpr int N = Pc::N, U = 4;
+  __shared__ TopShared<NT> S;
+  const int tid = threadIdx.x, V = A.V, np = V / N, lane = tid % 64, k = A.k;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int64_t t = blockIdx.x;
+  const char* x = row_at<BF16>(A.logits, t, A.ld);
+  if (tid == 0) S.n = S.over = 0;
+  const int it = np * N + tid;
+  float xt = it < V ? row_load(x, BF16, it) : -kInf;
+  constexpr int H = BF16 ? 2 : 1, G = U * H;  // groups: quarters of a step's pieces, 4 logits each
+  float gm[G], bound = 0.0f;
+#pragma unroll
+  for (int i = 0; i < G; ++i) gm[i] = -kInf;
+  gm[0] = xt;
+  const int waves = max(1, (min(np, NT) + 63) / 64), quota = (k + waves - 1) / waves;
+  MaxSum rest;
+  int mine = 0;  // this wave's candidates
+  // takes the lanes' logits that reach the bound; all lanes of the wave come here
+  auto take = [&](float v, int idx) {
+    const bool on = v >= bound;
+    const uint64_t lanes = __ballot(on);
+    if (!lanes) return false;
+    const int at = mine + __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
+    if (on && at < kWaveCandidates) S.own[wave][at] = top_place_key(logit_key(v), idx);
+    mine += __popcll(lanes);
+    return on;
+  };
+  // what of this wave's candidates no longer reaches the bound joins the rest
+  auto prune = [&] {
+    int kept = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < mine; e0 += 64) {
+      const uint64_t c = S.own[wave][min(e0 + lane, kWaveCandidates - 1)];
+      const float v = key_logit((uint32_t)(c >> 32));
+      const bool on = e0 + lane < mine, keep = on && v >= bound;
+      const uint64_t lanes = __ballot(keep);
+      const int at = kept + __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
+      if (keep) S.own[wave][at] = c;
+      if (on && !keep) rest.add(v, A.c);
+      kept += __popcll(lanes);
+    }
+    mine = kept;
+  };
+  int steps = 0, next_bound = 0;
+#pragma unroll 1
+  for (int j0 = tid; j0 - tid < np || steps == 0; j0 += NT * U, ++steps) {
+    Pc pc[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int j = j0 + i * NT;
+      if (j < np)
+        pc[i].load(x, j);
+      else
+        pc[i].fill();
+    }
+    float pm[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      pm[i] = -kInf;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float m = pc[i].at(4 * h);
+        m = max3(m, pc[i].at(4 * h + 1), pc[i].at(4 * h + 2));
+        m = fmaxf(m, pc[i].at(4 * h + 3));
+        gm[i * H + h] = fmaxf(gm[i * H + h], m);
+        pm[i] = fmaxf(pm[i], m);
+      }
+      pc[i].packed();
+    }
+    if (steps == next_bound) {
+      bound = top_bound<NT>(S, gm, quota, waves);
+      next_bound = 2 * steps + 1;
+      if (mine > kWaveCandidates) S.over = 1, mine = kWaveCandidates;
+      prune();
+    }
+    if (steps == 0) {
+      if (take(xt, it)) xt = -kInf;
+      rest.add(xt, A.c);
+    }
+    float mm = rest.m;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (__any(pm[i] >= bound)) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int q = 0; q < N; ++q) bits |= take(pc[i].at(q), (j0 + i * NT) * N + q) ? 1u << q : 0u;
+        pc[i].mask(bits);
+        pm[i] = -kInf;
+#pragma unroll
+        for (int q = 0; q < N; q += 2) pm[i] = max3(pm[i], pc[i].at(q), pc[i].at(q + 1));
+      }
+      pc[i].packed();
+      mm = fmaxf(mm, pm[i]);
+    }
+    const float ref = mm == -kInf ? 0.0f : mm;
+    rest.s *= exp_scaled(rest.m - ref, A.c);
+    rest.m = mm;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int q = 0; q < N; ++q) rest.s += exp_scaled(pc[i].at(q) - ref, A.c);
+  }
+  if (mine > kWaveCandidates) S.over = 1, mine = kWaveCandidates;
+  if (steps > 1) {
+    bound = top_bound<NT>(S, gm, quota, waves);
+    prune();
+  }
+  int first = 0;
+  if (lane == 0) first = atomicAdd(&S.n, mine);
+  first = __builtin_amdgcn_readfirstlane(first);
+#pragma unroll 1
+  for (int e = lane; e < mine; e += 64)
+    if (first + e < kCandidates<NT>) S.cand[first + e] = S.own[wave][e];
+  __syncthreads();
+  const int n = S.n;
+  if (n <= kCandidates<NT> && !S.over) {
+    top_places<NT>(A, S, n, rest);
+    if (top_record<NT>(A, S, t, min(n, k), rest, false)) return;
+  }
+  __syncthreads();
+  top_by_bits<NT>(A, S, t, x, BF16);
 }
 
 }  // namespace
 
 hipError_t launch_logits_top(const void* logits, nq_dtype dt, int64_t T, int64_t V, int64_t ld, int k, float temperature,
                              int32_t* ids, float* logp, float* rest, hipStream_t s) {
-  hipLaunchKernelGGL(logits_top_kernel, dim3((unsigned)T), dim3(kTopThreads), 0, s, logits, (int)(dt == NQ_BF16), (int)V,
-                     ld, k, 1.0 / (double)temperature, exp_scale(temperature), ids, logp, rest);
+  const TopArgs A{logits, ld, (int)V, k, exp_scale(temperature), 1.0 / (double)temperature, ids, logp, rest};
+  const bool bf16 = dt == NQ_BF16;
+  const int64_t np = V / (bf16 ? 8 : 4);
+  // as for the loss (launch_distill_t); a larger k needs the larger workgroups' room for candidates
+  int nt = np <= 1024 || T > 1024 ? 256 : np <= 2048 ? 512 : 1024;
+  if (k > 128) nt = k > 256 ? 1024 : nt < 512 ? 512 : nt;
+  const auto kernel = nt == 256   ? (bf16 ? logits_top_kernel<true, 256> : logits_top_kernel<false, 256>)
+                      : nt == 512 ? (bf16 ? logits_top_kernel<true, 512> : logits_top_kernel<false, 512>)
+                                  : (bf16 ? logits_top_kernel<true, 1024> : logits_top_kernel<false, 1024>);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(nt), 0, s, A);
   return hipGetLastError();
 }
 
