@@ -125,7 +125,8 @@ def epilogue_ref(v, act="none", bias=None, mul=None, residual=None):
 
     z = v + bias is off by one rounding, which reaches act by its derivative.  An activation's own arithmetic is within
     8 roundings of its value (two or three functions of at most two units each, a product, a quotient) and within 4
-    for each unit of its exponent; its derivative adds at most two such values.  mul and residual round once each."""
+    for each unit of its exponent; its derivative adds at most two such values.  mul and residual round once each.  The
+    hardware's 2^x and reciprocal are 0 below 2^-126, where z of it, and the derivative's parts with it, are lost."""
     v = np.asarray(v, dtype=np.float64)
     z = v if bias is None else v + np.asarray(bias, dtype=np.float64)
     with np.errstate(invalid="ignore"):
@@ -138,7 +139,8 @@ def epilogue_ref(v, act="none", bias=None, mul=None, residual=None):
         if residual is not None:
             y = y + np.asarray(residual, dtype=np.float64)
             err = err + np.abs(y) * EPS32
-    return y, z, err + 1e-37
+        tiny = (np.abs(z) + 1) * 2.0 ** -125 * (1 if mul is None else np.abs(np.asarray(mul, dtype=np.float64)))
+    return y, z, err + np.where(np.isfinite(tiny), tiny, 0.0)
 
 
 def act_grads_ref(act, z, dy, mul=None):
@@ -153,8 +155,9 @@ def act_grads_ref(act, z, dy, mul=None):
     # the derivative's parts are at most 1 + max |z q (1 - q) u'|, and fall off as the exponent grows
     e_da = parts * (8 + 4 * np.minimum(cond, 64.0)) * EPS32 * own
     dz, dmul = dy * m * da, dy * a
-    e_dz = np.abs(dy * m) * e_da + 2 * np.abs(dz) * EPS32 + 1e-37
-    e_dmul = np.abs(dy * a) * (1 + own * (8 + 4 * cond)) * EPS32 + 1e-37
+    tiny = (z * z + 2) * 2.0 ** -125
+    e_dz = np.abs(dy * m) * (e_da + tiny) + 2 * np.abs(dz) * EPS32
+    e_dmul = np.abs(dy * a) * (1 + own * (8 + 4 * cond)) * EPS32 + np.abs(dy) * tiny
     n = dz.shape[0]
     e_dbias = e_dz.sum(0) + n * EPS32 * np.abs(dz).sum(0)
     return dz, dmul, dz.sum(0), (e_dz, e_dmul, e_dbias)

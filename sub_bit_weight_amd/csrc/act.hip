@@ -20,28 +20,143 @@ __global__ __launch_bounds__(256) void epilogue_kernel(const float* __restrict__
 struct ActGrads {
   const void *z, *mul, *dy;
   void *dz, *dmul;
-  int act, z_bf16, mul_bf16, dy_bf16, dz_bf16, dmul_bf16;
+  int z_bf16, mul_bf16, dy_bf16, dz_bf16, dmul_bf16;
 };
 
-// One thread per column walks a chunk of tc tokens; the chunk's sum of dz goes to sums[chunk][d].
-__global__ __launch_bounds__(256) void act_grads_kernel(const ActGrads G, int64_t T, int64_t tc, int64_t d,
-                                                        float* __restrict__ sums) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= d) return;
-  const int64_t t0 = (int64_t)blockIdx.y * tc, t1 = imin(t0 + tc, T);
-  float acc = 0.0f;
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t i = t * d + c;
-    const float dy = epi_load(G.dy, G.dy_bf16, i);
-    float a = 0.0f, da = 1.0f;
-    if (G.z) act_value_grad(G.act, epi_load(G.z, G.z_bf16, i), a, da);
-    float dz = dy * da;
-    if (G.mul) dz *= epi_load(G.mul, G.mul_bf16, i);
-    if (G.dmul) epi_store(G.dmul, G.dmul_bf16, i, dy * a);
-    epi_store(G.dz, G.dz_bf16, i, dz);
-    acc += dz;
+// N elements of an operand from element i on, at any alignment of its elements.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+template <int N>
+struct Elements {
+  float v[N];
+  __device__ void load(const void* p, bool bf16, int64_t i) {
+    if (bf16) {
+      const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+      uint32_t w[N / 2];
+      if constexpr (N == 8) {
+        const u32x4 d = *reinterpret_cast<const u32x4_a2*>(q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = d[j];
+      } else {
+        const u32x2 d = *reinterpret_cast<const u32x2_a2*>(q);
+        w[0] = d[0], w[1] = d[1];
+      }
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    } else {
+      const float* q = static_cast<const float*>(p) + i;
+#pragma unroll
+      for (int j = 0; j < N; j += 4) {
+        const u32x4 d = *reinterpret_cast<const u32x4_a4*>(q + j);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[j + k] = __uint_as_float(d[k]);
+      }
+    }
   }
-  if (sums) sums[(int64_t)blockIdx.y * d + c] = acc;
+  __device__ void store(void* p, bool bf16, int64_t i) const {
+    if (bf16) {
+      uint16_t* q = static_cast<uint16_t*>(p) + i;
+      uint32_t w[N / 2];
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j)
+        w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * j], v[2 * j + 1]}, bf16x2));
+      if constexpr (N == 8)
+        *reinterpret_cast<u32x4_a2*>(q) = u32x4{w[0], w[1], w[2], w[3]};
+      else
+        *reinterpret_cast<u32x2_a2*>(q) = u32x2{w[0], w[1]};
+    } else {
+      float* q = static_cast<float*>(p) + i;
+#pragma unroll
+      for (int j = 0; j < N; j += 4)
+        *reinterpret_cast<u32x4_a4*>(q + j) = u32x4{__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
+                                                   __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])};
+    }
+  }
+};
+
+// One element's gradients.
+template <int ACT>
+__device__ inline void element_grads(float z, float mul, float dy, float& dz, float& dmul) {
+  float a, da;
+  act_value_grad<ACT>(z, a, da);
+  dz = dy * da * mul;
+  dmul = dy * a;
+}
+
+// A workgroup takes kCols columns' worth of N-element pieces and tc tokens; each of its kRows rows of
+// threads walks every kRows-th token, and the rows' sums of dz are added in order through LDS into
+// sums[chunk][d].  The columns past the last whole piece are one thread's, element by element.
+constexpr int kCols = 16, kRows = 16, kGradThreads = kCols * kRows;
+template <int ACT, int N>
+__global__ __launch_bounds__(kGradThreads) void act_grads_kernel(const ActGrads G, int64_t T, int64_t tc, int64_t d,
+                                                                 float* __restrict__ sums) {
+  __shared__ float part[kRows][kCols * N];
+  const int col = threadIdx.x % kCols, row = threadIdx.x / kCols;
+  const int64_t c0 = ((int64_t)blockIdx.x * kCols + col) * N;
+  const int64_t t0 = (int64_t)blockIdx.y * tc, t1 = imin(t0 + tc, T);
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+  if (c0 + N <= d) {
+    // two tokens at a time, all their loads ahead of their stores (a result may be in place)
+    constexpr int U = 2;
+    for (int64_t t = t0 + row; t < t1; t += U * kRows) {
+      Elements<N> z[U], mul[U], dy[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = imin(t + u * kRows, t1 - 1) * d + c0;
+        dy[u].load(G.dy, G.dy_bf16, i);
+        if (G.z) z[u].load(G.z, G.z_bf16, i);
+        if (G.mul) mul[u].load(G.mul, G.mul_bf16, i);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u * kRows >= t1) break;
+        const int64_t i = (t + u * kRows) * d + c0;
+        Elements<N> dz, dmul;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          element_grads<ACT>(G.z ? z[u].v[j] : 0.0f, G.mul ? mul[u].v[j] : 1.0f, dy[u].v[j], dz.v[j], dmul.v[j]);
+          acc[j] += dz.v[j];
+        }
+        dz.store(G.dz, G.dz_bf16, i);
+        if (G.dmul) dmul.store(G.dmul, G.dmul_bf16, i);
+      }
+    }
+  } else if (c0 < d) {
+    for (int64_t t = t0 + row; t < t1; t += kRows)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (c0 + j >= d) continue;
+        const int64_t i = t * d + c0 + j;
+        float dz, dmul;
+        element_grads<ACT>(G.z ? epi_load(G.z, G.z_bf16, i) : 0.0f, G.mul ? epi_load(G.mul, G.mul_bf16, i) : 1.0f,
+                           epi_load(G.dy, G.dy_bf16, i), dz, dmul);
+        acc[j] += dz;
+        epi_store(G.dz, G.dz_bf16, i, dz);
+        if (G.dmul) epi_store(G.dmul, G.dmul_bf16, i, dmul);
+      }
+  }
+  if (!sums) return;
+#pragma unroll
+  for (int j = 0; j < N; ++j) part[row][col * N + j] = acc[j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < kCols * N; c += kGradThreads) {
+    const int64_t at = (int64_t)blockIdx.x * kCols * N + c;
+    if (at >= d) break;
+    float s = part[0][c];
+#pragma unroll
+    for (int r = 1; r < kRows; ++r) s += part[r][c];
+    sums[(int64_t)blockIdx.y * d + at] = s;
+  }
 }
 
 __global__ __launch_bounds__(256) void chunk_sums_kernel(const float* __restrict__ sums, int64_t n, int64_t d,
@@ -49,12 +164,25 @@ __global__ __launch_bounds__(256) void chunk_sums_kernel(const float* __restrict
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= d) return;
   float acc = 0.0f;
+#pragma unroll 8
   for (int64_t q = 0; q < n; ++q) acc += sums[q * d + c];
   out[c] = acc;
 }
 
-// Tokens of a chunk: 64, more when T has more than 1024 such chunks.
-int64_t chunk_tokens(int64_t T) { return imax(64, cdiv(T, 1024)); }
+// Tokens of a chunk: all up to 256 (no second launch for their sums), else 128, more when T has more
+// than 1024 such chunks.
+int64_t chunk_tokens(int64_t T) { return T <= 256 ? T : imax(128, cdiv(T, 1024)); }
+
+template <int N>
+void launch_act_grads_n(int act, const ActGrads& G, int64_t T, int64_t tc, int64_t d, float* sums, hipStream_t s) {
+  const dim3 grid((unsigned)cdiv(d, kCols * N), (unsigned)cdiv(T, tc));
+  const auto kernel = act == NQ_ACT_RELU        ? act_grads_kernel<NQ_ACT_RELU, N>
+                      : act == NQ_ACT_GELU      ? act_grads_kernel<NQ_ACT_GELU, N>
+                      : act == NQ_ACT_GELU_TANH ? act_grads_kernel<NQ_ACT_GELU_TANH, N>
+                      : act == NQ_ACT_SILU      ? act_grads_kernel<NQ_ACT_SILU, N>
+                                                : act_grads_kernel<NQ_ACT_NONE, N>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kGradThreads), 0, s, G, T, tc, d, sums);
+}
 
 }  // namespace
 
@@ -72,11 +200,15 @@ size_t act_grads_workspace(int64_t T, int64_t d) {
 hipError_t launch_act_grads(int act, const void* z, nq_dtype zd, const void* mul, nq_dtype md, const void* dy,
                             nq_dtype dyd, int64_t T, int64_t d, void* dz, nq_dtype dzd, void* dmul, nq_dtype dmd,
                             float* dbias, void* ws, hipStream_t s) {
-  const ActGrads G{z,   mul,           dy,            dz,             dmul,           act,
+  const ActGrads G{z,   mul,           dy,            dz,             dmul,
                    zd == NQ_BF16, md == NQ_BF16, dyd == NQ_BF16, dzd == NQ_BF16, dmd == NQ_BF16};
   const int64_t tc = chunk_tokens(T), n = cdiv(T, tc);
   float* sums = !dbias ? nullptr : n > 1 ? static_cast<float*>(ws) : dbias;
-  hipLaunchKernelGGL(act_grads_kernel, dim3((unsigned)cdiv(d, 256), (unsigned)n), dim3(256), 0, s, G, T, tc, d, sums);
+  // pieces of 16 bytes of dy
+  if (dyd == NQ_BF16)
+    launch_act_grads_n<8>(act, G, T, tc, d, sums, s);
+  else
+    launch_act_grads_n<4>(act, G, T, tc, d, sums, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dbias || n == 1) return e;
   hipLaunchKernelGGL(chunk_sums_kernel, dim3((unsigned)cdiv(d, 256)), dim3(256), 0, s, sums, n, d, dbias);
