@@ -1,4 +1,4 @@
-// Epilogue of a packed linear and its gradients.
+// Gradients of a packed linear's epilogue.
 //
 // The layer y = s1 (.) U (V^T (s2 (.) x)) (research.samsung.com NanoQuant blog, section 2 "Low-Rank
 // Binary Factorization") stands in a block between a bias, an activation, a gate and a residual:
@@ -11,75 +11,10 @@
 namespace nq {
 namespace {
 
-__global__ __launch_bounds__(256) void epilogue_kernel(const float* __restrict__ v, int64_t n, int64_t d,
-                                                       const Epilogue E) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
-    epilogue_store(E, i, i % d, v[i]);
-}
-
 struct ActGrads {
   const void *z, *mul, *dy;
   void *dz, *dmul;
   int z_bf16, mul_bf16, dy_bf16, dz_bf16, dmul_bf16;
-};
-
-// N elements of an operand from element i on, at any alignment of its elements.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-template <int N>
-struct Elements {
-  float v[N];
-  __device__ void load(const void* p, bool bf16, int64_t i) {
-    if (bf16) {
-      const uint16_t* q = static_cast<const uint16_t*>(p) + i;
-      uint32_t w[N / 2];
-      if constexpr (N == 8) {
-        const u32x4 d = *reinterpret_cast<const u32x4_a2*>(q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = d[j];
-      } else {
-        const u32x2 d = *reinterpret_cast<const u32x2_a2*>(q);
-        w[0] = d[0], w[1] = d[1];
-      }
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-    } else {
-      const float* q = static_cast<const float*>(p) + i;
-#pragma unroll
-      for (int j = 0; j < N; j += 4) {
-        const u32x4 d = *reinterpret_cast<const u32x4_a4*>(q + j);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[j + k] = __uint_as_float(d[k]);
-      }
-    }
-  }
-  __device__ void store(void* p, bool bf16, int64_t i) const {
-    if (bf16) {
-      uint16_t* q = static_cast<uint16_t*>(p) + i;
-      uint32_t w[N / 2];
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j)
-        w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * j], v[2 * j + 1]}, bf16x2));
-      if constexpr (N == 8)
-        *reinterpret_cast<u32x4_a2*>(q) = u32x4{w[0], w[1], w[2], w[3]};
-      else
-        *reinterpret_cast<u32x2_a2*>(q) = u32x2{w[0], w[1]};
-    } else {
-      float* q = static_cast<float*>(p) + i;
-#pragma unroll
-      for (int j = 0; j < N; j += 4)
-        *reinterpret_cast<u32x4_a4*>(q + j) = u32x4{__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
-                                                   __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])};
-    }
-  }
 };
 
 // One element's gradients.
@@ -185,12 +120,6 @@ void launch_act_grads_n(int act, const ActGrads& G, int64_t T, int64_t tc, int64
 }
 
 }  // namespace
-
-hipError_t launch_epilogue(const float* v, int64_t T, int64_t d, const Epilogue& E, hipStream_t s) {
-  const int64_t n = T * d;
-  hipLaunchKernelGGL(epilogue_kernel, dim3((unsigned)imin(cdiv(n, 256), 8192)), dim3(256), 0, s, v, n, d, E);
-  return hipGetLastError();
-}
 
 size_t act_grads_workspace(int64_t T, int64_t d) {
   const int64_t n = cdiv(T, chunk_tokens(T));

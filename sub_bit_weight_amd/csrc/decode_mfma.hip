@@ -27,6 +27,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "epilogue.h"
 #include "nq_internal.h"
 
 namespace nq {
@@ -150,24 +151,39 @@ __device__ inline void wait_input(const StageDesc& S, int* err) {
   __syncthreads();
 }
 
+// A final output row, one value per token.  EPI: a linear's outputs (the stage that signals nothing) go
+// through the epilogue E.
+template <int T, bool EPI>
+__device__ __forceinline__ void store_row(const StageDesc& S, int64_t o, float sc, const float* acc, const Epilogue& E) {
+  if (EPI && !S.signal) {
+    float v[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) v[t] = sc * acc[t];
+    epilogue_store<T>(E, E.bias ? E.bias[o] : 0.0f, v, [&](int t) { return (int64_t)t * S.n_rows + o; });
+    return;
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    float* dst = S.out + (int64_t)t * S.n_rows + o;
+    if (S.signal)
+      store_agent(dst, sc * acc[t]);
+    else
+      gstore(dst, sc * acc[t]);
+  }
+}
+
 // End of a tile, one output row per thread (acc[t] = this tile's sum for row o,
 // token t): store the row (times the row scale), or publish the span's partial
 // sums and let the last span of the row block add them in span order.  Every
 // thread of the workgroup must call it; it ends with a barrier.
-template <int T>
-__device__ void finish_rows(const StageDesc& S, int rb, int ks, int64_t o, bool valid, const float* acc, int* s_flag) {
+template <int T, bool EPI>
+__device__ __forceinline__ void finish_rows(const StageDesc& S, int rb, int ks, int64_t o, bool valid, const float* acc, int* s_flag,
+                            const Epilogue& E) {
   const int tid = threadIdx.x;
   if (S.nks == 1) {
     if (valid) {
       const float sc = S.rowscale ? gload(S.rowscale + o) : 1.0f;
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        float* dst = S.out + (int64_t)t * S.n_rows + o;
-        if (S.signal)
-          store_agent(dst, sc * acc[t]);
-        else
-          gstore(dst, sc * acc[t]);
-      }
+      store_row<T, EPI>(S, o, sc, acc, E);
     }
   } else {
     if (valid) {
@@ -205,14 +221,7 @@ __device__ void finish_rows(const StageDesc& S, int rb, int ks, int64_t o, bool 
 #pragma unroll
             for (int t = 0; t < T; ++t) sum[t] += v[i][t];
       }
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        float* dst = S.out + (int64_t)t * S.n_rows + o;
-        if (S.signal)
-          store_agent(dst, sc * sum[t]);
-        else
-          gstore(dst, sc * sum[t]);
-      }
+      store_row<T, EPI>(S, o, sc, sum, E);
     }
     if (tid == 0) gstore(S.rb_count + rb, 0);  // all arrivals happened: ready for the next run
   }
@@ -692,8 +701,9 @@ __device__ inline float quad_sum(float v) {
 // FUSE (single calls): the span is one chunk whose pieces the tile makes
 // itself (tile_pieces); otherwise they are copied from the stage's
 // input-piece blocks chunk by chunk.
-template <int T, bool W4, bool FUSE>
-__device__ void mfma_tile(const StageDesc& S, int local, float* ldsf, int* s_flag, int* err, NextTile& next) {
+template <int T, bool W4, bool FUSE, bool EPI>
+__device__ __forceinline__ void mfma_tile(const StageDesc& S, int local, float* ldsf, int* s_flag, int* err, NextTile& next,
+                          const Epilogue& E) {
   static_assert(T <= kMfmaMaxT, "tokens");
   constexpr int G = col_groups<T>();
   int* lds = reinterpret_cast<int*>(ldsf);
@@ -847,7 +857,7 @@ __device__ void mfma_tile(const StageDesc& S, int local, float* ldsf, int* s_fla
     for (int t = 0; t < T; ++t) accr[t] = sums[t * kMRows + tid];
     const int rb = rb0 + ri;
     const int64_t o = (int64_t)rb * kMRows + tid;
-    finish_rows<T>(S, rb, ks, o, o < S.n_rows, accr, s_flag);  // ends with a barrier: sums are free again
+    finish_rows<T, EPI>(S, rb, ks, o, o < S.n_rows, accr, s_flag, E);  // ends with a barrier: sums are free again
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -950,22 +960,23 @@ static_assert(col_groups<kMfmaMaxT>() <= 2, "T <= 8 in two column groups");
 // SINGLE: a single call's tiles (kind 2 only); otherwise a sequence's (kinds
 // 0 and 1).  Kept apart so that neither kernel carries the other's code and
 // registers.
-template <int T, bool SINGLE>
-__device__ inline void stage_tile(const StageDesc& S, int local, float* lds, int* s_flag, int* err, NextTile& next) {
+template <int T, bool SINGLE, bool EPI>
+__device__ inline void stage_tile(const StageDesc& S, int local, float* lds, int* s_flag, int* err, NextTile& next,
+                                  const Epilogue& E) {
   if constexpr (SINGLE) {
     if (S.w_vec)
-      mfma_tile<T, true, true>(S, local, lds, s_flag, err, next);
+      mfma_tile<T, true, true, EPI>(S, local, lds, s_flag, err, next, E);
     else
-      mfma_tile<T, false, true>(S, local, lds, s_flag, err, next);
+      mfma_tile<T, false, true, EPI>(S, local, lds, s_flag, err, next, E);
   } else {
     if (S.kind == 1 && S.prep_tg == 1)
       mfma_prep_tile<T, 1>(S, local, lds, err, next);
     else if (S.kind == 1)
       mfma_prep_tile<T, T>(S, local, lds, err, next);
     else if (S.w_vec)
-      mfma_tile<T, true, false>(S, local, lds, s_flag, err, next);
+      mfma_tile<T, true, false, false>(S, local, lds, s_flag, err, next, E);
     else
-      mfma_tile<T, false, false>(S, local, lds, s_flag, err, next);
+      mfma_tile<T, false, false, false>(S, local, lds, s_flag, err, next, E);
   }
 }
 
@@ -974,8 +985,8 @@ __device__ inline void stage_tile(const StageDesc& S, int local, float* lds, int
 // from the counter at [1]; `lookup(tile, S, local)` gives a tile's descriptor
 // and its index within its stage.  The last workgroup to exit zeroes
 // [1 .. n_ints), so consecutive runs need no separate reset launch.
-template <int T, bool SINGLE, typename Lookup>
-__device__ inline void persistent_tiles(Lookup lookup, int ntiles, int* ints, int n_ints, float* lds) {
+template <int T, bool SINGLE, bool EPI, typename Lookup>
+__device__ inline void persistent_tiles(Lookup lookup, int ntiles, int* ints, int n_ints, float* lds, const Epilogue& E) {
   int& s_flag = reinterpret_cast<int*>(lds)[flag_off<T>()];
   int& s_tile = reinterpret_cast<int*>(lds)[flag_off<T>() + 1];
   int* err = ints;
@@ -990,7 +1001,7 @@ __device__ inline void persistent_tiles(Lookup lookup, int ntiles, int* ints, in
     StageDesc S;
     int local;
     lookup(tile, S, local);
-    stage_tile<T, SINGLE>(S, local, lds, &s_flag, err, next);
+    stage_tile<T, SINGLE, EPI>(S, local, lds, &s_flag, err, next, E);
     if (threadIdx.x == 0) s_tile = next.id;
     __syncthreads();
     tile = __builtin_amdgcn_readfirstlane(s_tile);
@@ -1015,12 +1026,12 @@ __global__ __launch_bounds__(kMRows) __attribute__((amdgpu_waves_per_eu(min_wave
 void dec_persistent_kernel(const StageDesc* __restrict__ segs, const int* __restrict__ tile_seg, int ntiles, int* ints,
                            int n_ints) {
   __shared__ __attribute__((aligned(16))) float lds[mfma_lds<T>()];
-  persistent_tiles<T, false>(
+  persistent_tiles<T, false, false>(
       [&](int tile, StageDesc& S, int& local) {
         S = segs[tile_seg[tile]];  // one lookup (a scan over the segments stalled for microseconds)
         local = tile - S.tile0;
       },
-      ntiles, ints, n_ints, lds);
+      ntiles, ints, n_ints, lds, Epilogue{});
 }
 
 // One linear (a single call): its descriptors travel in the kernel arguments.
@@ -1029,11 +1040,11 @@ struct LinearSched {
   int end[kMaxLinearDescs];  // cumulative tile counts
 };
 
-template <int T>
+template <int T, bool EPI>
 __global__ __launch_bounds__(kMRows) __attribute__((amdgpu_waves_per_eu(min_waves<T>())))
-void dec_linear_kernel(LinearSched L, int* ints, int n_ints) {
+void dec_linear_kernel(LinearSched L, int* ints, int n_ints, const Epilogue E) {
   __shared__ __attribute__((aligned(16))) float lds[mfma_lds<T>()];
-  persistent_tiles<T, true>(
+  persistent_tiles<T, true, EPI>(
       [&](int tile, StageDesc& S, int& local) {
         // the stage is uniform across the workgroup: select a pointer into the
         // argument segment (scalar loads), not a copy of each descriptor
@@ -1042,7 +1053,7 @@ void dec_linear_kernel(LinearSched L, int* ints, int n_ints) {
         S = *P;
         local = tile - P->tile0;
       },
-      L.end[kMaxLinearDescs - 1], ints, n_ints, lds);
+      L.end[kMaxLinearDescs - 1], ints, n_ints, lds, E);
 }
 
 __global__ void zero_ints_kernel(int* p, int64_t n) {
@@ -1362,7 +1373,7 @@ int* stream_slot(hipStream_t s) {
 }  // namespace
 
 hipError_t launch_dec_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y, void* ws,
-                             hipStream_t s) {
+                             hipStream_t s, const Epilogue* epi) {
   char* base = static_cast<char*>(ws);
   const int n_ints = 3 + dec_linear_counters(L, T, true);
   int* slot = n_ints <= kSlotInts ? stream_slot(s) : nullptr;
@@ -1385,8 +1396,15 @@ hipError_t launch_dec_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64_
   if (!slot && (e = launch_zero_ints(ints, n_ints, s)) != hipSuccess) return e;
   const int grid = (int)imin(tiles, dec_persistent_grid(T));
   switch (T) {
-#define NQ_CASE(TT)                                                                                        \
-  case TT: hipLaunchKernelGGL(dec_linear_kernel<TT>, dim3(grid), dim3(kMRows), 0, s, sched, ints, n_ints); break;
+#define NQ_CASE(TT)                                                                                            \
+  case TT:                                                                                                     \
+    if (epi)                                                                                                   \
+      hipLaunchKernelGGL((dec_linear_kernel<TT, true>), dim3(grid), dim3(kMRows), 0, s, sched, ints, n_ints,    \
+                         *epi);                                                                                \
+    else                                                                                                       \
+      hipLaunchKernelGGL((dec_linear_kernel<TT, false>), dim3(grid), dim3(kMRows), 0, s, sched, ints, n_ints,   \
+                         Epilogue{});                                                                          \
+    break;
     NQ_CASE(1) NQ_CASE(2) NQ_CASE(3) NQ_CASE(4) NQ_CASE(5) NQ_CASE(6) NQ_CASE(7) NQ_CASE(8)
 #undef NQ_CASE
     default: return hipErrorInvalidValue;

@@ -938,8 +938,16 @@ nq_status check_act(const char* who, nq_act act) {
   return NQ_OK;
 }
 
+// The regimes of launch_linear (but for the comparison kernels of NQ_DECODE_VARIANT, which have no
+// epilogue).
 size_t linear_act_workspace(const nq_lrb& L, int64_t T) {
-  return align_up(linear_workspace(L, T)) + (size_t)T * L.d_out * sizeof(float);
+  return T > kDecodeMaxT ? prefill_workspace_bytes(L, T) : dec_workspace_bytes(L, T);
+}
+hipError_t launch_linear_act(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, const Epilogue& E, void* ws,
+                             hipStream_t s) {
+  if (T > kDecodeMaxT) return launch_prefill(L, x, xd, T, nullptr, ws, s, true, nullptr, &E);
+  if (tiny_enabled() && tiny_fits(L, T)) return launch_tiny_linear(L, x, xd, T, nullptr, s, &E);
+  return launch_dec_linear(L, x, xd, T, nullptr, ws, s, &E);
 }
 
 }  // namespace
@@ -980,11 +988,8 @@ nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, in
                      E->residual_dtype == NQ_BF16,
                      E->z_dtype == NQ_BF16,
                      y_dtype == NQ_BF16};
-  float* v = reinterpret_cast<float*>(static_cast<char*>(workspace) + align_up(linear_workspace(*L, T)));
-  hipStream_t s = (hipStream_t)stream;
-  hipError_t e = launch_linear(*L, x, x_dtype, T, v, workspace, s);
-  if (e == hipSuccess) e = launch_epilogue(v, T, L->d_out, epi, s);
-  return hip_status(e, "nq_lrb_linear_act launch");
+  return hip_status(launch_linear_act(*L, x, x_dtype, T, epi, workspace, (hipStream_t)stream),
+                    "nq_lrb_linear_act launch");
 }
 
 size_t nq_act_grads_workspace_bytes(int64_t T, int64_t d) {

@@ -35,13 +35,18 @@ size_t linear_workspace(const nq_lrb& L, int64_t T, bool in_seq = false);
 hipError_t launch_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y, void* ws,
                          hipStream_t s, bool in_seq = false);
 
+// Bias, activation, gate and residual of a linear's outputs (epilogue.h); a launcher that is given one
+// sends its outputs through it instead of to y.
+struct Epilogue;
+
 // ---------------------------------------------------------------- launchers
 // Each returns the hipError_t of its launch (hipGetLastError after the launch).
 
 // Decode of a small layer (T <= 8) in one workgroup, no workspace (tiny.hip);
 // tiny_fits says which layers take it.
 bool tiny_fits(const nq_lrb& L, int64_t T);
-hipError_t launch_tiny_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y, hipStream_t s);
+hipError_t launch_tiny_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y, hipStream_t s,
+                              const Epilogue* epi = nullptr);
 hipError_t launch_pack(const float* src, int64_t n_out, int64_t n_red, int64_t so, int64_t sr,
                        uint32_t* dst, int64_t ld, hipStream_t s);
 hipError_t launch_unpack(const uint32_t* bits, int64_t n_out, int64_t n_red, int64_t ld, float* dst,
@@ -109,7 +114,7 @@ constexpr int kMaxLinearDescs = 4;
 int dec_stage_descs(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y, bool split,
                     char* ws_linear, int* ctr_base, StageDesc* d);
 hipError_t launch_dec_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y, void* ws,
-                             hipStream_t s);
+                             hipStream_t s, const Epilogue* epi = nullptr);
 hipError_t launch_zero_ints(int* p, int64_t n, hipStream_t s);
 int dec_persistent_grid(int64_t T);
 // ints: [0] error flag, [1] next tile, [2] exited workgroups, [3..n_ints) counters;
@@ -169,7 +174,8 @@ struct ProdEpilogue {
 };
 int64_t prefill_row_blocks(int64_t T);  // the 128-row blocks of a T-token output
 hipError_t launch_prefill(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y,
-                          void* ws, hipStream_t s, bool split = true, const ProdEpilogue* pe = nullptr);
+                          void* ws, hipStream_t s, bool split = true, const ProdEpilogue* pe = nullptr,
+                          const Epilogue* epi = nullptr);
 
 // Allows a kernel more than 64 KB of dynamic LDS, once per device (`done`: a bit
 // each; devices past 63 are set every time).
@@ -195,9 +201,7 @@ hipError_t launch_lora_grads(const nq_lora& P, const void* x, nq_dtype xd, const
                              const int32_t* ids, int64_t T, const float* dx_base, float* dx, float* da, float* db,
                              void* workspace, hipStream_t s);
 
-// Epilogue of a packed linear and its gradients (act.hip; epilogue.h has the element).
-struct Epilogue;
-hipError_t launch_epilogue(const float* v, int64_t T, int64_t d, const Epilogue& E, hipStream_t s);
+// The epilogue's gradients (act.hip).
 size_t act_grads_workspace(int64_t T, int64_t d);
 hipError_t launch_act_grads(int act, const void* z, nq_dtype zd, const void* mul, nq_dtype md, const void* dy,
                             nq_dtype dyd, int64_t T, int64_t d, void* dz, nq_dtype dzd, void* dmul, nq_dtype dmd,

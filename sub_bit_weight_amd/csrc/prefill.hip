@@ -27,6 +27,7 @@
 //   the prep kernel writes A in that interleaved order.
 // A GEMM with too few output tiles to fill the chip splits its reduction;
 // the partial sums are added in fixed order by the next kernel.
+#include "epilogue.h"
 #include "nq_internal.h"
 
 namespace nq {
@@ -460,17 +461,19 @@ struct Pipe {
 // order, row stride kpad_next, zero in columns [N, kpad_next).  en comes from
 // the prep kernel's bound, so no value reaches 2^14 and fp16 keeps 2^-11
 // relative accuracy for every value above 2^-14 (2^-28 of the bound).
-template <int NT, int MB, bool PROD, bool ROT, bool FUSE>
+// EPI: the outputs go through the epilogue E instead of to out (no split).
+template <int NT, int MB, bool PROD, bool ROT, bool FUSE, bool EPI>
 __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
     const _Float16* __restrict__ A, const int* __restrict__ erow, const float* __restrict__ crow,
     const uint32_t* __restrict__ bits, int64_t ldb,
     int64_t M, int64_t N, int64_t K, int64_t Kpad, int tiles_m, int tiles_n, int nsplit, int kts,
     uint32_t sign_mask, uint32_t one, const float* __restrict__ colscale, float* __restrict__ out,
     const void* __restrict__ pm, int pm_bf16, float* __restrict__ psum, int64_t ldp,
-    _Float16* __restrict__ out16, const int* __restrict__ en, int64_t kpad_next) {
+    _Float16* __restrict__ out16, const int* __restrict__ en, int64_t kpad_next, const Epilogue E) {
   using P = Pipe<NT, MB>;
   static_assert(!ROT || NT == 1, "the rotated encoding takes one fp16 term");
   static_assert(!(FUSE && PROD), "a fused stage-1 output has no column products");
+  static_assert(!(EPI && (FUSE || PROD)), "an epilogue is that of a linear's own outputs");
   extern __shared__ __attribute__((aligned(16))) char lds[];  // [S][A tiles | sign words]
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -659,6 +662,40 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
       }
     return;
   }
+  if constexpr (EPI) {
+    // the wave's outputs go through LDS, 32 rows at a time, so that the epilogue's operands and results
+    // are 16-byte pieces of rows (rows of kEpiLd floats: the two lane halves' rows fall on other banks)
+    constexpr int kEpiLd = 68;
+    static_assert(kWaves * 32 * kEpiLd * 4 <= P::LDS, "the epilogue's rows fit the pipeline's stages");
+    float* rows = reinterpret_cast<float*>(lds) + wave * 32 * kEpiLd;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      __syncthreads();  // the stages, or the rows before, have been read
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        const int64_t n = n0 + wn * 64 + nb * 32 + l32;
+        const float sc = n < N ? colscale[n] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = 8 * (i / 4) + 4 * h + i % 4;
+          const int64_t m = imin(m0 + wm * 32 * MB + mb * 32 + r, M - 1);
+          rows[r * kEpiLd + nb * 32 + l32] = sc * ldexpf(ROT ? acc[mb][nb][i] - cp[m] : acc[mb][nb][i], -ep[m]);
+        }
+      }
+      __syncthreads();
+      const int64_t o = n0 + wn * 64 + 8 * (lane % 8);
+      const int left = (int)imin(N - o, 8);
+#pragma unroll 1
+      for (int r = lane / 8; r < 32; r += 8) {
+        const int64_t m = m0 + wm * 32 * MB + mb * 32 + r;
+        if (m >= M || left <= 0) break;
+        Elements<8> v;
+        v.load(rows + r * kEpiLd + 8 * (lane % 8), false, 0);
+        epilogue_store8(E, m * N + o, o, left, v);
+      }
+    }
+    return;
+  }
   float* dst = (!PROD || out) ? out + (int64_t)split * M * N : nullptr;
   float colsum[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -731,6 +768,19 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
     float acc = part[i];
     for (int sp = 1; sp < nsplit; ++sp) acc += part[(int64_t)sp * MN + i];
     y[i] = colscale ? colscale[i % N] * acc : acc;
+  }
+}
+
+// The same sums through the epilogue E.
+__global__ __launch_bounds__(256) void split_sum_epilogue_kernel(const float* __restrict__ part, int nsplit, int64_t MN,
+                                                                 int64_t N, const float* __restrict__ colscale,
+                                                                 const Epilogue E) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < MN; i += (int64_t)gridDim.x * 256) {
+    float acc = part[i];
+    for (int sp = 1; sp < nsplit; ++sp) acc += part[(int64_t)sp * MN + i];
+    const int64_t n = i % N;
+    const float v[1] = {colscale[n] * acc};
+    epilogue_store<1>(E, E.bias ? E.bias[n] : 0.0f, v, [&](int) { return i; });
   }
 }
 
@@ -829,25 +879,21 @@ struct FuseOut {
   int64_t kpad;
 };
 
-template <int NT, int MB, bool PROD, bool ROT, bool FUSE>
+template <int NT, int MB, bool PROD, bool ROT, bool FUSE, bool EPI>
 hipError_t launch_gemm_t(const _Float16* A, const int* e, const float* c, const uint32_t* bits, int64_t ldb, int64_t M,
                          int64_t N, int64_t K, int64_t Kpad, Split sp, const float* colscale, float* out,
-                         const ProdEpilogue* pe, const FuseOut* fo, hipStream_t s) {
+                         const ProdEpilogue* pe, const FuseOut* fo, const Epilogue* epi, hipStream_t s) {
   using P = Pipe<NT, MB>;
-  const auto kernel = gemm_kernel<NT, MB, PROD, ROT, FUSE>;
-  static bool configured = false;
-  if (!configured) {
-    const hipError_t err =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, P::LDS);
-    if (err != hipSuccess) return err;
-    configured = true;
-  }
+  const auto kernel = gemm_kernel<NT, MB, PROD, ROT, FUSE, EPI>;
+  static std::atomic<uint64_t> done;
+  const hipError_t err = allow_lds(reinterpret_cast<const void*>(kernel), P::LDS, done);
+  if (err != hipSuccess) return err;
   const int tiles_m = (int)cdiv(M, P::BM), tiles_n = (int)cdiv(N, kBN);
   const unsigned grid = (unsigned)(8 * ((tiles_m * tiles_n * sp.n + 7) / 8));
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), P::LDS, s, A, e, c, bits, ldb, M, N, K, Kpad, tiles_m,
                      tiles_n, sp.n, sp.kts, kSignMask, kOnePair, colscale, out, pe ? pe->pm : nullptr,
                      pe ? (int)pe->pm_bf16 : 0, pe ? pe->psum : nullptr, pe ? pe->ldp : (int64_t)0,
-                     fo ? fo->out16 : nullptr, fo ? fo->en : nullptr, fo ? fo->kpad : (int64_t)0);
+                     fo ? fo->out16 : nullptr, fo ? fo->en : nullptr, fo ? fo->kpad : (int64_t)0, epi ? *epi : Epilogue{});
   return hipGetLastError();
 }
 
@@ -855,14 +901,19 @@ hipError_t launch_gemm_t(const _Float16* A, const int* e, const float* c, const 
 // encoding (A from a prep kernel) or pair order (A from a fused stage 1).
 hipError_t launch_gemm(int nt, bool rot, const _Float16* A, const int* e, const float* c, const uint32_t* bits,
                        int64_t ldb, int64_t M, int64_t N, int64_t K, int64_t Kpad, Split sp, const float* colscale,
-                       float* out, hipStream_t s, const ProdEpilogue* pe = nullptr, const FuseOut* fo = nullptr) {
+                       float* out, hipStream_t s, const ProdEpilogue* pe = nullptr, const FuseOut* fo = nullptr,
+                       const Epilogue* epi = nullptr) {
   constexpr int MB = kTileMB;
-#define NQ_GEMM(NT, PROD, ROT, FUSE) \
-  launch_gemm_t<NT, MB, PROD, ROT, FUSE>(A, e, c, bits, ldb, M, N, K, Kpad, sp, colscale, out, pe, fo, s)
-  if (fo) return rot ? NQ_GEMM(1, false, true, true) : hipErrorInvalidValue;  // stage 1 of bf16 activations
-  if (nt == 2) return pe ? NQ_GEMM(2, true, false, false) : NQ_GEMM(2, false, false, false);
-  if (rot) return pe ? NQ_GEMM(1, true, true, false) : NQ_GEMM(1, false, true, false);
-  return pe ? NQ_GEMM(1, true, false, false) : NQ_GEMM(1, false, false, false);
+#define NQ_GEMM(NT, PROD, ROT, FUSE, EPI) \
+  launch_gemm_t<NT, MB, PROD, ROT, FUSE, EPI>(A, e, c, bits, ldb, M, N, K, Kpad, sp, colscale, out, pe, fo, epi, s)
+  if (fo) return rot ? NQ_GEMM(1, false, true, true, false) : hipErrorInvalidValue;  // stage 1 of bf16 activations
+  if (epi) {
+    if (nt == 2) return NQ_GEMM(2, false, false, false, true);
+    return rot ? NQ_GEMM(1, false, true, false, true) : NQ_GEMM(1, false, false, false, true);
+  }
+  if (nt == 2) return pe ? NQ_GEMM(2, true, false, false, false) : NQ_GEMM(2, false, false, false, false);
+  if (rot) return pe ? NQ_GEMM(1, true, true, false, false) : NQ_GEMM(1, false, true, false, false);
+  return pe ? NQ_GEMM(1, true, false, false, false) : NQ_GEMM(1, false, false, false, false);
 #undef NQ_GEMM
 }
 
@@ -915,7 +966,7 @@ size_t prefill_workspace_bytes(const nq_lrb& L, int64_t T, bool split) {
 int64_t prefill_row_blocks(int64_t T) { return cdiv(T, kTileRows); }
 
 hipError_t launch_prefill(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, float* y, void* ws,
-                          hipStream_t s, bool split, const ProdEpilogue* pe) {
+                          hipStream_t s, bool split, const ProdEpilogue* pe, const Epilogue* epi) {
   const PrefillLayout d = prefill_layout(L, T, xd, split);
   char* base = static_cast<char*>(ws);
   _Float16* z = reinterpret_cast<_Float16*>(base + d.off_z);
@@ -943,7 +994,7 @@ hipError_t launch_prefill(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T
     if ((e = launch_gemm(1, true, z, e1, c1, L.vt_bits, L.ldv, T, L.r, L.d_in, d.kpad1, d.sp1, nullptr, nullptr, s,
                          nullptr, &fo)) != hipSuccess)
       return e;
-    return launch_gemm(1, false, t16, e2, c2, L.u_bits, L.ldu, T, L.d_out, L.r, d.kpad2, d.sp2, L.s1, y, s, pe);
+    return launch_gemm(1, false, t16, e2, c2, L.u_bits, L.ldu, T, L.d_out, L.r, d.kpad2, d.sp2, L.s1, y, s, pe, nullptr, epi);
   }
   const bool rot = d.nt == 1;
   if ((e = launch_gemm(d.nt, rot, z, e1, c1, L.vt_bits, L.ldv, T, L.r, L.d_in, d.kpad1, d.sp1, nullptr, t, s)) !=
@@ -954,7 +1005,7 @@ hipError_t launch_prefill(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T
       hipSuccess)
     return e;
   if (d.sp2.n == 1)
-    return launch_gemm(d.nt, rot, t16, e2, c2, L.u_bits, L.ldu, T, L.d_out, L.r, d.kpad2, d.sp2, L.s1, y, s, pe);
+    return launch_gemm(d.nt, rot, t16, e2, c2, L.u_bits, L.ldu, T, L.d_out, L.r, d.kpad2, d.sp2, L.s1, y, s, pe, nullptr, epi);
   if ((e = launch_gemm(d.nt, rot, t16, e2, c2, L.u_bits, L.ldu, T, L.d_out, L.r, d.kpad2, d.sp2, nullptr, y2, s)) !=
       hipSuccess)
     return e;
@@ -966,7 +1017,10 @@ hipError_t launch_prefill(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T
   }
   const int64_t MN = T * L.d_out;
   const unsigned grid = (unsigned)imin(cdiv(MN, 256), (int64_t)4096);
-  hipLaunchKernelGGL(split_sum_kernel, dim3(grid), dim3(256), 0, s, y2, d.sp2.n, MN, L.d_out, L.s1, y);
+  if (epi)
+    hipLaunchKernelGGL(split_sum_epilogue_kernel, dim3(grid), dim3(256), 0, s, y2, d.sp2.n, MN, L.d_out, L.s1, *epi);
+  else
+    hipLaunchKernelGGL(split_sum_kernel, dim3(grid), dim3(256), 0, s, y2, d.sp2.n, MN, L.d_out, L.s1, y);
   return hipGetLastError();
 }
 
