@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -44,6 +45,7 @@ EXPORTED = [
 
 # Size of the library's fixed per-GPU workspace array (NQ_NOALLOC_SCRATCH_BYTES in nq.h).
 NOALLOC_SCRATCH_BYTES = 16 << 20
+_SIZES_KEPT = 256  # workspace sizes that a pool, a layer or a call remembers
 
 
 class NqError(RuntimeError):
@@ -314,6 +316,15 @@ class Lrb:
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_struct", None)  # any field change re-validates
+        object.__setattr__(self, "_bytes", {})     # workspace sizes of lrb_linear_act per token count
+
+    def _act_bytes(self, T: int) -> int:
+        size = self._bytes.get(T)
+        if size is None:
+            if len(self._bytes) >= _SIZES_KEPT:  # token counts of a long-lived layer are without end
+                self._bytes.clear()
+            size = self._bytes[T] = int(lib().nq_lrb_act_workspace_bytes(ctypes.byref(self.struct()), T))
+        return size
 
     def struct(self) -> nq_lrb:
         """The C struct, after checking what the C ABI cannot see: dtypes,
@@ -537,9 +548,6 @@ def lrb_scale_grads_batch(layers, adjs, xs, gs, workspace: torch.Tensor | None =
 
 
 # ---------------------------------------------------------------- adapters
-
-_SIZES_KEPT = 256  # workspace sizes that a pool remembers
-
 
 @dataclass
 class Lora:
@@ -789,16 +797,25 @@ def _act_code(act: str) -> int:
     return code
 
 
+_DTYPES = {torch.float32: NQ_F32, torch.bfloat16: NQ_BF16}
+
+
 def _rows(t: torch.Tensor | None, name: str, shape: tuple, device) -> int:
     """The dtype code of an optional operand [T][d] (NQ_F32 where there is none)."""
     if t is None:
         return NQ_F32
-    _dev(t, name)
-    if tuple(t.shape) != shape or t.device != device:
-        raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name} dtype {t.dtype} not supported (float32 or bfloat16)")
-    return NQ_BF16 if t.dtype == torch.bfloat16 else NQ_F32
+    code = _DTYPES.get(t.dtype)
+    if t.shape != shape or t.device != device or code is None or not t.is_contiguous():  # say which
+        _dev(t, name)
+        if code is None:
+            raise ValueError(f"{name} dtype {t.dtype} not supported (float32 or bfloat16)")
+        raise ValueError(f"{name} must be {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+    return code
+
+
+@functools.lru_cache(maxsize=_SIZES_KEPT)
+def _act_grads_bytes(T: int, d: int) -> int:
+    return int(lib().nq_act_grads_workspace_bytes(T, d))
 
 
 def lrb_act_workspace_bytes(layer: Lrb, T: int) -> int:
@@ -837,8 +854,7 @@ def lrb_linear_act(layer: Lrb, x: torch.Tensor, act: str = "none", bias: torch.T
         if y is None:
             y = torch.empty(shape, dtype=out_dtype, device=dev)
         if workspace is None:
-            need = int(lib().nq_lrb_act_workspace_bytes(ctypes.byref(s), T))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(max(layer._act_bytes(T), 1), dtype=torch.uint8, device=dev)
         epi = nq_epilogue(code, _ptr(bias), _ptr(mul), md, _ptr(residual), rd, _ptr(z), zd)
         _check(lib().nq_lrb_linear_act(ctypes.byref(s), _ptr(x), xd, T, ctypes.byref(epi), _ptr(y), yd, _ptr(workspace),
                                        workspace.numel() * workspace.element_size(), _stream(stream, dev.index)))
@@ -854,15 +870,15 @@ def act_grads(act: str, z: torch.Tensor | None, dy: torch.Tensor, mul: torch.Ten
     _dev(dy, "dy")
     if dy.dim() != 2 or dy.numel() == 0:
         raise ValueError(f"dy must be [T][d], got {tuple(dy.shape)}")
-    code, shape, dev = _act_code(act), tuple(dy.shape), dy.device
+    code, shape, dev = _act_code(act), dy.shape, dy.device
     dyd = _rows(dy, "dy", shape, dev)
     zd, md = _rows(z, "z", shape, dev), _rows(mul, "mul", shape, dev)
     if z is None and (act != "none" or mul is not None):
         raise ValueError("z is needed but for act 'none' without mul")
     if dmul is not None and mul is None:
         raise ValueError("dmul without mul")
-    for t, name in ((dz, "dz"), (dmul, "dmul")):
-        _rows(t, name, shape, dev)
+    dzd = dyd if dz is None else _rows(dz, "dz", shape, dev)
+    dmd = md if dmul is None else _rows(dmul, "dmul", shape, dev)
     _workspace_on(workspace, dev)
     with _call_on(dev, stream):
         if dz is None:
@@ -873,12 +889,10 @@ def act_grads(act: str, z: torch.Tensor | None, dy: torch.Tensor, mul: torch.Ten
         size = 0
         if bias:
             if workspace is None:
-                need = int(lib().nq_act_grads_workspace_bytes(*shape))
-                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+                workspace = torch.empty(max(_act_grads_bytes(*shape), 1), dtype=torch.uint8, device=dev)
             size = workspace.numel() * workspace.element_size()
-        _check(lib().nq_act_grads(code, _ptr(z), zd, _ptr(mul), md, _ptr(dy), dyd, shape[0], shape[1], _ptr(dz),
-                                  _rows(dz, "dz", shape, dev), _ptr(dmul), _rows(dmul, "dmul", shape, dev), _ptr(dbias),
-                                  _ptr(workspace), size, _stream(stream, dev.index)))
+        _check(lib().nq_act_grads(code, _ptr(z), zd, _ptr(mul), md, _ptr(dy), dyd, shape[0], shape[1], _ptr(dz), dzd,
+                                  _ptr(dmul), dmd, _ptr(dbias), _ptr(workspace), size, _stream(stream, dev.index)))
     return dz, dmul, dbias
 
 
