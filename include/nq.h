@@ -482,8 +482,9 @@ typedef struct {
  *   y's type (and z to its own).  y may be mul or residual where the types are
  *   equal (in place); z may not be any of them.  silu and gelu of -inf are NaN,
  *   the products -inf * 0 of their formulas.
- *   workspace: at least nq_lrb_act_workspace_bytes(L, T) bytes, 256-byte aligned.
- *   Streams, graphs and determinism: as for nq_lrb_linear.
+ *   workspace: at least nq_lrb_act_workspace_bytes(L, T) bytes, 256-byte aligned
+ *   (0 bytes: none, it may be null: small layers at T <= 8).  Streams, graphs and
+ *   determinism: as for nq_lrb_linear (NQ_DECODE_TINY does not count here).
  * Errors: as for nq_lrb_linear; NQ_ERR_ARG for a null epilogue, an unknown
  * activation or dtype, or a pointer not aligned to its elements.
  */
@@ -502,10 +503,11 @@ nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, in
  *   arithmetic, each result rounded once; relu'(0) = 0; dbias sums the unrounded dz
  *   in fp32 in a fixed order (deterministic).
  *   workspace: at least nq_act_grads_workspace_bytes(T, d) bytes, 256-byte aligned
- *   (null with dbias null); calls that may overlap need one each.
+ *   (0 bytes, or dbias null: none, it may be null); calls that may overlap need one
+ *   each.
  * Errors: NQ_ERR_ARG for null or misaligned pointers, sizes < 1, unknown
  * activations or dtypes; NQ_ERR_UNSUPPORTED for T or d > 2^24; NQ_ERR_WORKSPACE;
- * NQ_ERR_HIP.  The size query returns 0 for invalid arguments.
+ * NQ_ERR_HIP.  The size query also returns 0 for invalid arguments.
  */
 size_t nq_act_grads_workspace_bytes(int64_t T, int64_t d);
 nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* mul, nq_dtype mul_dtype, const void* dy,

@@ -219,6 +219,8 @@ def _on(stream):
 
 
 _NO_CONTEXT = contextlib.nullcontext()
+# without torch.cuda.current_device's check for initialisation: a device tensor is at hand
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 @contextlib.contextmanager
@@ -230,7 +232,7 @@ def _device_and_stream(dev, stream):
 def _call_on(dev: torch.device, stream):
     """Allocation and launch context of a call whose tensors are on `dev`: that
     device current, and `stream` (see _on)."""
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev.index == _current_device():
         return _NO_CONTEXT
     return _device_and_stream(dev, stream)
 
@@ -357,12 +359,14 @@ class Lrb:
         return st
 
 
+_DTYPES = {torch.float32: NQ_F32, torch.bfloat16: NQ_BF16}
+
+
 def _x_dtype(x: torch.Tensor) -> int:
-    if x.dtype == torch.float32:
-        return NQ_F32
-    if x.dtype == torch.bfloat16:
-        return NQ_BF16
-    raise ValueError(f"x dtype {x.dtype} not supported (float32 or bfloat16)")
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise ValueError(f"x dtype {x.dtype} not supported (float32 or bfloat16)")
+    return code
 
 
 def lrb_workspace_bytes(layer: Lrb, T: int) -> int:
@@ -797,9 +801,6 @@ def _act_code(act: str) -> int:
     return code
 
 
-_DTYPES = {torch.float32: NQ_F32, torch.bfloat16: NQ_BF16}
-
-
 def _rows(t: torch.Tensor | None, name: str, shape: tuple, device) -> int:
     """The dtype code of an optional operand [T][d] (NQ_F32 where there is none)."""
     if t is None:
@@ -836,28 +837,41 @@ def lrb_linear_act(layer: Lrb, x: torch.Tensor, act: str = "none", bias: torch.T
     s = layer.struct()
     if layer.s1.device != dev:
         raise ValueError(f"the layer and x must share a device: {layer.s1.device}, {dev}")
-    T, shape = x.shape[0], (x.shape[0], layer.d_out)
+    T = x.shape[0]
+    shape = (T, layer.d_out)
+    epi = nq_epilogue(code)
     if bias is not None:
         _f32_rows(bias, "bias", (layer.d_out,), dev)
-    md, rd, zd = _rows(mul, "mul", shape, dev), _rows(residual, "residual", shape, dev), _rows(z, "z", shape, dev)
+        epi.bias = bias.data_ptr()
+    if mul is not None:
+        epi.mul_dtype, epi.mul = _rows(mul, "mul", shape, dev), mul.data_ptr()
+    if residual is not None:
+        epi.residual_dtype, epi.residual = _rows(residual, "residual", shape, dev), residual.data_ptr()
+    if z is not None:
+        epi.z_dtype, epi.z = _rows(z, "z", shape, dev), z.data_ptr()
     if y is not None:
         yd = _rows(y, "y", shape, dev)
         if out_dtype is not None and y.dtype != out_dtype:
             raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
     else:
         out_dtype = x.dtype if out_dtype is None else out_dtype
-        if out_dtype not in (torch.float32, torch.bfloat16):
+        yd = _DTYPES.get(out_dtype)
+        if yd is None:
             raise ValueError(f"output dtype {out_dtype} not supported (float32 or bfloat16)")
-        yd = NQ_BF16 if out_dtype == torch.bfloat16 else NQ_F32
-    _workspace_on(workspace, dev)
+    if workspace is not None:
+        _workspace_on(workspace, dev)
     with _call_on(dev, stream):
         if y is None:
             y = torch.empty(shape, dtype=out_dtype, device=dev)
+        size = 0
         if workspace is None:
-            workspace = torch.empty(max(layer._act_bytes(T), 1), dtype=torch.uint8, device=dev)
-        epi = nq_epilogue(code, _ptr(bias), _ptr(mul), md, _ptr(residual), rd, _ptr(z), zd)
-        _check(lib().nq_lrb_linear_act(ctypes.byref(s), _ptr(x), xd, T, ctypes.byref(epi), _ptr(y), yd, _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), _stream(stream, dev.index)))
+            size = layer._act_bytes(T)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        else:
+            size = workspace.numel() * workspace.element_size()
+        _check(lib().nq_lrb_linear_act(ctypes.byref(s), x.data_ptr(), xd, T, ctypes.byref(epi), y.data_ptr(), yd,
+                                       _ptr(workspace), size, _stream(stream, dev.index)))
     return y
 
 
@@ -887,9 +901,11 @@ def act_grads(act: str, z: torch.Tensor | None, dy: torch.Tensor, mul: torch.Ten
             dmul = torch.empty_like(mul)
         dbias = torch.empty(shape[1], dtype=torch.float32, device=dev) if bias else None
         size = 0
-        if bias:
-            if workspace is None:
-                workspace = torch.empty(max(_act_grads_bytes(*shape), 1), dtype=torch.uint8, device=dev)
+        if bias and workspace is None:
+            size = _act_grads_bytes(*shape)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        elif workspace is not None:
             size = workspace.numel() * workspace.element_size()
         _check(lib().nq_act_grads(code, _ptr(z), zd, _ptr(mul), md, _ptr(dy), dyd, shape[0], shape[1], _ptr(dz), dzd,
                                   _ptr(dmul), dmd, _ptr(dbias), _ptr(workspace), size, _stream(stream, dev.index)))
@@ -933,17 +949,18 @@ class Teacher:
 
 def _logits(t: torch.Tensor, name: str) -> int:
     """Checks rows of logits [T][V] (a view whose rows are contiguous will do); the row stride."""
-    if t.dim() != 2 or t.numel() == 0:
-        raise ValueError(f"{name} must be [T][V], got {tuple(t.shape)}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] == 0 or shape[1] == 0:
+        raise ValueError(f"{name} must be [T][V], got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] == 1:  # one row may carry any stride
-        return max(t.stride(0), t.shape[1])
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} must have rows that do not overlap, got strides {t.stride()}")
-    return t.stride(0)
+    if stride[0] >= shape[1]:
+        return stride[0]
+    if shape[0] == 1:  # one row may carry any stride
+        return shape[1]
+    raise ValueError(f"{name} must have rows that do not overlap, got strides {stride}")
 
 
 def logits_top(logits: torch.Tensor, k: int, temperature: float = 1.0, stream=None) -> Teacher:

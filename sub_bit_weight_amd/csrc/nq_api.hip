@@ -938,15 +938,16 @@ nq_status check_act(const char* who, nq_act act) {
   return NQ_OK;
 }
 
-// The regimes of launch_linear (but for the comparison kernels of NQ_DECODE_VARIANT, which have no
-// epilogue).
+// The regimes of launch_linear (whatever NQ_DECODE_VARIANT and NQ_DECODE_TINY say: the comparison
+// kernels have no epilogue, and a size must hold until its call).
 size_t linear_act_workspace(const nq_lrb& L, int64_t T) {
-  return T > kDecodeMaxT ? prefill_workspace_bytes(L, T) : dec_workspace_bytes(L, T);
+  if (T > kDecodeMaxT) return prefill_workspace_bytes(L, T);
+  return tiny_fits(L, T) ? 0 : dec_workspace_bytes(L, T);
 }
 hipError_t launch_linear_act(const nq_lrb& L, const void* x, nq_dtype xd, int64_t T, const Epilogue& E, void* ws,
                              hipStream_t s) {
   if (T > kDecodeMaxT) return launch_prefill(L, x, xd, T, nullptr, ws, s, true, nullptr, &E);
-  if (tiny_enabled() && tiny_fits(L, T)) return launch_tiny_linear(L, x, xd, T, nullptr, s, &E);
+  if (tiny_fits(L, T)) return launch_tiny_linear(L, x, xd, T, nullptr, s, &E);
   return launch_dec_linear(L, x, xd, T, nullptr, ws, s, &E);
 }
 
@@ -977,7 +978,8 @@ nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, in
     return set_error("%s: y in place of an operand of another dtype", who), NQ_ERR_ARG;
   if (E->z && (E->z == y || E->z == E->mul || E->z == E->residual))
     return set_error("%s: z in place of y or an operand", who), NQ_ERR_ARG;
-  if ((st = check_workspace(who, workspace, workspace_bytes, linear_act_workspace(*L, T))) != NQ_OK) return st;
+  const size_t need = linear_act_workspace(*L, T);
+  if (need && (st = check_workspace(who, workspace, workspace_bytes, need)) != NQ_OK) return st;
   const Epilogue epi{E->bias,
                      E->mul,
                      E->residual,
@@ -994,7 +996,7 @@ nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, in
 
 size_t nq_act_grads_workspace_bytes(int64_t T, int64_t d) {
   const int64_t most = int64_t(1) << 24;
-  return T < 1 || d < 1 || T > most || d > most ? 0 : std::max<size_t>(act_grads_workspace(T, d), kAlign);
+  return T < 1 || d < 1 || T > most || d > most ? 0 : act_grads_workspace(T, d);
 }
 
 nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* mul, nq_dtype mul_dtype, const void* dy,
@@ -1028,8 +1030,8 @@ nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* 
   for (const auto& p : pairs)
     if (p.out && p.out == p.in && p.od != p.id)
       return set_error("%s: a result in place of an operand of another dtype", who), NQ_ERR_ARG;
-  if (dbias && (st = check_workspace(who, workspace, workspace_bytes, nq_act_grads_workspace_bytes(T, d))) != NQ_OK)
-    return st;
+  const size_t need = dbias ? act_grads_workspace(T, d) : 0;
+  if (need && (st = check_workspace(who, workspace, workspace_bytes, need)) != NQ_OK) return st;
   return hip_status(launch_act_grads(act, z, z_dtype, mul, mul_dtype, dy, dy_dtype, T, d, dz, dz_dtype, dmul, dmul_dtype,
                                      dbias, workspace, (hipStream_t)stream),
                     "nq_act_grads launch");

@@ -52,13 +52,13 @@ def _layer(**kw):
     return nq.nq_lrb(**d)
 
 
-def _linear(L=None, x=DUMMY, xd=nq.NQ_BF16, T=3, y=2 * DUMMY, yd=nq.NQ_BF16, ws=DUMMY, wsb=1 << 40, null=False, **kw):
+def _linear(L=None, x=DUMMY, xd=nq.NQ_BF16, T=20, y=2 * DUMMY, yd=nq.NQ_BF16, ws=DUMMY, wsb=1 << 40, null=False, **kw):
     e = nq.nq_epilogue(**{**dict(act=0), **kw})
     L = L or _layer()
     return nq.lib().nq_lrb_linear_act(ctypes.byref(L), x, xd, T, None if null else ctypes.byref(e), y, yd, ws, wsb, None)
 
 
-def _grads(act=4, z=DUMMY, zd=1, mul=3 * DUMMY, md=1, dy=5 * DUMMY, dyd=1, T=3, d=64, dz=7 * DUMMY, dzd=1, dmul=9 * DUMMY,
+def _grads(act=4, z=DUMMY, zd=1, mul=3 * DUMMY, md=1, dy=5 * DUMMY, dyd=1, T=300, d=64, dz=7 * DUMMY, dzd=1, dmul=9 * DUMMY,
            dmd=1, db=DUMMY, ws=DUMMY, wsb=1 << 30):
     return nq.lib().nq_act_grads(act, z, zd, mul, md, dy, dyd, T, d, dz, dzd, dmul, dmd, db, ws, wsb, None)
 
@@ -80,8 +80,10 @@ def test_linear_rejects_workspace_and_sizes():
     assert _linear(T=(1 << 24) + 1) == nq.NQ_ERR_UNSUPPORTED
     q = nq.lib().nq_lrb_act_workspace_bytes
     assert q(ctypes.byref(_layer(r=0)), 3) == 0 and q(ctypes.byref(_layer()), 0) == 0
+    assert q(ctypes.byref(_layer()), 8) == 0  # one workgroup needs none
     for T in (1, 8, 9, 1000):
-        assert q(ctypes.byref(_layer()), T) >= nq.lib().nq_lrb_workspace_bytes(ctypes.byref(_layer()), T)
+        L = _layer(d_out=2000, ldu=2000)
+        assert q(ctypes.byref(L), T) >= nq.lib().nq_lrb_workspace_bytes(ctypes.byref(L), T) > 0
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -96,7 +98,7 @@ def test_grads_reject(kw, status):
 
 def test_grads_workspace_query():
     q = nq.lib().nq_act_grads_workspace_bytes
-    assert q(0, 4) == 0 and q(4, 0) == 0 and q(1 << 25, 1) == 0 and q(1, 1) >= 1 and q(4096, 1000) >= 1
+    assert q(0, 4) == 0 and q(4, 0) == 0 and q(1 << 25, 1) == 0 and q(256, 9) == 0 and q(4096, 1000) >= 4000
 
 
 # ---------------------------------------------------------------- GPU
@@ -294,9 +296,12 @@ def test_binding_refuses_wrong_tensors():
                dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
         with pytest.raises(ValueError):
             nq.lrb_linear_act(**{**dict(layer=layer, x=x), **kw})
-    for kw in (dict(y=row, z=row), dict(mul=row.bfloat16(), y=row.bfloat16(), workspace=torch.empty(16, dtype=torch.uint8, device=DEV))):
-        with pytest.raises(nq.NqError):
-            nq.lrb_linear_act(layer, x, **kw)
+    with pytest.raises(nq.NqError):
+        nq.lrb_linear_act(layer, x, y=row, z=row)
+    with pytest.raises(nq.NqError):
+        nq.lrb_linear_act(layer, torch.zeros(20, 130, device=DEV), workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(nq.NqError):
+        nq.act_grads("none", None, torch.zeros(300, 7, device=DEV), workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     for kw in (dict(z=None), dict(z=row[:2]), dict(dy=row.half()), dict(mul=row[:, :9]), dict(dmul=row), dict(dz=row[:1]),
                dict(act="x"), dict(dy=row[0]), dict(dz=row.cpu())):
         with pytest.raises(ValueError):
