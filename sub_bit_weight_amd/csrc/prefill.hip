@@ -45,22 +45,28 @@ constexpr uint32_t kSignMask = 0x80008000u, kOnePair = 0x3C003C00u;  // fp16 pai
 
 enum ASrc { kAF32Scaled = 0, kABF16Scaled = 1, kAF32 = 2 };
 
+// 16 bytes at any alignment of their elements (one load each on this chip).
+typedef u32x4 bf16x8_at __attribute__((aligned(2)));
+typedef float f32x4_at __attribute__((ext_vector_type(4), aligned(4)));
+
 // Activations of one 32-element block of row m, already multiplied by the
 // column scale (zero past K).  Stage 2 may hold `nsplit` partial sums of t,
-// added here in split order.
+// added here in split order.  Whole blocks are read as 16-byte vectors at any
+// alignment of the rows (element by element, rows of lengths that are no
+// multiple of 16 bytes took several times as long: a call of 92 tokens through
+// 1813 x 1716, rank 259, 60 us).
 template <int SRC>
 __device__ inline void load_block(const void* __restrict__ a, const float* __restrict__ cs, int64_t M, int64_t K,
-                                  int nsplit, bool vec, int64_t m, int64_t blk, float (&v)[32]) {
+                                  int nsplit, int64_t m, int64_t blk, float (&v)[32]) {
   const int64_t k0 = blk * 32;
-  const bool full = vec && k0 + 32 <= K;
+  const bool full = k0 + 32 <= K;
   if (SRC == kABF16Scaled && full) {
-    const uint4* xp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a) + m * K + k0);
-    const float4* sp = reinterpret_cast<const float4*>(cs + k0);
+    const bf16x8_at* xp = reinterpret_cast<const bf16x8_at*>(static_cast<const uint16_t*>(a) + m * K + k0);
+    const f32x4_at* sp = reinterpret_cast<const f32x4_at*>(cs + k0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 w = xp[i];
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      const float4 s0 = sp[2 * i], s1 = sp[2 * i + 1];
+      const u32x4 u = xp[i];
+      const f32x4_at s0 = sp[2 * i], s1 = sp[2 * i + 1];
       const float sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -71,10 +77,10 @@ __device__ inline void load_block(const void* __restrict__ a, const float* __res
     return;
   }
   if (SRC != kABF16Scaled && full) {
-    const float4* base = reinterpret_cast<const float4*>(static_cast<const float*>(a) + m * K + k0);
+    const float* base = static_cast<const float*>(a) + m * K + k0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 p = base[i];
+      const f32x4_at p = reinterpret_cast<const f32x4_at*>(base)[i];
       v[4 * i] = p.x;
       v[4 * i + 1] = p.y;
       v[4 * i + 2] = p.z;
@@ -82,10 +88,10 @@ __device__ inline void load_block(const void* __restrict__ a, const float* __res
     }
 #pragma unroll 1
     for (int sp = 1; sp < nsplit; ++sp) {  // partial sums of a split reduction, in order
-      const float4* ps = base + (int64_t)sp * M * K / 4;
+      const f32x4_at* ps = reinterpret_cast<const f32x4_at*>(base + (int64_t)sp * M * K);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float4 p = ps[i];
+        const f32x4_at p = ps[i];
         v[4 * i] += p.x;
         v[4 * i + 1] += p.y;
         v[4 * i + 2] += p.z;
@@ -93,10 +99,10 @@ __device__ inline void load_block(const void* __restrict__ a, const float* __res
       }
     }
     if (SRC == kAF32Scaled) {
-      const float4* sp4 = reinterpret_cast<const float4*>(cs + k0);
+      const f32x4_at* sp4 = reinterpret_cast<const f32x4_at*>(cs + k0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float4 c = sp4[i];
+        const f32x4_at c = sp4[i];
         v[4 * i] *= c.x;
         v[4 * i + 1] *= c.y;
         v[4 * i + 2] *= c.z;
@@ -106,7 +112,7 @@ __device__ inline void load_block(const void* __restrict__ a, const float* __res
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {  // ragged tail or unaligned data: element by element
+  for (int i = 0; i < 32; ++i) {  // the row's ragged end, element by element
     const int64_t k = k0 + i;
     float x = 0.0f;
     if (k < K) {
@@ -156,8 +162,7 @@ __device__ constexpr int rot_element(int j) {
 //   that takes this operand (one row of t), so 2^e_next puts all of that row
 //   below 2^14, the exponent of the next stage's operand written by the GEMM
 //   itself (see gemm_kernel, FUSE).
-// A thread handles whole 32-element blocks: 16-byte loads when `vec` (rows and
-// scales 16-byte aligned), 16 output dwords.  Pieces of up to 256 blocks stay
+// A thread handles whole 32-element blocks: 16-byte loads, 16 output dwords.  Pieces of up to 256 blocks stay
 // in registers between the two passes; longer ones are read twice.
 // Convert one 32-element block (values v, already in registers) to its fp16
 // terms in the block's slot order and store them; returns the block's part of
@@ -219,8 +224,8 @@ __device__ inline float wg_reduce(float x, float* red) {
 
 template <int SRC, bool ROT, int NTH, int BPT>
 __global__ __launch_bounds__(NTH) void prep_kernel(const void* __restrict__ a, const float* __restrict__ cs,
-                                                   int64_t M, int64_t K, int64_t Kpad, int nt, int nsum, int vec,
-                                                   int bps, _Float16* __restrict__ out, int* __restrict__ e_out,
+                                                   int64_t M, int64_t K, int64_t Kpad, int nt, int nsum, int bps,
+                                                   _Float16* __restrict__ out, int* __restrict__ e_out,
                                                    float* __restrict__ c_out, int* __restrict__ e_next) {
   constexpr int NW = NTH / 64;
   __shared__ float red[NW];
@@ -238,7 +243,7 @@ __global__ __launch_bounds__(NTH) void prep_kernel(const void* __restrict__ a, c
 #pragma unroll
     for (int i = 0; i < BPT; ++i) {
       const int64_t blk = base + (int64_t)i * NTH;
-      if (blk < b1) load_block<SRC>(a, cs, M, K, nsum, vec != 0, m, blk, v[i]);
+      if (blk < b1) load_block<SRC>(a, cs, M, K, nsum, m, blk, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < BPT; ++i)
@@ -260,7 +265,7 @@ __global__ __launch_bounds__(NTH) void prep_kernel(const void* __restrict__ a, c
     for (int i = 0; i < BPT; ++i) {
       const int64_t blk = base + (int64_t)i * NTH;
       if (blk < b1) {
-        if (!in_regs) load_block<SRC>(a, cs, M, K, nsum, vec != 0, m, blk, v[i]);
+        if (!in_regs) load_block<SRC>(a, cs, M, K, nsum, m, blk, v[i]);
         csum += convert_block<ROT>(v[i], e, M, Kpad, nt, m, blk, out, l1);
       }
     }
@@ -531,6 +536,21 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
                                      4, 0, 0);
   };
 
+  // The tile's row exponents (and correction sums, and the next stage's exponents): thread r < BM reads
+  // row r's here and hands them over through LDS after the reduction.  (Read by every lane for each of
+  // its rows in the epilogue, they cost a memory latency per row: 128 rows of 256 columns at a
+  // reduction of 256 took 14-21 us, nearly all of it there.)
+  __shared__ int s_exp[P::BM], s_next[FUSE ? P::BM : 1];
+  __shared__ float s_cor[ROT ? P::BM : 1];
+  int row_exp = 0, row_next = 0;
+  float row_cor = 0.0f;
+  if (threadIdx.x < P::BM) {
+    const int64_t m = imin(m0 + threadIdx.x, M - 1);
+    row_exp = erow[(int64_t)split * M + m];
+    if (ROT) row_cor = crow[(int64_t)split * M + m];
+    if (FUSE) row_next = en[m];
+  }
+
   f32x16 acc[MB][2];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
@@ -636,8 +656,12 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
   // With psum (only without a split), each column's products pm * v over the
   // tile's rows are summed: per lane over its 16 rows of each 32-row block in
   // order, then the two lane halves, then the two wave rows through LDS.
-  const int* ep = erow + (int64_t)split * M;
-  const float* cp = crow + (int64_t)split * M;
+  if (threadIdx.x < P::BM) {
+    s_exp[threadIdx.x] = row_exp;
+    if (ROT) s_cor[threadIdx.x] = row_cor;
+    if (FUSE) s_next[threadIdx.x] = row_next;
+  }
+  __syncthreads();
   if constexpr (FUSE) {
     // column n is element l32 of its 32-element block, pair-order slot
     // 2*(l32 % 16) + l32/16; lanes l32 = 0..31 of a row write one 64-byte run
@@ -655,8 +679,8 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
           for (int c = 0; c < 4; ++c) {
             const int64_t m = m0 + wm * 32 * MB + mb * 32 + 8 * a + 4 * h + c;
             if (m < M) {
-              const float v = ROT ? acc[mb][nb][4 * a + c] - cp[m] : acc[mb][nb][4 * a + c];
-              out16[m * kpad_next + col] = n < N ? (_Float16)ldexpf(v, en[m] - ep[m]) : (_Float16)0.0f;
+              const float v = ROT ? acc[mb][nb][4 * a + c] - s_cor[m - m0] : acc[mb][nb][4 * a + c];
+              out16[m * kpad_next + col] = n < N ? (_Float16)ldexpf(v, s_next[m - m0] - s_exp[m - m0]) : (_Float16)0.0f;
             }
           }
       }
@@ -679,7 +703,7 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
         for (int i = 0; i < 16; ++i) {
           const int r = 8 * (i / 4) + 4 * h + i % 4;
           const int64_t m = imin(m0 + wm * 32 * MB + mb * 32 + r, M - 1);
-          rows[r * kEpiLd + nb * 32 + l32] = sc * ldexpf(ROT ? acc[mb][nb][i] - cp[m] : acc[mb][nb][i], -ep[m]);
+          rows[r * kEpiLd + nb * 32 + l32] = sc * ldexpf(ROT ? acc[mb][nb][i] - s_cor[m - m0] : acc[mb][nb][i], -s_exp[m - m0]);
         }
       }
       __syncthreads();
@@ -710,7 +734,7 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
         for (int c = 0; c < 4; ++c) {
           const int64_t m = m0 + wm * 32 * MB + mb * 32 + 8 * a + 4 * h + c;
           if (m < M && n < N) {
-            const float v = ldexpf(ROT ? acc[mb][nb][4 * a + c] - cp[m] : acc[mb][nb][4 * a + c], -ep[m]);
+            const float v = ldexpf(ROT ? acc[mb][nb][4 * a + c] - s_cor[m - m0] : acc[mb][nb][4 * a + c], -s_exp[m - m0]);
             if (!PROD || dst) dst[m * N + n] = sc * v;
             if constexpr (PROD) colsum[nb] = fmaf(load_prod(pm, pm_bf16, m * N + n), v, colsum[nb]);
           }
@@ -814,7 +838,7 @@ hipError_t launch_prep(const void* a, const float* cs, int64_t M, int64_t K, int
   // 1 to 8 waves per (row, piece), the fewest that hold the piece in registers
   const int64_t pblk = imin((int64_t)bps, Kpad / 32);
 #define NQ_PREP(ROT, NTH, BPT)                                                                                    \
-  hipLaunchKernelGGL((prep_kernel<SRC, ROT, NTH, BPT>), grid, dim3(NTH), 0, s, a, cs, M, K, Kpad, nt, nsum, vec, bps, \
+  hipLaunchKernelGGL((prep_kernel<SRC, ROT, NTH, BPT>), grid, dim3(NTH), 0, s, a, cs, M, K, Kpad, nt, nsum, bps, \
                      out, e, c, e_next)
   // bf16 sources: two blocks per thread in registers; fp32 sources (whose
   // loads need more registers): one
