@@ -536,12 +536,12 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
                                      4, 0, 0);
   };
 
-  // The tile's row exponents (and correction sums, and the next stage's exponents): thread r < BM reads
-  // row r's here and hands them over through LDS after the reduction.  (Read by every lane for each of
+  // The tile's row exponents (and correction sums, and the next stage's exponents) into LDS: thread r < BM
+  // takes row r's.  (Read by every lane for each of
   // its rows in the epilogue, they cost a memory latency per row: 128 rows of 256 columns at a
   // reduction of 256 took 14-21 us, nearly all of it there.)
-  __shared__ int s_exp[P::BM], s_next[FUSE ? P::BM : 1];
-  __shared__ float s_cor[ROT ? P::BM : 1];
+  __shared__ __attribute__((aligned(16))) int s_exp[P::BM], s_next[FUSE ? P::BM : 4];
+  __shared__ __attribute__((aligned(16))) float s_cor[ROT ? P::BM : 4];
   int row_exp = 0, row_next = 0;
   float row_cor = 0.0f;
   if (threadIdx.x < P::BM) {
@@ -562,6 +562,11 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
 #pragma unroll
   for (int kt = 0; kt < P::S - 1; ++kt)
     if (kt < nk) issue(kt, kt);
+  if (threadIdx.x < P::BM) {
+    s_exp[threadIdx.x] = row_exp;
+    if (ROT) s_cor[threadIdx.x] = row_cor;
+    if (FUSE) s_next[threadIdx.x] = row_next;
+  }
 
   asm volatile("" : "+v"(one));  // keep `one` in a VGPR: one SGPR operand per VOP3 (sign_mask)
 
@@ -656,87 +661,113 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
   // With psum (only without a split), each column's products pm * v over the
   // tile's rows are summed: per lane over its 16 rows of each 32-row block in
   // order, then the two lane halves, then the two wave rows through LDS.
-  if (threadIdx.x < P::BM) {
-    s_exp[threadIdx.x] = row_exp;
-    if (ROT) s_cor[threadIdx.x] = row_cor;
-    if (FUSE) s_next[threadIdx.x] = row_next;
-  }
-  __syncthreads();
+  __syncthreads();  // the stages have been read, the rows' exponents are there
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int r = wm * 32 * MB + mb * 32 + 8 * a + 4 * h;  // this lane's rows r .. r + 3 of the tile
+      const int4 e = *reinterpret_cast<const int4*>(s_exp + r);
+      int sh[4] = {-e.x, -e.y, -e.z, -e.w};
+      if constexpr (FUSE) {
+        const int4 n4 = *reinterpret_cast<const int4*>(s_next + r);
+        sh[0] += n4.x, sh[1] += n4.y, sh[2] += n4.z, sh[3] += n4.w;
+      }
+      float cor[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (ROT) {
+        const float4 c4 = *reinterpret_cast<const float4*>(s_cor + r);
+        cor[0] = c4.x, cor[1] = c4.y, cor[2] = c4.z, cor[3] = c4.w;
+      }
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float v = acc[mb][nb][4 * a + c];
+          acc[mb][nb][4 * a + c] = ldexpf(ROT ? v - cor[c] : v, sh[c]);
+        }
+    }
+  // The wave's tile goes through LDS (its own part of the stages), so that memory sees 16-byte pieces of
+  // rows: a lane's own results are one value of each row.
+  const int64_t wcol = n0 + wn * 64, wrow = m0 + wm * 32 * MB;  // the wave's first column and row
   if constexpr (FUSE) {
-    // column n is element l32 of its 32-element block, pair-order slot
-    // 2*(l32 % 16) + l32/16; lanes l32 = 0..31 of a row write one 64-byte run
+    // column n is element l32 of its 32-element block, pair-order slot 2*(l32 % 16) + l32/16; kpad_next is
+    // a multiple of 64, so a wave's columns are all inside or all past it
+    constexpr int kLd = 72;
+    static_assert(kWaves * 32 * MB * kLd * 2 <= P::LDS, "the wave's rows fit the pipeline's stages");
+    _Float16* rows = reinterpret_cast<_Float16*>(lds) + wave * 32 * MB * kLd;
     const int slot = 2 * (l32 % 16) + l32 / 16;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        const int64_t n = n0 + wn * 64 + nb * 32 + l32;
-        if (n >= kpad_next) continue;
-        const int64_t col = n - l32 + slot;
+      for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int i = 0; i < 16; ++i)
+          rows[(mb * 32 + 8 * (i / 4) + 4 * h + i % 4) * kLd + nb * 32 + slot] =
+              wcol + nb * 32 + l32 < N ? (_Float16)acc[mb][nb][i] : (_Float16)0.0f;
+    __syncthreads();
+    if (wcol >= kpad_next) return;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int64_t m = m0 + wm * 32 * MB + mb * 32 + 8 * a + 4 * h + c;
-            if (m < M) {
-              const float v = ROT ? acc[mb][nb][4 * a + c] - s_cor[m - m0] : acc[mb][nb][4 * a + c];
-              out16[m * kpad_next + col] = n < N ? (_Float16)ldexpf(v, s_next[m - m0] - s_exp[m - m0]) : (_Float16)0.0f;
-            }
-          }
-      }
+    for (int r = lane / 8; r < 32 * MB; r += 8)
+      if (wrow + r < M)
+        *reinterpret_cast<u32x4*>(out16 + (wrow + r) * kpad_next + wcol + 8 * (lane % 8)) =
+            *reinterpret_cast<const u32x4*>(rows + r * kLd + 8 * (lane % 8));
     return;
   }
-  if constexpr (EPI) {
-    // the wave's outputs go through LDS, 32 rows at a time, so that the epilogue's operands and results
-    // are 16-byte pieces of rows (rows of kEpiLd floats: the two lane halves' rows fall on other banks)
-    constexpr int kEpiLd = 68;
-    static_assert(kWaves * 32 * kEpiLd * 4 <= P::LDS, "the epilogue's rows fit the pipeline's stages");
-    float* rows = reinterpret_cast<float*>(lds) + wave * 32 * kEpiLd;
+  float* dst = (!PROD || out) ? out + (int64_t)split * M * N : nullptr;
+  if constexpr (!PROD) {
+    // 32 rows at a time (rows of kLd floats: the two lane halves' rows fall on other banks)
+    constexpr int kLd = 68;
+    static_assert(kWaves * 32 * kLd * 4 <= P::LDS, "the wave's rows fit the pipeline's stages");
+    float* rows = reinterpret_cast<float*>(lds) + wave * 32 * kLd;
+    const int64_t o = wcol + 8 * (lane % 8);
+    const int left = (int)imax(0, imin(N - o, 8));
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      __syncthreads();  // the stages, or the rows before, have been read
+      if (mb) __syncthreads();  // the rows before have been read
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb) {
-        const int64_t n = n0 + wn * 64 + nb * 32 + l32;
-        const float sc = n < N ? colscale[n] : 0.0f;
+        const int64_t n = wcol + nb * 32 + l32;
+        const float sc = n < N && colscale ? colscale[n] : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = 8 * (i / 4) + 4 * h + i % 4;
-          const int64_t m = imin(m0 + wm * 32 * MB + mb * 32 + r, M - 1);
-          rows[r * kEpiLd + nb * 32 + l32] = sc * ldexpf(ROT ? acc[mb][nb][i] - s_cor[m - m0] : acc[mb][nb][i], -s_exp[m - m0]);
-        }
+        for (int i = 0; i < 16; ++i)
+          rows[(8 * (i / 4) + 4 * h + i % 4) * kLd + nb * 32 + l32] = sc * acc[mb][nb][i];
       }
       __syncthreads();
-      const int64_t o = n0 + wn * 64 + 8 * (lane % 8);
-      const int left = (int)imin(N - o, 8);
 #pragma unroll 1
       for (int r = lane / 8; r < 32; r += 8) {
-        const int64_t m = m0 + wm * 32 * MB + mb * 32 + r;
-        if (m >= M || left <= 0) break;
+        const int64_t m = wrow + mb * 32 + r;
+        if (m >= M) break;
         Elements<8> v;
-        v.load(rows + r * kEpiLd + 8 * (lane % 8), false, 0);
-        epilogue_store8(E, m * N + o, o, left, v);
+        v.load(rows + r * kLd + 8 * (lane % 8), false, 0);
+        if constexpr (EPI) {
+          if (left > 0) epilogue_store8(E, m * N + o, o, left, v);
+        } else if (left == 8) {
+          v.store(dst, false, m * N + o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 7; ++j)
+            if (j < left) dst[m * N + o + j] = v.v[j];
+        }
       }
     }
     return;
   }
-  float* dst = (!PROD || out) ? out + (int64_t)split * M * N : nullptr;
   float colsum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb) {
-      const int64_t n = n0 + wn * 64 + nb * 32 + l32;
+      const int64_t n = wcol + nb * 32 + l32;
       const float sc = (n < N && colscale) ? colscale[n] : 1.0f;
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int64_t m = m0 + wm * 32 * MB + mb * 32 + 8 * a + 4 * h + c;
+          const int64_t m = wrow + mb * 32 + 8 * a + 4 * h + c;
           if (m < M && n < N) {
-            const float v = ldexpf(ROT ? acc[mb][nb][4 * a + c] - s_cor[m - m0] : acc[mb][nb][4 * a + c], -s_exp[m - m0]);
-            if (!PROD || dst) dst[m * N + n] = sc * v;
-            if constexpr (PROD) colsum[nb] = fmaf(load_prod(pm, pm_bf16, m * N + n), v, colsum[nb]);
+            const float v = acc[mb][nb][4 * a + c];
+            if (dst) dst[m * N + n] = sc * v;
+            colsum[nb] = fmaf(load_prod(pm, pm_bf16, m * N + n), v, colsum[nb]);
           }
         }
     }
