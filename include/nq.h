@@ -479,9 +479,9 @@ typedef struct {
  *   (a factor or term that is null is left out).  x, T: as in nq_lrb_linear;
  *   y: [T][d_out], fp32 or bf16 (y_dtype).  W x is computed as by nq_lrb_linear
  *   (the same regimes and arithmetic); the epilogue is fp32 and rounds once, to
- *   y's type (and z to its own).  y may be mul or residual where the types are
- *   equal (in place); z may not be any of them.  silu and gelu of -inf are NaN,
- *   the products -inf * 0 of their formulas.
+ *   y's type (and z to its own).  mul and residual may be x; y may be mul or residual
+ *   where the types are equal (in place), but not x; z may not be any of them.  silu
+ *   and gelu of -inf are NaN, the products -inf * 0 of their formulas.
  *   workspace: at least nq_lrb_act_workspace_bytes(L, T) bytes, 256-byte aligned
  *   (0 bytes: none, it may be null: small layers at T <= 8).  Streams, graphs and
  *   determinism: as for nq_lrb_linear (NQ_DECODE_TINY does not count here).
@@ -552,8 +552,8 @@ nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* 
  *   dlogits: [T] rows of V, row stride ldd >= V elements, fp32 or bf16
  *   (dlogits_dtype); columns past V are not written; it may be logits itself with
  *   the same type and stride (in place).  loss may be null.
- * Both read the logits from memory once for V up to 131072 (bf16) or 65536 (fp32);
- * exponentials are fp32, the sums over a row fp32 per thread and fp64 across, the
+ * The loss reads the logits once; the gradient goes over a row a second time, at once,
+ * while the last of it is in registers and the rest in the caches.  Exponentials are fp32, the sums over a row fp32 per thread and fp64 across, the
  * loss is formed in fp64 and rounded once, each gradient rounded once.  Deterministic;
  * the order of the sums depends on T, V and the call, so the two calls' losses agree
  * to rounding.

@@ -113,7 +113,8 @@ __device__ inline void act_value_grad(float z, float& a, float& da) {
   } else if constexpr (ACT == NQ_ACT_GELU_TANH) {
     const float q = sigmoid_f(2.0f * kGeluA * (z + kGeluB * z * z * z));
     a = z * q;
-    da = q + a * (1.0f - q) * 2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
+    // a (1 - q) is 0 where z^2 overflows, and its product with an infinity would be NaN
+    da = q + a * (1.0f - q) * 2.0f * kGeluA * (1.0f + fminf(3.0f * kGeluB * z * z, __FLT_MAX__));
   } else if constexpr (ACT == NQ_ACT_SILU) {
     const float q = sigmoid_f(z);
     a = z * q;
@@ -147,10 +148,10 @@ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
-// N outputs of one column (bias: the column's, or 0): v, W x before the bias, at elements at(j), or none
-// where that is negative.  The operands of all are loaded ahead of the first store, which no load can be
-// moved across (y may be one of them): an element at a time pays a memory latency each (8 tokens of an
-// 11008 x 4096 layer of rank 2368: 45.7 us instead of 33.3).
+// N outputs of one column (bias: the column's, or 0): v, W x before the bias, at elements at(j).  The
+// operands of all are loaded ahead of the first store, which no load can be moved across (y may be one of
+// them): an element at a time pays a memory latency each (8 tokens of an 11008 x 4096 layer of rank 2368:
+// 45.7 us instead of 33.3).
 // kAtOnce activations are computed side by side (all of them at once spilled registers).
 constexpr int kAtOnce = 2;
 template <int N, typename At>
@@ -158,10 +159,10 @@ __device__ __forceinline__ void epilogue_store(const Epilogue& E, float bias, co
   float mul[N], res[N];
   if (E.mul)
 #pragma unroll
-    for (int j = 0; j < N; ++j) mul[j] = at(j) >= 0 ? epi_load(E.mul, E.mul_bf16, at(j)) : 0.0f;
+    for (int j = 0; j < N; ++j) mul[j] = epi_load(E.mul, E.mul_bf16, at(j));
   if (E.residual)
 #pragma unroll
-    for (int j = 0; j < N; ++j) res[j] = at(j) >= 0 ? epi_load(E.residual, E.residual_bf16, at(j)) : 0.0f;
+    for (int j = 0; j < N; ++j) res[j] = epi_load(E.residual, E.residual_bf16, at(j));
   with_act(E.act, [&](auto act) __attribute__((always_inline)) {
     // v is rounded before the bias is added: the layer's output, as without an epilogue
 #pragma clang fp contract(off)
@@ -172,7 +173,6 @@ __device__ __forceinline__ void epilogue_store(const Epilogue& E, float bias, co
       float a = act(z);
       if (E.mul) a *= mul[j];
       if (E.residual) a += res[j];
-      if (at(j) < 0) continue;
       if (E.z) epi_store(E.z, E.z_bf16, at(j), z);
       epi_store(E.y, E.y_bf16, at(j), a);
     }

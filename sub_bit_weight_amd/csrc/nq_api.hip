@@ -978,6 +978,8 @@ nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, in
     return set_error("%s: y in place of an operand of another dtype", who), NQ_ERR_ARG;
   if (E->z && (E->z == y || E->z == E->mul || E->z == E->residual))
     return set_error("%s: z in place of y or an operand", who), NQ_ERR_ARG;
+  // x may be the residual, but its rows are read until the last output is made
+  if (y == x || E->z == x) return set_error("%s: y or z in place of x", who), NQ_ERR_ARG;
   const size_t need = linear_act_workspace(*L, T);
   if (need && (st = check_workspace(who, workspace, workspace_bytes, need)) != NQ_OK) return st;
   const Epilogue epi{E->bias,

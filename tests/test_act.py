@@ -69,7 +69,8 @@ def _grads(act=4, z=DUMMY, zd=1, mul=3 * DUMMY, md=1, dy=5 * DUMMY, dyd=1, T=300
     dict(mul=DUMMY, mul_dtype=3), dict(residual=DUMMY + 2, residual_dtype=0), dict(residual=DUMMY, residual_dtype=-1),
     dict(z=DUMMY, z_dtype=9), dict(z=DUMMY + 1, z_dtype=1), dict(z=2 * DUMMY, z_dtype=1),
     dict(z=DUMMY, z_dtype=1, mul=DUMMY, mul_dtype=1), dict(mul=2 * DUMMY, mul_dtype=0),
-    dict(residual=2 * DUMMY, residual_dtype=0), dict(ws=DUMMY + 4), dict(L=_layer(d_in=0)), dict(L=_layer(ldu=1))])
+    dict(residual=2 * DUMMY, residual_dtype=0), dict(y=DUMMY), dict(y=DUMMY, residual=DUMMY, residual_dtype=1),
+    dict(z=DUMMY, z_dtype=1), dict(ws=DUMMY + 4), dict(L=_layer(d_in=0)), dict(L=_layer(ldu=1))])
 def test_linear_rejects(kw):
     assert _linear(**kw) == nq.NQ_ERR_ARG and nq.last_error() != ""
 
@@ -248,6 +249,30 @@ def test_act_grads_mixed_types_in_place_and_strange_operands():
     z[3], dy[5] = float("nan"), 0.0
     dz4, _, db4 = nq.act_grads("silu", z, dy)
     assert torch.isnan(dz4[3]).all() and torch.isnan(db4).all() and (dz4[5] == 0).all() and torch.isfinite(dz4[6]).all()
+
+
+@gpu
+def test_act_grads_of_extreme_values():
+    """Where a square or a cube of z leaves fp32, the derivatives have reached their limits."""
+    z = torch.tensor([0.0, 30.0, 104.0, 1e4, 1e13, 1e19, 1.9e19, 1e20, 3e38], device=DEV)
+    z = torch.cat((z, -z))[None].repeat(2, 1)
+    for act in ACTS:
+        for dt in (torch.float32, torch.bfloat16):
+            zt, dy = z.to(dt), _rand("x/dy", tuple(z.shape), dt)
+            dz, _, dbias = nq.act_grads(act, zt, dy)
+            wz, _, wb, (ez, _, _) = D.act_grads_ref(act, _np(zt), _np(dy))
+            # the lost parts' bound grows with z^2; the derivatives themselves are within 8 roundings of 0 or 1 there
+            ez = np.minimum(ez, np.abs(_np(dy)) * 512 * D.EPS32)
+            _close(dz, wz, ez, (act, dt))
+            _close(dbias, wb, ez.sum(0) + 2 * D.EPS32 * np.abs(wz).sum(0), (act, dt))
+    # x is the residual: a result of its own
+    layer, _ = _act_layer(96, 96, 40)
+    for T in (3, 20):
+        x = _rand("x/res", (T, 96), torch.float32)
+        want = nq.lrb_linear(layer, x) + x
+        assert torch.equal(nq.lrb_linear_act(layer, x, residual=x), want)
+        with pytest.raises(nq.NqError):
+            nq.lrb_linear_act(layer, x, residual=x, y=x)
 
 
 @gpu
