@@ -354,6 +354,13 @@ struct Piece {
       }
     }
   }
+  // element i of a lane's own choice (by masks: a choice of array elements would put the piece in memory)
+  __device__ float pick(int i) const {
+    const int w = BF16 ? i / 2 : i;
+    const uint32_t odd = __builtin_amdgcn_sbfe(w, 0, 1), up = __builtin_amdgcn_sbfe(w, 1, 1);
+    const uint32_t lo = v[0] ^ ((v[0] ^ v[1]) & odd), hi = v[2] ^ ((v[2] ^ v[3]) & odd), u = lo ^ ((lo ^ hi) & up);
+    return __uint_as_float(!BF16 ? u : i & 1 ? u & 0xFFFF0000u : u << 16);
+  }
   // the bits of piece j in the bitmap
   __device__ static uint32_t bits(const uint32_t* listed, int j) {
     if (BF16) return reinterpret_cast<const uint8_t*>(listed)[j];
@@ -714,15 +721,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void lo
   const int waves = max(1, (min(np, NT) + 63) / 64), quota = (k + waves - 1) / waves;
   MaxSum rest;
   int mine = 0;  // this wave's candidates
-  // takes the lanes' logits that reach the bound; all lanes of the wave come here
-  auto take = [&](float v, int idx) {
-    const bool on = v >= bound;
-    const uint64_t lanes = __ballot(on);
-    if (!lanes) return false;
+  // takes the logits of those lanes, one of each; all lanes of the wave come here
+  auto take = [&](uint64_t lanes, bool on, float v, int idx) {
     const int at = mine + __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
     if (on && at < kWaveCandidates) S.own[wave][at] = top_place_key(logit_key(v), idx);
     mine += __popcll(lanes);
-    return on;
   };
   // what of this wave's candidates no longer reaches the bound joins the rest
   auto prune = [&] {
@@ -740,7 +743,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void lo
     }
     mine = kept;
   };
-  int steps = 0, next_bound = 0;
+  int steps = 0, next_bound = 0, last_bound = 0;
 #pragma unroll 1
   for (int j0 = tid; j0 - tid < np || steps == 0; j0 += NT * U, ++steps) {
     Pc pc[U];
@@ -768,21 +771,30 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void lo
     }
     if (steps == next_bound) {
       bound = top_bound<NT>(S, gm, quota, waves);
+      last_bound = steps;
       next_bound = 2 * steps + 1;
       if (mine > kWaveCandidates) S.over = 1, mine = kWaveCandidates;
       prune();
     }
     if (steps == 0) {
-      if (take(xt, it)) xt = -kInf;
-      rest.add(xt, A.c);
+      const bool on = xt >= bound;
+      if (const uint64_t lanes = __ballot(on)) take(lanes, on, xt, it);
+      rest.add(on ? -kInf : xt, A.c);
     }
     float mm = rest.m;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (__any(pm[i] >= bound)) {
+        // each lane's in turn: two turns mostly, where a vote on every element costs N
         uint32_t bits = 0;
 #pragma unroll
-        for (int q = 0; q < N; ++q) bits |= take(pc[i].at(q), (j0 + i * NT) * N + q) ? 1u << q : 0u;
+        for (int q = 0; q < N; ++q) bits |= pc[i].at(q) >= bound ? 1u << q : 0u;
+        uint32_t left = bits;
+        while (const uint64_t lanes = __ballot(left != 0)) {
+          const int q = __builtin_ctz(left | 1u << 31);
+          take(lanes, left != 0, pc[i].pick(q), (j0 + i * NT) * N + q);
+          left &= left - 1;
+        }
         pc[i].mask(bits);
         pm[i] = -kInf;
 #pragma unroll
@@ -800,7 +812,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void lo
       for (int q = 0; q < N; ++q) rest.s += exp_scaled(pc[i].at(q) - ref, A.c);
   }
   if (mine > kWaveCandidates) S.over = 1, mine = kWaveCandidates;
-  if (steps > 1) {
+  if (last_bound < steps - 1) {
     bound = top_bound<NT>(S, gm, quota, waves);
     prune();
   }
