@@ -354,6 +354,13 @@ struct Piece {
       }
     }
   }
+  __device__ void choose(bool other, const Piece& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = v[i], b = o.v[i];
+      v[i] = other ? b : a;
+    }
+  }
   // element i of a lane's own choice (by masks: a choice of array elements would put the piece in memory)
   __device__ float pick(int i) const {
     const int w = BF16 ? i / 2 : i;
@@ -781,25 +788,39 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void lo
       if (const uint64_t lanes = __ballot(on)) take(lanes, on, xt, it);
       rest.add(on ? -kInf : xt, A.c);
     }
+    // Pieces with candidates, one of each lane in turn (of 64 lanes' 4 pieces two thirds have one when 64 of
+    // 32000 are wanted, but hardly a lane has it in two of its own): the lane's element by element in turn.
+    for (;;) {
+      int which = -1;
+#pragma unroll
+      for (int i = U - 1; i >= 0; --i) which = pm[i] >= bound ? i : which;
+      if (!__any(which >= 0)) break;
+      Pc p = pc[0];
+#pragma unroll
+      for (int i = 1; i < U; ++i) p.choose(which == i, pc[i]);
+      uint32_t bits = 0;
+#pragma unroll
+      for (int q = 0; q < N; ++q) bits |= p.at(q) >= bound ? 1u << q : 0u;
+      if (which < 0) bits = 0;
+      uint32_t left = bits;
+      while (const uint64_t lanes = __ballot(left != 0)) {
+        const int q = __builtin_ctz(left | 1u << 31);
+        take(lanes, left != 0, p.pick(q), (j0 + which * NT) * N + q);
+        left &= left - 1;
+      }
+      p.mask(bits);
+      float m = -kInf;
+#pragma unroll
+      for (int q = 0; q < N; q += 2) m = max3(m, p.at(q), p.at(q + 1));
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        pc[i].choose(which == i, p);
+        pm[i] = which == i ? m : pm[i];
+      }
+    }
     float mm = rest.m;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (__any(pm[i] >= bound)) {
-        // each lane's in turn: two turns mostly, where a vote on every element costs N
-        uint32_t bits = 0;
-#pragma unroll
-        for (int q = 0; q < N; ++q) bits |= pc[i].at(q) >= bound ? 1u << q : 0u;
-        uint32_t left = bits;
-        while (const uint64_t lanes = __ballot(left != 0)) {
-          const int q = __builtin_ctz(left | 1u << 31);
-          take(lanes, left != 0, pc[i].pick(q), (j0 + i * NT) * N + q);
-          left &= left - 1;
-        }
-        pc[i].mask(bits);
-        pm[i] = -kInf;
-#pragma unroll
-        for (int q = 0; q < N; q += 2) pm[i] = max3(pm[i], pc[i].at(q), pc[i].at(q + 1));
-      }
       pc[i].packed();
       mm = fmaxf(mm, pm[i]);
     }
