@@ -26,21 +26,25 @@ __device__ inline void element_grads(float z, float mul, float dy, float& dz, fl
   dmul = dy * a;
 }
 
-// A workgroup takes kCols columns' worth of N-element pieces and tc tokens; each of its kRows rows of
-// threads walks every kRows-th token, and the rows' sums of dz are added in order through LDS into
-// sums[chunk][d].  The columns past the last whole piece are one thread's, element by element.
-constexpr int kCols = 16, kRows = 16, kGradThreads = kCols * kRows;
-template <int ACT, int N>
-__global__ __launch_bounds__(kGradThreads) void act_grads_kernel(const ActGrads G, int64_t T, int64_t tc, int64_t d,
+// A workgroup takes kCols pieces of N columns and tc tokens; each of its kRows rows of threads walks every
+// kRows-th token, and the rows' sums of dz are added in order through LDS into sums[chunk][d].  The d % N
+// columns past the last whole piece are pieces of one column (all of them one thread's took longer than
+// everything else: 256 x 1117 bf16, gelu, 30 us, 17.8 so).  Bound by the loads and stores where the chip is
+// full (2048 x 28672 bf16, silu and gate: 119 us, 4.9 TB/s), else by the chain of a thread's tokens.
+constexpr int kCols = 16;
+template <int ACT, int N, int kRows>
+__global__ __launch_bounds__(kCols* kRows) void act_grads_kernel(const ActGrads G, int64_t T, int64_t tc, int64_t d,
                                                                  float* __restrict__ sums) {
   __shared__ float part[kRows][kCols * N];
   const int col = threadIdx.x % kCols, row = threadIdx.x / kCols;
-  const int64_t c0 = ((int64_t)blockIdx.x * kCols + col) * N;
+  const int64_t np = d / N, first = (int64_t)blockIdx.x * kCols;
+  const bool whole = first + col < np;
+  const int64_t c0 = whole ? (first + col) * N : np * N + (first + col - np);
   const int64_t t0 = (int64_t)blockIdx.y * tc, t1 = imin(t0 + tc, T);
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-  if (c0 + N <= d) {
+  if (whole) {
     // two tokens at a time, all their loads ahead of their stores (a result may be in place)
     constexpr int U = 2;
     for (int64_t t = t0 + row; t < t1; t += U * kRows) {
@@ -67,26 +71,35 @@ __global__ __launch_bounds__(kGradThreads) void act_grads_kernel(const ActGrads 
       }
     }
   } else if (c0 < d) {
-    for (int64_t t = t0 + row; t < t1; t += kRows)
+    constexpr int U = 4;
+    for (int64_t t = t0 + row; t < t1; t += U * kRows) {
+      float z[U], mul[U], dy[U];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (c0 + j >= d) continue;
-        const int64_t i = t * d + c0 + j;
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = imin(t + u * kRows, t1 - 1) * d + c0;
+        dy[u] = epi_load(G.dy, G.dy_bf16, i);
+        z[u] = G.z ? epi_load(G.z, G.z_bf16, i) : 0.0f;
+        mul[u] = G.mul ? epi_load(G.mul, G.mul_bf16, i) : 1.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u * kRows >= t1) break;
+        const int64_t i = (t + u * kRows) * d + c0;
         float dz, dmul;
-        element_grads<ACT>(G.z ? epi_load(G.z, G.z_bf16, i) : 0.0f, G.mul ? epi_load(G.mul, G.mul_bf16, i) : 1.0f,
-                           epi_load(G.dy, G.dy_bf16, i), dz, dmul);
-        acc[j] += dz;
+        element_grads<ACT>(z[u], mul[u], dy[u], dz, dmul);
+        acc[0] += dz;
         epi_store(G.dz, G.dz_bf16, i, dz);
         if (G.dmul) epi_store(G.dmul, G.dmul_bf16, i, dmul);
       }
+    }
   }
   if (!sums) return;
 #pragma unroll
   for (int j = 0; j < N; ++j) part[row][col * N + j] = acc[j];
   __syncthreads();
-  for (int c = threadIdx.x; c < kCols * N; c += kGradThreads) {
-    const int64_t at = (int64_t)blockIdx.x * kCols * N + c;
-    if (at >= d) break;
+  for (int c = threadIdx.x; c < kCols * N; c += kCols * kRows) {
+    const int64_t piece = first + c / N, at = piece < np ? piece * N + c % N : np * N + (piece - np);
+    if (at >= d || (piece >= np && c % N)) continue;
     float s = part[0][c];
 #pragma unroll
     for (int r = 1; r < kRows; ++r) s += part[r][c];
@@ -108,15 +121,26 @@ __global__ __launch_bounds__(256) void chunk_sums_kernel(const float* __restrict
 // than 1024 such chunks.
 int64_t chunk_tokens(int64_t T) { return T <= 256 ? T : imax(128, cdiv(T, 1024)); }
 
+template <int N, int kRows>
+void launch_act_grads_t(int act, const ActGrads& G, int64_t T, int64_t tc, int64_t d, float* sums, hipStream_t s) {
+  const dim3 grid((unsigned)cdiv(d / N + d % N, kCols), (unsigned)cdiv(T, tc));
+  const auto kernel = act == NQ_ACT_RELU        ? act_grads_kernel<NQ_ACT_RELU, N, kRows>
+                      : act == NQ_ACT_GELU      ? act_grads_kernel<NQ_ACT_GELU, N, kRows>
+                      : act == NQ_ACT_GELU_TANH ? act_grads_kernel<NQ_ACT_GELU_TANH, N, kRows>
+                      : act == NQ_ACT_SILU      ? act_grads_kernel<NQ_ACT_SILU, N, kRows>
+                                                : act_grads_kernel<NQ_ACT_NONE, N, kRows>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kCols * kRows), 0, s, G, T, tc, d, sums);
+}
+// Rows of threads: 16, or 64 where that leaves the chip (256 units) with few workgroups and a thread with
+// many tokens (us with 16 / 64, gelu; bf16: 77 tokens of 4096 9.0 / 6.4, 256 of 11008, 86 workgroups,
+// 24.0 / 15.8, 2048 of 4096, 512 workgroups, 22.2 / 23.7; fp32: 16 tokens of 1117 3.5 / 3.8, 2048 of 4096,
+// 1024 workgroups, 22.0 / 25.6).
 template <int N>
 void launch_act_grads_n(int act, const ActGrads& G, int64_t T, int64_t tc, int64_t d, float* sums, hipStream_t s) {
-  const dim3 grid((unsigned)cdiv(d, kCols * N), (unsigned)cdiv(T, tc));
-  const auto kernel = act == NQ_ACT_RELU        ? act_grads_kernel<NQ_ACT_RELU, N>
-                      : act == NQ_ACT_GELU      ? act_grads_kernel<NQ_ACT_GELU, N>
-                      : act == NQ_ACT_GELU_TANH ? act_grads_kernel<NQ_ACT_GELU_TANH, N>
-                      : act == NQ_ACT_SILU      ? act_grads_kernel<NQ_ACT_SILU, N>
-                                                : act_grads_kernel<NQ_ACT_NONE, N>;
-  hipLaunchKernelGGL(kernel, grid, dim3(kGradThreads), 0, s, G, T, tc, d, sums);
+  if (tc > 16 && cdiv(d, kCols * N) * cdiv(T, tc) < 512)
+    launch_act_grads_t<N, 64>(act, G, T, tc, d, sums, s);
+  else
+    launch_act_grads_t<N, 16>(act, G, T, tc, d, sums, s);
 }
 
 }  // namespace
