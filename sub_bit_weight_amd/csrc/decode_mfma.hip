@@ -151,16 +151,19 @@ __device__ inline void wait_input(const StageDesc& S, int* err) {
   __syncthreads();
 }
 
-// A final output row, one value per token.  EPI: a linear's outputs (the stage that signals nothing) go
-// through the epilogue E.
-template <int T, bool EPI>
-__device__ __forceinline__ void store_row(const StageDesc& S, int64_t o, float sc, const float* acc, const Epilogue& E) {
-  if (EPI && !S.signal) {
-    float v[T];
+// A final output row, one value per token.  With an Epilogue a linear's outputs (the stage that signals
+// nothing) go through it.
+template <int T, typename E>
+__device__ __forceinline__ void store_row(const StageDesc& S, int64_t o, float sc, const float* acc,
+                                          const E& epi) {
+  if constexpr (is_epilogue<E>) {
+    if (!S.signal) {
+      float v[T];
 #pragma unroll
-    for (int t = 0; t < T; ++t) v[t] = sc * acc[t];
-    epilogue_store<T>(E, E.bias ? E.bias[o] : 0.0f, v, [&](int t) { return (int64_t)t * S.n_rows + o; });
-    return;
+      for (int t = 0; t < T; ++t) v[t] = sc * acc[t];
+      epilogue_store<T>(epi, epi.bias ? epi.bias[o] : 0.0f, v, [&](int t) { return (int64_t)t * S.n_rows + o; });
+      return;
+    }
   }
 #pragma unroll
   for (int t = 0; t < T; ++t) {
@@ -176,14 +179,14 @@ __device__ __forceinline__ void store_row(const StageDesc& S, int64_t o, float s
 // token t): store the row (times the row scale), or publish the span's partial
 // sums and let the last span of the row block add them in span order.  Every
 // thread of the workgroup must call it; it ends with a barrier.
-template <int T, bool EPI>
-__device__ __forceinline__ void finish_rows(const StageDesc& S, int rb, int ks, int64_t o, bool valid, const float* acc, int* s_flag,
-                            const Epilogue& E) {
+template <int T, typename E>
+__device__ __forceinline__ void finish_rows(const StageDesc& S, int rb, int ks, int64_t o, bool valid,
+                                            const float* acc, int* s_flag, const E& epi) {
   const int tid = threadIdx.x;
   if (S.nks == 1) {
     if (valid) {
       const float sc = S.rowscale ? gload(S.rowscale + o) : 1.0f;
-      store_row<T, EPI>(S, o, sc, acc, E);
+      store_row<T>(S, o, sc, acc, epi);
     }
   } else {
     if (valid) {
@@ -221,7 +224,7 @@ __device__ __forceinline__ void finish_rows(const StageDesc& S, int rb, int ks, 
 #pragma unroll
             for (int t = 0; t < T; ++t) sum[t] += v[i][t];
       }
-      store_row<T, EPI>(S, o, sc, sum, E);
+      store_row<T>(S, o, sc, sum, epi);
     }
     if (tid == 0) gstore(S.rb_count + rb, 0);  // all arrivals happened: ready for the next run
   }
@@ -701,9 +704,12 @@ __device__ inline float quad_sum(float v) {
 // FUSE (single calls): the span is one chunk whose pieces the tile makes
 // itself (tile_pieces); otherwise they are copied from the stage's
 // input-piece blocks chunk by chunk.
-template <int T, bool W4, bool FUSE, bool EPI>
-__device__ __forceinline__ void mfma_tile(const StageDesc& S, int local, float* ldsf, int* s_flag, int* err, NextTile& next,
-                          const Epilogue& E) {
+// Inlined as the compiler sees fit: forced, the plain kernel came out with more
+// registers and slower (8 tokens, two 11008 x 4096 layers and a 4096 x 11008 one,
+// r 2368: 94.2 us, 93.3 so).
+template <int T, bool W4, bool FUSE, typename E>
+__device__ void mfma_tile(const StageDesc& S, int local, float* ldsf, int* s_flag, int* err, NextTile& next,
+                          const E& epi) {
   static_assert(T <= kMfmaMaxT, "tokens");
   constexpr int G = col_groups<T>();
   int* lds = reinterpret_cast<int*>(ldsf);
@@ -857,7 +863,7 @@ __device__ __forceinline__ void mfma_tile(const StageDesc& S, int local, float* 
     for (int t = 0; t < T; ++t) accr[t] = sums[t * kMRows + tid];
     const int rb = rb0 + ri;
     const int64_t o = (int64_t)rb * kMRows + tid;
-    finish_rows<T, EPI>(S, rb, ks, o, o < S.n_rows, accr, s_flag, E);  // ends with a barrier: sums are free again
+    finish_rows<T>(S, rb, ks, o, o < S.n_rows, accr, s_flag, epi);  // ends with a barrier: sums are free again
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -960,23 +966,29 @@ static_assert(col_groups<kMfmaMaxT>() <= 2, "T <= 8 in two column groups");
 // SINGLE: a single call's tiles (kind 2 only); otherwise a sequence's (kinds
 // 0 and 1).  Kept apart so that neither kernel carries the other's code and
 // registers.
-template <int T, bool SINGLE, bool EPI>
+template <int T, bool SINGLE, typename E>
 __device__ inline void stage_tile(const StageDesc& S, int local, float* lds, int* s_flag, int* err, NextTile& next,
-                                  const Epilogue& E) {
-  if constexpr (SINGLE) {
+                                  const E& epi) {
+  if constexpr (SINGLE && is_epilogue<E>) {
+    // left to itself the compiler makes calls of these from four tokens on
     if (S.w_vec)
-      mfma_tile<T, true, true, EPI>(S, local, lds, s_flag, err, next, E);
+      [[clang::always_inline]] mfma_tile<T, true, true>(S, local, lds, s_flag, err, next, epi);
     else
-      mfma_tile<T, false, true, EPI>(S, local, lds, s_flag, err, next, E);
+      [[clang::always_inline]] mfma_tile<T, false, true>(S, local, lds, s_flag, err, next, epi);
+  } else if constexpr (SINGLE) {
+    if (S.w_vec)
+      mfma_tile<T, true, true>(S, local, lds, s_flag, err, next, epi);
+    else
+      mfma_tile<T, false, true>(S, local, lds, s_flag, err, next, epi);
   } else {
     if (S.kind == 1 && S.prep_tg == 1)
       mfma_prep_tile<T, 1>(S, local, lds, err, next);
     else if (S.kind == 1)
       mfma_prep_tile<T, T>(S, local, lds, err, next);
     else if (S.w_vec)
-      mfma_tile<T, true, false, false>(S, local, lds, s_flag, err, next, E);
+      mfma_tile<T, true, false>(S, local, lds, s_flag, err, next, epi);
     else
-      mfma_tile<T, false, false, false>(S, local, lds, s_flag, err, next, E);
+      mfma_tile<T, false, false>(S, local, lds, s_flag, err, next, epi);
   }
 }
 
@@ -985,8 +997,8 @@ __device__ inline void stage_tile(const StageDesc& S, int local, float* lds, int
 // from the counter at [1]; `lookup(tile, S, local)` gives a tile's descriptor
 // and its index within its stage.  The last workgroup to exit zeroes
 // [1 .. n_ints), so consecutive runs need no separate reset launch.
-template <int T, bool SINGLE, bool EPI, typename Lookup>
-__device__ inline void persistent_tiles(Lookup lookup, int ntiles, int* ints, int n_ints, float* lds, const Epilogue& E) {
+template <int T, bool SINGLE, typename Lookup, typename E>
+__device__ inline void persistent_tiles(Lookup lookup, int ntiles, int* ints, int n_ints, float* lds, const E& epi) {
   int& s_flag = reinterpret_cast<int*>(lds)[flag_off<T>()];
   int& s_tile = reinterpret_cast<int*>(lds)[flag_off<T>() + 1];
   int* err = ints;
@@ -1001,7 +1013,7 @@ __device__ inline void persistent_tiles(Lookup lookup, int ntiles, int* ints, in
     StageDesc S;
     int local;
     lookup(tile, S, local);
-    stage_tile<T, SINGLE, EPI>(S, local, lds, &s_flag, err, next, E);
+    stage_tile<T, SINGLE>(S, local, lds, &s_flag, err, next, epi);
     if (threadIdx.x == 0) s_tile = next.id;
     __syncthreads();
     tile = __builtin_amdgcn_readfirstlane(s_tile);
@@ -1026,12 +1038,12 @@ __global__ __launch_bounds__(kMRows) __attribute__((amdgpu_waves_per_eu(min_wave
 void dec_persistent_kernel(const StageDesc* __restrict__ segs, const int* __restrict__ tile_seg, int ntiles, int* ints,
                            int n_ints) {
   __shared__ __attribute__((aligned(16))) float lds[mfma_lds<T>()];
-  persistent_tiles<T, false, false>(
+  persistent_tiles<T, false>(
       [&](int tile, StageDesc& S, int& local) {
         S = segs[tile_seg[tile]];  // one lookup (a scan over the segments stalled for microseconds)
         local = tile - S.tile0;
       },
-      ntiles, ints, n_ints, lds, Epilogue{});
+      ntiles, ints, n_ints, lds, NoEpilogue{});
 }
 
 // One linear (a single call): its descriptors travel in the kernel arguments.
@@ -1040,11 +1052,11 @@ struct LinearSched {
   int end[kMaxLinearDescs];  // cumulative tile counts
 };
 
-template <int T, bool EPI>
+template <int T, typename E>
 __global__ __launch_bounds__(kMRows) __attribute__((amdgpu_waves_per_eu(min_waves<T>())))
-void dec_linear_kernel(LinearSched L, int* ints, int n_ints, const Epilogue E) {
+void dec_linear_kernel(LinearSched L, int* ints, int n_ints, const E epi) {
   __shared__ __attribute__((aligned(16))) float lds[mfma_lds<T>()];
-  persistent_tiles<T, true, EPI>(
+  persistent_tiles<T, true>(
       [&](int tile, StageDesc& S, int& local) {
         // the stage is uniform across the workgroup: select a pointer into the
         // argument segment (scalar loads), not a copy of each descriptor
@@ -1053,7 +1065,7 @@ void dec_linear_kernel(LinearSched L, int* ints, int n_ints, const Epilogue E) {
         S = *P;
         local = tile - P->tile0;
       },
-      L.end[kMaxLinearDescs - 1], ints, n_ints, lds, E);
+      L.end[kMaxLinearDescs - 1], ints, n_ints, lds, epi);
 }
 
 __global__ void zero_ints_kernel(int* p, int64_t n) {
@@ -1399,11 +1411,11 @@ hipError_t launch_dec_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64_
 #define NQ_CASE(TT)                                                                                            \
   case TT:                                                                                                     \
     if (epi)                                                                                                   \
-      hipLaunchKernelGGL((dec_linear_kernel<TT, true>), dim3(grid), dim3(kMRows), 0, s, sched, ints, n_ints,    \
+      hipLaunchKernelGGL((dec_linear_kernel<TT, Epilogue>), dim3(grid), dim3(kMRows), 0, s, sched, ints, n_ints,    \
                          *epi);                                                                                \
     else                                                                                                       \
-      hipLaunchKernelGGL((dec_linear_kernel<TT, false>), dim3(grid), dim3(kMRows), 0, s, sched, ints, n_ints,   \
-                         Epilogue{});                                                                          \
+      hipLaunchKernelGGL((dec_linear_kernel<TT, NoEpilogue>), dim3(grid), dim3(kMRows), 0, s, sched, ints, n_ints,   \
+                         NoEpilogue{});                                                                        \
     break;
     NQ_CASE(1) NQ_CASE(2) NQ_CASE(3) NQ_CASE(4) NQ_CASE(5) NQ_CASE(6) NQ_CASE(7) NQ_CASE(8)
 #undef NQ_CASE

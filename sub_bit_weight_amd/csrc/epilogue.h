@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "nq_internal.h"
 
 namespace nq {
@@ -135,6 +137,11 @@ struct Epilogue {
   int act;
   int mul_bf16, residual_bf16, z_bf16, y_bf16;
 };
+
+// What a kernel without an epilogue takes in its place, so that a plain linear carries nothing of it.
+struct NoEpilogue {};
+template <typename E>
+constexpr bool is_epilogue = std::is_same<E, Epilogue>::value;
 
 // f(the activation), by one uniform branch.
 template <typename F>

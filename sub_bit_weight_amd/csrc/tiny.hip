@@ -25,11 +25,11 @@ __device__ inline float tiny_bf16(uint16_t h) { return __uint_as_float((uint32_t
 // LDS: z [T][in_p] then t [T][r_p]; in_p and r_p are d_in and r rounded up to
 // whole words, the tails zero, so each word's 32 positions are summed without
 // a bound check (their sign bits are 0).
-// EPI: the outputs go through the epilogue E instead of to y.
-template <int T, bool EPI>
+// With an Epilogue the outputs go through it instead of to y.
+template <int T, typename E>
 __global__ __launch_bounds__(kTinyThreads) void tiny_linear_kernel(const nq_lrb L, const void* __restrict__ x,
                                                                    int x_bf16, float* __restrict__ y,
-                                                                   const Epilogue E) {
+                                                                   const E epi) {
   extern __shared__ __attribute__((aligned(16))) float sm[];
   const int d_in = (int)L.d_in, r = (int)L.r, d_out = (int)L.d_out;
   const int in_p = (d_in + 31) & ~31, r_p = (r + 31) & ~31;
@@ -91,8 +91,8 @@ __global__ __launch_bounds__(kTinyThreads) void tiny_linear_kernel(const nq_lrb 
     const float sc = L.s1 ? L.s1[i] : 1.0f;
 #pragma unroll
     for (int tt = 0; tt < T; ++tt) acc[tt] *= sc;
-    if constexpr (EPI) {
-      epilogue_store<T>(E, E.bias ? E.bias[i] : 0.0f, acc, [&](int tt) { return (int64_t)tt * d_out + i; });
+    if constexpr (is_epilogue<E>) {
+      epilogue_store<T>(epi, epi.bias ? epi.bias[i] : 0.0f, acc, [&](int tt) { return (int64_t)tt * d_out + i; });
     } else {
 #pragma unroll
       for (int tt = 0; tt < T; ++tt) y[(int64_t)tt * d_out + i] = acc[tt];
@@ -121,11 +121,11 @@ hipError_t launch_tiny_linear(const nq_lrb& L, const void* x, nq_dtype xd, int64
 #define NQ_CASE(TT)                                                                                                 \
   case TT:                                                                                                          \
     if (epi)                                                                                                        \
-      hipLaunchKernelGGL((tiny_linear_kernel<TT, true>), dim3(1), dim3(kTinyThreads), lds, s, L, x,                  \
+      hipLaunchKernelGGL((tiny_linear_kernel<TT, Epilogue>), dim3(1), dim3(kTinyThreads), lds, s, L, x,              \
                          (int)(xd == NQ_BF16), y, *epi);                                                            \
     else                                                                                                            \
-      hipLaunchKernelGGL((tiny_linear_kernel<TT, false>), dim3(1), dim3(kTinyThreads), lds, s, L, x,                 \
-                         (int)(xd == NQ_BF16), y, Epilogue{});                                                      \
+      hipLaunchKernelGGL((tiny_linear_kernel<TT, NoEpilogue>), dim3(1), dim3(kTinyThreads), lds, s, L, x,            \
+                         (int)(xd == NQ_BF16), y, NoEpilogue{});                                                    \
     break;
     NQ_CASE(1) NQ_CASE(2) NQ_CASE(3) NQ_CASE(4) NQ_CASE(5) NQ_CASE(6) NQ_CASE(7) NQ_CASE(8)
 #undef NQ_CASE
