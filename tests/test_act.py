@@ -391,3 +391,83 @@ def test_a_step_of_scale_only_reconstruction(T):
             assert np.linalg.norm(_np(a) - b.grad.numpy()) <= 8e-5 * np.linalg.norm(b.grad.numpy()), n
     for a, b in ((dx, x64), (dbias, b64)):
         assert np.linalg.norm(_np(a) - b.grad.numpy()) <= 8e-5 * np.linalg.norm(b.grad.numpy())
+
+
+# ---------------------------------------------------------------- tails
+
+
+def _tail_bounds(act, z):
+    """(act(z), act'(z), bounds of their errors before the result's own rounding), relative in the tails.  A function of
+    the hardware is within one unit, two roundings; erfc within 16 units (OpenCL's bound).  The logistic q = E r or r,
+    p = r or E r, r = 1 / (1 + E), E = exp(-|u|): exp2 2, its argument (in [-1/2, 1/2]) 1, the sum 1, the reciprocal 2,
+    the products 2, so 8; u of gelu_tanh is off by 7 roundings of its own size (four products, two constants, a sum).
+    A value below 2^-126 is off by at most 2^-149 besides."""
+    z = np.asarray(z, dtype=np.float64)
+    a, da, _ = D.act_ref(act, z)
+    lost = (np.abs(z) + 2) * 2.0 ** -148
+    if act == "gelu":
+        cdf, pdf = np.where(z == 0, 0.5, a / np.where(z == 0, 1.0, z)), np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+        c = cdf * (34 + 2 * z * z)  # the argument's two roundings, felt z^2 times at most
+        return a, da, (np.abs(z) * c + np.abs(a)) * D.EPS32 + lost, (
+            c + np.abs(z) * pdf * (12 + z * z) + np.abs(da)) * D.EPS32 + lost
+    if act == "silu":
+        u, du, own = z, np.ones_like(z), 0.0
+    else:
+        k, b = np.sqrt(2 / np.pi), 0.044715
+        u, du, own = 2 * k * (z + b * z ** 3), 2 * k * (1 + 3 * b * z * z), 7.0
+    q, p = 1 / (1 + np.exp(-u)), 1 / (1 + np.exp(u))
+    e_q, e_p = q * (8 + own * np.abs(u) * p), p * (8 + own * np.abs(u) * q)
+    e_da = e_q + np.abs(z * du) * (e_q * p + q * e_p + 8 * p * q) + np.abs(da)
+    return a, da, (np.abs(z) * e_q + np.abs(a)) * D.EPS32 + lost, e_da * D.EPS32 + lost * np.abs(du)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_tail_bounds_are_relative(act):
+    """Far out on the left the bounds are a small part of the value: a result of 0 there does not pass."""
+    z = np.array([-3.0, -5.0, -7.0])
+    a, da, ea, eda = _tail_bounds(act, z)
+    assert (ea < 1e-4 * np.abs(a)).all() and (eda < 1e-4 * np.abs(da)).all()
+
+
+@gpu
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_in_the_tails(act):
+    """Values and derivatives keep their bits where they are small: the layer's input is zero, so z is the bias."""
+    far = 91.0 if act == "silu" else 12.9  # to where the results leave fp32's normal numbers
+    for d_out, d_in, r in ((256, 256, 64), (1100, 130, 70)):  # one workgroup; decode and the matrix-core regime
+        layer, _ = _act_layer(d_out, d_in, r)
+        bias = torch.linspace(-far, far, d_out, device=DEV)
+        a, _, err, _ = _tail_bounds(act, _np(bias))
+        for T in (1, 3, 20):
+            x = torch.zeros(T, d_in, device=DEV)
+            _close(nq.lrb_linear_act(layer, x, act, bias=bias), np.tile(a, (T, 1)), np.tile(err, (T, 1)), (act, T))
+    z = torch.linspace(-far, far, 4099, device=DEV)[None].repeat(3, 1)
+    a, da, err, derr = _tail_bounds(act, _np(z))
+    dz, dmul, _ = nq.act_grads(act, z, torch.ones_like(z), mul=torch.ones_like(z))
+    _close(dz, da, derr, (act, "dz"))
+    _close(dmul, a, err, (act, "dmul"))
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_of_infinities(act):
+    """Infinite values are the formulas' (and products of infinity and zero NaN), as the derivatives' are."""
+    layer, _ = _act_layer(300, 40, 33)
+    inf = float("inf")
+    bias = torch.zeros(300, device=DEV)
+    bias[:4] = torch.tensor([inf, -inf, float("nan"), 3e38], device=DEV)
+    for T in (1, 5, 20):
+        x = torch.zeros(T, 40, device=DEV)
+        res = torch.zeros(T, 300, device=DEV)
+        res[:, 7], res[:, 8], res[:, 0] = inf, -inf, 5.0
+        got = _np(nq.lrb_linear_act(layer, x, act, bias=bias, residual=res))
+        with np.errstate(all="ignore"):
+            want = D.epilogue_ref(np.zeros((T, 300)), act, _np(bias), None, _np(res))[0]
+        odd = ~np.isfinite(want)
+        assert odd[:, [0, 2, 7, 8]].all() and np.array_equal(got[odd], want[odd], equal_nan=True), act
+        assert np.isfinite(got[~odd]).all()
+    z = torch.tensor([inf, -inf, float("nan"), 1.0], device=DEV)[None]
+    with np.errstate(all="ignore"):
+        want = D.act_ref(act, _np(z))[1]
+    dz = _np(nq.act_grads(act, z, torch.ones_like(z))[0])
+    assert np.array_equal(np.isnan(dz), np.isnan(want)) and np.array_equal(dz[0, :2], want[0, :2], equal_nan=True)
