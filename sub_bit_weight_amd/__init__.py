@@ -219,8 +219,6 @@ def _on(stream):
 
 
 _NO_CONTEXT = contextlib.nullcontext()
-# without torch.cuda.current_device's check for initialisation: a device tensor is at hand
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 @contextlib.contextmanager
@@ -232,7 +230,7 @@ def _device_and_stream(dev, stream):
 def _call_on(dev: torch.device, stream):
     """Allocation and launch context of a call whose tensors are on `dev`: that
     device current, and `stream` (see _on)."""
-    if stream is None and dev.index == _current_device():
+    if stream is None and dev.index == torch.cuda.current_device():
         return _NO_CONTEXT
     return _device_and_stream(dev, stream)
 

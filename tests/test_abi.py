@@ -347,3 +347,8 @@ def test_every_dtype_value_is_checked(dtype):
     lib = nq.lib()
     assert _linear(_layer(), dtype=dtype) == nq.NQ_ERR_ARG
     assert lib.nq_lrb_linear_noalloc(ctypes.byref(_layer()), DUMMY, dtype, 1, DUMMY, None) == nq.NQ_ERR_ARG
+
+
+def test_the_binding_asks_for_the_current_device_by_its_public_name():
+    src = open(nq.__file__).read()
+    assert "_cuda_getDevice" not in src and "torch.cuda.current_device()" in src
