@@ -302,8 +302,16 @@ def fill_random_words(n: int, seed: int, device="cuda", out: torch.Tensor | None
 # ---------------------------------------------------------------- layer
 
 
+class _Handle:
+    """Tensors whose C struct is kept between calls.  The struct holds addresses, so a copy or a saved file goes
+    without it; it is built anew there."""
+
+    def __getstate__(self):
+        return {**self.__dict__, "_struct": None}
+
+
 @dataclass
-class Lrb:
+class Lrb(_Handle):
     """One packed LRB matrix on the device (the tensors are kept alive here)."""
     d_out: int
     d_in: int
@@ -552,7 +560,7 @@ def lrb_scale_grads_batch(layers, adjs, xs, gs, workspace: torch.Tensor | None =
 # ---------------------------------------------------------------- adapters
 
 @dataclass
-class Lora:
+class Lora(_Handle):
     """A pool of low-rank adapters of one linear on the device: adapter i adds
     scale[i] * b[i] @ a[i].  a and b share a dtype (float32 or bfloat16) and may
     be strided views whose last dimension is contiguous."""
@@ -914,7 +922,7 @@ def act_grads(act: str, z: torch.Tensor | None, dy: torch.Tensor, mul: torch.Ten
 
 
 @dataclass
-class Teacher:
+class Teacher(_Handle):
     """A teacher's record on the device: per row the ids and log-probabilities (at `temperature`) of its
     likeliest tokens, and the log-probability of all the others together (rest; None: the listed
     probabilities are divided by their sum).  ids < 0: no entry.  Made by logits_top or loaded."""

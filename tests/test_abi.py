@@ -1,10 +1,14 @@
 """The C-ABI library loads, exports every declared symbol, and rejects bad
 arguments on the host before any HIP call (no GPU needed)."""
+import copy
 import ctypes
+import dataclasses
 import os
+import pickle
 import re
 
 import pytest
+import torch
 
 from tests.conftest import ROOT
 
@@ -352,3 +356,19 @@ def test_every_dtype_value_is_checked(dtype):
 def test_the_binding_asks_for_the_current_device_by_its_public_name():
     src = open(nq.__file__).read()
     assert "_cuda_getDevice" not in src and "torch.cuda.current_device()" in src
+
+
+def test_layers_adapters_and_records_are_copied_and_saved_after_use():
+    """The C struct that a handle keeps between its calls holds addresses: a copy or a saved file goes without it."""
+    t = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype)
+    handles = (nq.Lrb(4, 3, 2, t(1, 4, dtype=torch.int32), t(1, 2, dtype=torch.int32), t(4), t(3)),
+               nq.Teacher(t(5, 2, dtype=torch.int32), t(5, 2), t(5), 2.0),
+               nq.Lora(t(1, 2, 3), t(1, 4, 2), t(1)))
+    for h, struct in zip(handles, (nq.nq_lrb, nq.nq_teacher, nq.nq_lora)):
+        object.__setattr__(h, "_struct", struct())  # as struct() leaves it
+        for twin in (copy.copy(h), copy.deepcopy(h), pickle.loads(pickle.dumps(h))):
+            assert type(twin) is type(h) and twin._struct is None
+            for f in dataclasses.fields(h):
+                a, b = getattr(h, f.name), getattr(twin, f.name)
+                assert torch.equal(a, b) if isinstance(a, torch.Tensor) else a == b
+        assert h._struct is not None
