@@ -482,3 +482,107 @@ def test_binding_refuses_wrong_tensors():
                  lambda: nq.distill_loss(nq.Teacher(ids, logp, left, -1.0), x)):
         with pytest.raises(nq.NqError):
             call()
+
+
+# ---------------------------------------------------------------- every kernel that a rule chooses
+
+
+def _many_rows(tag, V):
+    """Distinct rows of every kind (spread, sorted, in runs, equal, masked, not finite), and which of them each of 1030
+    rows is: more rows than 1024 choose fewer threads per row."""
+    rows = np.concatenate([_rows(f"{tag}/{V}", 12, V, "bf16"), synth.round_bf16(_orders(V)), _odd_rows(f"{tag}/odd", V)])
+    order = synth.rng(f"distill/{tag}/{V}/order").permutation(1030) % len(rows)
+    first = np.array([np.flatnonzero(order == i)[0] for i in range(len(rows))])
+    return rows, order, first
+
+
+def _pick(teacher, at):
+    at = torch.from_numpy(at).to(DEV)
+    return nq.Teacher(teacher.ids[at].contiguous(), teacher.logp[at].contiguous(), teacher.rest[at].contiguous(),
+                      teacher.temperature)
+
+
+@gpu
+@pytest.mark.parametrize("V,k", [(32003, 64), (20011, 200), (9000, 128), (40001, 300)])
+def test_top_of_many_rows(V, k):
+    """256 threads a row over several steps (512 for k to 256, 1024 beyond): bounds taken anew, candidates pruned and
+    more than a wave has room for."""
+    rows, order, first = _many_rows("many", V)
+    for dtype in ("bf16", "f32"):
+        z = _dev(rows, dtype)[torch.from_numpy(order).to(DEV)]
+        got = nq.logits_top(z, k)
+        _check_top(rows, k, 1.0, _pick(got, first))
+        again = torch.from_numpy(first[order]).to(DEV)  # rows of the same logits have the same record
+        assert torch.equal(got.ids[again], got.ids)
+        assert torch.equal(got.logp[again].nan_to_num(3.0), got.logp.nan_to_num(3.0))
+        assert torch.equal(got.rest[again].nan_to_num(3.0), got.rest.nan_to_num(3.0))
+
+
+@gpu
+@pytest.mark.parametrize("rest", [True, False])
+@pytest.mark.parametrize("V,k", [(32003, 64), (20011, 700)])
+def test_loss_of_many_rows(V, k, rest):
+    """A loss of more than 1024 rows takes 256 threads a row over several steps."""
+    rows, order, first = _many_rows("manyloss", V)
+    ids, logp, left = _record(f"manyloss/{V}", len(rows), V, k, 1.0, rest)
+    ids[2, 3], ids[3, 5:9], ids[4, 1] = ids[2, 0], -1, V
+    w = (0.25 + synth.rng(f"distill/{V}/w").random(len(rows))).astype(np.float32)
+    w[5] = 0.0
+    P = nq.Teacher(_dev(ids[order]), _dev(logp[order]), None if left is None else _dev(left[order]))
+    at = torch.from_numpy(first).to(DEV)
+    for dtype in ("bf16", "f32"):
+        x = _dev(rows, dtype)[torch.from_numpy(order).to(DEV)]
+        loss = nq.distill_loss(P, x, _dev(w[order]))
+        _check_distill(ids, logp, left, 1.0, rows, w, loss[at])
+        assert torch.equal(loss[at][torch.from_numpy(order).to(DEV)].nan_to_num(-7.0), loss.nan_to_num(-7.0))
+        loss2, grad = nq.distill_grads(P, x, _dev(w[order]))
+        _check_distill(ids, logp, left, 1.0, rows, w, loss2[at], grad[at], dtype)
+
+
+@gpu
+@pytest.mark.parametrize("tau", [2.0 ** -20, 2.0 ** 20])
+@pytest.mark.parametrize("V,k", [(300, 8), (9001, 40)])
+def test_temperatures_at_both_limits(V, k, tau):
+    """The coldest softmax is one token's (or none's beside it), the hottest even; a weight of the temperature keeps
+    the gradient's scale."""
+    T = 4
+    w = np.full(T, min(tau, 1.0), np.float32)
+    for dtype in ("f32", "bf16"):
+        z, s = _rows(f"limits/{V}/z", T, V, dtype), _rows(f"limits/{V}/s", T, V, dtype)
+        s[1] = z[1]
+        s[2, :5] = s[2].max() + 1.0  # several that share the largest value
+        _check_top(z, k, tau, nq.logits_top(_dev(z, dtype), k, temperature=tau))
+        for rest in (True, False):
+            ids, logp, left = _record(f"limits/{V}", T, V, k, tau, rest)
+            P = nq.Teacher(_dev(ids), _dev(logp), None if left is None else _dev(left), tau)
+            loss, grad = nq.distill_grads(P, _dev(s, dtype), _dev(w))
+            _check_distill(ids, logp, left, tau, s, w, loss, grad, dtype)
+            _check_distill(ids, logp, left, tau, s, w, nq.distill_loss(P, _dev(s, dtype), _dev(w)))
+
+
+@gpu
+@pytest.mark.parametrize("rest", [True, False])
+@pytest.mark.parametrize("V,k", [(500, 7), (5003, 60), (40001, 300)])
+def test_listed_gradients_are_those_of_exact_probabilities(V, k, rest):
+    """The listed probabilities and their sums are formed in fp64, so a listed token's gradient is off by the rest's sum
+    alone, w / tau * total q q_rest d, and by the rounding of the result."""
+    T, tau = 3, 1.3
+    ids, logp, left = _record(f"listed/{V}", T, V, k, tau, rest)
+    ids[0, 4] = ids[0, 2]
+    s = _rows(f"listed/{V}/s", T, V, "f32")
+    P = nq.Teacher(_dev(ids), _dev(logp), None if left is None else _dev(left), tau)
+    grad = _host(nq.distill_grads(P, _dev(s))[1])
+    # the call's temperature is an fp32 number, 3.7e-8 below 1.3, and every gradient is in proportion to 1 / temperature:
+    # 0.6 of the rounding that the bound leaves the result
+    tau = float(np.float32(tau))
+    want = D.distill_ref(ids, logp, left, tau, s)[1]
+    for t in range(T):
+        x = s[t].astype(np.float64) / tau
+        listed = np.zeros(V, bool)
+        listed[ids[t]] = True
+        d = D.exp_error(x, listed, THREADS)
+        e = np.exp(x - x.max())
+        q, away = e / e.sum(), e[~listed].sum() / e.sum()
+        total = 1.0 if left is None else np.exp(logp[t].astype(np.float64)).sum() + np.exp(float(left[t]))
+        tol = (total * q * away * d + 1e-14) / tau + EPS * np.abs(want[t])
+        assert (np.abs(grad[t] - want[t]) <= tol)[listed].all(), t
