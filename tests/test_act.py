@@ -471,3 +471,134 @@ def test_activations_of_infinities(act):
         want = D.act_ref(act, _np(z))[1]
     dz = _np(nq.act_grads(act, z, torch.ones_like(z))[0])
     assert np.array_equal(np.isnan(dz), np.isnan(want)) and np.array_equal(dz[0, :2], want[0, :2], equal_nan=True)
+
+
+# ---------------------------------------------------------------- every kernel that a rule chooses
+
+
+@gpu
+@pytest.mark.parametrize("T,d", [(1037, 8195), (5000, 2051), (300, 28677)])
+def test_act_grads_of_many_workgroups(T, d):
+    """Sizes that fill the chip with 16 rows of threads (512 workgroups and more), each walking several tokens in
+    several chunks, with ragged tokens and columns.  Columns are independent, so some are compared: the ends, those
+    around a workgroup's (64 and 128 wide) and the ragged ones."""
+    cols = sorted({0, 1, 7, 63, 64, 127, 128, 129, d // 2, d - 9, d - 8, d - 5, d - 4, d - 3, d - 2, d - 1})
+    for i, act in enumerate(ACTS):
+        for dt in (torch.float32, torch.bfloat16):
+            z, dy = 2 * _rand("w/z", (T, d), dt), _rand("w/dy", (T, d), dt)
+            mul = _rand("w/mul", (T, d), dt) if i % 2 else None
+            dz, dmul, dbias = nq.act_grads(act, z, dy, mul=mul)
+            wz, wm, wb, (ez, em, eb) = D.act_grads_ref(act, _np(z[:, cols]), _np(dy[:, cols]),
+                                                       None if mul is None else _np(mul[:, cols]))
+            _close(dz[:, cols], wz, ez, (act, "dz"))
+            _close(dbias[cols], wb, eb, (act, "dbias"))
+            if mul is not None:
+                _close(dmul[:, cols], wm, em, (act, "dmul"))
+            a, b = dy.clone(), None if mul is None else mul.clone()
+            got = nq.act_grads(act, z, a, mul=b, dz=a, dmul=b)  # in place
+            assert got[0] is a and torch.equal(a, dz) and torch.equal(got[2], dbias)
+            assert mul is None or torch.equal(b, dmul)
+
+
+@gpu
+@pytest.mark.parametrize("T", [9, 40, 200])
+@pytest.mark.parametrize("d_out,d_in,r", [(1100, 1030, 70), (1111, 2050, 130)])
+def test_linear_act_of_a_split_first_stage(d_out, d_in, r, T):
+    """A long input dimension before a small rank: the first product's reduction is split, the second's is not and
+    takes the prepared t and the epilogue in one kernel."""
+    test_linear_act(d_out, d_in, r, T)
+
+
+UNSPLIT = [(1100, 130, 70), (1111, 130, 70), (1111, 1030, 70)]  # the second product whole: its tiles apply the epilogue
+
+
+@gpu
+@pytest.mark.parametrize("d_out,d_in,r", UNSPLIT)
+@pytest.mark.parametrize("T", [30, 130])
+def test_linear_act_in_place_by_tiles(d_out, d_in, r, T):
+    layer, _ = _act_layer(d_out, d_in, r)
+    for dt in (torch.float32, torch.bfloat16):
+        x, mul, res = _rand("it/x", (T, d_in), dt), _rand("it/mul", (T, d_out), dt), _rand("it/res", (T, d_out), dt)
+        z = torch.empty(T, d_out, dtype=dt, device=DEV)
+        want = nq.lrb_linear_act(layer, x, "silu", mul=mul, residual=res, z=z)
+        a, b, z2 = mul.clone(), res.clone(), torch.empty_like(z)
+        assert nq.lrb_linear_act(layer, x, "silu", mul=a, residual=res, y=a, z=z2) is a
+        assert torch.equal(a, want) and torch.equal(z2, z)
+        assert torch.equal(nq.lrb_linear_act(layer, x, "silu", mul=mul, residual=b, y=b), want)
+        both = mul.clone()
+        want2 = nq.lrb_linear_act(layer, x, "gelu", mul=mul, residual=mul)
+        assert torch.equal(nq.lrb_linear_act(layer, x, "gelu", mul=both, residual=both, y=both), want2)
+        y = torch.full((T + 2, d_out), 3.0, dtype=dt, device=DEV)  # rows at any alignment, nothing beside them written
+        nq.lrb_linear_act(layer, x, "silu", mul=mul, residual=res, y=y[1:T + 1])
+        assert torch.equal(y[1:T + 1], want) and (y[0] == 3).all() and (y[T + 1] == 3).all()
+
+
+@gpu
+@pytest.mark.parametrize("d_out,d_in,r", UNSPLIT)
+def test_captured_calls_by_tiles(d_out, d_in, r):
+    layer, _ = _act_layer(d_out, d_in, r)
+    T = 50
+    for dt in (torch.float32, torch.bfloat16):
+        xs = [_rand(f"ct/{i}", (T, d_in), dt) for i in range(3)]
+        mul, res = _rand("ct/mul", (T, d_out), dt), _rand("ct/res", (T, d_out), dt)
+
+        def run(x, z):
+            return nq.lrb_linear_act(layer, x, "gelu_tanh", mul=mul, residual=res, z=z), z
+        want = [run(x, torch.empty(T, d_out, dtype=dt, device=DEV)) for x in xs]
+        x, z = xs[0].clone(), torch.empty(T, d_out, dtype=dt, device=DEV)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run(x, z)
+        for i in (0, 1, 2, 1):
+            x.copy_(xs[i])
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i])), i
+            run(xs[0], torch.empty_like(z))  # eager work between the replays
+
+
+@gpu
+@pytest.mark.parametrize("T", [6, 40])
+def test_a_captured_step_of_scale_only_reconstruction(T):
+    """The step of test_a_step_of_scale_only_reconstruction in one graph, replayed on new inputs and records with
+    eager work between: every result is the eager step's."""
+    d, f, V, k = 96, 260, 1000, 30
+    names = dict(up=(f, d, 60), gate=(f, d, 60), down=(d, f, 60), head=(V, d, 70))
+    dev = {n: _act_layer(*shape)[0] for n, shape in names.items()}
+    adj = {n: nq.Adjoint.of(v) for n, v in dev.items()}
+    bias = 0.1 * _rand("step/bias", (f,), torch.float32)
+    w = torch.full((T,), 1.0 / T, device=DEV)
+
+    def step(x, teacher_logits):
+        teacher = nq.logits_top(teacher_logits, k)
+        up = nq.lrb_linear_act(dev["up"], x)
+        z = torch.empty(T, f, device=DEV)
+        h = nq.lrb_linear_act(dev["gate"], x, "silu", bias=bias, mul=up, z=z)
+        hidden = nq.lrb_linear_act(dev["down"], h, residual=x)
+        logits = nq.lrb_linear_act(dev["head"], hidden)
+        loss, dlogits = nq.distill_grads(teacher, logits, weight=w)
+        dhidden, *head = nq.lrb_scale_grads(dev["head"], adj["head"], hidden, dlogits)
+        dh, *down = nq.lrb_scale_grads(dev["down"], adj["down"], h, dhidden)
+        dz, dup, dbias = nq.act_grads("silu", z, dh, mul=up)
+        dx, *gate = nq.lrb_scale_grads(dev["gate"], adj["gate"], x, dz)
+        dx_up, *ups = nq.lrb_scale_grads(dev["up"], adj["up"], x, dup)
+        return [teacher.ids, teacher.logp, teacher.rest, loss, dlogits, dz, dup, dbias, dx, dx_up, *head, *down, *gate, *ups]
+
+    xs = [_rand(f"step/{T}/x/{i}", (T, d), torch.float32) for i in range(3)]
+    ts = [3 * _rand(f"step/{T}/teacher/{i}", (T, V), torch.float32) for i in range(3)]
+    want = [[t.clone() for t in step(a, b)] for a, b in zip(xs, ts)]
+    assert not torch.equal(want[0][3], want[1][3])
+    x, t = xs[0].clone(), ts[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, t)
+    for i in (0, 1, 2, 1):
+        x.copy_(xs[i]), t.copy_(ts[i])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i])), (i, [torch.equal(a, b) for a, b in zip(out, want[i])])
+        step(xs[2], ts[0])  # eager work between the replays
