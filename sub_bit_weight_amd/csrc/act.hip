@@ -77,9 +77,9 @@ __global__ __launch_bounds__(kCols* kRows) void act_grads_kernel(const ActGrads 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t i = imin(t + u * kRows, t1 - 1) * d + c0;
-        dy[u] = epi_load(G.dy, G.dy_bf16, i);
-        z[u] = G.z ? epi_load(G.z, G.z_bf16, i) : 0.0f;
-        mul[u] = G.mul ? epi_load(G.mul, G.mul_bf16, i) : 1.0f;
+        dy[u] = load_element(G.dy, G.dy_bf16, i);
+        z[u] = G.z ? load_element(G.z, G.z_bf16, i) : 0.0f;
+        mul[u] = G.mul ? load_element(G.mul, G.mul_bf16, i) : 1.0f;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -88,8 +88,8 @@ __global__ __launch_bounds__(kCols* kRows) void act_grads_kernel(const ActGrads 
         float dz, dmul;
         element_grads<ACT>(z[u], mul[u], dy[u], dz, dmul);
         acc[0] += dz;
-        epi_store(G.dz, G.dz_bf16, i, dz);
-        if (G.dmul) epi_store(G.dmul, G.dmul_bf16, i, dmul);
+        store_element(G.dz, G.dz_bf16, i, dz);
+        if (G.dmul) store_element(G.dmul, G.dmul_bf16, i, dmul);
       }
     }
   }

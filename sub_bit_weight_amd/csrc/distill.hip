@@ -11,6 +11,7 @@
 //              = exp(s_v / tau - lse_R) ((P + r) exp(lse_R - lse) - r) / tau        otherwise.
 // The rest has a maximum and a sum of its own, so that neither its mass nor its gradient is the
 // difference of two larger numbers.  One workgroup per row.
+#include "elements.h"
 #include "nq_internal.h"
 
 namespace nq {
@@ -18,16 +19,6 @@ namespace {
 
 constexpr float kInf = __builtin_inff();
 constexpr double kLog2e = 1.4426950408889634;
-
-__device__ inline float row_load(const void* p, bool bf16, int64_t i) {
-  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
-}
-__device__ inline void row_store(void* p, bool bf16, int64_t i, float v) {
-  if (bf16)
-    static_cast<uint16_t*>(p)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
-  else
-    static_cast<float*>(p)[i] = v;
-}
 
 // exp(d / tau) for d <= 0, c = log2(e) / tau: the hardware's 2^x, one unit in the last place and 0 below
 // 2^-126.  c's rounding and the product's are felt |d / tau| times each, as is the difference's.
@@ -165,7 +156,7 @@ __device__ bool row_entries(const DistillArgs& A, int64_t t, const char* x, cons
       S.bad = 1;
     } else if (id >= 0) {
       if (atomicOr(&L.listed[id / 32], 1u << (id % 32)) >> (id % 32) & 1u) S.dup = 1;
-      s = row_load(x, BF16, id);
+      s = load_element(x, BF16, id);
       const double lp = A.P.logp[t * k + e];
       p = exp(lp);
       mass += p;
@@ -299,7 +290,7 @@ __device__ inline void row_listed_grads(const DistillArgs& A, char* dx, const Ro
   for (int e = threadIdx.x; e < (int)A.P.k; e += NT)
     if (L.ids[e] >= 0) {
       const double q = exp(((double)L.sv[e] - R.base) * rtau) * R.inv;
-      row_store(dx, DBF16, L.ids[e], (float)(R.w * (R.total * q - R.scale * L.ps[e])));
+      store_element(dx, DBF16, L.ids[e], (float)(R.w * (R.total * q - R.scale * L.ps[e])));
     }
 }
 
@@ -308,15 +299,10 @@ __device__ inline void constant_row(const DistillArgs& A, int64_t t, char* dx, f
   if (threadIdx.x == 0 && A.loss) A.loss[t] = v;
   if (GRADS)
 #pragma unroll 1
-    for (int i = threadIdx.x; i < A.V; i += NT) row_store(dx, DBF16, i, v);
+    for (int i = threadIdx.x; i < A.V; i += NT) store_element(dx, DBF16, i, v);
 }
 
 // 16 bytes of a row at any alignment of its elements.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 template <bool BF16>
 struct Piece {
   static constexpr int N = BF16 ? 8 : 4;  // elements
@@ -374,11 +360,6 @@ struct Piece {
     return reinterpret_cast<const uint8_t*>(listed)[j / 2] >> (4 * (j % 2)) & 15u;
   }
 };
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ inline uint32_t bf16_pair(float a, float b) {  // one conversion for both
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
 // N results as piece j of a row, past the caches: a gradient's rows are not read again by the call, and
 // what they would push out of the caches is (4096 rows of 131072 bf16: 522 us with plain stores, 456).
 template <int N, bool BF16>
@@ -426,7 +407,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
     return constant_row<NT, GRADS, DBF16>(A, t, dx, __builtin_nanf(""));
   if (S.dup) row_repetitions<NT>(A, L);
   const int it = np * N + tid;
-  float xt = it < V ? row_load(x, BF16, it) : -kInf;
+  float xt = it < V ? load_element(x, BF16, it) : -kInf;
   if (it < V && (L.listed[it / 32] >> (it % 32) & 1u)) xt = -kInf;
   float m = xt, s = exp_scaled(xt - (xt == -kInf ? 0.0f : xt), A.c);
   Pc pc[U];
@@ -470,7 +451,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void di
   const RowConsts R = row_finish<NT, GRADS>(A, t, w, m, s, mass, plogp, L, S);
   if (!GRADS) return;
   if (R.zero) return constant_row<NT, GRADS, DBF16>(A, t, dx, 0.0f);
-  if (it < V) row_store(dx, DBF16, it, R.coef * exp_scaled(xt - R.ref, A.c));
+  if (it < V) store_element(dx, DBF16, it, R.coef * exp_scaled(xt - R.ref, A.c));
   for (;; j0 -= NT * U) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -610,7 +591,7 @@ __device__ void top_by_bits(const TopArgs& A, TopShared<NT>& S, int64_t t, const
     const uint32_t key = at | 1u << b;
     int n = 0;
 #pragma unroll 1
-    for (int i = tid; i < V; i += NT) n += logit_key(row_load(x, bf16, i)) >= key;
+    for (int i = tid; i < V; i += NT) n += logit_key(load_element(x, bf16, i)) >= key;
     if (wg_count<NT>(n, red) >= k) at = key;
   }
   int last = 0x7fffffff;
@@ -619,14 +600,14 @@ __device__ void top_by_bits(const TopArgs& A, TopShared<NT>& S, int64_t t, const
   } else {
     int above = 0;
 #pragma unroll 1
-    for (int i = tid; i < V; i += NT) above += logit_key(row_load(x, bf16, i)) > at;
+    for (int i = tid; i < V; i += NT) above += logit_key(load_element(x, bf16, i)) > at;
     const int need = k - wg_count<NT>(above, red);
     int lo = 0, hi = V - 1;  // the smallest index up to which `need` keys equal the k-th
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
       int n = 0;
 #pragma unroll 1
-      for (int i = tid; i <= mid; i += NT) n += logit_key(row_load(x, bf16, i)) == at;
+      for (int i = tid; i <= mid; i += NT) n += logit_key(load_element(x, bf16, i)) == at;
       if (wg_count<NT>(n, red) >= need)
         hi = mid;
       else
@@ -640,7 +621,7 @@ __device__ void top_by_bits(const TopArgs& A, TopShared<NT>& S, int64_t t, const
   MaxSum rest;
 #pragma unroll 1
   for (int i = tid; i < V; i += NT) {
-    const float v = row_load(x, bf16, i);
+    const float v = load_element(x, bf16, i);
     const uint32_t key = logit_key(v);
     if (key > at || (key == at && i <= last))
       S.cand[atomicAdd(&S.n, 1)] = top_place_key(key, i);  // at most k
@@ -724,7 +705,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void lo
   const char* x = row_at<BF16>(A.logits, t, A.ld);
   if (tid == 0) S.n = S.over = 0;
   const int it = np * N + tid;
-  float xt = it < V ? row_load(x, BF16, it) : -kInf;
+  float xt = it < V ? load_element(x, BF16, it) : -kInf;
   constexpr int H = BF16 ? 2 : 1, G = U * H;  // groups: quarters of a step's pieces, 4 logits each
   float gm[G], bound = 0.0f;
 #pragma unroll

@@ -6,82 +6,10 @@
 
 #include <type_traits>
 
+#include "elements.h"
 #include "nq_internal.h"
 
 namespace nq {
-
-__device__ inline float epi_load(const void* p, bool bf16, int64_t i) {
-  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
-}
-
-// Round to nearest even; NaN stays NaN.
-__device__ inline uint16_t bf16_round(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-
-__device__ inline void epi_store(void* p, bool bf16, int64_t i, float v) {
-  if (bf16)
-    static_cast<uint16_t*>(p)[i] = bf16_round(v);
-  else
-    static_cast<float*>(p)[i] = v;
-}
-
-// N elements of an operand from element i on, at any alignment of its elements.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-template <int N>
-struct Elements {
-  float v[N];
-  __device__ void load(const void* p, bool bf16, int64_t i) {
-    if (bf16) {
-      const uint16_t* q = static_cast<const uint16_t*>(p) + i;
-      uint32_t w[N / 2];
-      if constexpr (N == 8) {
-        const u32x4 d = *reinterpret_cast<const u32x4_a2*>(q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = d[j];
-      } else {
-        const u32x2 d = *reinterpret_cast<const u32x2_a2*>(q);
-        w[0] = d[0], w[1] = d[1];
-      }
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-    } else {
-      const float* q = static_cast<const float*>(p) + i;
-#pragma unroll
-      for (int j = 0; j < N; j += 4) {
-        const u32x4 d = *reinterpret_cast<const u32x4_a4*>(q + j);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[j + k] = __uint_as_float(d[k]);
-      }
-    }
-  }
-  __device__ void store(void* p, bool bf16, int64_t i) const {
-    if (bf16) {
-      uint16_t* q = static_cast<uint16_t*>(p) + i;
-      uint32_t w[N / 2];
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j)
-        w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * j], v[2 * j + 1]}, bf16x2));
-      if constexpr (N == 8)
-        *reinterpret_cast<u32x4_a2*>(q) = u32x4{w[0], w[1], w[2], w[3]};
-      else
-        *reinterpret_cast<u32x2_a2*>(q) = u32x2{w[0], w[1]};
-    } else {
-      float* q = static_cast<float*>(p) + i;
-#pragma unroll
-      for (int j = 0; j < N; j += 4)
-        *reinterpret_cast<u32x4_a4*>(q + j) = u32x4{__float_as_uint(v[j]), __float_as_uint(v[j + 1]),
-                                                   __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3])};
-    }
-  }
-};
 
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
@@ -187,10 +115,10 @@ __device__ __forceinline__ void epilogue_store(const Epilogue& E, float bias, co
   float mul[N], res[N];
   if (E.mul)
 #pragma unroll
-    for (int j = 0; j < N; ++j) mul[j] = epi_load(E.mul, E.mul_bf16, at(j));
+    for (int j = 0; j < N; ++j) mul[j] = load_element(E.mul, E.mul_bf16, at(j));
   if (E.residual)
 #pragma unroll
-    for (int j = 0; j < N; ++j) res[j] = epi_load(E.residual, E.residual_bf16, at(j));
+    for (int j = 0; j < N; ++j) res[j] = load_element(E.residual, E.residual_bf16, at(j));
   with_act(E.act, [&](auto act) __attribute__((always_inline)) {
     // v is rounded before the bias is added: the layer's output, as without an epilogue
 #pragma clang fp contract(off)
@@ -201,8 +129,8 @@ __device__ __forceinline__ void epilogue_store(const Epilogue& E, float bias, co
       float a = act(z);
       if (E.mul) a *= mul[j];
       if (E.residual) a += res[j];
-      if (E.z) epi_store(E.z, E.z_bf16, at(j), z);
-      epi_store(E.y, E.y_bf16, at(j), a);
+      if (E.z) store_element(E.z, E.z_bf16, at(j), z);
+      store_element(E.y, E.y_bf16, at(j), a);
     }
   });
 }
