@@ -480,8 +480,10 @@ typedef struct {
  *   y: [T][d_out], fp32 or bf16 (y_dtype).  W x is computed as by nq_lrb_linear
  *   (the same regimes and arithmetic); the epilogue is fp32 and rounds once, to
  *   y's type (and z to its own).  mul and residual may be x; y may be mul or residual
- *   where the types are equal (in place), but not x; z may not be any of them.  silu
- *   and gelu of -inf are NaN, the products -inf * 0 of their formulas.
+ *   where the types are equal (in place), but not x; z may not be any of them.  z
+ *   and an fp32 y carry the error of W x: of bf16 x at T > 8 that of fp16 operands
+ *   (3e-4 normwise).  silu and gelu of -inf are NaN, the products -inf * 0 of their
+ *   formulas.
  *   workspace: at least nq_lrb_act_workspace_bytes(L, T) bytes, 256-byte aligned
  *   (0 bytes: none, it may be null: small layers at T <= 8).  Streams, graphs and
  *   determinism: as for nq_lrb_linear (NQ_DECODE_TINY does not count here).
@@ -500,8 +502,9 @@ nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, in
  *   dmul must be null; dmul and dbias may be null (not computed); z may be null
  *   where neither act' nor dmul needs it (NQ_ACT_NONE without dmul).  dz may be dy
  *   or z and dmul may be mul where the types are equal (in place).  fp32
- *   arithmetic, each result rounded once; relu'(0) = 0; dbias sums the unrounded dz
- *   in fp32 in a fixed order (deterministic).
+ *   arithmetic, each result rounded once; relu'(0) = 0; silu' and gelu' of +-inf are
+ *   NaN, as their formulas' products inf * 0; dbias sums the unrounded dz in fp32 in
+ *   a fixed order (deterministic).
  *   workspace: at least nq_act_grads_workspace_bytes(T, d) bytes, 256-byte aligned
  *   (0 bytes, or dbias null: none, it may be null); calls that may overlap need one
  *   each.
@@ -532,6 +535,11 @@ nq_status nq_act_grads(nq_act act, const void* z, nq_dtype z_dtype, const void* 
  *   there on, and rest is -inf where nothing else is left (a row of -inf alone: an
  *   empty record).  A row with NaN or +inf has NaN logp and rest (NaN counts as the
  *   largest logit).
+ *   A row is read once; one whose logits are largely equal (padding rows of one
+ *   value, say) or NaN, and some rows of fewer than 8 NQ_TOP_MAX logits, are read
+ *   some 34 + log2 V times instead: a call waits for its slowest row (V = 32000,
+ *   bf16: 0.2 ms for one such row, 1.6 ms among more than 1024 rows; 11 and 53 us
+ *   a call without).
  *
  * nq_distill_loss -- the divergence of a student from the record, row by row.  With
  *   q = softmax(s[t] / temperature), p_e = exp(logp[t][e]), r = exp(rest[t]) and

@@ -690,10 +690,15 @@ __device__ float top_bound(TopShared<NT>& S, const float (&gm)[G], int quota, in
 // One pass over the row.  The maxima of the first step's groups give a bound that at least k logits
 // reach; from there on logits that reach it are candidates, which each wave keeps in LDS in the order it
 // meets them, and the others are the rest, whose sum is taken as in distill_kernel.  The bound is taken
-// anew where the steps double and at the end, and what no longer reaches it joins the rest.  Rows with too
-// many candidates (long runs of equal logits, the largest in few groups) or with NaN are done by bits
-// instead.  Bound by vector instructions, 2900 a wave: 2048 rows of 32000 bf16, k 64, 51 us where their
-// reads alone are 27; one row is a chain of dependent steps, 11.4 us.
+// anew where the steps double and at the end, and what no longer reaches it joins the rest.  Bound by vector
+// instructions, 2900 a wave: 2048 rows of 32000 bf16, k 64, 51 us where their reads alone are 27; one row is
+// a chain of dependent steps, 11.4 us.
+// Rows with more candidates than there is room for or with NaN are done by bits instead: long runs of equal
+// logits, the largest in few groups, and short rows whose last wave has fewer groups than its quota, which
+// makes the bound the lowest finite value (fewer pieces than threads, and not a multiple of 64 of them, or
+// nearly).  us for one row / 2048 of them, bf16: 520, k 64, 42 / 60 where 512 take 9.4 / 15; 1544, k 32,
+// 58 / 89 where 1536 take 9.3 / 17; 3153, k 217, 71 / 193.  A constant row of 32000, k 64, takes 224 alone
+// and 1600 with 256 threads, and a call of 2048 rows as long with one such row in 16 as with nothing else.
 template <bool BF16, int NT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(8))) void logits_top_kernel(const TopArgs A) {
   using Pc = Piece<BF16>;
@@ -876,8 +881,9 @@ hipError_t launch_rows(K kernel, int64_t T, int nt, const DistillArgs& A, std::a
 //   a loss of many rows needs no more than 256 either, the rows fill the chip (2048 rows of 32000: 28 /
 //     29 / 37, of 131072: 100 / 109 / 102), one of few needs them (16 of 131072: 22 / 14 / 13);
 //   a gradient reads back what its threads' registers do not hold, and the fewer rows are under way at
-//     once the more of that is still in the caches (2048 of 131072: 283 / 267 / 240; 16: 41 / 26 / 22);
-//     rows of up to 2048 pieces fit 512 threads' (512 rows of 16384: 12.9 / 12.0 / 14.4).
+//     once the more of that is still in the caches (2048 of 131072: 283 / 267 / 241; 16: 41 / 26 / 22; 2048
+//     of 32000: 61.7 / 61.2 / 60.3, 4096 of them 124 / 123 / 133, 512 22 / 18 / 18); rows of up to 2048
+//     pieces fit 512 threads' (512 rows of 16384: 12.9 / 12.0 / 14.4).
 template <bool GRADS, bool BF16, bool DBF16>
 hipError_t launch_distill_t(int64_t T, const DistillArgs& A, hipStream_t s) {
   static std::atomic<uint64_t> done[3];

@@ -688,9 +688,10 @@ __global__ __launch_bounds__(kThreads, MB == 2 ? 4 : 2) void gemm_kernel(
         }
     }
   // The wave's tile goes through LDS (its own part of the stages), so that memory sees 16-byte pieces of
-  // rows: a lane's own results are one value of each row (560 linears of 2048 tokens: 212.7 ms without, 205.2
-  // with it; an epilogue's operands are read in the same pieces, 2048 x 28672 x 8192 of rank 6336 with silu,
-  // gate and z 953 us element by element, 740 so).
+  // rows: a lane's own results are one value of each row (560 linears of 2048 tokens, two runs of each in turn on
+  // one machine: 216.3 and 216.4 ms without this and the exponents' way, 211.3 and 211.4 with them; an epilogue's
+  // operands are read in the same pieces, 2048 x 28672 x 8192 of rank 6336 with silu, gate and z 953 us element
+  // by element, 740 so).
   const int64_t wcol = n0 + wn * 64, wrow = m0 + wm * 32 * MB;  // the wave's first column and row
   if constexpr (FUSE) {
     // column n is element l32 of its 32-element block, pair-order slot 2*(l32 % 16) + l32/16; kpad_next is
