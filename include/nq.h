@@ -503,8 +503,8 @@ nq_status nq_lrb_linear_act(const nq_lrb* L, const void* x, nq_dtype x_dtype, in
  *   where neither act' nor dmul needs it (NQ_ACT_NONE without dmul).  dz may be dy
  *   or z and dmul may be mul where the types are equal (in place).  fp32
  *   arithmetic, each result rounded once; relu'(0) = 0; silu' and gelu' of +-inf are
- *   NaN, as their formulas' products inf * 0; dbias sums the unrounded dz in fp32 in
- *   a fixed order (deterministic).
+ *   NaN, as their formulas' products inf * 0; dbias sums the unrounded dz in a fixed
+ *   order (deterministic), in fp32 per thread and fp64 across threads and chunks.
  *   workspace: at least nq_act_grads_workspace_bytes(T, d) bytes, 256-byte aligned
  *   (0 bytes, or dbias null: none, it may be null); calls that may overlap need one
  *   each.

@@ -27,7 +27,7 @@ __device__ inline void element_grads(float z, float mul, float dy, float& dz, fl
 }
 
 // A workgroup takes kCols pieces of N columns and tc tokens; each of its kRows rows of threads walks every
-// kRows-th token, and the rows' sums of dz are added in order through LDS into sums[chunk][d].  The d % N
+// kRows-th token, and the rows' sums of dz are added in order, in fp64, through LDS into sums[chunk][d].  The d % N
 // columns past the last whole piece are pieces of one column (all of them one thread's took longer than
 // everything else: 256 x 1117 bf16, gelu, 30 us, 17.8 so).  Bound by the loads and stores where the chip is
 // full (2048 x 28672 bf16, silu and gate: 119 us, 4.9 TB/s), else by the chain of a thread's tokens.
@@ -100,10 +100,10 @@ __global__ __launch_bounds__(kCols* kRows) void act_grads_kernel(const ActGrads 
   for (int c = threadIdx.x; c < kCols * N; c += kCols * kRows) {
     const int64_t piece = first + c / N, at = piece < np ? piece * N + c % N : np * N + (piece - np);
     if (at >= d || (piece >= np && c % N)) continue;
-    float s = part[0][c];
+    double s = part[0][c];
 #pragma unroll
     for (int r = 1; r < kRows; ++r) s += part[r][c];
-    sums[(int64_t)blockIdx.y * d + at] = s;
+    sums[(int64_t)blockIdx.y * d + at] = (float)s;
   }
 }
 
@@ -111,10 +111,10 @@ __global__ __launch_bounds__(256) void chunk_sums_kernel(const float* __restrict
                                                          float* __restrict__ out) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= d) return;
-  float acc = 0.0f;
+  double acc = 0.0;
 #pragma unroll 8
   for (int64_t q = 0; q < n; ++q) acc += sums[q * d + c];
-  out[c] = acc;
+  out[c] = (float)acc;
 }
 
 // Tokens of a chunk: all up to 256 (no second launch for their sums), else 128, more when T has more

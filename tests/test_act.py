@@ -602,3 +602,14 @@ def test_a_captured_step_of_scale_only_reconstruction(T):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i])), (i, [torch.equal(a, b) for a, b in zip(out, want[i])])
         step(xs[2], ts[0])  # eager work between the replays
+
+
+@gpu
+@pytest.mark.parametrize("T,d", [(16, 1117), (64, 1117), (64, 300)])
+def test_bias_gradients_add_across_threads_in_fp64(T, d):
+    """With one token to a thread (16 rows of threads, or 64) nothing is added in fp32: the sum is rounded once."""
+    for dt in (torch.float32, torch.bfloat16):
+        dy = (1 + _rand("once/dy", (T, d), torch.float32).abs()).to(dt)
+        want = _np(dy).sum(0)
+        dbias = _np(nq.act_grads("none", None, dy)[2])
+        assert (np.abs(dbias - want) <= D.EPS32 * (1 + 2.0 ** -20) * want).all()
