@@ -14,29 +14,22 @@ namespace nq {
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// exp(x), x <= 0, as m 2^n: the hardware's 2^x (one unit in the last place) of what x log2(e) is from the
-// nearest whole number, which two constants give with one rounding.  So m is within two units at any x, and
-// ldexp keeps results below the hardware's smallest, 2^-126 (silu of -88 to -104).  One 2^x of the rounded
+// exp(x), x <= 0: the hardware's 2^x (one unit in the last place) of what x log2(e) is from the nearest
+// whole number, which two constants give with one rounding, so that the result is within two units at any x;
+// ldexp keeps what is below the hardware's smallest, 2^-126 (silu of -88 to -104).  One 2^x of the rounded
 // product is off by up to |x| roundings more and 0 there; the linear of 2048 x 28672 x 8192, rank 6336, with
 // silu, gate and z takes 737 us with it, 749 so.
-__device__ inline float exp_parts(float x, int& n) {
+__device__ inline float exp_f(float x) {
   x = fmaxf(x, -256.0f);  // 0 all the same (NaN too: the callers' products keep it)
   const float w = rintf(x * 1.44269502f);
-  n = (int)w;
-  return __builtin_amdgcn_exp2f(fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -w)));
-}
-__device__ inline float exp_f(float x) {
-  int n;
-  const float m = exp_parts(x, n);
-  return ldexpf(m, n);
+  return ldexpf(__builtin_amdgcn_exp2f(fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -w))), (int)w);
 }
 // q = 1 / (1 + exp(-u)) and p = 1 - q = 1 / (1 + exp(u)), each to its own last places.
 struct Logistic {
   float q, p;
 };
 __device__ inline Logistic logistic(float u) {
-  int n;
-  const float m = exp_parts(-fabsf(u), n), r = __builtin_amdgcn_rcpf(1.0f + ldexpf(m, n)), s = ldexpf(m * r, n);
+  const float e = exp_f(-fabsf(u)), r = __builtin_amdgcn_rcpf(1.0f + e), s = e * r;
   return u < 0.0f ? Logistic{s, r} : Logistic{r, s};
 }
 
