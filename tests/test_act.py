@@ -613,3 +613,53 @@ def test_bias_gradients_add_across_threads_in_fp64(T, d):
         want = _np(dy).sum(0)
         dbias = _np(nq.act_grads("none", None, dy)[2])
         assert (np.abs(dbias - want) <= D.EPS32 * (1 + 2.0 ** -20) * want).all()
+
+
+@gpu
+def test_operands_of_more_than_2_to_31_elements():
+    """Rows far behind, at offsets that 32 bits do not hold: 128 rows repeated give their results again."""
+    n, d = 600, 28672
+    T = 128 * n
+    assert T * d > 2 ** 31
+    layer, _ = _act_layer(d, 64, 40)
+    x, mul = _rand("far/x", (128, 64), torch.bfloat16), _rand("far/mul", (128, d), torch.bfloat16)
+    xs, muls = x.repeat(n, 1), mul.repeat(n, 1)
+    z = torch.empty_like(muls)
+    y = nq.lrb_linear_act(layer, xs, "silu", mul=muls, z=z)
+    want, _, err = D.epilogue_ref(_np(nq.lrb_linear(layer, xs[:128].contiguous())), "silu", None, _np(mul))
+    # another number of tokens, another split of the reduction: fp16 operands either way
+    assert np.linalg.norm(_np(y[:128]) - want) <= 2 * G.prefill_tol("bf16") * np.linalg.norm(want) + np.linalg.norm(
+        HALF[torch.bfloat16] * np.abs(want))
+    for at in (T // 2, T - 128 * 21, T - 256, T - 128):
+        assert torch.equal(y[at:at + 128], y[:128]) and torch.equal(z[at:at + 128], z[:128]), at
+    dz, dmul, dbias = nq.act_grads("silu", z, y, mul=muls, dz=y, dmul=muls)
+    for at in (T // 2, T - 128 * 21, T - 256, T - 128):
+        assert torch.equal(dz[at:at + 128], dz[:128]) and torch.equal(dmul[at:at + 128], dmul[:128]), at
+    assert not torch.equal(dz[:128], dmul[:128]) and torch.isfinite(dbias).all()
+
+
+@gpu
+@pytest.mark.parametrize("T", [4, 50])
+def test_calls_on_two_streams_at_once(T):
+    """Linears with an epilogue, plain ones and gradients on two streams, workspaces of each call's own."""
+    layers = [_act_layer(1100, 600, 530)[0], _act_layer(1111, 1030, 70)[0]]
+    xs = [_rand(f"two/x/{L.d_in}", (T, L.d_in), torch.bfloat16) for L in layers]
+    muls = [_rand(f"two/mul/{L.d_out}", (T, L.d_out), torch.bfloat16) for L in layers]
+
+    def run(i):
+        L, x, m = layers[i], xs[i], muls[i]
+        z = torch.empty_like(m)
+        y = nq.lrb_linear_act(L, x, "silu", mul=m, z=z)
+        return [y, z, nq.lrb_linear(L, x), *nq.act_grads("gelu", z, y, mul=m)]
+    want = [run(i) for i in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))

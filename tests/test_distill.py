@@ -586,3 +586,22 @@ def test_listed_gradients_are_those_of_exact_probabilities(V, k, rest):
         total = 1.0 if left is None else np.exp(logp[t].astype(np.float64)).sum() + np.exp(float(left[t]))
         tol = (total * q * away * d + 1e-14) / tau + EPS * np.abs(want[t])
         assert (np.abs(grad[t] - want[t]) <= tol)[listed].all(), t
+
+
+@gpu
+def test_logits_of_more_than_2_to_31_elements():
+    """Rows far behind, at offsets that 32 bits do not hold: eight rows repeated give their results again."""
+    V, n, k = 131072, 2100, 9
+    T = 8 * n
+    assert T * V > 2 ** 31
+    rows = _rows("far", 8, V, "bf16")
+    x = _dev(rows, "bf16").repeat(n, 1)
+    top = nq.logits_top(x, k)
+    _check_top(rows, k, 1.0, nq.Teacher(top.ids[-8:].contiguous(), top.logp[-8:].contiguous(), top.rest[-8:].contiguous()))
+    ids, logp, left = _record("far", 8, V, k, 1.0)
+    P = nq.Teacher(_dev(np.tile(ids, (n, 1))), _dev(np.tile(logp, (n, 1))), _dev(np.tile(left, n)))
+    _check_distill(ids, logp, left, 1.0, rows, None, nq.distill_loss(P, x)[-8:])
+    loss, grad = nq.distill_grads(P, x, dlogits=x)
+    _check_distill(ids, logp, left, 1.0, rows, None, loss[-8:], grad[-8:], "bf16")
+    for t in (T // 2 // 8 * 8, T - 16):
+        assert torch.equal(top.ids[t:t + 8], top.ids[-8:]) and torch.equal(grad[t:t + 8], grad[-8:])
