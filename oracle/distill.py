@@ -125,8 +125,8 @@ def epilogue_ref(v, act="none", bias=None, mul=None, residual=None):
 
     z = v + bias is off by one rounding, which reaches act by its derivative.  An activation's own arithmetic is within
     8 roundings of its value (two or three functions of at most two units each, a product, a quotient) and within 4
-    for each unit of its exponent; its derivative adds at most two such values.  mul and residual round once each.  The
-    hardware's 2^x and reciprocal are 0 below 2^-126, where z of it, and the derivative's parts with it, are lost."""
+    for each unit of its exponent; its derivative adds at most two such values.  mul and residual round once each.
+    Parts below 2^-125, of z of it and of the derivative, are not held to the value."""
     v = np.asarray(v, dtype=np.float64)
     z = v if bias is None else v + np.asarray(bias, dtype=np.float64)
     with np.errstate(invalid="ignore"):
